@@ -6,10 +6,13 @@ of ``include/fp4.h``). This module only marshals arguments:
 
 * ``fp4_quantize``, ``fp4_quantize_noalloc``, ``fp4_dequantize``,
   ``fp4_gemm``, ``fp4_gemm_grouped``, ``fp4_gemm_quantize_output``,
-  ``fp4_quantize_workspace``, ``fp4_status_str`` -- the C entry points with
+  ``fp4_kv_append``, ``fp4_kv_read``, ``fp4_kv_attention``,
+  ``fp4_kv_attention_workspace``, ``fp4_quantize_workspace``,
+  ``fp4_status_str`` -- the C entry points with
   the same names and argument order (integers for device pointers);
 * ``quantize``, ``dequantize``, ``gemm``, ``gemm_grouped``,
-  ``gemm_quantize_output`` -- conveniences over torch device
+  ``gemm_quantize_output``, and ``KVCache`` with ``kv_append``, ``kv_read``,
+  ``kv_attention`` -- conveniences over torch device
   tensors that allocate outputs with torch, pass the current HIP stream and
   raise ``Fp4Error`` on a non-OK status.
 
@@ -19,7 +22,7 @@ raised.
 from __future__ import annotations
 
 import ctypes
-from ctypes import c_int32, c_int64, c_size_t, c_uint32, c_uint64, c_void_p, c_char_p
+from ctypes import c_float, c_int32, c_int64, c_size_t, c_uint32, c_uint64, c_void_p, c_char_p
 from dataclasses import dataclass
 from pathlib import Path
 from typing import Optional
@@ -49,9 +52,13 @@ FP4_STOCHASTIC = 8
 FP4_HADAMARD = 16
 FP4_SCALE_SEARCH = 32
 FP4_TENSOR_SCALE = 64
+# fp4_kv_append_args.flags, fp4_kv_attention_args.flags
+FP4_KV_INTERLEAVED = 256
+FP4_KV_CAUSAL = 1
 
 EXPORTED_SYMBOLS = ("fp4_quantize_workspace", "fp4_quantize", "fp4_quantize_noalloc", "fp4_dequantize", "fp4_gemm",
-                    "fp4_gemm_grouped", "fp4_gemm_quantize_output", "fp4_status_str")
+                    "fp4_gemm_grouped", "fp4_gemm_quantize_output", "fp4_kv_append", "fp4_kv_read",
+                    "fp4_kv_attention_workspace", "fp4_kv_attention", "fp4_status_str")
 
 
 class fp4_quant_opts(ctypes.Structure):
@@ -63,6 +70,82 @@ class fp4_quant_opts(ctypes.Structure):
         ("seed", c_uint64),
         ("offset", c_uint64),
         ("amax_in", c_void_p),
+    ]
+
+
+class fp4_kv_cache(ctypes.Structure):
+    _fields_ = [
+        ("size", c_uint32),
+        ("format", c_int32),
+        ("num_pages", c_int64),
+        ("page_size", c_int32),
+        ("kv_heads", c_int32),
+        ("head_dim", c_int32),
+        ("reserved", c_int32),
+        ("k_codes", c_void_p),
+        ("k_scales", c_void_p),
+        ("v_codes", c_void_p),
+        ("v_scales", c_void_p),
+        ("codes_page_stride", c_int64),
+        ("scales_page_stride", c_int64),
+        ("k_tensor_scale", c_void_p),
+        ("v_tensor_scale", c_void_p),
+    ]
+
+
+class fp4_kv_append_args(ctypes.Structure):
+    _fields_ = [
+        ("size", c_uint32),
+        ("dtype", c_int32),
+        ("flags", c_uint32),
+        ("q_heads", c_int32),
+        ("tokens", c_int64),
+        ("k", c_void_p),
+        ("v", c_void_p),
+        ("q", c_void_p),
+        ("q_out", c_void_p),
+        ("k_token_stride", c_int64),
+        ("k_head_stride", c_int64),
+        ("v_token_stride", c_int64),
+        ("v_head_stride", c_int64),
+        ("q_token_stride", c_int64),
+        ("q_head_stride", c_int64),
+        ("q_out_token_stride", c_int64),
+        ("q_out_head_stride", c_int64),
+        ("slots", c_void_p),
+        ("positions", c_void_p),
+        ("cos_table", c_void_p),
+        ("sin_table", c_void_p),
+        ("max_position", c_int64),
+        ("rotary", c_int32),
+        ("reserved", c_int32),
+    ]
+
+
+class fp4_kv_attention_args(ctypes.Structure):
+    _fields_ = [
+        ("size", c_uint32),
+        ("dtype", c_int32),
+        ("flags", c_uint32),
+        ("q_heads", c_int32),
+        ("batch", c_int64),
+        ("tokens", c_int64),
+        ("q_offsets", c_void_p),
+        ("kv_lens", c_void_p),
+        ("block_table", c_void_p),
+        ("table_stride", c_int64),
+        ("table_width", c_int64),
+        ("max_kv_len", c_int64),
+        ("q", c_void_p),
+        ("out", c_void_p),
+        ("lse", c_void_p),
+        ("q_token_stride", c_int64),
+        ("q_head_stride", c_int64),
+        ("out_token_stride", c_int64),
+        ("out_head_stride", c_int64),
+        ("scale", c_float),
+        ("softcap", c_float),
+        ("window", c_int64),
     ]
 
 
@@ -117,6 +200,16 @@ def lib() -> ctypes.CDLL:
             c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int64, c_void_p,
             ctypes.POINTER(fp4_quant_opts), c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int64, c_void_p,
             c_void_p]
+        L.fp4_kv_append.restype = c_int32
+        L.fp4_kv_append.argtypes = [ctypes.POINTER(fp4_kv_cache), ctypes.POINTER(fp4_kv_append_args), c_void_p]
+        L.fp4_kv_read.restype = c_int32
+        L.fp4_kv_read.argtypes = [ctypes.POINTER(fp4_kv_cache), c_int64, c_void_p, c_void_p, c_void_p, c_int32,
+                                  c_void_p]
+        L.fp4_kv_attention_workspace.restype = c_size_t
+        L.fp4_kv_attention_workspace.argtypes = [ctypes.POINTER(fp4_kv_cache), ctypes.POINTER(fp4_kv_attention_args)]
+        L.fp4_kv_attention.restype = c_int32
+        L.fp4_kv_attention.argtypes = [ctypes.POINTER(fp4_kv_cache), ctypes.POINTER(fp4_kv_attention_args), c_void_p,
+                                       c_size_t, c_void_p]
         L.fp4_status_str.restype = c_char_p
         L.fp4_status_str.argtypes = [c_int32]
         _lib = L
@@ -195,6 +288,22 @@ def fp4_gemm_grouped(fmt, groups, group_offsets, M, N, K, a_codes, lda, a_scales
     return lib().fp4_gemm_grouped(fmt, groups, group_offsets, M, N, K, a_codes, lda, a_scales, lda_scales,
                                   a_tensor_scale, b_codes, ldb, b_group_stride, b_scales, ldb_scales,
                                   b_scales_group_stride, b_tensor_scale, c, c_dtype, ldc, stream)
+
+
+def fp4_kv_append(cache: fp4_kv_cache, args: fp4_kv_append_args, stream) -> int:
+    return lib().fp4_kv_append(ctypes.byref(cache), ctypes.byref(args), stream)
+
+
+def fp4_kv_read(cache: fp4_kv_cache, tokens, slots, k_out, v_out, y_dtype, stream) -> int:
+    return lib().fp4_kv_read(ctypes.byref(cache), tokens, slots, k_out, v_out, y_dtype, stream)
+
+
+def fp4_kv_attention_workspace(cache: fp4_kv_cache, args: fp4_kv_attention_args) -> int:
+    return lib().fp4_kv_attention_workspace(ctypes.byref(cache), ctypes.byref(args))
+
+
+def fp4_kv_attention(cache: fp4_kv_cache, args: fp4_kv_attention_args, workspace, workspace_bytes, stream) -> int:
+    return lib().fp4_kv_attention(ctypes.byref(cache), ctypes.byref(args), workspace, workspace_bytes, stream)
 
 
 # ---------------------------------------------------------------------------
@@ -437,3 +546,252 @@ def gemm_grouped(a: Quantized, b: Quantized, offsets, out_dtype=None, stream=Non
                           _stream(stream))
     _check(st, "fp4_gemm_grouped")
     return c
+
+
+# ---------------------------------------------------------------------------
+# the paged 4-bit key-value cache
+# ---------------------------------------------------------------------------
+class KVCache:
+    """A paged key-value cache in FP4: the handle of its buffers, made once
+    and used by every call on them.
+
+    k_codes, v_codes [pages, kv_heads, page_size, head_dim / 2] and k_scales,
+    v_scales [pages, kv_heads, page_size, head_dim / block] are uint8 device
+    tensors whose pages are dense (keys and values may be halves of one
+    buffer); NVFP4 has fp32 device vectors [kv_heads] of tensor scales. The
+    handle keeps references to them, and their addresses."""
+
+    def __init__(self, fmt, k_codes, k_scales, v_codes, v_scales, k_tensor_scale=None, v_tensor_scale=None):
+        import torch
+        self.fmt = _fmt(fmt)
+        blk = 16 if self.fmt == FP4_NVFP4 else 32
+        if k_codes.dim() != 4:
+            raise ValueError("cache buffers are [pages, kv_heads, page_size, bytes]")
+        pages, heads, page_size, half = k_codes.shape
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page_size, 2 * half
+        self.device = k_codes.device
+        for t, width in ((k_codes, half), (v_codes, half), (k_scales, 2 * half // blk), (v_scales, 2 * half // blk)):
+            if t.dtype != torch.uint8 or t.device != self.device or not t.is_cuda:
+                raise ValueError("cache buffers must be uint8 tensors on one GPU")
+            if tuple(t.shape) != (pages, heads, page_size, width):
+                raise ValueError(f"cache buffer of shape {tuple(t.shape)}, expected {(pages, heads, page_size, width)}")
+            if pages and tuple(t.stride()[1:]) != (page_size * width, width, 1):
+                raise ValueError("the pages of a cache buffer must be dense")
+        for a, b in ((k_codes, v_codes), (k_scales, v_scales)):
+            if pages > 1 and a.stride(0) != b.stride(0):
+                raise ValueError("keys and values must have the same page stride")
+        if self.fmt == FP4_NVFP4:
+            for t in (k_tensor_scale, v_tensor_scale):
+                if (t is None or t.dtype != torch.float32 or t.device != self.device or tuple(t.shape) != (heads,)
+                        or not t.is_contiguous()):
+                    raise ValueError("NVFP4 needs fp32 tensor scales [kv_heads] on the cache's GPU")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.k_tensor_scale, self.v_tensor_scale = k_tensor_scale, v_tensor_scale
+        nv = self.fmt == FP4_NVFP4
+        self.handle = fp4_kv_cache(
+            ctypes.sizeof(fp4_kv_cache), self.fmt, pages, page_size, heads, self.head_dim, 0, k_codes.data_ptr(),
+            k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+            k_codes.stride(0) if pages > 1 else heads * page_size * half,
+            k_scales.stride(0) if pages > 1 else heads * page_size * (2 * half // blk),
+            k_tensor_scale.data_ptr() if nv else None, v_tensor_scale.data_ptr() if nv else None)
+        self._ref = ctypes.byref(self.handle)
+
+    @classmethod
+    def empty(cls, fmt, num_pages, page_size, kv_heads, head_dim, *, k_amax=None, v_amax=None, four_over_six=False,
+              device="cuda"):
+        """A cache of zeros. NVFP4: k_amax and v_amax are the largest
+        magnitudes expected of rotated keys and of values (a number, or one
+        per kv head), from which the tensor scales derive as in quantize()."""
+        import torch
+        fmt = _fmt(fmt)
+        blk = 16 if fmt == FP4_NVFP4 else 32
+        shape = (num_pages, kv_heads, page_size)
+        bufs = [torch.zeros(*shape, w, dtype=torch.uint8, device=device)
+                for w in (head_dim // 2, head_dim // blk, head_dim // 2, head_dim // blk)]
+        scales = [None, None]
+        if fmt == FP4_NVFP4:
+            if k_amax is None or v_amax is None:
+                raise ValueError("NVFP4 needs k_amax and v_amax")
+            # a quotient of tensors is correctly rounded, as fp4_quantize's is (one by a number need not be)
+            div = torch.tensor(1792.0 if four_over_six else 2688.0, dtype=torch.float32, device=device)
+            scales = [(torch.as_tensor(a, dtype=torch.float32, device=device).expand(kv_heads)
+                       / div.expand(kv_heads)).contiguous() for a in (k_amax, v_amax)]
+        return cls(fmt, *bufs, *scales)
+
+
+def _kv_dtype(t, what):
+    import torch
+    if t.dtype is torch.bfloat16:
+        return FP4_BF16
+    if t.dtype is torch.float32:
+        return FP4_F32
+    raise ValueError(f"{what} must be bfloat16 or float32")
+
+
+def _kv_rows(t, cache, tokens, what):
+    """Check a [tokens, heads, head_dim] operand; rows dense, any strides."""
+    if t.dim() != 3 or t.shape[2] != cache.head_dim or (tokens is not None and t.shape[0] != tokens):
+        raise ValueError(f"{what} must be [tokens, heads, head_dim]")
+    if t.stride(2) != 1:
+        raise ValueError(f"{what} rows must be contiguous")
+    if t.device != cache.device:
+        raise ValueError(f"{what} must be on the cache's GPU")
+
+
+def _kv_index(t, cache, shape, dtype, what):
+    if t.dtype is not dtype or tuple(t.shape) != shape or t.device != cache.device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} on the cache's GPU")
+
+
+def _kv_call(cache, stream, call, *owned):
+    """call(stream) on the cache's GPU; `owned` are tensors allocated here: on
+    a stream other than torch's current one, their memory must not be reused
+    before that stream has passed the call."""
+    import torch
+    if cache.device.index != torch.cuda.current_device():
+        with torch.cuda.device(cache.device):
+            return _kv_call(cache, stream, call, *owned)
+    current = torch.cuda.current_stream().cuda_stream
+    if stream is not None and stream != current:
+        for t in owned:
+            if t is not None:
+                t.record_stream(torch.cuda.ExternalStream(stream, device=cache.device))
+        current = stream
+    return call(current)
+
+
+def kv_append(cache: KVCache, k, v, slots, *, q=None, positions=None, cos=None, sin=None, interleaved=False,
+              four_over_six=False, q_out=None, stream=None):
+    """Rotate, quantize and store the keys and values [tokens, kv_heads,
+    head_dim] (bf16 or fp32, any token and head strides) of a step's tokens at
+    their `slots` (int64 [tokens]: page * page_size + row, -1 for padding),
+    and rotate the step's queries [tokens, heads, head_dim]; returns those
+    (q_out if given, else a new tensor; None without q).
+
+    cos, sin: fp32 [positions, rotary / 2] tables, rotary being the number of
+    leading elements of a row that are rotated, in pairs (i, i + rotary / 2),
+    or (2i, 2i + 1) if `interleaved`; positions: int64 [tokens]. Without
+    tables nothing is rotated."""
+    import torch
+    tokens = k.shape[0]
+    _kv_rows(k, cache, None, "k")
+    _kv_rows(v, cache, tokens, "v")
+    dt = _kv_dtype(k, "k")
+    if v.dtype != k.dtype or k.shape[1] != cache.kv_heads or v.shape[1] != cache.kv_heads:
+        raise ValueError("k and v must be [tokens, kv_heads, head_dim] of one dtype")
+    _kv_index(slots, cache, (tokens,), torch.int64, "slots")
+    rotary = max_position = 0
+    if cos is not None:
+        if sin is None or positions is None:
+            raise ValueError("rotation needs cos, sin and positions")
+        max_position, half = cos.shape
+        rotary = 2 * half
+        for t, what in ((cos, "cos"), (sin, "sin")):
+            _kv_index(t, cache, (max_position, half), torch.float32, what)
+        _kv_index(positions, cache, (tokens,), torch.int64, "positions")
+    elif sin is not None:
+        raise ValueError("rotation needs cos, sin and positions")
+    heads = 0
+    made = None
+    qs = os_ = (0, 0)
+    if q is not None:
+        _kv_rows(q, cache, tokens, "q")
+        if q.dtype != k.dtype:
+            raise ValueError("q, k and v must have one dtype")
+        heads = q.shape[1]
+        if q_out is None:
+            q_out = made = torch.empty((tokens, heads, cache.head_dim), dtype=q.dtype, device=q.device)
+        else:
+            _kv_rows(q_out, cache, tokens, "q_out")
+            if q_out.dtype != q.dtype or q_out.shape != q.shape:
+                raise ValueError("q_out must be like q")
+        qs, os_ = q.stride(), q_out.stride()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    ks, vs = k.stride(), v.stride()
+    args = fp4_kv_append_args(
+        ctypes.sizeof(fp4_kv_append_args), dt,
+        (FP4_FOUR_OVER_SIX if four_over_six else 0) | (FP4_KV_INTERLEAVED if interleaved else 0), heads, tokens,
+        k.data_ptr(), v.data_ptr(), q.data_ptr() if heads else None, q_out.data_ptr() if heads else None,
+        ks[0], ks[1], vs[0], vs[1], qs[0], qs[1], os_[0], os_[1], slots.data_ptr(),
+        positions.data_ptr() if rotary else None, cos.data_ptr() if rotary else None,
+        sin.data_ptr() if rotary else None, max_position, rotary, 0)
+    st = _kv_call(cache, stream, lambda s: lib().fp4_kv_append(cache._ref, ctypes.byref(args), s), made)
+    _check(st, "fp4_kv_append")
+    return q_out if q is not None else None
+
+
+def kv_read(cache: KVCache, slots, dtype=None, stream=None):
+    """The keys and values of the given slots (int64 [tokens]) as plain
+    numbers: two [tokens, kv_heads, head_dim] tensors of `dtype` (bf16 unless
+    given, or fp32). A slot outside the cache reads as zeros."""
+    import torch
+    dtype = dtype or torch.bfloat16
+    _kv_index(slots, cache, (slots.numel(),), torch.int64, "slots")
+    shape = (slots.numel(), cache.kv_heads, cache.head_dim)
+    k = torch.empty(shape, dtype=dtype, device=cache.device)
+    v = torch.empty(shape, dtype=dtype, device=cache.device)
+    dt = _kv_dtype(k, "dtype")
+    st = _kv_call(cache, stream, lambda s: lib().fp4_kv_read(cache._ref, shape[0], slots.data_ptr(), k.data_ptr(),
+                                                             v.data_ptr(), dt, s), k, v)
+    _check(st, "fp4_kv_read")
+    return k, v
+
+
+def kv_attention(q, cache: KVCache, block_table, kv_lens, *, q_offsets=None, max_kv_len=None, causal=True, window=0,
+                 softcap=0.0, scale=None, return_lse=False, out=None, stream=None):
+    """Softmax attention of queries [tokens, heads, head_dim] (bf16 or fp32)
+    over the cached rows of their sequences; heads is a multiple of the
+    cache's kv_heads, consecutive heads share a kv head.
+
+    block_table int32 [batch, width]: the pages of each sequence in order;
+    kv_lens int32 [batch]: its cached rows. q_offsets int32 [batch + 1]: the
+    queries of sequence b are rows q_offsets[b]:q_offsets[b + 1]; without it
+    every sequence has one. All three are read on the device; max_kv_len
+    (default: all the table can hold) bounds kv_lens on the host.
+
+    causal: a sequence's queries are its last tokens, each sees the rows up to
+    its own, and with window > 0 only the last `window` of them; otherwise
+    every query sees every row. softcap > 0: scores become
+    softcap * tanh(score / softcap). scale: default head_dim ** -0.5.
+    Returns out (like q), or (out, lse) with fp32 lse [tokens, heads], the
+    logarithm of each row's sum of exponentials; rows that see nothing are 0
+    and -inf."""
+    import torch
+    _kv_rows(q, cache, None, "q")
+    dt = _kv_dtype(q, "q")
+    tokens, heads, dim = q.shape
+    if block_table.dim() != 2 or block_table.dtype is not torch.int32 or block_table.device != cache.device:
+        raise ValueError("block_table must be an int32 [batch, width] tensor on the cache's GPU")
+    batch, width = block_table.shape
+    if width > 1 and block_table.stride(1) != 1:
+        raise ValueError("block_table rows must be contiguous")
+    _kv_index(kv_lens, cache, (batch,), torch.int32, "kv_lens")
+    if q_offsets is not None:
+        _kv_index(q_offsets, cache, (batch + 1,), torch.int32, "q_offsets")
+    made = out
+    if out is None:
+        out = made = torch.empty((tokens, heads, dim), dtype=q.dtype, device=q.device)
+    else:
+        made = None
+        _kv_rows(out, cache, tokens, "out")
+        if out.dtype != q.dtype or out.shape != q.shape:
+            raise ValueError("out must be like q")
+    lse = torch.empty((tokens, heads), dtype=torch.float32, device=q.device) if return_lse else None
+    capacity = width * cache.page_size
+    qs, os_ = q.stride(), out.stride()
+    args = fp4_kv_attention_args(
+        ctypes.sizeof(fp4_kv_attention_args), dt, FP4_KV_CAUSAL if causal else 0, heads, batch, tokens,
+        q_offsets.data_ptr() if q_offsets is not None else None, kv_lens.data_ptr(), block_table.data_ptr(),
+        block_table.stride(0) if batch > 1 else width, width,
+        capacity if max_kv_len is None else min(max_kv_len, capacity), q.data_ptr(), out.data_ptr(),
+        lse.data_ptr() if return_lse else None, qs[0], qs[1], os_[0], os_[1],
+        dim ** -0.5 if scale is None else scale, softcap, window)
+    ref = ctypes.byref(args)
+    L = lib()
+    need = L.fp4_kv_attention_workspace(cache._ref, ref)
+    ws = torch.empty((need,), dtype=torch.uint8, device=q.device) if need else None
+    st = _kv_call(cache, stream, lambda s: L.fp4_kv_attention(cache._ref, ref, ws.data_ptr() if need else None, need, s),
+                  made, lse, ws)
+    _check(st, "fp4_kv_attention")
+    return (out, lse) if return_lse else out

@@ -500,3 +500,242 @@ fp4_status fp4_gemm_grouped(int32_t format, int64_t groups, const int32_t* group
 }
 
 }  // extern "C"
+
+namespace {
+
+bool finite(float x) { return x - x == 0.0f; }
+
+// Checks of a cache handle, and its form for the kernels.
+fp4_status plan_kv_cache(const fp4_kv_cache* c, KvCache* k) {
+  if (!c || c->size != sizeof(fp4_kv_cache) || c->reserved != 0) return FP4_ERR_INVALID;
+  if (c->format != FP4_MXFP4 && c->format != FP4_NVFP4) return FP4_ERR_INVALID;
+  const bool nv = c->format == FP4_NVFP4;
+  const int blk = nv ? 16 : 32;
+  if (c->num_pages < 0 || c->kv_heads < 1 || c->head_dim < blk || c->head_dim > 256 || c->head_dim % blk != 0)
+    return FP4_ERR_INVALID;
+  if (c->page_size < 16 || c->page_size > 32768 || (c->page_size & (c->page_size - 1)) != 0) return FP4_ERR_INVALID;
+  if (c->kv_heads > kMaxGridYZ) return FP4_ERR_UNSUPPORTED;
+  // slots and page offsets are 64-bit; one page of one buffer stays below 2 GiB
+  const int64_t rows = (int64_t)c->kv_heads * c->page_size;
+  if (rows * (c->head_dim / 2) >= (int64_t(1) << 31)) return FP4_ERR_UNSUPPORTED;
+  if (c->num_pages > (int64_t(1) << 31) - 1) return FP4_ERR_UNSUPPORTED;
+  if (c->codes_page_stride < rows * (c->head_dim / 2) || c->scales_page_stride < rows * (c->head_dim / blk))
+    return FP4_ERR_INVALID;
+  if (c->num_pages > 0) {
+    if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales) return FP4_ERR_INVALID;
+    // the last byte's offset is a 64-bit number
+    if (c->codes_page_stride > INT64_MAX / c->num_pages || c->scales_page_stride > INT64_MAX / c->num_pages)
+      return FP4_ERR_INVALID;
+  }
+  if (nv && (!c->k_tensor_scale || !c->v_tensor_scale)) return FP4_ERR_INVALID;
+  if (!aligned(c->k_codes, 16) || !aligned(c->k_scales, 16) || !aligned(c->v_codes, 16) || !aligned(c->v_scales, 16) ||
+      c->codes_page_stride % 16 != 0 || c->scales_page_stride % 16 != 0)
+    return FP4_ERR_ALIGN;
+  if (nv && (!aligned(c->k_tensor_scale, 4) || !aligned(c->v_tensor_scale, 4))) return FP4_ERR_ALIGN;
+  k->nvfp4 = nv;
+  k->pages = c->num_pages;
+  k->page_shift = __builtin_ctz((unsigned)c->page_size);
+  k->heads = c->kv_heads;
+  k->dim = c->head_dim;
+  k->kc = c->k_codes;
+  k->ks = c->k_scales;
+  k->vc = c->v_codes;
+  k->vs = c->v_scales;
+  k->codes_ps = c->codes_page_stride;
+  k->scales_ps = c->scales_page_stride;
+  k->k_ts = c->k_tensor_scale;
+  k->v_ts = c->v_tensor_scale;
+  return FP4_OK;
+}
+
+// A strided [tokens, heads, dim] operand: strides wide enough that rows do
+// not run into each other (either stride may be the outer one), aligned.
+fp4_status check_rows(const void* p, int64_t tokens, int64_t heads, int64_t dim, int64_t ts, int64_t hs, int64_t esize,
+                      bool written) {
+  if (!p || ts < 0 || hs < 0) return FP4_ERR_INVALID;
+  if (written) {
+    const bool token_outer = (heads == 1 || hs >= dim) && (tokens == 1 || ts >= (heads - 1) * hs + dim);
+    const bool head_outer = (tokens == 1 || ts >= dim) && (heads == 1 || hs >= (tokens - 1) * ts + dim);
+    if (!token_outer && !head_outer) return FP4_ERR_INVALID;
+  }
+  if (!aligned(p, 16) || (tokens > 1 && (ts * esize) % 16 != 0) || (heads > 1 && (hs * esize) % 16 != 0))
+    return FP4_ERR_ALIGN;
+  return FP4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+fp4_status fp4_kv_append(const fp4_kv_cache* cache, const fp4_kv_append_args* args, void* stream) {
+  KvAppendArgs a{};
+  fp4_status st = plan_kv_cache(cache, &a.c);
+  if (st != FP4_OK) return st;
+  if (!args || args->size != sizeof(fp4_kv_append_args) || args->reserved != 0) return FP4_ERR_INVALID;
+  if (args->dtype != FP4_F32 && args->dtype != FP4_BF16) return FP4_ERR_INVALID;
+  if (args->flags & ~(uint32_t)(FP4_FOUR_OVER_SIX | FP4_KV_INTERLEAVED)) return FP4_ERR_INVALID;
+  if (args->tokens < 0 || args->q_heads < 0) return FP4_ERR_INVALID;
+  if (args->rotary < 0 || args->rotary > cache->head_dim || args->rotary % 2 != 0 || args->max_position < 0)
+    return FP4_ERR_INVALID;
+  if (args->q_heads > kMaxGridYZ || args->tokens > (int64_t(1) << 30)) return FP4_ERR_UNSUPPORTED;
+  if (args->tokens == 0) return FP4_OK;
+  const int64_t es = args->dtype == FP4_BF16 ? 2 : 4, T = args->tokens, D = cache->head_dim;
+  if (!args->slots) return FP4_ERR_INVALID;
+  if (args->rotary > 0 && (!args->positions || !args->cos_table || !args->sin_table)) return FP4_ERR_INVALID;
+  st = check_rows(args->k, T, cache->kv_heads, D, args->k_token_stride, args->k_head_stride, es, false);
+  if (st != FP4_OK) return st;
+  st = check_rows(args->v, T, cache->kv_heads, D, args->v_token_stride, args->v_head_stride, es, false);
+  if (st != FP4_OK) return st;
+  if (args->q_heads > 0) {
+    st = check_rows(args->q, T, args->q_heads, D, args->q_token_stride, args->q_head_stride, es, false);
+    if (st != FP4_OK) return st;
+    st = check_rows(args->q_out, T, args->q_heads, D, args->q_out_token_stride, args->q_out_head_stride, es, true);
+    if (st != FP4_OK) return st;
+  }
+  if (!aligned(args->slots, 8) || !aligned(args->positions, 8) || !aligned(args->cos_table, 4) ||
+      !aligned(args->sin_table, 4))
+    return FP4_ERR_ALIGN;
+  st = check_device();
+  if (st != FP4_OK) return st;
+  a.bf16 = args->dtype == FP4_BF16;
+  a.four_over_six = (args->flags & FP4_FOUR_OVER_SIX) != 0;
+  a.interleaved = (args->flags & FP4_KV_INTERLEAVED) != 0;
+  a.tokens = T;
+  a.q_heads = args->q_heads;
+  a.rotary = args->rotary;
+  a.k = args->k;
+  a.v = args->v;
+  a.q = args->q;
+  a.q_out = args->q_out;
+  a.k_ts_ = args->k_token_stride;
+  a.k_hs = args->k_head_stride;
+  a.v_ts_ = args->v_token_stride;
+  a.v_hs = args->v_head_stride;
+  a.q_ts_ = args->q_token_stride;
+  a.q_hs = args->q_head_stride;
+  a.o_ts_ = args->q_out_token_stride;
+  a.o_hs = args->q_out_head_stride;
+  a.slots = args->slots;
+  a.positions = args->positions;
+  a.cos_t = args->cos_table;
+  a.sin_t = args->sin_table;
+  a.max_position = args->max_position;
+  (void)hipGetLastError();
+  return launch_kv_append(a, static_cast<hipStream_t>(stream)) == hipSuccess ? FP4_OK : FP4_ERR_HIP;
+}
+
+fp4_status fp4_kv_read(const fp4_kv_cache* cache, int64_t tokens, const int64_t* slots, void* k_out, void* v_out,
+                       int32_t y_dtype, void* stream) {
+  KvReadArgs a{};
+  fp4_status st = plan_kv_cache(cache, &a.c);
+  if (st != FP4_OK) return st;
+  if (y_dtype != FP4_F32 && y_dtype != FP4_BF16) return FP4_ERR_INVALID;
+  if (tokens < 0) return FP4_ERR_INVALID;
+  if (tokens > (int64_t(1) << 30) ||
+      (tokens * cache->kv_heads * (cache->head_dim / 16) + 255) / 256 > kMaxGridX)
+    return FP4_ERR_UNSUPPORTED;
+  if (tokens == 0) return FP4_OK;
+  if (!slots || !k_out || !v_out) return FP4_ERR_INVALID;
+  if (!aligned(slots, 8) || !aligned(k_out, 16) || !aligned(v_out, 16)) return FP4_ERR_ALIGN;
+  st = check_device();
+  if (st != FP4_OK) return st;
+  a.tokens = tokens;
+  a.slots = slots;
+  a.k = k_out;
+  a.v = v_out;
+  a.bf16 = y_dtype == FP4_BF16;
+  (void)hipGetLastError();
+  return launch_kv_read(a, static_cast<hipStream_t>(stream)) == hipSuccess ? FP4_OK : FP4_ERR_HIP;
+}
+
+// Checks of the attention call that need sizes only, and its plan.
+static fp4_status plan_kv_attention_call(const fp4_kv_cache* cache, const fp4_kv_attention_args* args, KvAttnArgs* a,
+                                         KvAttnPlan* p) {
+  fp4_status st = plan_kv_cache(cache, &a->c);
+  if (st != FP4_OK) return st;
+  if (!args || args->size != sizeof(fp4_kv_attention_args)) return FP4_ERR_INVALID;
+  if (args->dtype != FP4_F32 && args->dtype != FP4_BF16) return FP4_ERR_INVALID;
+  if (args->flags & ~(uint32_t)FP4_KV_CAUSAL) return FP4_ERR_INVALID;
+  if (args->batch < 0 || args->tokens < 0 || args->q_heads < 1 || args->q_heads % cache->kv_heads != 0)
+    return FP4_ERR_INVALID;
+  if (args->table_width < 0 || args->table_stride < args->table_width || args->max_kv_len < 0 || args->window < 0)
+    return FP4_ERR_INVALID;
+  if (args->table_width > (int64_t(1) << 31) - 1) return FP4_ERR_UNSUPPORTED;
+  if (args->max_kv_len > args->table_width * cache->page_size) return FP4_ERR_INVALID;
+  if (args->window > 0 && !(args->flags & FP4_KV_CAUSAL)) return FP4_ERR_INVALID;
+  if (!finite(args->scale) || !finite(args->softcap) || args->softcap < 0.0f) return FP4_ERR_INVALID;
+  if (!args->q_offsets && args->tokens != args->batch) return FP4_ERR_INVALID;
+  // rows and keys are counted in 32 bits
+  if (args->q_heads > kMaxGridYZ || args->batch > (1 << 24) || args->tokens > (1 << 24) ||
+      args->tokens * (args->q_heads / cache->kv_heads) > (1 << 30) || args->max_kv_len > (1 << 30))
+    return FP4_ERR_UNSUPPORTED;
+  a->bf16 = args->dtype == FP4_BF16;
+  a->causal = (args->flags & FP4_KV_CAUSAL) != 0;
+  a->q_heads = args->q_heads;
+  a->group = args->q_heads / cache->kv_heads;
+  a->batch = args->batch;
+  a->tokens = args->tokens;
+  a->offs = args->q_offsets;
+  a->table_stride = args->table_stride;
+  a->table_width = args->table_width;
+  a->max_len = args->max_kv_len;
+  a->window = args->window;
+  *p = KvAttnPlan{};
+  if (args->batch > 0 && args->tokens > 0) {
+    *p = plan_kv_attention(*a);
+    if (p->tiles * p->splits * cache->kv_heads > kMaxGridX) return FP4_ERR_UNSUPPORTED;
+  }
+  return FP4_OK;
+}
+
+size_t fp4_kv_attention_workspace(const fp4_kv_cache* cache, const fp4_kv_attention_args* args) {
+  KvAttnArgs a{};
+  KvAttnPlan p;
+  if (plan_kv_attention_call(cache, args, &a, &p) != FP4_OK) return 0;
+  return p.ws;
+}
+
+fp4_status fp4_kv_attention(const fp4_kv_cache* cache, const fp4_kv_attention_args* args, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  KvAttnArgs a{};
+  KvAttnPlan p;
+  fp4_status st = plan_kv_attention_call(cache, args, &a, &p);
+  if (st != FP4_OK) return st;
+  if (args->batch == 0 || args->tokens == 0) return FP4_OK;
+  if (!args->kv_lens) return FP4_ERR_INVALID;
+  // a table without a column, or a cache without a page, can only serve
+  // sequences without rows
+  if (args->max_kv_len > 0 && (!args->block_table || cache->num_pages == 0)) return FP4_ERR_INVALID;
+  const int64_t es = args->dtype == FP4_BF16 ? 2 : 4;
+  st = check_rows(args->q, args->tokens, args->q_heads, cache->head_dim, args->q_token_stride, args->q_head_stride, es,
+                  false);
+  if (st != FP4_OK) return st;
+  st = check_rows(args->out, args->tokens, args->q_heads, cache->head_dim, args->out_token_stride,
+                  args->out_head_stride, es, true);
+  if (st != FP4_OK) return st;
+  if (!aligned(args->kv_lens, 4) || !aligned(args->q_offsets, 4) || !aligned(args->block_table, 4) ||
+      !aligned(args->lse, 4))
+    return FP4_ERR_ALIGN;
+  if (p.ws > 0) {
+    if (!workspace || workspace_bytes < p.ws) return FP4_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return FP4_ERR_ALIGN;
+  }
+  st = check_device();
+  if (st != FP4_OK) return st;
+  a.lens = args->kv_lens;
+  a.table = args->block_table;
+  a.q = args->q;
+  a.out = args->out;
+  a.lse = args->lse;
+  a.q_ts_ = args->q_token_stride;
+  a.q_hs = args->q_head_stride;
+  a.o_ts_ = args->out_token_stride;
+  a.o_hs = args->out_head_stride;
+  a.scale = args->scale;
+  a.softcap = args->softcap;
+  a.ws = static_cast<float*>(workspace);
+  (void)hipGetLastError();
+  return launch_kv_attention(a, p, static_cast<hipStream_t>(stream)) == hipSuccess ? FP4_OK : FP4_ERR_HIP;
+}
+
+}  // extern "C"

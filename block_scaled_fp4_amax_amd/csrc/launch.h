@@ -106,6 +106,72 @@ struct GemmArgs {
 
 hipError_t launch_gemm(const GemmArgs& g, hipStream_t stream);
 
+// The paged key-value cache, as the kernels take it (strides in bytes).
+struct KvCache {
+  bool nvfp4;
+  int64_t pages;
+  int page_shift;  // page_size = 1 << page_shift
+  int heads, dim;
+  uint8_t *kc, *ks, *vc, *vs;
+  int64_t codes_ps, scales_ps;
+  const float *k_ts, *v_ts;
+};
+
+struct KvAppendArgs {
+  KvCache c;
+  bool bf16, four_over_six, interleaved;
+  int64_t tokens;
+  int q_heads, rotary;
+  const void *k, *v, *q;
+  void* q_out;
+  int64_t k_ts_, k_hs, v_ts_, v_hs, q_ts_, q_hs, o_ts_, o_hs;  // token and head strides, elements
+  const int64_t *slots, *positions;
+  const float *cos_t, *sin_t;
+  int64_t max_position;
+};
+
+hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t stream);
+
+struct KvReadArgs {
+  KvCache c;
+  int64_t tokens;
+  const int64_t* slots;
+  void *k, *v;
+  bool bf16;
+};
+
+hipError_t launch_kv_read(const KvReadArgs& a, hipStream_t stream);
+
+struct KvAttnArgs {
+  KvCache c;
+  bool bf16, causal;
+  int q_heads, group;  // group = q_heads / kv heads
+  int64_t batch, tokens;
+  const int32_t *offs, *lens, *table;  // offs NULL: one query per sequence
+  int64_t table_stride, table_width, max_len;
+  const void* q;
+  void* out;
+  float* lse;
+  int64_t q_ts_, q_hs, o_ts_, o_hs;
+  float scale, softcap;
+  int64_t window;
+  float* ws;
+};
+
+// How a call's work is cut: row tiles (16 rows of one sequence and kv head,
+// or more), and each tile's visible keys into chunks of chunk_keys, at most
+// `splits` of them.
+struct KvAttnPlan {
+  int rows;        // rows of a tile
+  int64_t tiles;   // upper bound over the batch, per kv head
+  int64_t chunk;   // keys
+  int64_t splits;
+  size_t ws;       // bytes of partial results
+};
+
+KvAttnPlan plan_kv_attention(const KvAttnArgs& a);
+hipError_t launch_kv_attention(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t stream);
+
 // Compute units of the current device (cached per device).
 int device_cu_count();
 

@@ -306,6 +306,166 @@ fp4_status fp4_gemm_grouped(int32_t format, int64_t groups, const int32_t* group
                             const uint8_t* b_scales, int64_t ldb_scales, int64_t b_scales_group_stride,
                             const float* b_tensor_scale, void* c, int32_t c_dtype, int64_t ldc, void* stream);
 
+/*
+ * The 4-bit key-value cache of an attention layer ("FP4", section "Inferencia
+ * e Treinamento FP4": serving in FP4; the page's W4A4 layers leave the cache
+ * as the largest tensor of a long context).
+ *
+ * The cache is `num_pages` pages of `page_size` token slots each; slot s lies
+ * at row s % page_size of page s / page_size. A page holds, for each kv head,
+ * page_size rows back to back:
+ *   codes   [kv_heads][page_size][head_dim / 2] bytes,
+ *   scales  [kv_heads][page_size][head_dim / blk] bytes,
+ * packed as every FP4 row of this library (blocks run along head_dim), once
+ * for keys and once for values. Page p starts p * codes_page_stride (p *
+ * scales_page_stride) bytes after the base, so keys and values may share one
+ * buffer. NVFP4: one fp32 tensor scale S_t per kv head for keys and one for
+ * values, fixed by the caller for the cache's life (S_t = T / (6 * 448) with T
+ * the largest magnitude expected, 4 * 448 under FP4_FOUR_OVER_SIX; larger
+ * values saturate); finite normal numbers, anything else counts as 1.
+ *   head_dim   a multiple of blk, 16 to 256
+ *   page_size  a power of two, 16 to 32768
+ *   bases 16-byte aligned, page strides multiples of 16
+ * The struct and the args structs below are host memory, read during the call.
+ */
+typedef struct fp4_kv_cache {
+  uint32_t size;             /* must equal sizeof(fp4_kv_cache) */
+  int32_t format;            /* fp4_format */
+  int64_t num_pages;
+  int32_t page_size;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t reserved;          /* 0 */
+  uint8_t* k_codes;
+  uint8_t* k_scales;
+  uint8_t* v_codes;
+  uint8_t* v_scales;
+  int64_t codes_page_stride;  /* bytes */
+  int64_t scales_page_stride; /* bytes */
+  const float* k_tensor_scale; /* NVFP4: device float[kv_heads]; MXFP4: ignored */
+  const float* v_tensor_scale;
+} fp4_kv_cache;
+
+/* fp4_kv_append_args.flags: FP4_FOUR_OVER_SIX as for fp4_quantize, and */
+enum {
+  /* Rotation pairs are elements (2i, 2i + 1) instead of (i, i + rotary / 2). */
+  FP4_KV_INTERLEAVED = 256u
+};
+
+typedef struct fp4_kv_append_args {
+  uint32_t size;      /* must equal sizeof(fp4_kv_append_args) */
+  int32_t dtype;      /* fp4_dtype of k, v, q and q_out */
+  uint32_t flags;     /* FP4_FOUR_OVER_SIX, FP4_KV_INTERLEAVED; others -> FP4_ERR_INVALID */
+  int32_t q_heads;    /* 0: no queries */
+  int64_t tokens;
+  const void* k;      /* element (t, h, d) at k[t * k_token_stride + h * k_head_stride + d] (elements) */
+  const void* v;
+  const void* q;      /* queries to rotate, or NULL with q_heads = 0 */
+  void* q_out;        /* rotated queries, rounded once to dtype; may be q itself */
+  int64_t k_token_stride, k_head_stride;
+  int64_t v_token_stride, v_head_stride;
+  int64_t q_token_stride, q_head_stride;
+  int64_t q_out_token_stride, q_out_head_stride;
+  const int64_t* slots;     /* device [tokens]: where each token's rows go */
+  const int64_t* positions; /* device [tokens]: row of the tables; unused when rotary = 0 */
+  const float* cos_table;   /* device [max_position][rotary / 2] */
+  const float* sin_table;
+  int64_t max_position;
+  int32_t rotary;           /* elements rotated at the head of each row: even, 0 to head_dim */
+  int32_t reserved;         /* 0 */
+} fp4_kv_append_args;
+
+/*
+ * fp4_kv_append -- rotate, quantize and store the keys and values of `tokens`
+ * tokens, and rotate their queries, in one launch.
+ *   Each pair (a, b) of the first `rotary` elements of a key or query row
+ *   becomes (a c - b s, b c + a s), c and s from row positions[t] of the
+ *   tables, in fp32 with each product and sum rounded once; the rest of the
+ *   row, and values, pass unchanged. Keys and values are then quantized from
+ *   fp32, without rounding in between, exactly as fp4_quantize quantizes rows
+ *   under the given S_t.
+ *   A slot outside [0, num_pages * page_size) stores nothing (padding rows:
+ *   slot -1). A position outside [0, max_position) stores nothing and makes
+ *   the token's q_out rows NaN. Two tokens of one call with the same slot
+ *   leave it unspecified.
+ * Pointers of k, v, q and q_out 16-byte aligned, strides multiples of 16
+ * bytes; q_out either is q with q's strides or does not overlap it.
+ * Errors: FP4_ERR_INVALID (sizes, strides, NULLs), FP4_ERR_UNSUPPORTED (too
+ * many tokens or heads for one launch), FP4_ERR_ALIGN, FP4_ERR_DEVICE,
+ * FP4_ERR_HIP. tokens = 0 is a valid empty call.
+ */
+fp4_status fp4_kv_append(const fp4_kv_cache* cache, const fp4_kv_append_args* args, void* stream);
+
+/*
+ * fp4_kv_read -- the cached rows of `tokens` slots as plain numbers, as
+ * fp4_dequantize gives them: k_out and v_out [tokens][kv_heads][head_dim] of
+ * y_dtype, dense, 16-byte aligned. A slot outside the cache gives zeros.
+ */
+fp4_status fp4_kv_read(const fp4_kv_cache* cache, int64_t tokens, const int64_t* slots, void* k_out, void* v_out,
+                       int32_t y_dtype, void* stream);
+
+/* fp4_kv_attention_args.flags */
+enum {
+  /* Query i of a sequence's n queries, over L cached rows, sees rows 0 to
+   * L - n + i (the queries are the sequence's last tokens). Otherwise every
+   * query sees all L rows. */
+  FP4_KV_CAUSAL = 1u
+};
+
+typedef struct fp4_kv_attention_args {
+  uint32_t size;     /* must equal sizeof(fp4_kv_attention_args) */
+  int32_t dtype;     /* fp4_dtype of q and out */
+  uint32_t flags;    /* FP4_KV_CAUSAL; others -> FP4_ERR_INVALID */
+  int32_t q_heads;   /* a multiple of kv_heads: heads h * G to h * G + G - 1 share kv head h */
+  int64_t batch;     /* sequences */
+  int64_t tokens;    /* queries of all sequences, back to back */
+  const int32_t* q_offsets; /* device [batch + 1]; NULL: one query per sequence (tokens = batch) */
+  const int32_t* kv_lens;   /* device [batch]: cached rows of each sequence */
+  const int32_t* block_table; /* device [batch][table_width]: entry j is the page of rows j * page_size ... */
+  int64_t table_stride;     /* entries from one sequence's row to the next */
+  int64_t table_width;
+  int64_t max_kv_len;       /* upper bound of kv_lens (longer ones are cut), at most table_width * page_size */
+  const void* q;            /* element (t, h, d) at q[t * q_token_stride + h * q_head_stride + d] */
+  void* out;                /* likewise, at its own strides */
+  float* lse;               /* [tokens][q_heads] dense, or NULL */
+  int64_t q_token_stride, q_head_stride;
+  int64_t out_token_stride, out_head_stride;
+  float scale;              /* multiplies q . k */
+  float softcap;            /* > 0: scores become softcap * tanh(score / softcap); 0: off */
+  int64_t window;           /* > 0 (causal only): the last `window` of the rows a query sees; 0: off */
+} fp4_kv_attention_args;
+
+/* Bytes of device workspace fp4_kv_attention needs for these sizes (0 when
+ * none, and for arguments it would reject). Depends on sizes only, not on
+ * pointers. */
+size_t fp4_kv_attention_workspace(const fp4_kv_cache* cache, const fp4_kv_attention_args* args);
+
+/*
+ * fp4_kv_attention -- softmax attention of each sequence's queries over its
+ * cached rows, read in 4 bits:
+ *   s_ij = scale * (q_i . k_j), capped and masked as above;
+ *   lse_i = log sum_j exp(s_ij); out_i = sum_j exp(s_ij - lse_i) v_j,
+ * with k_j and v_j the values the cache stands for, products accumulated and
+ * the softmax's statistics held in fp32. A query that sees no row gets
+ * out = 0 and lse = -inf. bf16: the weights are rounded to 16 bits for the
+ * product with V, out is rounded once. fp32: queries and weights are split
+ * into 16-bit terms, so that the result has fp32 accuracy.
+ *   kv_lens are cut to [0, max_kv_len] and q_offsets clamped into [0, tokens]
+ *   and made nondecreasing, page numbers clamped into [0, num_pages), so no
+ *   device value makes the kernel access memory outside the operands. Table
+ *   entries past a sequence's last page are not used; the rows of its last
+ *   page past its end may hold anything. Rows of out and lse outside every
+ *   sequence are not written.
+ *   q and out 16-byte aligned with strides multiples of 16 bytes.
+ *   workspace: at least fp4_kv_attention_workspace() bytes, 16-byte aligned;
+ *   contents on entry do not matter; not shared by concurrent calls.
+ * Errors: as fp4_kv_append, and FP4_ERR_WORKSPACE; a window without
+ * FP4_KV_CAUSAL, a softcap or scale that is not finite or a negative softcap
+ * -> FP4_ERR_INVALID; num_pages = 0 with work to do -> FP4_ERR_INVALID.
+ */
+fp4_status fp4_kv_attention(const fp4_kv_cache* cache, const fp4_kv_attention_args* args, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
 /* Static string naming a status code; never NULL. */
 const char* fp4_status_str(int32_t status);
 
