@@ -569,7 +569,7 @@ class KVCache:
             raise ValueError("cache buffers are [pages, kv_heads, page_size, bytes]")
         pages, heads, page_size, half = k_codes.shape
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page_size, 2 * half
-        self.device = k_codes.device
+        self.device, self.index = k_codes.device, k_codes.get_device()
         for t, width in ((k_codes, half), (v_codes, half), (k_scales, 2 * half // blk), (v_scales, 2 * half // blk)):
             if t.dtype != torch.uint8 or t.device != self.device or not t.is_cuda:
                 raise ValueError("cache buffers must be uint8 tensors on one GPU")
@@ -621,45 +621,63 @@ class KVCache:
 
 def _kv_dtype(t, what):
     import torch
-    if t.dtype is torch.bfloat16:
+    d = t.dtype
+    if d is torch.bfloat16:
         return FP4_BF16
-    if t.dtype is torch.float32:
+    if d is torch.float32:
         return FP4_F32
     raise ValueError(f"{what} must be bfloat16 or float32")
 
 
 def _kv_rows(t, cache, tokens, what):
-    """Check a [tokens, heads, head_dim] operand; rows dense, any strides."""
-    if t.dim() != 3 or t.shape[2] != cache.head_dim or (tokens is not None and t.shape[0] != tokens):
+    """Check a [tokens, heads, head_dim] operand (rows dense, any strides);
+    returns its shape and strides."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != cache.head_dim or (tokens is not None and shape[0] != tokens):
         raise ValueError(f"{what} must be [tokens, heads, head_dim]")
-    if t.stride(2) != 1:
+    if strides[2] != 1:
         raise ValueError(f"{what} rows must be contiguous")
-    if t.device != cache.device:
+    if t.get_device() != cache.index:
         raise ValueError(f"{what} must be on the cache's GPU")
+    return shape, strides
 
 
 def _kv_index(t, cache, shape, dtype, what):
-    if t.dtype is not dtype or tuple(t.shape) != shape or t.device != cache.device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != cache.index or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} on the cache's GPU")
 
 
-def _kv_call(cache, stream, call, *owned):
-    """call(stream) on the cache's GPU; `owned` are tensors allocated here: on
-    a stream other than torch's current one, their memory must not be reused
-    before that stream has passed the call."""
+def _kv_stream(cache, stream, *made):
+    """The stream to launch on, the current device being the cache's. Tensors
+    made by this call (`made`) for a stream other than torch's current one
+    must not have their memory reused before that stream has passed the call."""
     import torch
-    if cache.device.index != torch.cuda.current_device():
-        with torch.cuda.device(cache.device):
-            return _kv_call(cache, stream, call, *owned)
-    current = torch.cuda.current_stream().cuda_stream
-    if stream is not None and stream != current:
-        for t in owned:
-            if t is not None:
-                t.record_stream(torch.cuda.ExternalStream(stream, device=cache.device))
-        current = stream
-    return call(current)
+    # the handle torch.cuda.current_stream() wraps, without making the object
+    current = torch._C._cuda_getCurrentRawStream(cache.index)
+    if stream is None or stream == current:
+        return current
+    for t in made:
+        if t is not None:
+            t.record_stream(torch.cuda.ExternalStream(stream, device=cache.device))
+    return stream
 
 
+def _on_cache_gpu(call):
+    """Make the cache's GPU current for the call (outputs and the launch)."""
+    import functools
+
+    @functools.wraps(call)
+    def wrapped(*args, **kw):
+        import torch
+        cache = kw.get("cache") or (args[0] if isinstance(args[0], KVCache) else args[1])
+        if torch.cuda.current_device() == cache.index:
+            return call(*args, **kw)
+        with torch.cuda.device(cache.index):
+            return call(*args, **kw)
+    return wrapped
+
+
+@_on_cache_gpu
 def kv_append(cache: KVCache, k, v, slots, *, q=None, positions=None, cos=None, sin=None, interleaved=False,
               four_over_six=False, q_out=None, stream=None):
     """Rotate, quantize and store the keys and values [tokens, kv_heads,
@@ -673,71 +691,73 @@ def kv_append(cache: KVCache, k, v, slots, *, q=None, positions=None, cos=None, 
     or (2i, 2i + 1) if `interleaved`; positions: int64 [tokens]. Without
     tables nothing is rotated."""
     import torch
-    tokens = k.shape[0]
-    _kv_rows(k, cache, None, "k")
-    _kv_rows(v, cache, tokens, "v")
+    kshape, ks = _kv_rows(k, cache, None, "k")
+    tokens = kshape[0]
+    vshape, vs = _kv_rows(v, cache, tokens, "v")
     dt = _kv_dtype(k, "k")
-    if v.dtype != k.dtype or k.shape[1] != cache.kv_heads or v.shape[1] != cache.kv_heads:
+    if v.dtype is not k.dtype or kshape[1] != cache.kv_heads or vshape[1] != cache.kv_heads:
         raise ValueError("k and v must be [tokens, kv_heads, head_dim] of one dtype")
     _kv_index(slots, cache, (tokens,), torch.int64, "slots")
-    rotary = max_position = 0
+    rotary = max_position = heads = 0
+    at_pos = at_cos = at_sin = at_q = at_out = made = None
+    qs = os_ = (0, 0)
     if cos is not None:
         if sin is None or positions is None:
             raise ValueError("rotation needs cos, sin and positions")
         max_position, half = cos.shape
         rotary = 2 * half
-        for t, what in ((cos, "cos"), (sin, "sin")):
-            _kv_index(t, cache, (max_position, half), torch.float32, what)
+        _kv_index(cos, cache, (max_position, half), torch.float32, "cos")
+        _kv_index(sin, cache, (max_position, half), torch.float32, "sin")
         _kv_index(positions, cache, (tokens,), torch.int64, "positions")
+        if rotary:
+            at_pos, at_cos, at_sin = positions.data_ptr(), cos.data_ptr(), sin.data_ptr()
     elif sin is not None:
         raise ValueError("rotation needs cos, sin and positions")
-    heads = 0
-    made = None
-    qs = os_ = (0, 0)
     if q is not None:
-        _kv_rows(q, cache, tokens, "q")
-        if q.dtype != k.dtype:
+        qshape, qs = _kv_rows(q, cache, tokens, "q")
+        if q.dtype is not k.dtype:
             raise ValueError("q, k and v must have one dtype")
-        heads = q.shape[1]
+        heads = qshape[1]
         if q_out is None:
-            q_out = made = torch.empty((tokens, heads, cache.head_dim), dtype=q.dtype, device=q.device)
-        else:
-            _kv_rows(q_out, cache, tokens, "q_out")
-            if q_out.dtype != q.dtype or q_out.shape != q.shape:
-                raise ValueError("q_out must be like q")
-        qs, os_ = q.stride(), q_out.stride()
+            q_out = made = torch.empty(qshape, dtype=q.dtype, device=cache.device)
+        elif q_out.dtype is not q.dtype or q_out.shape != qshape:
+            raise ValueError("q_out must be like q")
+        os_ = _kv_rows(q_out, cache, tokens, "q_out")[1]
+        at_q, at_out = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    ks, vs = k.stride(), v.stride()
     args = fp4_kv_append_args(
         ctypes.sizeof(fp4_kv_append_args), dt,
         (FP4_FOUR_OVER_SIX if four_over_six else 0) | (FP4_KV_INTERLEAVED if interleaved else 0), heads, tokens,
-        k.data_ptr(), v.data_ptr(), q.data_ptr() if heads else None, q_out.data_ptr() if heads else None,
-        ks[0], ks[1], vs[0], vs[1], qs[0], qs[1], os_[0], os_[1], slots.data_ptr(),
-        positions.data_ptr() if rotary else None, cos.data_ptr() if rotary else None,
-        sin.data_ptr() if rotary else None, max_position, rotary, 0)
-    st = _kv_call(cache, stream, lambda s: lib().fp4_kv_append(cache._ref, ctypes.byref(args), s), made)
-    _check(st, "fp4_kv_append")
-    return q_out if q is not None else None
+        k.data_ptr(), v.data_ptr(), at_q, at_out, ks[0], ks[1], vs[0], vs[1], qs[0], qs[1], os_[0], os_[1],
+        slots.data_ptr(), at_pos, at_cos, at_sin, max_position, rotary, 0)
+    st = lib().fp4_kv_append(cache._ref, ctypes.byref(args), _kv_stream(cache, stream, made))
+    if st != FP4_OK:
+        raise Fp4Error(st, "fp4_kv_append")
+    return q_out
 
 
+@_on_cache_gpu
 def kv_read(cache: KVCache, slots, dtype=None, stream=None):
     """The keys and values of the given slots (int64 [tokens]) as plain
     numbers: two [tokens, kv_heads, head_dim] tensors of `dtype` (bf16 unless
     given, or fp32). A slot outside the cache reads as zeros."""
     import torch
-    dtype = dtype or torch.bfloat16
-    _kv_index(slots, cache, (slots.numel(),), torch.int64, "slots")
-    shape = (slots.numel(), cache.kv_heads, cache.head_dim)
-    k = torch.empty(shape, dtype=dtype, device=cache.device)
-    v = torch.empty(shape, dtype=dtype, device=cache.device)
-    dt = _kv_dtype(k, "dtype")
-    st = _kv_call(cache, stream, lambda s: lib().fp4_kv_read(cache._ref, shape[0], slots.data_ptr(), k.data_ptr(),
-                                                             v.data_ptr(), dt, s), k, v)
-    _check(st, "fp4_kv_read")
+    tokens = slots.numel()
+    _kv_index(slots, cache, (tokens,), torch.int64, "slots")
+    # one allocation: keys, then values
+    both = torch.empty((2, tokens, cache.kv_heads, cache.head_dim), dtype=dtype or torch.bfloat16,
+                       device=cache.device)
+    dt = _kv_dtype(both, "dtype")
+    k, v = both.unbind(0)
+    st = lib().fp4_kv_read(cache._ref, tokens, slots.data_ptr(), k.data_ptr(), v.data_ptr(), dt,
+                           _kv_stream(cache, stream, both))
+    if st != FP4_OK:
+        raise Fp4Error(st, "fp4_kv_read")
     return k, v
 
 
+@_on_cache_gpu
 def kv_attention(q, cache: KVCache, block_table, kv_lens, *, q_offsets=None, max_kv_len=None, causal=True, window=0,
                  softcap=0.0, scale=None, return_lse=False, out=None, stream=None):
     """Softmax attention of queries [tokens, heads, head_dim] (bf16 or fp32)
@@ -758,40 +778,42 @@ def kv_attention(q, cache: KVCache, block_table, kv_lens, *, q_offsets=None, max
     logarithm of each row's sum of exponentials; rows that see nothing are 0
     and -inf."""
     import torch
-    _kv_rows(q, cache, None, "q")
+    qshape, qs = _kv_rows(q, cache, None, "q")
     dt = _kv_dtype(q, "q")
-    tokens, heads, dim = q.shape
-    if block_table.dim() != 2 or block_table.dtype is not torch.int32 or block_table.device != cache.device:
+    tokens, heads, dim = qshape
+    if block_table.dim() != 2 or block_table.dtype is not torch.int32 or block_table.get_device() != cache.index:
         raise ValueError("block_table must be an int32 [batch, width] tensor on the cache's GPU")
     batch, width = block_table.shape
-    if width > 1 and block_table.stride(1) != 1:
+    tstride = block_table.stride()
+    if width > 1 and tstride[1] != 1:
         raise ValueError("block_table rows must be contiguous")
     _kv_index(kv_lens, cache, (batch,), torch.int32, "kv_lens")
+    at_offs = None
     if q_offsets is not None:
         _kv_index(q_offsets, cache, (batch + 1,), torch.int32, "q_offsets")
-    made = out
+        at_offs = q_offsets.data_ptr()
+    made = lse = ws = at_lse = at_ws = None
     if out is None:
-        out = made = torch.empty((tokens, heads, dim), dtype=q.dtype, device=q.device)
-    else:
-        made = None
-        _kv_rows(out, cache, tokens, "out")
-        if out.dtype != q.dtype or out.shape != q.shape:
-            raise ValueError("out must be like q")
-    lse = torch.empty((tokens, heads), dtype=torch.float32, device=q.device) if return_lse else None
+        out = made = torch.empty(qshape, dtype=q.dtype, device=cache.device)
+    elif out.dtype is not q.dtype or out.shape != qshape:
+        raise ValueError("out must be like q")
+    os_ = _kv_rows(out, cache, tokens, "out")[1]
+    if return_lse:
+        lse = torch.empty((tokens, heads), dtype=torch.float32, device=cache.device)
+        at_lse = lse.data_ptr()
     capacity = width * cache.page_size
-    qs, os_ = q.stride(), out.stride()
     args = fp4_kv_attention_args(
-        ctypes.sizeof(fp4_kv_attention_args), dt, FP4_KV_CAUSAL if causal else 0, heads, batch, tokens,
-        q_offsets.data_ptr() if q_offsets is not None else None, kv_lens.data_ptr(), block_table.data_ptr(),
-        block_table.stride(0) if batch > 1 else width, width,
-        capacity if max_kv_len is None else min(max_kv_len, capacity), q.data_ptr(), out.data_ptr(),
-        lse.data_ptr() if return_lse else None, qs[0], qs[1], os_[0], os_[1],
-        dim ** -0.5 if scale is None else scale, softcap, window)
+        ctypes.sizeof(fp4_kv_attention_args), dt, FP4_KV_CAUSAL if causal else 0, heads, batch, tokens, at_offs,
+        kv_lens.data_ptr(), block_table.data_ptr(), tstride[0] if batch > 1 else width, width,
+        capacity if max_kv_len is None else min(max_kv_len, capacity), q.data_ptr(), out.data_ptr(), at_lse, qs[0],
+        qs[1], os_[0], os_[1], dim ** -0.5 if scale is None else scale, softcap, window)
     ref = ctypes.byref(args)
     L = lib()
     need = L.fp4_kv_attention_workspace(cache._ref, ref)
-    ws = torch.empty((need,), dtype=torch.uint8, device=q.device) if need else None
-    st = _kv_call(cache, stream, lambda s: L.fp4_kv_attention(cache._ref, ref, ws.data_ptr() if need else None, need, s),
-                  made, lse, ws)
-    _check(st, "fp4_kv_attention")
+    if need:
+        ws = torch.empty((need,), dtype=torch.uint8, device=cache.device)
+        at_ws = ws.data_ptr()
+    st = L.fp4_kv_attention(cache._ref, ref, at_ws, need, _kv_stream(cache, stream, made, lse, ws))
+    if st != FP4_OK:
+        raise Fp4Error(st, "fp4_kv_attention")
     return (out, lse) if return_lse else out

@@ -2,11 +2,11 @@
 //
 //   s = scale (q . k), p = exp(s - max), out = sum(p v) / sum(p)
 //
-// in one pass over the keys with a running maximum and sum. A workgroup of
-// four waves takes 16 rows (row = (query, head of the kv head's group)) of
-// one sequence and kv head and a chunk of their visible keys; each wave takes
-// every fourth 32-key tile of the chunk on its own, with no barrier until the
-// four results are joined through LDS. Long key ranges are cut into chunks
+// in one pass over the keys with a running maximum and sum. A workgroup takes
+// 16 rows (row = (query, head of the kv head's group)) of one sequence and kv
+// head and a chunk of their visible keys; each of its waves takes every n-th
+// 32-key tile of the chunk on its own, with no barrier until the waves'
+// results are joined through LDS. Long key ranges are cut into chunks
 // whose partial results (fp32 sum, maximum, denominator) go to the workspace
 // and are joined by a second kernel.
 //
@@ -28,6 +28,10 @@
 // two per row first, so that no bf16 or fp32 query leaves fp16's range.
 // fp32 calls split the queries (3 bf16 or 2 fp16 terms) and the weights (2
 // terms) and multiply every term.
+// (The block-scaled matrix instruction could take MXFP4 codes as they are,
+// against queries split into two E4M3 terms. It was tried and left: it sums
+// products of an 8-bit operand in groups of eight with about 16 bits, and
+// scores came out up to 2^-16 of sum |q k| off, 300 times fp32's error.)
 #include "fp4_device.h"
 #include "launch.h"
 
@@ -37,7 +41,6 @@ using namespace fp4dev;
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kWaves = 4;
 constexpr int kTileKeys = 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -230,27 +233,52 @@ __device__ __forceinline__ float tensor_scale_of(const float* ts, int h) {
   return s >= kFltMin && s <= 3.40282347e38f ? s : 1.0f;
 }
 
-template <bool BF16>
-__device__ __forceinline__ void store_row(const KvAttnArgs& a, int token, int head, int d, const float* v, int n) {
+// N consecutive elements of a result row.
+template <bool BF16, int N>
+__device__ __forceinline__ void store_row(const KvAttnArgs& a, int token, int head, int d, const float* v) {
+  typedef uint32_t words __attribute__((ext_vector_type(N / 2 > 4 ? 4 : N / 2)));
+  typedef float floats __attribute__((ext_vector_type(N > 4 ? 4 : N)));
   if constexpr (BF16) {
     uint16_t* o = static_cast<uint16_t*>(a.out) + token * a.o_ts_ + head * a.o_hs + d;
+    constexpr int W = N / 2 > 4 ? 4 : N / 2;
 #pragma unroll
-    for (int i = 0; i < n; i += 4)
-      *reinterpret_cast<uint2*>(o + i) = make_uint2(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]));
+    for (int i = 0; i < N; i += 2 * W) {
+      words w;
+#pragma unroll
+      for (int j = 0; j < W; j++) w[j] = pack_bf16(v[i + 2 * j], v[i + 2 * j + 1]);
+      *reinterpret_cast<words*>(o + i) = w;
+    }
   } else {
     float* o = static_cast<float*>(a.out) + token * a.o_ts_ + head * a.o_hs + d;
+    constexpr int W = N > 4 ? 4 : N;
 #pragma unroll
-    for (int i = 0; i < n; i += 4)
-      *reinterpret_cast<float4*>(o + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    for (int i = 0; i < N; i += W) {
+      floats w;
+#pragma unroll
+      for (int j = 0; j < W; j++) w[j] = v[i + j];
+      *reinterpret_cast<floats*>(o + i) = w;
+    }
   }
 }
 
-// A tile's codes and scale bytes in one lane's registers.
-template <int DP, bool NV>
-struct TileRegs {
+// The result of a row: its weighted sum by its denominator, and lse.
+template <bool NV>
+__device__ __forceinline__ float row_factor(const KvAttnArgs& a, int h, float sum) {
+  return sum == 0.0f ? 0.0f : (NV ? tensor_scale_of(a.c.v_ts, h) : 1.0f) / sum;
+}
+template <bool NV>
+__device__ __forceinline__ float row_lse(float top, float sum) {
+  return sum == 0.0f ? -__builtin_huge_valf() : kLn2 * ((NV ? top - kF16Lift : top) + __builtin_amdgcn_logf(sum));
+}
+
+// How one lane holds a 32-key tile's codes and scale bytes.
+template <int DP, bool NV, bool BF16>
+struct Tile {
   static constexpr int kBlk = NV ? 16 : 32;
-  static constexpr int kKWords = DP / 32;                             // of one key row
-  static constexpr int kKScales = DP / 4 > kBlk ? DP / 4 / kBlk : 1;  // blocks those cover
+  // K: words of 8 codes of one key per lane, elements g * DP/4 on, and the
+  // scale bytes over them
+  static constexpr int kKWords = DP / 32;
+  static constexpr int kKScales = DP / 4 > kBlk ? DP / 4 / kBlk : 1;
   static constexpr int kVWords = DP > 128 ? 2 : 1;
   uint32_t k[2][kKWords];
   uint32_t ks[2][kKScales];
@@ -258,18 +286,23 @@ struct TileRegs {
   uint32_t vs[8];
 };
 
-template <int DP, bool NV, bool BF16>
-__global__ __launch_bounds__(256) void kv_attn_kernel(KvAttnArgs a, int splits, int64_t chunk) {
-  using Regs = TileRegs<DP, NV>;
+// Where a tile's rows lie: the pages of its two 16-key halves.
+struct TilePages {
+  int p[2];
+};
+
+// NW waves; FULL: the head size is DP itself.
+template <int DP, bool NV, bool BF16, bool FULL, int NW>
+__global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : DP == 128 ? 2 : 3) void kv_attn_kernel(KvAttnArgs a, int splits, int64_t chunk) {
+  using Regs = Tile<DP, NV, BF16>;
   constexpr int kRows = 16;
   constexpr int kBlk = Regs::kBlk;
   constexpr int kChunkV = DP / 16;  // elements of V per lane = number of O tiles
   constexpr int kQTerms = BF16 ? 1 : NV ? 2 : 3;
   constexpr int kPTerms = BF16 ? 1 : 2;
-  constexpr int kPart = kChunkV < 8 ? kChunkV : 8;  // elements a thread joins at once
-  constexpr int kParts = kChunkV / kPart;
-  __shared__ float s_o[kWaves][kRows][16 * kPart + 4];
-  __shared__ float s_m[kWaves][kRows], s_l[kWaves][kRows];
+  constexpr int kStep = kTileKeys * NW;
+  __shared__ float s_o[NW][kRows][DP + 4];
+  __shared__ float s_m[NW][kRows], s_l[NW][kRows];
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
@@ -281,7 +314,7 @@ __global__ __launch_bounds__(256) void kv_attn_kernel(KvAttnArgs a, int splits, 
   if (split >= tile_chunks(r, chunk)) return;
   const int c_lo = r.lo + (int)(split * chunk);
   const int c_hi = (int)min((int64_t)r.hi, c_lo + chunk);
-  const int D = a.c.dim, G = a.group;
+  const int D = FULL ? DP : a.c.dim, G = a.group;
 
   // this lane's row: its query, and the keys [my_lo, my_hi) it sees
   const int row = r.row0 + c;
@@ -295,9 +328,89 @@ __global__ __launch_bounds__(256) void kv_attn_kernel(KvAttnArgs a, int splits, 
   const int all_hi = a.causal ? min(max(r.len - r.n + t_first + 1, 0), r.len) : r.len;
   const int all_lo = a.window > 0 ? (int)max((int64_t)0, (int64_t)r.len - r.n + t_last + 1 - a.window) : 0;
 
-  // queries, in the order of the K operand
+  const int shift = a.c.page_shift, in_page = (1 << shift) - 1;
+  const int32_t* table = a.table + r.b * a.table_stride;
+  const int row_codes = D >> 1, row_scales = D / kBlk;
+  const int last16 = (r.len - 1) & ~15;  // the last 16 keys that exist
+  // lane offsets within a 16-key half; elements past the head size are read
+  // from the row's beginning and meet queries of 0, or results not stored
+  uint32_t k_at[Regs::kKWords], ks_at[Regs::kKScales];
+#pragma unroll
+  for (int w = 0; w < Regs::kKWords; w++) {
+    const int d = g * (DP / 4) + 8 * w;
+    k_at[w] = c * row_codes + (FULL || d < D ? d >> 1 : 0);
+  }
+#pragma unroll
+  for (int i = 0; i < Regs::kKScales; i++) {
+    const int b = g * (DP / 4) / kBlk + i;
+    ks_at[i] = c * row_scales + (FULL || b < row_scales ? b : 0);
+  }
+  const int vd = FULL || kChunkV * c < D ? kChunkV * c : 0;
+  const uint32_t v_at = 4 * g * row_codes + (vd >> 1), vs_at = 4 * g * row_scales + vd / kBlk;
+
+  auto pages_of = [&](int kt) {
+    TilePages p;
+#pragma unroll
+    for (int sub = 0; sub < 2; sub++) p.p[sub] = table[min(kt + 16 * sub, last16) >> shift];
+    return p;
+  };
+  // 16 keys lie in one page. Keys past the end are read as they lie in the
+  // last page (their scores are masked, their values zeroed below); a half
+  // past the last page is read from there.
+  auto load = [&](int kt, const TilePages& p, Regs& x) {
+#pragma unroll
+    for (int sub = 0; sub < 2; sub++) {
+      const int64_t page = min(max((int64_t)p.p[sub], (int64_t)0), a.c.pages - 1);
+      const int row0 = (h << shift) + (min(kt + 16 * sub, last16) & in_page);
+      const int64_t at_c = page * a.c.codes_ps + (int64_t)row0 * row_codes;
+      const int64_t at_s = page * a.c.scales_ps + (int64_t)row0 * row_scales;
+      const uint8_t *kc = a.c.kc + at_c, *ks = a.c.ks + at_s, *vc = a.c.vc + at_c, *vs = a.c.vs + at_s;
+      if constexpr (FULL && Regs::kKWords == 2) {
+        const u32x2 y = *reinterpret_cast<const u32x2*>(kc + k_at[0]);
+        x.k[sub][0] = y.x;
+        x.k[sub][1] = y.y;
+      } else if constexpr (FULL) {
+#pragma unroll
+        for (int w = 0; w < Regs::kKWords; w += 4) {
+          const u32x4 y = *reinterpret_cast<const u32x4*>(kc + k_at[w]);
+#pragma unroll
+          for (int i = 0; i < 4; i++) x.k[sub][w + i] = y[i];
+        }
+      } else {
+#pragma unroll
+        for (int w = 0; w < Regs::kKWords; w++) x.k[sub][w] = *reinterpret_cast<const uint32_t*>(kc + k_at[w]);
+      }
+#pragma unroll
+      for (int i = 0; i < Regs::kKScales; i++) x.ks[sub][i] = ks[ks_at[i]];
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const uint8_t* y = vc + (v_at + i * row_codes);
+        if constexpr (DP == 64) {
+          x.v[4 * sub + i][0] = *reinterpret_cast<const uint16_t*>(y);
+        } else if constexpr (Regs::kVWords == 2) {
+          const u32x2 z = *reinterpret_cast<const u32x2*>(y);
+          x.v[4 * sub + i][0] = z.x;
+          x.v[4 * sub + i][1] = z.y;
+        } else {
+          x.v[4 * sub + i][0] = *reinterpret_cast<const uint32_t*>(y);
+        }
+        x.vs[4 * sub + i] = vs[vs_at + i * row_scales];
+      }
+    }
+  };
+
+  // the first tile's codes are on their way while the queries are laid out
+  Regs tiles[2];
+  TilePages ahead{};
+  int kt = c_lo + kTileKeys * wave;
+  if (kt < c_hi) {
+    load(kt, pages_of(kt), tiles[0]);
+    if (kt + kStep < c_hi) ahead = pages_of(kt + kStep);
+  }
+
+  // queries, in the order of the K operand; a negative scale goes into them
   u32x4 q[kQTerms][DP / 32];
-  float score_scale = a.scale;
+  float score_scale = __builtin_fabsf(a.scale);
   {
     float x[DP / 4];
 #pragma unroll
@@ -306,7 +419,7 @@ __global__ __launch_bounds__(256) void kv_attn_kernel(KvAttnArgs a, int splits, 
 #pragma unroll
       for (int i = 0; i < 8; i++) x[8 * w + i] = 0.0f;
       if (live && d < D) {
-        const int64_t at = (r.q0 + t) * a.q_ts_ + head * a.q_hs + d;
+        const int64_t at = (int64_t)(r.q0 + t) * a.q_ts_ + (int64_t)head * a.q_hs + d;
         if constexpr (BF16) {
           const uint4 p = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at);
           x[8 * w + 0] = bf16_lo(p.x); x[8 * w + 1] = bf16_hi(p.x);
@@ -318,6 +431,10 @@ __global__ __launch_bounds__(256) void kv_attn_kernel(KvAttnArgs a, int splits, 
           const float4 p0 = p[0], p1 = p[1];
           x[8 * w + 0] = p0.x; x[8 * w + 1] = p0.y; x[8 * w + 2] = p0.z; x[8 * w + 3] = p0.w;
           x[8 * w + 4] = p1.x; x[8 * w + 5] = p1.y; x[8 * w + 6] = p1.z; x[8 * w + 7] = p1.w;
+        }
+        if (a.scale < 0.0f) {
+#pragma unroll
+          for (int i = 0; i < 8; i++) x[8 * w + i] = -x[8 * w + i];
         }
       }
     }
@@ -351,69 +468,7 @@ __global__ __launch_bounds__(256) void kv_attn_kernel(KvAttnArgs a, int splits, 
   for (int j = 0; j < kChunkV; j++) o[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   float m = kNoMax, l = 0.0f;
 
-  const int shift = a.c.page_shift, in_page = (1 << shift) - 1;
-  const int32_t* table = a.table + r.b * a.table_stride;
-  const int row_codes = D >> 1, row_scales = D / kBlk;
-
-  auto load = [&](int kt, Regs& x) {
-#pragma unroll
-    for (int sub = 0; sub < 2; sub++) {
-      const int key0 = kt + 16 * sub;
-      // 16 keys lie in one page; rows past the end hold nothing to be read as
-      // a number, pages past it may not even exist
-      if (key0 < r.len) {
-        const int64_t page = min(max((int64_t)table[key0 >> shift], (int64_t)0), a.c.pages - 1);
-        const int row0 = (h << shift) + (key0 & in_page);
-        const uint8_t* kc = a.c.kc + page * a.c.codes_ps + (int64_t)row0 * row_codes;
-        const uint8_t* ks = a.c.ks + page * a.c.scales_ps + (int64_t)row0 * row_scales;
-        const uint8_t* vc = a.c.vc + page * a.c.codes_ps + (int64_t)row0 * row_codes;
-        const uint8_t* vs = a.c.vs + page * a.c.scales_ps + (int64_t)row0 * row_scales;
-#pragma unroll
-        for (int w = 0; w < Regs::kKWords; w++) {
-          const int d = g * (DP / 4) + 8 * w;
-          x.k[sub][w] = d < D ? *reinterpret_cast<const uint32_t*>(kc + c * row_codes + (d >> 1)) : 0u;
-        }
-#pragma unroll
-        for (int w = 0; w < Regs::kKScales; w++) {
-          const int bi = g * (DP / 4) / kBlk + w;
-          x.ks[sub][w] = bi < row_scales ? ks[c * row_scales + bi] : 0u;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const int k = 4 * g + i, d = kChunkV * c;
-          const bool there = key0 + k < r.len && d < D;
-          const uint8_t* p = vc + k * row_codes + (d >> 1);
-          if constexpr (DP == 64) {
-            x.v[4 * sub + i][0] = there ? *reinterpret_cast<const uint16_t*>(p) : 0u;
-          } else {
-#pragma unroll
-            for (int w = 0; w < Regs::kVWords; w++)
-              x.v[4 * sub + i][w] = there ? reinterpret_cast<const uint32_t*>(p)[w] : 0u;
-          }
-          x.vs[4 * sub + i] = there ? vs[k * row_scales + d / kBlk] : 0u;
-        }
-      } else {
-#pragma unroll
-        for (int w = 0; w < Regs::kKWords; w++) x.k[sub][w] = 0u;
-#pragma unroll
-        for (int w = 0; w < Regs::kKScales; w++) x.ks[sub][w] = 0u;
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-#pragma unroll
-          for (int w = 0; w < Regs::kVWords; w++) x.v[4 * sub + i][w] = 0u;
-          x.vs[4 * sub + i] = 0u;
-        }
-      }
-    }
-  };
-
-  Regs next;
-  int kt = c_lo + kTileKeys * wave;
-  if (kt < c_hi) load(kt, next);
-  for (; kt < c_hi; kt += kTileKeys * kWaves) {
-    const Regs x = next;
-    if (kt + kTileKeys * kWaves < c_hi) load(kt + kTileKeys * kWaves, next);
-
+  auto compute = [&](int kt, Regs& x) {
     float s[8];
 #pragma unroll
     for (int sub = 0; sub < 2; sub++) {
@@ -425,22 +480,32 @@ __global__ __launch_bounds__(256) void kv_attn_kernel(KvAttnArgs a, int splits, 
         for (int n = 0; n < kQTerms; n++) acc = mfma16<NV>(kk, q[n][w], acc);
       }
 #pragma unroll
-      for (int i = 0; i < 4; i++) s[4 * sub + i] = acc[i] * score_scale;
+      for (int i = 0; i < 4; i++) s[4 * sub + i] = acc[i];
     }
+    float factor = score_scale;  // of s, to scores in powers of two
     if (capped) {
 #pragma unroll
-      for (int i = 0; i < 8; i++) s[i] = cap2 * tanh_exp(s[i]);
+      for (int i = 0; i < 8; i++) s[i] = cap2 * tanh_exp(s[i] * score_scale);
+      factor = 1.0f;
     }
     if (kt + kTileKeys > all_hi || kt < all_lo) {
 #pragma unroll
       for (int i = 0; i < 8; i++) {
         const int key = kt + 16 * (i >> 2) + 4 * g + (i & 3);
-        s[i] = key < my_hi && key >= my_lo ? s[i] : -__builtin_huge_valf();
+        s[i] = key < my_hi && key >= my_lo ? s[i] * factor : -__builtin_huge_valf();
+        // a weight of 0 must meet a number
+        if (key >= r.len) {
+#pragma unroll
+          for (int w = 0; w < Regs::kVWords; w++) x.v[i][w] = 0u;
+          x.vs[i] = 0u;
+        }
       }
+      factor = 1.0f;
     }
     float top = s[0];
 #pragma unroll
     for (int i = 1; i < 8; i++) top = __builtin_fmaxf(top, s[i]);
+    top *= factor;
     if (__any(top > m + kSlack)) {
       top = __builtin_fmaxf(top, xor_shfl<16>(top));
       top = __builtin_fmaxf(top, xor_shfl<32>(top));
@@ -454,10 +519,8 @@ __global__ __launch_bounds__(256) void kv_attn_kernel(KvAttnArgs a, int splits, 
     const float base = NV ? m - kF16Lift : m;
     float p[8];
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-      p[i] = __builtin_amdgcn_exp2f(s[i] - base);
-      l += p[i];
-    }
+    for (int i = 0; i < 8; i++) p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], factor, -base));
+    l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
     u32x4 pw[kPTerms];
 #pragma unroll
     for (int n = 0; n < kPTerms; n++) {
@@ -478,113 +541,147 @@ __global__ __launch_bounds__(256) void kv_attn_kernel(KvAttnArgs a, int splits, 
         for (int n = 0; n < kPTerms; n++) o[8 * w + j] = mfma16<NV>(vv, pw[n], o[8 * w + j]);
       }
     }
+  };
+
+  // two tiles' registers in turn: one is loaded while the other is used, and
+  // the page numbers are fetched a tile earlier still
+  for (; kt < c_hi; kt += 2 * kStep) {
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+      const int now = kt + k * kStep;
+      if (now + kStep < c_hi) {
+        load(now + kStep, ahead, tiles[1 - k]);
+        if (now + 2 * kStep < c_hi) ahead = pages_of(now + 2 * kStep);
+      }
+      if (now < c_hi) compute(now, tiles[k]);
+    }
   }
   l += xor_shfl<16>(l);
   l += xor_shfl<32>(l);
 
-  // join the four waves
+  // join the waves: O tile j holds of row c the elements kChunkV * (4g + i) + j
   if (g == 0) {
     s_m[wave][c] = m;
     s_l[wave][c] = l;
   }
-  const int jr = threadIdx.x >> 4, jc = threadIdx.x & 15;  // row and V chunk this thread joins
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+#pragma unroll
+    for (int j = 0; j < kChunkV; j++) s_o[wave][c][(4 * g + i) * kChunkV + j] = o[j][i];
+  }
+  __syncthreads();
+  constexpr int kEach = kRows * DP / (64 * NW);  // elements a thread joins
+  constexpr int kPerRow = DP / kEach;
+  const int jr = threadIdx.x / kPerRow, d = threadIdx.x % kPerRow * kEach;
   const int jrow = r.row0 + jr;
-  const bool jlive = jrow < r.n * G;
-  const int jt = jlive ? jrow / G : 0, jhead = jlive ? h * G + jrow - jt * G : 0;
-  float* part = a.ws ? a.ws + (int64_t)blockIdx.x * (kRows * (D + 2)) : nullptr;
+  if (jrow >= r.n * G || d >= D) return;
+  const int jt = jrow / G, jhead = h * G + jrow - jt * G;
+  float top = s_m[0][jr];
 #pragma unroll
-  for (int half = 0; half < kParts; half++) {
-    if (half) __syncthreads();
+  for (int w = 1; w < NW; w++) top = __builtin_fmaxf(top, s_m[w][jr]);
+  float sum = 0.0f, acc[kEach];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
+  for (int j = 0; j < kEach; j++) acc[j] = 0.0f;
 #pragma unroll
-      for (int j = 0; j < kPart; j++) s_o[wave][c][(4 * g + i) * kPart + j] = o[half * kPart + j][i];
+  for (int w = 0; w < NW; w++) {
+    const float f = __builtin_amdgcn_exp2f(s_m[w][jr] - top);
+    sum += f * s_l[w][jr];
+#pragma unroll
+    for (int j = 0; j < kEach; j++) acc[j] += f * s_o[w][jr][d + j];
+  }
+  if (splits > 1) {
+    float* part = a.ws + (int64_t)blockIdx.x * (kRows * (D + 2));
+#pragma unroll
+    for (int j = 0; j < kEach; j++) part[jr * D + d + j] = acc[j];
+    if (d == 0) {
+      part[kRows * D + jr] = top;
+      part[kRows * (D + 1) + jr] = sum;
     }
-    __syncthreads();
-    float top = s_m[0][jr];
+  } else {
+    const float f = row_factor<NV>(a, h, sum);
 #pragma unroll
-    for (int w = 1; w < kWaves; w++) top = __builtin_fmaxf(top, s_m[w][jr]);
-    float sum = 0.0f, acc[kPart];
-#pragma unroll
-    for (int j = 0; j < kPart; j++) acc[j] = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWaves; w++) {
-      const float f = __builtin_amdgcn_exp2f(s_m[w][jr] - top);
-      sum += f * s_l[w][jr];
-#pragma unroll
-      for (int j = 0; j < kPart; j++) acc[j] += f * s_o[w][jr][jc * kPart + j];
-    }
-    const int d = kChunkV * jc + half * kPart;
-    if (jlive && d < D) {
-      if (splits > 1) {
-        float* po = part + jr * D + d;
-#pragma unroll
-        for (int j = 0; j < kPart; j += 4)
-          *reinterpret_cast<float4*>(po + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-        if (d == 0) {
-          part[kRows * D + jr] = top;
-          part[kRows * (D + 1) + jr] = sum;
-        }
-      } else {
-        const float f = sum > 0.0f || sum != sum ? (NV ? tensor_scale_of(a.c.v_ts, h) : 1.0f) / sum : 0.0f;
-#pragma unroll
-        for (int j = 0; j < kPart; j++) acc[j] *= f;
-        store_row<BF16>(a, r.q0 + jt, jhead, d, acc, kPart);
-        if (d == 0 && a.lse)
-          a.lse[(int64_t)(r.q0 + jt) * a.q_heads + jhead] =
-              sum == 0.0f ? -__builtin_huge_valf() : kLn2 * ((NV ? top - kF16Lift : top) + __builtin_amdgcn_logf(sum));
-      }
-    }
+    for (int j = 0; j < kEach; j++) acc[j] *= f;
+    store_row<BF16, kEach>(a, r.q0 + jt, jhead, d, acc);
+    if (d == 0 && a.lse) a.lse[(int64_t)(r.q0 + jt) * a.q_heads + jhead] = row_lse<NV>(top, sum);
   }
 }
 
-// Joins a row tile's chunks: thread (row, 1/16 of the head).
-template <int DP, bool NV, bool BF16>
-__global__ __launch_bounds__(256) void kv_attn_join_kernel(KvAttnArgs a, int splits, int64_t chunk) {
+// Joins the chunks of one row: DP / 4 lanes take four elements each, and the
+// rest of the workgroup every kGroups-th chunk.
+template <int DP, bool NV, bool BF16, int THREADS>
+__global__ __launch_bounds__(THREADS) void kv_attn_join_kernel(KvAttnArgs a, int splits, int64_t chunk) {
   constexpr int kRows = 16;
-  constexpr int kChunkV = DP / 16;
-  const int h = blockIdx.x % a.c.heads, tile = blockIdx.x / a.c.heads;
+  constexpr int kLanes = DP / 4, kGroups = THREADS / kLanes;
+  __shared__ float s_acc[kGroups][DP + 4];
+  __shared__ float s_m[kGroups], s_l[kGroups];
+  const int jr = blockIdx.x % kRows, th = blockIdx.x / kRows;
+  const int h = th % a.c.heads, tile = th / a.c.heads;
   RowTile r;
   if (!find_tile<kRows>(a, tile, r)) return;
-  const int n = tile_chunks(r, chunk);
   const int D = a.c.dim, G = a.group;
-  const int jr = threadIdx.x >> 4, d = kChunkV * (threadIdx.x & 15);
   const int row = r.row0 + jr;
-  if (row >= r.n * G || d >= D) return;
+  if (row >= r.n * G) return;
+  const int n = tile_chunks(r, chunk);
   const int t = row / G, head = h * G + row - t * G;
   const int64_t step = kRows * (D + 2);
-  const float* part = a.ws + (int64_t)blockIdx.x * splits * step;
-  float top = kNoMax;
-  for (int k = 0; k < n; k++) top = __builtin_fmaxf(top, part[k * step + kRows * D + jr]);
-  float sum = 0.0f, acc[kChunkV];
-#pragma unroll
-  for (int j = 0; j < kChunkV; j++) acc[j] = 0.0f;
+  const float* part = a.ws + (int64_t)th * splits * step;
+  const int grp = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
+  float top = kNoMax, sum = 0.0f;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (d < D) {
 #pragma unroll 4
-  for (int k = 0; k < n; k++) {
-    const float f = __builtin_amdgcn_exp2f(part[k * step + kRows * D + jr] - top);
-    sum += f * part[k * step + kRows * (D + 1) + jr];
-    const float* po = part + k * step + jr * D + d;
-#pragma unroll
-    for (int j = 0; j < kChunkV; j += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(po + j);
-      acc[j] += f * v.x;
-      acc[j + 1] += f * v.y;
-      acc[j + 2] += f * v.z;
-      acc[j + 3] += f * v.w;
+    for (int k = grp; k < n; k += kGroups) {
+      const float* p = part + k * step;
+      const float pm = p[kRows * D + jr], pl = p[kRows * (D + 1) + jr];
+      const float4 v = *reinterpret_cast<const float4*>(p + jr * D + d);
+      const float raised = __builtin_fmaxf(top, pm);
+      const float fo = __builtin_amdgcn_exp2f(top - raised), fn = __builtin_amdgcn_exp2f(pm - raised);
+      top = raised;
+      sum = sum * fo + pl * fn;
+      acc.x = acc.x * fo + v.x * fn;
+      acc.y = acc.y * fo + v.y * fn;
+      acc.z = acc.z * fo + v.z * fn;
+      acc.w = acc.w * fo + v.w * fn;
     }
   }
-  const float f = sum > 0.0f || sum != sum ? (NV ? tensor_scale_of(a.c.v_ts, h) : 1.0f) / sum : 0.0f;
+  if (d == 0) {
+    s_m[grp] = top;
+    s_l[grp] = sum;
+  }
+  *reinterpret_cast<float4*>(&s_acc[grp][d]) = acc;
+  __syncthreads();
+  if (grp != 0 || d >= D) return;
+  const int used = n < kGroups ? n : kGroups;
+  float all = s_m[0];
+  for (int k = 1; k < used; k++) all = __builtin_fmaxf(all, s_m[k]);
+  sum = 0.0f;
+  float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int k = 0; k < used; k++) {
+    const float f = __builtin_amdgcn_exp2f(s_m[k] - all);
+    sum += f * s_l[k];
+    const float4 v = *reinterpret_cast<const float4*>(&s_acc[k][d]);
+    y[0] += f * v.x;
+    y[1] += f * v.y;
+    y[2] += f * v.z;
+    y[3] += f * v.w;
+  }
+  const float f = row_factor<NV>(a, h, sum);
 #pragma unroll
-  for (int j = 0; j < kChunkV; j++) acc[j] *= f;
-  store_row<BF16>(a, r.q0 + t, head, d, acc, kChunkV);
-  if (d == 0 && a.lse)
-    a.lse[(int64_t)(r.q0 + t) * a.q_heads + head] =
-        sum == 0.0f ? -__builtin_huge_valf() : kLn2 * ((NV ? top - kF16Lift : top) + __builtin_amdgcn_logf(sum));
+  for (int j = 0; j < 4; j++) y[j] *= f;
+  store_row<BF16, 4>(a, r.q0 + t, head, d, y);
+  if (d == 0 && a.lse) a.lse[(int64_t)(r.q0 + t) * a.q_heads + head] = row_lse<NV>(all, sum);
 }
+
+namespace {
+constexpr int kWaves = 4;
+// waves of the wide form: as many as its registers allow (heads past 128: no wide form)
+constexpr int wide_waves(int dp) { return dp <= 128 ? 8 : kWaves; }
+}  // namespace
 
 KvAttnPlan plan_kv_attention(const KvAttnArgs& a) {
   KvAttnPlan p{};
   p.rows = 16;
+  p.waves = kWaves;
   const int64_t rows = a.tokens * a.group;
   p.tiles = a.offs ? rows / p.rows + a.batch : a.batch * ((a.group + p.rows - 1) / p.rows);
   // keys a tile can see at most: all, or the windows of its queries
@@ -593,12 +690,21 @@ KvAttnPlan plan_kv_attention(const KvAttnArgs& a) {
     const int64_t w = a.window + p.rows + kTileKeys;
     keys = keys < w ? keys : w;
   }
-  const int64_t per_pass = kTileKeys * kWaves;
-  const int64_t want = 1024;
   const int64_t work = p.tiles * a.c.heads;
+  // Little work: one launch whose workgroups have many waves, rather than
+  // chunks and a second launch to join them.
+  const int wide = wide_waves(a.c.dim);
+  if (work <= 256 && keys <= 4 * wide * kTileKeys) {
+    p.waves = wide;
+    p.chunk = keys > 0 ? keys : 1;
+    p.splits = 1;
+    return p;
+  }
+  const int64_t per_pass = kTileKeys * kWaves;
+  const int64_t want = 4096;
   int64_t splits = work >= want ? 1 : (want + work - 1) / work;
   int64_t chunk = ((keys + splits - 1) / splits + per_pass - 1) / per_pass * per_pass;
-  if (chunk < per_pass) chunk = per_pass;
+  if (chunk < 4 * per_pass) chunk = 4 * per_pass;
   p.chunk = chunk;
   p.splits = keys <= chunk ? 1 : (keys + chunk - 1) / chunk;
   p.ws = p.splits > 1 ? (size_t)(work * p.splits) * (size_t)(p.rows * (a.c.dim + 2)) * sizeof(float) : 0;
@@ -607,12 +713,29 @@ KvAttnPlan plan_kv_attention(const KvAttnArgs& a) {
 
 template <int DP, bool NV, bool BF16>
 static hipError_t launch_rows(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t s) {
+  constexpr int kWide = wide_waves(DP);
   const int64_t work = p.tiles * a.c.heads;
-  hipLaunchKernelGGL((kv_attn_kernel<DP, NV, BF16>), dim3((unsigned)(work * p.splits)), dim3(256), 0, s, a,
-                     (int)p.splits, p.chunk);
-  if (p.splits > 1)
-    hipLaunchKernelGGL((kv_attn_join_kernel<DP, NV, BF16>), dim3((unsigned)work), dim3(256), 0, s, a, (int)p.splits,
-                       p.chunk);
+  const dim3 grid((unsigned)(work * p.splits));
+  const int n = (int)p.splits;
+  if (p.waves == kWaves) {
+    if (a.c.dim == DP)
+      hipLaunchKernelGGL((kv_attn_kernel<DP, NV, BF16, true, kWaves>), grid, dim3(64 * kWaves), 0, s, a, n, p.chunk);
+    else
+      hipLaunchKernelGGL((kv_attn_kernel<DP, NV, BF16, false, kWaves>), grid, dim3(64 * kWaves), 0, s, a, n, p.chunk);
+  } else {
+    if (a.c.dim == DP)
+      hipLaunchKernelGGL((kv_attn_kernel<DP, NV, BF16, true, kWide>), grid, dim3(64 * kWide), 0, s, a, n, p.chunk);
+    else
+      hipLaunchKernelGGL((kv_attn_kernel<DP, NV, BF16, false, kWide>), grid, dim3(64 * kWide), 0, s, a, n, p.chunk);
+  }
+  if (n > 1) {
+    const dim3 rows((unsigned)(work * p.rows));
+    // few chunks: more threads would have nothing to do
+    if (n <= 16)
+      hipLaunchKernelGGL((kv_attn_join_kernel<DP, NV, BF16, 128>), rows, dim3(128), 0, s, a, n, p.chunk);
+    else
+      hipLaunchKernelGGL((kv_attn_join_kernel<DP, NV, BF16, 1024>), rows, dim3(1024), 0, s, a, n, p.chunk);
+  }
   return hipGetLastError();
 }
 

@@ -163,6 +163,7 @@ struct KvAttnArgs {
 // `splits` of them.
 struct KvAttnPlan {
   int rows;        // rows of a tile
+  int waves;       // of a workgroup
   int64_t tiles;   // upper bound over the batch, per kv head
   int64_t chunk;   // keys
   int64_t splits;
