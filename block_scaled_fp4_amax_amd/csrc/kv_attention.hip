@@ -2,21 +2,30 @@
 //
 //   s = scale (q . k), p = exp(s - max), out = sum(p v) / sum(p)
 //
-// in one pass over the keys with a running maximum and sum. A workgroup takes
-// 16 rows (row = (query, head of the kv head's group)) of one sequence and kv
-// head and a chunk of their visible keys; each of its waves takes every n-th
-// 32-key tile of the chunk on its own, with no barrier until the waves'
-// results are joined through LDS. Long key ranges are cut into chunks
-// whose partial results (fp32 sum, maximum, denominator) go to the workspace
-// and are joined by a second kernel.
+// in one pass over the keys with a running maximum and sum, in tiles of 32
+// keys. A row is (query, head of the kv head's group). Two forms:
+//
+// Few rows (a token or a few per sequence; bound by reading the cache): a
+// workgroup takes 16 rows of one sequence and kv head; each of its waves takes
+// every n-th key tile on its own, with no barrier until the waves' results
+// are joined through LDS. Where that alone would leave the GPU unevenly
+// loaded, the key tiles of the whole batch are cut into equal runs, one for
+// each workgroup that fits on the GPU at once; partial results (fp32 sum,
+// maximum, denominator) of rows whose keys lie in several runs go to the
+// workspace and are joined by a second kernel.
+//
+// Many rows (prompts; bound by arithmetic): a workgroup's four waves have rows
+// of their own, 16 to 64 each, and go through the key tiles together. Each
+// wave converts a quarter of the next tile and leaves it in LDS as the matrix
+// instructions' operands, while all of them use the present one.
 //
 // One wave, one tile of 32 keys, on v_mfma_f32_16x16x32 (lane l: c = l % 16,
 // g = l / 16):
 //   S^T = K Q^T: the A operand's rows are 16 keys, lane (c, g) holding of key
 //     c the head's elements g * D/4 .. g * D/4 + D/4 - 1, so one row's codes
 //     are read by four lanes, D/8 bytes each, and converted in registers. The
-//     result has a query per column: lane (c, g) holds row c's scores of keys
-//     4g .. 4g + 3 of both 16-key halves.
+//     result has a query per column: lane (c, g) holds row c's scores of four
+//     keys of both 16-key halves.
 //   O^T += V^T P^T: those eight scores are exactly the lane's part of the B
 //     operand if the contraction runs over the keys in that order, so the
 //     weights never leave their lane. The A operand needs, for one element d
@@ -64,6 +73,47 @@ struct RowTile {
   int lo, hi;   // keys that any row of the tile may see; lo is a multiple of kTileKeys
 };
 
+// A sequence's queries (q0, n), cut into the tokens there are.
+__device__ __forceinline__ void seq_queries(const KvAttnArgs& a, int b, int& q0, int& n) {
+  q0 = b;
+  n = 1;
+  if (a.offs) {
+    const int T = (int)a.tokens;
+    q0 = min(max(a.offs[b], 0), T);
+    n = max(min(max(a.offs[b + 1], 0), T) - q0, 0);
+  }
+}
+__device__ __forceinline__ int seq_len(const KvAttnArgs& a, int b) { return min(max(a.lens[b], 0), (int)a.max_len); }
+
+// First key that query t of a sequence may see, and the key after its last.
+__device__ __forceinline__ int first_key(const KvAttnArgs& a, int len, int n, int t) {
+  const int64_t k = (int64_t)len - n + t + 1 - a.window;
+  return a.window > 0 && k > 0 ? (int)k : 0;
+}
+__device__ __forceinline__ int end_key(const KvAttnArgs& a, int len, int n, int t) {
+  return a.causal ? min(max(len - n + t + 1, 0), len) : len;
+}
+
+// The keys of the tile of `rows` rows from r.row0 on.
+__device__ __forceinline__ void tile_keys(const KvAttnArgs& a, int rows, RowTile& r) {
+  // both ends grow with the query
+  const int t0 = r.row0 / a.group, t1 = min((r.row0 + rows - 1) / a.group, r.n - 1);
+  r.hi = end_key(a, r.len, r.n, t1);
+  r.lo = min(first_key(a, r.len, r.n, t0), r.hi) & ~(kTileKeys - 1);
+}
+
+// Inclusive sum over the wave's lanes.
+__device__ __forceinline__ int wave_prefix(int x) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(x, d, 64);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
+// The tile-th row tile of the batch.
 template <int ROWS>
 __device__ __forceinline__ bool find_tile(const KvAttnArgs& a, int tile, RowTile& r) {
   const int G = a.group;
@@ -75,30 +125,21 @@ __device__ __forceinline__ bool find_tile(const KvAttnArgs& a, int tile, RowTile
     r.n = 1;
     if (r.b >= a.batch) return false;
   } else {
-    const int lane = threadIdx.x & 63;
-    const int T = (int)a.tokens, B = (int)a.batch;
+    const int lane = threadIdx.x & 63, B = (int)a.batch;
     int before = 0;
     bool found = false;
     for (int b0 = 0; b0 < B; b0 += 64) {
       const int b = b0 + lane;
-      int s = 0, e = 0;
-      if (b < B) {
-        s = min(max(a.offs[b], 0), T);
-        e = max(min(max(a.offs[b + 1], 0), T), s);
-      }
-      const int mine = (int)(((int64_t)(e - s) * G + ROWS - 1) / ROWS);
-      int upto = mine;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int x = __shfl_up(upto, d, 64);
-        if (lane >= d) upto += x;
-      }
+      int s = 0, n = 0;
+      if (b < B) seq_queries(a, b, s, n);
+      const int mine = (int)(((int64_t)n * G + ROWS - 1) / ROWS);
+      const int upto = wave_prefix(mine);
       const uint64_t hit = __ballot(before + upto > tile);
       if (hit) {
         const int src = __builtin_ctzll(hit);
         r.b = b0 + src;
         r.q0 = __builtin_amdgcn_readlane(s, src);
-        r.n = __builtin_amdgcn_readlane(e, src) - r.q0;
+        r.n = __builtin_amdgcn_readlane(n, src);
         r.row0 = (tile - before - __builtin_amdgcn_readlane(upto - mine, src)) * ROWS;
         found = true;
         break;
@@ -107,24 +148,79 @@ __device__ __forceinline__ bool find_tile(const KvAttnArgs& a, int tile, RowTile
     }
     if (!found) return false;
   }
-  r.len = min(max(a.lens[r.b], 0), (int)a.max_len);
-  // the last visible key grows with the query, and so does the first
-  const int t0 = r.row0 / G, t1 = min((r.row0 + ROWS - 1) / G, r.n - 1);
-  r.hi = a.causal ? min(max(r.len - r.n + t1 + 1, 0), r.len) : r.len;
-  r.lo = 0;
-  if (a.window > 0) {
-    const int64_t first = (int64_t)r.len - r.n + t0 + 1 - a.window;
-    r.lo = first > 0 ? (int)first & ~(kTileKeys - 1) : 0;
-  }
-  if (r.lo > r.hi) r.lo = r.hi & ~(kTileKeys - 1);
+  r.len = seq_len(a, r.b);
+  tile_keys(a, ROWS, r);
   return true;
 }
 
-// Chunks that the tile's keys make (at least one: a tile without keys still
-// writes its empty result).
-__device__ __forceinline__ int tile_chunks(const RowTile& r, int64_t chunk) {
-  const int64_t n = r.hi - r.lo;
-  return n <= chunk ? 1 : (int)((n + chunk - 1) / chunk);
+// The balanced form. The items (sequence, row tile, kv head), in that order,
+// each count the key tiles of their sequence (`span` of them from `lo` on),
+// and all those key tiles, one after another, are cut into equal runs, one
+// for each workgroup. An item within one run is finished there. Otherwise
+// each run it touches leaves a partial result in one of its two slots: 2 w
+// for an item that began before run w, 2 w + 1 for one that begins in it.
+struct SeqWork {
+  int b, q0, n, len;
+  int lo, span;    // keys lo .. lo + span * kTileKeys hold all that any query sees
+  int row_tiles;
+};
+
+template <int ROWS>
+__device__ __forceinline__ SeqWork seq_work(const KvAttnArgs& a, int b) {
+  SeqWork w;
+  w.b = b;
+  seq_queries(a, b, w.q0, w.n);
+  w.len = seq_len(a, b);
+  w.row_tiles = (w.n * a.group + ROWS - 1) / ROWS;
+  w.lo = w.n > 0 ? min(first_key(a, w.len, w.n, 0), w.len) & ~(kTileKeys - 1) : 0;
+  w.span = max((w.len - w.lo + kTileKeys - 1) / kTileKeys, 1);
+  return w;
+}
+
+// Key tiles of the whole batch.
+template <int ROWS>
+__device__ __forceinline__ int total_work(const KvAttnArgs& a) {
+  const int lane = threadIdx.x & 63, B = (int)a.batch;
+  int sum = 0;
+  for (int b = lane; b < B; b += 64) {
+    const SeqWork w = seq_work<ROWS>(a, b);
+    sum += w.row_tiles * a.c.heads * w.span;
+  }
+  return __builtin_amdgcn_readlane(wave_prefix(sum), 63);
+}
+__device__ __forceinline__ int run_length(int total, int runs, int least) {
+  return max((total + runs - 1) / runs, least);
+}
+
+// The sequence that holds key tile `at` (ITEM: item `at`) of the batch;
+// `before` are the key tiles of the sequences before it, and `at` becomes
+// the place within the sequence.
+template <int ROWS, bool ITEM>
+__device__ __forceinline__ bool find_work(const KvAttnArgs& a, int& at, SeqWork& w, int& before) {
+  const int lane = threadIdx.x & 63, B = (int)a.batch;
+  int tiles = 0, items = 0;
+  for (int b0 = 0; b0 < B; b0 += 64) {
+    const SeqWork mine = seq_work<ROWS>(a, min(b0 + lane, B - 1));
+    const int my_items = b0 + lane < B ? mine.row_tiles * a.c.heads : 0, my_tiles = my_items * mine.span;
+    const int upto_tiles = wave_prefix(my_tiles), upto_items = ITEM ? wave_prefix(my_items) : 0;
+    const uint64_t hit = __ballot((ITEM ? items + upto_items : tiles + upto_tiles) > at);
+    if (hit) {
+      const int src = __builtin_ctzll(hit);
+      w.b = b0 + src;
+      w.q0 = __builtin_amdgcn_readlane(mine.q0, src);
+      w.n = __builtin_amdgcn_readlane(mine.n, src);
+      w.len = __builtin_amdgcn_readlane(mine.len, src);
+      w.lo = __builtin_amdgcn_readlane(mine.lo, src);
+      w.span = __builtin_amdgcn_readlane(mine.span, src);
+      w.row_tiles = __builtin_amdgcn_readlane(mine.row_tiles, src);
+      before = tiles + __builtin_amdgcn_readlane(upto_tiles - my_tiles, src);
+      at -= ITEM ? items + __builtin_amdgcn_readlane(upto_items - my_items, src) : before;
+      return true;
+    }
+    tiles += __builtin_amdgcn_readlane(upto_tiles, 63);
+    if (ITEM) items += __builtin_amdgcn_readlane(upto_items, 63);
+  }
+  return false;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
@@ -271,303 +367,483 @@ __device__ __forceinline__ float row_lse(float top, float sum) {
   return sum == 0.0f ? -__builtin_huge_valf() : kLn2 * ((NV ? top - kF16Lift : top) + __builtin_amdgcn_logf(sum));
 }
 
-// How one lane holds a 32-key tile's codes and scale bytes.
-template <int DP, bool NV, bool BF16>
+// A 32-key tile's codes and scale bytes: in LDS as the copies lay them down,
+// and where a lane finds its part. DP: the head size the kernel is made for
+// (64, 128, 256), FULL: the head size is DP itself, else it is smaller.
+template <int DP, bool NV>
 struct Tile {
   static constexpr int kBlk = NV ? 16 : 32;
   // K: words of 8 codes of one key per lane, elements g * DP/4 on, and the
   // scale bytes over them
   static constexpr int kKWords = DP / 32;
   static constexpr int kKScales = DP / 4 > kBlk ? DP / 4 / kBlk : 1;
+  // V: elements per lane and key, the number of O tiles, and their words
+  static constexpr int kChunkV = DP / 16;
   static constexpr int kVWords = DP > 128 ? 2 : 1;
-  uint32_t k[2][kKWords];
-  uint32_t ks[2][kKScales];
-  uint32_t v[8][kVWords];
-  uint32_t vs[8];
+  static constexpr int kPairs = kChunkV >= 8 ? 4 : 2;  // of elements, in a word
+
+  // LDS slot: the keys' codes of both 16-key halves, the values', then the
+  // scales in the order K half 0, K half 1, V half 0, V half 1
+  static constexpr int kHalf = 16 * DP / 2;
+  static constexpr int kVAt = 2 * kHalf, kScalesAt = 4 * kHalf;
+  static constexpr int kSlot = kScalesAt + 4 * 16 * DP / kBlk;
+  // copies of 64 x 16 bytes: kCopies of K, as many of V, one of all the scales
+  static constexpr int kCopies = 2 * kHalf / 1024;
+  static constexpr int kLoads = 2 * kCopies + 1;
+  static __device__ __forceinline__ constexpr int k_scale(int w) {
+    return w * 8 / kBlk < kKScales ? w * 8 / kBlk : 0;
+  }
 };
 
-// Where a tile's rows lie: the pages of its two 16-key halves.
-struct TilePages {
-  int p[2];
+// Direct-to-LDS copy of 16 bytes per active lane: lane i's bytes at its
+// address (or base + offset) land at LDS address lds + 16 i (lds
+// wave-uniform, passed in m0). Inline assembly, so that the compiler, which
+// cannot match copies in flight to what is read from LDS, adds no waits of
+// its own: every wait on these copies is explicit below. The instruction has
+// no output register. It writes m0, which cannot be named as clobbered; the
+// compiler sets m0 itself right before each instruction of its own that reads
+// it.
+__device__ __forceinline__ void copy16(const uint8_t* p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+               :
+               : "v"(p), "s"(__builtin_amdgcn_readfirstlane(lds))
+               : "memory");
+}
+__device__ __forceinline__ void copy16(const uint8_t* base, uint32_t offset, uint32_t lds) {
+  // base and lds are wave-uniform
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)b), hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
+  const uint64_t u = (uint64_t)hi << 32 | lo;
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(offset), "s"(u), "s"(__builtin_amdgcn_readfirstlane(lds))
+               : "memory");
+}
+// LDS byte address of a __shared__ object
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+// s_waitcnt vmcnt(N) and lgkmcnt(0) (gfx9 encoding), the other counters free
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+  asm volatile("" ::: "memory");
+}
+__device__ __forceinline__ void wait_lds() {
+  __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));
+  asm volatile("" ::: "memory");
+}
+
+// The cached rows of one sequence and kv head, copied to LDS tile by tile.
+// Score row c of a half is its key turned = 4 (c % 4) + c / 4, so that lane
+// (c, g) gets the scores of keys 4 i + g, and its reads of V fall on other LDS
+// banks than those of the other g.
+template <int DP, bool NV, bool FULL>
+struct CacheReader {
+  using T = Tile<DP, NV>;
+  const KvAttnArgs& a;
+  // Read through the scalar cache (the kernel never writes it): a vector load
+  // would be waited for in order with the copies in flight.
+  const __attribute__((address_space(4))) int32_t* table;
+  int h, len, last16, D, row_codes, row_scales;
+  uint32_t k_from, v_from;      // this lane's part of a copy of K, of V
+  const uint8_t* scales_from;   // and of the scales: part 0 and 1 of K's
+  int part;                     // halves, 2 and 3 of V's, 4 on none
+
+  __device__ __forceinline__ CacheReader(const KvAttnArgs& a_, const RowTile& r, int h_, int lane) : a(a_) {
+    h = h_;
+    len = r.len;
+    last16 = (len - 1) & ~15;  // the last 16 keys that exist
+    table = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)(a.table + r.b * a.table_stride);
+    D = FULL ? DP : a.c.dim;
+    row_codes = D >> 1;
+    row_scales = D / T::kBlk;
+    const int c = lane & 15, g = lane >> 4, turned = 4 * (c & 3) + (c >> 2);
+    // K of a whole head size: a lane copies what lane (c, g) will read, so
+    // that these reads are linear; else, and V, as the rows lie
+    constexpr int kPerHalf = T::kHalf / 16;  // lanes
+    v_from = 16 * (lane % kPerHalf);
+    k_from = !FULL       ? v_from
+             : DP == 64  ? turned * row_codes + 16 * (g & 1)
+             : DP == 128 ? turned * row_codes + 16 * g
+                         : turned * row_codes + 32 * g;
+    part = lane / row_scales;  // a half's scales are row_scales copies of 16 bytes
+    scales_from = (part & 2 ? a.c.vs : a.c.ks) + 16 * (lane - part * row_scales);
+  }
+
+  // Pages of the two halves of the tile at kt. Sequences end inside pages and
+  // tiles: a half past the last page is read from there.
+  __device__ __forceinline__ int2 pages(int kt) const {
+    const int i = __builtin_amdgcn_readfirstlane(min(kt, last16) >> a.c.page_shift);
+    const int j = __builtin_amdgcn_readfirstlane(min(kt + 16, last16) >> a.c.page_shift);
+    return make_int2(table[i], table[j]);
+  }
+
+  // Byte offsets of a half's codes and scales. 16 keys lie in one page, their
+  // rows back to back.
+  __device__ __forceinline__ void half_at(int key, int page, uint64_t& codes, uint64_t& scales) const {
+    const uint32_t pg = (uint32_t)min(max(page, 0), (int)a.c.pages - 1);
+    const uint32_t row = ((uint32_t)h << a.c.page_shift) + (min(key, last16) & ((1 << a.c.page_shift) - 1));
+    codes = (uint64_t)pg * (uint64_t)a.c.codes_ps + row * (uint32_t)row_codes;
+    scales = (uint64_t)pg * (uint64_t)a.c.scales_ps + row * (uint32_t)row_scales;
+  }
+
+  // Starts copies of the tile at kt into an LDS slot: those whose bit in
+  // `which` is set (bit i: copy i of K, kCopies + i: of V; the scales always).
+  // Keys past the sequence's end are copied as they lie in the last page:
+  // their scores are masked, their values zeroed before use.
+  __device__ __forceinline__ void copy(int kt, int2 page, uint32_t slot, int lane, uint32_t which) const {
+    uint64_t c0, s0, c1, s1;
+    half_at(kt, page.x, c0, s0);
+    if (a.c.page_shift >= 5 && kt + 16 <= last16) {
+      c1 = c0 + 16 * row_codes;  // a tile lies in one page
+      s1 = s0 + 16 * row_scales;
+    } else {
+      half_at(kt + 16, page.y, c1, s1);
+    }
+    if constexpr (DP == 64) {
+      // one copy for both halves
+      const uint64_t at = lane < 32 ? c0 : c1;
+      if (FULL || (int)v_from < 16 * row_codes) {
+        if (which & 1) copy16(a.c.kc + at + k_from, slot);
+        if (which & 2) copy16(a.c.vc + at + v_from, slot + T::kVAt);
+      }
+    } else {
+      constexpr int kEach = T::kCopies / 2;  // copies of a half
+#pragma unroll
+      for (int i = 0; i < T::kCopies; i++) {
+        const int sub = i / kEach, n = i % kEach;
+        const uint64_t at = sub ? c1 : c0;
+        if (FULL || (int)v_from + n * 1024 < 16 * row_codes) {
+          if (which >> i & 1) copy16(a.c.kc + at, k_from + n * (FULL ? 16 : 1024), slot + sub * T::kHalf + n * 1024);
+          if (which >> (T::kCopies + i) & 1)
+            copy16(a.c.vc + at, v_from + n * 1024, slot + T::kVAt + sub * T::kHalf + n * 1024);
+        }
+      }
+    }
+    if (part < 4) copy16(scales_from + (part & 1 ? s1 : s0), slot + T::kScalesAt);
+  }
+
+  // Where in a slot this lane's codes and scale bytes of one key lie: word w
+  // (scale i) of K of half 0, V (its scale) of the half's key 4 i + g.
+  __device__ __forceinline__ uint32_t k_word(int c, int g, int w) const {
+    if (FULL && DP == 64) return (g >> 1) * 256 + c * 16 + (g & 1) * 8 + 4 * w;
+    if (FULL) return (w / 4) * 1024 + (16 * g + c) * 16 + 4 * (w % 4);
+    const int d = g * (DP / 4) + 8 * w;  // past the head size: meets queries of 0
+    return (4 * (c & 3) + (c >> 2)) * row_codes + (d < D ? d >> 1 : 0);
+  }
+  __device__ __forceinline__ uint32_t k_scale(int c, int g, int i) const {
+    const int b = g * (DP / 4) / T::kBlk + i;
+    return T::kScalesAt + (4 * (c & 3) + (c >> 2)) * row_scales + (FULL || b < row_scales ? b : 0);
+  }
+  __device__ __forceinline__ uint32_t v_code(int c, int g) const {
+    const int d = T::kChunkV * c;  // past the head size: results not stored
+    return T::kVAt + g * row_codes + (FULL || d < D ? d >> 1 : 0);
+  }
+  __device__ __forceinline__ uint32_t v_scale(int c, int g) const {
+    const int d = T::kChunkV * c;
+    return T::kScalesAt + 2 * 16 * row_scales + g * row_scales + (FULL || d < D ? d / T::kBlk : 0);
+  }
 };
 
-// NW waves; FULL: the head size is DP itself.
-template <int DP, bool NV, bool BF16, bool FULL, int NW>
-__global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : DP == 128 ? 2 : 3) void kv_attn_kernel(KvAttnArgs a, int splits, int64_t chunk) {
-  using Regs = Tile<DP, NV, BF16>;
-  constexpr int kRows = 16;
-  constexpr int kBlk = Regs::kBlk;
-  constexpr int kChunkV = DP / 16;  // elements of V per lane = number of O tiles
-  constexpr int kQTerms = BF16 ? 1 : NV ? 2 : 3;
-  constexpr int kPTerms = BF16 ? 1 : 2;
-  constexpr int kStep = kTileKeys * NW;
-  __shared__ float s_o[NW][kRows][DP + 4];
-  __shared__ float s_m[NW][kRows], s_l[NW][kRows];
+// A V word in LDS: the codes of up to 8 elements of one key.
+template <int DP>
+__device__ __forceinline__ uint32_t v_word(const uint8_t* p, int w) {
+  if constexpr (DP == 64) return *reinterpret_cast<const uint16_t*>(p);
+  else return reinterpret_cast<const uint32_t*>(p)[w];
+}
 
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  const int split = blockIdx.x % splits;
-  const int th = blockIdx.x / splits;
-  const int h = th % a.c.heads, tile = th / a.c.heads;
-  RowTile r;
-  if (!find_tile<kRows>(a, tile, r)) return;
-  if (split >= tile_chunks(r, chunk)) return;
-  const int c_lo = r.lo + (int)(split * chunk);
-  const int c_hi = (int)min((int64_t)r.hi, c_lo + chunk);
-  const int D = FULL ? DP : a.c.dim, G = a.group;
+// RT tiles of 16 rows in one wave: their queries, running statistics and
+// weighted sums.
+template <int DP, bool NV, bool BF16, bool FULL, int RT>
+struct Rows {
+  static constexpr int kChunkV = DP / 16;
+  static constexpr int kQTerms = BF16 ? 1 : NV ? 2 : 3;
+  static constexpr int kPTerms = BF16 ? 1 : 2;
+  bool live[RT];
+  int token[RT], head[RT];
+  int my_lo[RT], my_hi[RT];  // the keys this lane's rows see
+  int all_lo, all_hi;        // keys that every row sees
+  u32x4 q[RT][kQTerms][DP / 32];
+  float score_scale[RT];
+  f32x4 o[RT][kChunkV];
+  float m[RT], l[RT];
 
-  // this lane's row: its query, and the keys [my_lo, my_hi) it sees
-  const int row = r.row0 + c;
-  const bool live = row < r.n * G;
-  const int t = live ? row / G : r.n - 1;
-  const int head = h * G + (live ? row - t * G : 0);
-  const int my_hi = a.causal ? min(max(r.len - r.n + t + 1, 0), r.len) : r.len;
-  const int my_lo = a.window > 0 ? (int)max((int64_t)0, (int64_t)r.len - r.n + t + 1 - a.window) : 0;
-  // keys that every row of the tile sees
-  const int t_first = r.row0 / G, t_last = min((r.row0 + kRows - 1) / G, r.n - 1);
-  const int all_hi = a.causal ? min(max(r.len - r.n + t_first + 1, 0), r.len) : r.len;
-  const int all_lo = a.window > 0 ? (int)max((int64_t)0, (int64_t)r.len - r.n + t_last + 1 - a.window) : 0;
-
-  const int shift = a.c.page_shift, in_page = (1 << shift) - 1;
-  const int32_t* table = a.table + r.b * a.table_stride;
-  const int row_codes = D >> 1, row_scales = D / kBlk;
-  const int last16 = (r.len - 1) & ~15;  // the last 16 keys that exist
-  // lane offsets within a 16-key half; elements past the head size are read
-  // from the row's beginning and meet queries of 0, or results not stored
-  uint32_t k_at[Regs::kKWords], ks_at[Regs::kKScales];
+  // Rows r.row0 on of kv head h.
+  __device__ __forceinline__ void start(const KvAttnArgs& a, const RowTile& r, int h, int c, int g) {
+    const int D = FULL ? DP : a.c.dim, G = a.group;
+    all_hi = end_key(a, r.len, r.n, r.row0 / G);
+    all_lo = first_key(a, r.len, r.n, min((r.row0 + 16 * RT - 1) / G, r.n - 1));
 #pragma unroll
-  for (int w = 0; w < Regs::kKWords; w++) {
-    const int d = g * (DP / 4) + 8 * w;
-    k_at[w] = c * row_codes + (FULL || d < D ? d >> 1 : 0);
-  }
+    for (int rt = 0; rt < RT; rt++) {
+      const int row = r.row0 + 16 * rt + c;
+      live[rt] = row < r.n * G;
+      const int t = live[rt] ? row / G : r.n - 1;
+      token[rt] = r.q0 + t;
+      head[rt] = h * G + (live[rt] ? row - t * G : 0);
+      my_hi[rt] = end_key(a, r.len, r.n, t);
+      my_lo[rt] = first_key(a, r.len, r.n, t);
+      m[rt] = kNoMax;
+      l[rt] = 0.0f;
 #pragma unroll
-  for (int i = 0; i < Regs::kKScales; i++) {
-    const int b = g * (DP / 4) / kBlk + i;
-    ks_at[i] = c * row_scales + (FULL || b < row_scales ? b : 0);
-  }
-  const int vd = FULL || kChunkV * c < D ? kChunkV * c : 0;
-  const uint32_t v_at = 4 * g * row_codes + (vd >> 1), vs_at = 4 * g * row_scales + vd / kBlk;
-
-  auto pages_of = [&](int kt) {
-    TilePages p;
-#pragma unroll
-    for (int sub = 0; sub < 2; sub++) p.p[sub] = table[min(kt + 16 * sub, last16) >> shift];
-    return p;
-  };
-  // 16 keys lie in one page. Keys past the end are read as they lie in the
-  // last page (their scores are masked, their values zeroed below); a half
-  // past the last page is read from there.
-  auto load = [&](int kt, const TilePages& p, Regs& x) {
-#pragma unroll
-    for (int sub = 0; sub < 2; sub++) {
-      const int64_t page = min(max((int64_t)p.p[sub], (int64_t)0), a.c.pages - 1);
-      const int row0 = (h << shift) + (min(kt + 16 * sub, last16) & in_page);
-      const int64_t at_c = page * a.c.codes_ps + (int64_t)row0 * row_codes;
-      const int64_t at_s = page * a.c.scales_ps + (int64_t)row0 * row_scales;
-      const uint8_t *kc = a.c.kc + at_c, *ks = a.c.ks + at_s, *vc = a.c.vc + at_c, *vs = a.c.vs + at_s;
-      if constexpr (FULL && Regs::kKWords == 2) {
-        const u32x2 y = *reinterpret_cast<const u32x2*>(kc + k_at[0]);
-        x.k[sub][0] = y.x;
-        x.k[sub][1] = y.y;
-      } else if constexpr (FULL) {
-#pragma unroll
-        for (int w = 0; w < Regs::kKWords; w += 4) {
-          const u32x4 y = *reinterpret_cast<const u32x4*>(kc + k_at[w]);
-#pragma unroll
-          for (int i = 0; i < 4; i++) x.k[sub][w + i] = y[i];
-        }
-      } else {
-#pragma unroll
-        for (int w = 0; w < Regs::kKWords; w++) x.k[sub][w] = *reinterpret_cast<const uint32_t*>(kc + k_at[w]);
-      }
-#pragma unroll
-      for (int i = 0; i < Regs::kKScales; i++) x.ks[sub][i] = ks[ks_at[i]];
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const uint8_t* y = vc + (v_at + i * row_codes);
-        if constexpr (DP == 64) {
-          x.v[4 * sub + i][0] = *reinterpret_cast<const uint16_t*>(y);
-        } else if constexpr (Regs::kVWords == 2) {
-          const u32x2 z = *reinterpret_cast<const u32x2*>(y);
-          x.v[4 * sub + i][0] = z.x;
-          x.v[4 * sub + i][1] = z.y;
-        } else {
-          x.v[4 * sub + i][0] = *reinterpret_cast<const uint32_t*>(y);
-        }
-        x.vs[4 * sub + i] = vs[vs_at + i * row_scales];
-      }
+      for (int j = 0; j < kChunkV; j++) o[rt][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-  };
-
-  // the first tile's codes are on their way while the queries are laid out
-  Regs tiles[2];
-  TilePages ahead{};
-  int kt = c_lo + kTileKeys * wave;
-  if (kt < c_hi) {
-    load(kt, pages_of(kt), tiles[0]);
-    if (kt + kStep < c_hi) ahead = pages_of(kt + kStep);
-  }
-
-  // queries, in the order of the K operand; a negative scale goes into them
-  u32x4 q[kQTerms][DP / 32];
-  float score_scale = __builtin_fabsf(a.scale);
-  {
-    float x[DP / 4];
+    // queries, in the order of the K operand; a negative scale goes into them
 #pragma unroll
-    for (int w = 0; w < DP / 32; w++) {
-      const int d = g * (DP / 4) + 8 * w;
-#pragma unroll
-      for (int i = 0; i < 8; i++) x[8 * w + i] = 0.0f;
-      if (live && d < D) {
-        const int64_t at = (int64_t)(r.q0 + t) * a.q_ts_ + (int64_t)head * a.q_hs + d;
-        if constexpr (BF16) {
-          const uint4 p = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at);
-          x[8 * w + 0] = bf16_lo(p.x); x[8 * w + 1] = bf16_hi(p.x);
-          x[8 * w + 2] = bf16_lo(p.y); x[8 * w + 3] = bf16_hi(p.y);
-          x[8 * w + 4] = bf16_lo(p.z); x[8 * w + 5] = bf16_hi(p.z);
-          x[8 * w + 6] = bf16_lo(p.w); x[8 * w + 7] = bf16_hi(p.w);
-        } else {
-          const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
-          const float4 p0 = p[0], p1 = p[1];
-          x[8 * w + 0] = p0.x; x[8 * w + 1] = p0.y; x[8 * w + 2] = p0.z; x[8 * w + 3] = p0.w;
-          x[8 * w + 4] = p1.x; x[8 * w + 5] = p1.y; x[8 * w + 6] = p1.z; x[8 * w + 7] = p1.w;
-        }
-        if (a.scale < 0.0f) {
-#pragma unroll
-          for (int i = 0; i < 8; i++) x[8 * w + i] = -x[8 * w + i];
-        }
-      }
-    }
-    if constexpr (NV) {
-      // the row's largest magnitude to [2^14, 2^15)
-      float amax = 0.0f;
-#pragma unroll
-      for (int i = 0; i < DP / 4; i++) amax = __builtin_fmaxf(amax, __builtin_fabsf(x[i]));
-      amax = __builtin_fmaxf(amax, xor_shfl<16>(amax));
-      amax = __builtin_fmaxf(amax, xor_shfl<32>(amax));
-      const int up = 141 - (int)(__builtin_bit_cast(uint32_t, amax) >> 23);
-#pragma unroll
-      for (int i = 0; i < DP / 4; i++) x[i] = __builtin_ldexpf(x[i], up);
-      score_scale = __builtin_ldexpf(score_scale * tensor_scale_of(a.c.k_ts, h), -up);
-    }
-#pragma unroll
-    for (int k = 0; k < kQTerms; k++) {
+    for (int rt = 0; rt < RT; rt++) {
+      float x[DP / 4];
 #pragma unroll
       for (int w = 0; w < DP / 32; w++) {
+        const int d = g * (DP / 4) + 8 * w;
 #pragma unroll
-        for (int i = 0; i < 4; i++) q[k][w][i] = split16bit<NV>(x[8 * w + 2 * i], x[8 * w + 2 * i + 1]);
+        for (int i = 0; i < 8; i++) x[8 * w + i] = 0.0f;
+        if (live[rt] && d < D) {
+          const int64_t at = (int64_t)token[rt] * a.q_ts_ + (int64_t)head[rt] * a.q_hs + d;
+          if constexpr (BF16) {
+            const uint4 p = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at);
+            x[8 * w + 0] = bf16_lo(p.x); x[8 * w + 1] = bf16_hi(p.x);
+            x[8 * w + 2] = bf16_lo(p.y); x[8 * w + 3] = bf16_hi(p.y);
+            x[8 * w + 4] = bf16_lo(p.z); x[8 * w + 5] = bf16_hi(p.z);
+            x[8 * w + 6] = bf16_lo(p.w); x[8 * w + 7] = bf16_hi(p.w);
+          } else {
+            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
+            const float4 p0 = p[0], p1 = p[1];
+            x[8 * w + 0] = p0.x; x[8 * w + 1] = p0.y; x[8 * w + 2] = p0.z; x[8 * w + 3] = p0.w;
+            x[8 * w + 4] = p1.x; x[8 * w + 5] = p1.y; x[8 * w + 6] = p1.z; x[8 * w + 7] = p1.w;
+          }
+          if (a.scale < 0.0f) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) x[8 * w + i] = -x[8 * w + i];
+          }
+        }
       }
+      float f = __builtin_fabsf(a.scale);
+      if constexpr (NV) {
+        // the row's largest magnitude to [2^14, 2^15)
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < DP / 4; i++) amax = __builtin_fmaxf(amax, __builtin_fabsf(x[i]));
+        amax = __builtin_fmaxf(amax, xor_shfl<16>(amax));
+        amax = __builtin_fmaxf(amax, xor_shfl<32>(amax));
+        const int up = 141 - (int)(__builtin_bit_cast(uint32_t, amax) >> 23);
+#pragma unroll
+        for (int i = 0; i < DP / 4; i++) x[i] = __builtin_ldexpf(x[i], up);
+        f = __builtin_ldexpf(f * tensor_scale_of(a.c.k_ts, h), -up);
+      }
+#pragma unroll
+      for (int k = 0; k < kQTerms; k++) {
+#pragma unroll
+        for (int w = 0; w < DP / 32; w++) {
+#pragma unroll
+          for (int i = 0; i < 4; i++) q[rt][k][w][i] = split16bit<NV>(x[8 * w + 2 * i], x[8 * w + 2 * i + 1]);
+        }
+      }
+      score_scale[rt] = a.softcap > 0.0f ? f / a.softcap : f * kLog2e;
     }
   }
-  const bool capped = a.softcap > 0.0f;
-  const float cap2 = a.softcap * kLog2e;
-  score_scale = capped ? score_scale / a.softcap : score_scale * kLog2e;
 
-  f32x4 o[kChunkV];
+  // The products s[rt][4 sub + i] (key kt + 16 sub + 4 i + g) to weights in
+  // 16 bits, in the order of V's operand; the statistics and sums follow.
+  __device__ __forceinline__ void weigh(const KvAttnArgs& a, int kt, int g, float s[RT][8], u32x4 pw[RT][kPTerms]) {
+    float factor[RT];  // of s, to scores in powers of two
 #pragma unroll
-  for (int j = 0; j < kChunkV; j++) o[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  float m = kNoMax, l = 0.0f;
-
-  auto compute = [&](int kt, Regs& x) {
-    float s[8];
+    for (int rt = 0; rt < RT; rt++) factor[rt] = score_scale[rt];
+    if (a.softcap > 0.0f) {
+      const float cap2 = a.softcap * kLog2e;
 #pragma unroll
-    for (int sub = 0; sub < 2; sub++) {
-      f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int rt = 0; rt < RT; rt++) {
 #pragma unroll
-      for (int w = 0; w < Regs::kKWords; w++) {
-        const u32x4 kk = convert8<NV>(x.k[sub][w], x.ks[sub][w * 8 / kBlk < Regs::kKScales ? w * 8 / kBlk : 0]);
-#pragma unroll
-        for (int n = 0; n < kQTerms; n++) acc = mfma16<NV>(kk, q[n][w], acc);
+        for (int i = 0; i < 8; i++) s[rt][i] = cap2 * tanh_exp(s[rt][i] * score_scale[rt]);
+        factor[rt] = 1.0f;
       }
-#pragma unroll
-      for (int i = 0; i < 4; i++) s[4 * sub + i] = acc[i];
-    }
-    float factor = score_scale;  // of s, to scores in powers of two
-    if (capped) {
-#pragma unroll
-      for (int i = 0; i < 8; i++) s[i] = cap2 * tanh_exp(s[i] * score_scale);
-      factor = 1.0f;
     }
     if (kt + kTileKeys > all_hi || kt < all_lo) {
 #pragma unroll
       for (int i = 0; i < 8; i++) {
-        const int key = kt + 16 * (i >> 2) + 4 * g + (i & 3);
-        s[i] = key < my_hi && key >= my_lo ? s[i] * factor : -__builtin_huge_valf();
-        // a weight of 0 must meet a number
-        if (key >= r.len) {
+        const int key = kt + 16 * (i >> 2) + 4 * (i & 3) + g;
 #pragma unroll
-          for (int w = 0; w < Regs::kVWords; w++) x.v[i][w] = 0u;
-          x.vs[i] = 0u;
-        }
+        for (int rt = 0; rt < RT; rt++)
+          s[rt][i] = key < my_hi[rt] && key >= my_lo[rt] ? s[rt][i] * factor[rt] : -__builtin_huge_valf();
       }
-      factor = 1.0f;
+#pragma unroll
+      for (int rt = 0; rt < RT; rt++) factor[rt] = 1.0f;
     }
-    float top = s[0];
+    float top[RT];
+    bool raise = false;
 #pragma unroll
-    for (int i = 1; i < 8; i++) top = __builtin_fmaxf(top, s[i]);
-    top *= factor;
-    if (__any(top > m + kSlack)) {
-      top = __builtin_fmaxf(top, xor_shfl<16>(top));
-      top = __builtin_fmaxf(top, xor_shfl<32>(top));
-      const float raised = __builtin_fmaxf(m, top);
-      const float down = __builtin_amdgcn_exp2f(m - raised);
-      l *= down;
+    for (int rt = 0; rt < RT; rt++) {
+      top[rt] = s[rt][0];
 #pragma unroll
-      for (int j = 0; j < kChunkV; j++) o[j] *= down;
-      m = raised;
+      for (int i = 1; i < 8; i++) top[rt] = __builtin_fmaxf(top[rt], s[rt][i]);
+      top[rt] *= factor[rt];
+      raise = raise || top[rt] > m[rt] + kSlack;
     }
-    const float base = NV ? m - kF16Lift : m;
-    float p[8];
+    if (__any(raise)) {
 #pragma unroll
-    for (int i = 0; i < 8; i++) p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], factor, -base));
-    l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-    u32x4 pw[kPTerms];
+      for (int rt = 0; rt < RT; rt++) {
+        top[rt] = __builtin_fmaxf(top[rt], xor_shfl<16>(top[rt]));
+        top[rt] = __builtin_fmaxf(top[rt], xor_shfl<32>(top[rt]));
+        const float raised = __builtin_fmaxf(m[rt], top[rt]);
+        const float down = __builtin_amdgcn_exp2f(m[rt] - raised);
+        l[rt] *= down;
 #pragma unroll
-    for (int n = 0; n < kPTerms; n++) {
-#pragma unroll
-      for (int i = 0; i < 4; i++) pw[n][i] = split16bit<NV>(p[2 * i], p[2 * i + 1]);
-    }
-#pragma unroll
-    for (int w = 0; w < Regs::kVWords; w++) {
-      constexpr int kPairs = kChunkV >= 8 ? 4 : 2;
-      uint32_t vt[4][2 * kPairs];
-#pragma unroll
-      for (int i = 0; i < 4; i++)
-        convert_key_pair<NV, kPairs>(x.v[2 * i][w], x.v[2 * i + 1][w], x.vs[2 * i], x.vs[2 * i + 1], vt[i]);
-#pragma unroll
-      for (int j = 0; j < 2 * kPairs; j++) {
-        const u32x4 vv = {vt[0][j], vt[1][j], vt[2][j], vt[3][j]};
-#pragma unroll
-        for (int n = 0; n < kPTerms; n++) o[8 * w + j] = mfma16<NV>(vv, pw[n], o[8 * w + j]);
+        for (int j = 0; j < kChunkV; j++) o[rt][j] *= down;
+        m[rt] = raised;
       }
     }
-  };
-
-  // two tiles' registers in turn: one is loaded while the other is used, and
-  // the page numbers are fetched a tile earlier still
-  for (; kt < c_hi; kt += 2 * kStep) {
 #pragma unroll
-    for (int k = 0; k < 2; k++) {
-      const int now = kt + k * kStep;
-      if (now + kStep < c_hi) {
-        load(now + kStep, ahead, tiles[1 - k]);
-        if (now + 2 * kStep < c_hi) ahead = pages_of(now + 2 * kStep);
+    for (int rt = 0; rt < RT; rt++) {
+      const float base = NV ? m[rt] - kF16Lift : m[rt];
+      float p[8];
+#pragma unroll
+      for (int i = 0; i < 8; i++) p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][i], factor[rt], -base));
+      l[rt] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+#pragma unroll
+      for (int n = 0; n < kPTerms; n++) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) pw[rt][n][i] = split16bit<NV>(p[2 * i], p[2 * i + 1]);
       }
-      if (now < c_hi) compute(now, tiles[k]);
     }
   }
-  l += xor_shfl<16>(l);
-  l += xor_shfl<32>(l);
 
-  // join the waves: O tile j holds of row c the elements kChunkV * (4g + i) + j
+  // s += K operand . queries (word w); sums += V operand j . weights.
+  __device__ __forceinline__ void times_k(u32x4 kk, int w, f32x4 acc[RT]) const {
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++) {
+#pragma unroll
+      for (int n = 0; n < kQTerms; n++) acc[rt] = mfma16<NV>(kk, q[rt][n][w], acc[rt]);
+    }
+  }
+  __device__ __forceinline__ void times_v(u32x4 vv, int j, const u32x4 pw[RT][kPTerms]) {
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++) {
+#pragma unroll
+      for (int n = 0; n < kPTerms; n++) o[rt][j] = mfma16<NV>(vv, pw[rt][n], o[rt][j]);
+    }
+  }
+
+  __device__ __forceinline__ void sum_denominators() {
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++) {
+      l[rt] += xor_shfl<16>(l[rt]);
+      l[rt] += xor_shfl<32>(l[rt]);
+    }
+  }
+};
+
+// Few rows: a workgroup's LDS, its waves' tiles and afterwards their results.
+template <int DP, bool NV, int NW>
+union FewSpace {
+  // tiles on their way or in use per wave
+  static constexpr int kDepth = 2;
+  uint8_t tiles[NW][kDepth][Tile<DP, NV>::kSlot];
+  struct {
+    float o[NW][16][DP + 4];
+    float m[NW][16], l[NW][16];
+  } join;
+};
+
+// 16 rows of kv head h over their keys from c_lo (a multiple of kTileKeys) to
+// c_hi, each wave every NW-th tile; the result to `out`, or (part) the
+// partial result to a slot.
+template <int DP, bool NV, bool BF16, bool FULL, int NW>
+__device__ __forceinline__ void attend_few(const KvAttnArgs& a, const RowTile& r, int h, int c_lo, int c_hi,
+                                           float* part, FewSpace<DP, NV, NW>& lds) {
+  using T = Tile<DP, NV>;
+  constexpr int kRows = 16;
+  constexpr int kStep = kTileKeys * NW;
+  constexpr int kDepth = FewSpace<DP, NV, NW>::kDepth;
+  constexpr uint32_t kAllCopies = (1u << 2 * T::kCopies) - 1;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const int D = FULL ? DP : a.c.dim, G = a.group;
+  const CacheReader<DP, NV, FULL> in(a, r, h, lane);
+  const uint32_t ring = lds_address(&lds.tiles[wave][0][0]);
+
+  // This wave's tiles, kDepth of them on their way or in use (the first while
+  // the queries are laid out); the page numbers come one earlier still. Past
+  // its last tile a wave copies that one again rather than nothing, so that
+  // the number of copies in flight is always the same.
+  int kt = c_lo + kTileKeys * wave;
+  const int last = kt + (c_hi - 1 - kt) / kStep * kStep;
+  int2 ahead = make_int2(0, 0);
+  if (kt < c_hi) {
+#pragma unroll
+    for (int i = 0; i < kDepth; i++)
+      in.copy(min(kt + i * kStep, last), in.pages(min(kt + i * kStep, last)), ring + i * T::kSlot, lane, kAllCopies);
+    ahead = in.pages(min(kt + kDepth * kStep, last));
+  }
+  Rows<DP, NV, BF16, FULL, 1> rows;
+  rows.start(a, r, h, c, g);
+
+  uint32_t slot = 0;
+  for (; kt < c_hi; kt += kStep) {
+    wait_copies<(kDepth - 1) * T::kLoads>();
+    const uint8_t* y = &lds.tiles[wave][0][0] + slot;
+    float s[1][8];
+#pragma unroll
+    for (int sub = 0; sub < 2; sub++) {
+      f32x4 acc[1] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+      for (int w = 0; w < T::kKWords; w++) {
+        const uint32_t code = *reinterpret_cast<const uint32_t*>(y + sub * T::kHalf + in.k_word(c, g, w));
+        const uint32_t scale = y[in.k_scale(c, g, T::k_scale(w)) + sub * 16 * in.row_scales];
+        rows.times_k(convert8<NV>(code, scale), w, acc);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; i++) s[0][4 * sub + i] = acc[0][i];
+    }
+    uint32_t v[8][T::kVWords], vs[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const int key = 16 * (i >> 2) + 4 * (i & 3);
+      vs[i] = y[in.v_scale(c, g) + key * in.row_scales];
+#pragma unroll
+      for (int w = 0; w < T::kVWords; w++)
+        v[i][w] = v_word<DP>(y + in.v_code(c, g) + (i >> 2) * T::kHalf + 4 * (i & 3) * in.row_codes, w);
+    }
+    if (kt + kTileKeys > r.len) {
+      asm volatile("");  // a branch, not selects on every tile
+      // a weight of 0 must meet a number
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        if (kt + 16 * (i >> 2) + 4 * (i & 3) + g >= r.len) {
+          vs[i] = 0u;
+#pragma unroll
+          for (int w = 0; w < T::kVWords; w++) v[i][w] = 0u;
+        }
+      }
+    }
+    u32x4 pw[1][Rows<DP, NV, BF16, FULL, 1>::kPTerms];
+    rows.weigh(a, kt, g, s, pw);
+#pragma unroll
+    for (int w = 0; w < T::kVWords; w++) {
+      uint32_t vt[4][2 * T::kPairs];
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        convert_key_pair<NV, T::kPairs>(v[2 * i][w], v[2 * i + 1][w], vs[2 * i], vs[2 * i + 1], vt[i]);
+#pragma unroll
+      for (int j = 0; j < 2 * T::kPairs; j++) rows.times_v(u32x4{vt[0][j], vt[1][j], vt[2][j], vt[3][j]}, 8 * w + j, pw);
+    }
+    // the slot has been read: the next tile's copies may land in it
+    wait_lds();
+    in.copy(min(kt + kDepth * kStep, last), ahead, ring + slot, lane, kAllCopies);
+    ahead = in.pages(min(kt + (kDepth + 1) * kStep, last));
+    slot = slot == (kDepth - 1) * T::kSlot ? 0 : slot + T::kSlot;
+  }
+  wait_copies<0>();
+  rows.sum_denominators();
+  __syncthreads();
+
+  // O tile j holds of row c the elements kChunkV * (4g + i) + j
   if (g == 0) {
-    s_m[wave][c] = m;
-    s_l[wave][c] = l;
+    lds.join.m[wave][c] = rows.m[0];
+    lds.join.l[wave][c] = rows.l[0];
   }
 #pragma unroll
   for (int i = 0; i < 4; i++) {
 #pragma unroll
-    for (int j = 0; j < kChunkV; j++) s_o[wave][c][(4 * g + i) * kChunkV + j] = o[j][i];
+    for (int j = 0; j < T::kChunkV; j++) lds.join.o[wave][c][(4 * g + i) * T::kChunkV + j] = rows.o[0][j][i];
   }
   __syncthreads();
   constexpr int kEach = kRows * DP / (64 * NW);  // elements a thread joins
@@ -576,21 +852,20 @@ __global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : DP == 128 ? 2 : 3) void kv
   const int jrow = r.row0 + jr;
   if (jrow >= r.n * G || d >= D) return;
   const int jt = jrow / G, jhead = h * G + jrow - jt * G;
-  float top = s_m[0][jr];
+  float top = lds.join.m[0][jr];
 #pragma unroll
-  for (int w = 1; w < NW; w++) top = __builtin_fmaxf(top, s_m[w][jr]);
+  for (int w = 1; w < NW; w++) top = __builtin_fmaxf(top, lds.join.m[w][jr]);
   float sum = 0.0f, acc[kEach];
 #pragma unroll
   for (int j = 0; j < kEach; j++) acc[j] = 0.0f;
 #pragma unroll
   for (int w = 0; w < NW; w++) {
-    const float f = __builtin_amdgcn_exp2f(s_m[w][jr] - top);
-    sum += f * s_l[w][jr];
+    const float f = __builtin_amdgcn_exp2f(lds.join.m[w][jr] - top);
+    sum += f * lds.join.l[w][jr];
 #pragma unroll
-    for (int j = 0; j < kEach; j++) acc[j] += f * s_o[w][jr][d + j];
+    for (int j = 0; j < kEach; j++) acc[j] += f * lds.join.o[w][jr][d + j];
   }
-  if (splits > 1) {
-    float* part = a.ws + (int64_t)blockIdx.x * (kRows * (D + 2));
+  if (part) {
 #pragma unroll
     for (int j = 0; j < kEach; j++) part[jr * D + d + j] = acc[j];
     if (d == 0) {
@@ -606,32 +881,240 @@ __global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : DP == 128 ? 2 : 3) void kv
   }
 }
 
-// Joins the chunks of one row: DP / 4 lanes take four elements each, and the
-// rest of the workgroup every kGroups-th chunk.
+// One workgroup for each row tile and kv head.
+template <int DP, bool NV, bool BF16, bool FULL, int NW>
+__global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 3) void kv_attn_kernel(KvAttnArgs a) {
+  __shared__ __attribute__((aligned(16))) FewSpace<DP, NV, NW> lds;
+  const int h = blockIdx.x % a.c.heads, tile = blockIdx.x / a.c.heads;
+  RowTile r;
+  if (!find_tile<16>(a, tile, r)) return;
+  attend_few<DP, NV, BF16, FULL, NW>(a, r, h, r.lo, r.hi, nullptr, lds);
+}
+
+// The balanced form: one workgroup for each run of key tiles.
+template <int DP, bool NV, bool BF16, bool FULL, int NW>
+__global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 3) void kv_attn_runs_kernel(KvAttnArgs a, int least) {
+  constexpr int kRows = 16;
+  __shared__ __attribute__((aligned(16))) FewSpace<DP, NV, NW> lds;
+  const int total = total_work<kRows>(a);
+  const int per = run_length(total, gridDim.x, least);
+  int at = (int)min((int64_t)blockIdx.x * per, (int64_t)total);
+  int left = min(per, total - at);
+  if (left <= 0) return;
+  SeqWork w;
+  int before;
+  if (!find_work<kRows, false>(a, at, w, before)) return;
+  int item = at / w.span, k = at - item * w.span;
+  while (true) {
+    const int take = min(w.span - k, left);
+    RowTile r;
+    r.b = w.b;
+    r.q0 = w.q0;
+    r.n = w.n;
+    r.len = w.len;
+    r.row0 = item / a.c.heads * kRows;
+    tile_keys(a, kRows, r);
+    const int c_lo = max(w.lo + k * kTileKeys, r.lo), c_hi = min(w.lo + (k + take) * kTileKeys, r.hi);
+    float* part =
+        take == w.span ? nullptr : a.ws + (int64_t)(2 * blockIdx.x + (k == 0 ? 1 : 0)) * (kRows * (a.c.dim + 2));
+    attend_few<DP, NV, BF16, FULL, NW>(a, r, item % a.c.heads, c_lo, c_hi, part, lds);
+    left -= take;
+    if (left == 0) return;
+    k = 0;
+    if (++item == w.row_tiles * a.c.heads) {
+      item = 0;
+      do {
+        if (w.b + 1 >= a.batch) return;
+        w = seq_work<kRows>(a, w.b + 1);
+      } while (w.row_tiles == 0);
+    }
+    __syncthreads();  // the join's LDS is used again
+  }
+}
+
+// Many rows: NW waves with RT tiles of 16 rows each.
+template <int DP, bool NV>
+struct ManySpace {
+  static constexpr int kRing = 4;  // raw tiles: one being converted, two on their way, one being started
+  static constexpr int kKParts = 2 * (DP / 32), kVParts = DP / 16;  // operands of a tile, 64 lanes x 16 bytes each
+  uint8_t raw[kRing][Tile<DP, NV>::kSlot];
+  u32x4 k[2][kKParts][64];
+  u32x4 v[2][kVParts][64];
+};
+
+template <int DP, bool NV, bool FULL, int RT>
+__global__ __launch_bounds__(256, 2) void kv_attn_many_kernel(KvAttnArgs a) {
+  using T = Tile<DP, NV>;
+  using Space = ManySpace<DP, NV>;
+  constexpr int NW = 4;
+  constexpr int kRows = 16 * RT * NW;
+  __shared__ __attribute__((aligned(16))) Space lds;
+  // The last rows have the most keys under a causal order: they begin first.
+  const int back = gridDim.x - 1 - blockIdx.x;
+  const int h = back % a.c.heads;
+  RowTile r;
+  if (!find_tile<kRows>(a, back / a.c.heads, r)) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const int D = FULL ? DP : a.c.dim;
+  const CacheReader<DP, NV, FULL> in(a, r, h, lane);
+  const int first = r.lo, end = r.hi;  // of the workgroup's keys
+  const int last = first + (end - 1 - first) / kTileKeys * kTileKeys;
+  // this wave's copies of a tile: every NW-th
+  uint32_t mine = 0;
+#pragma unroll
+  for (int i = 0; i < 2 * T::kCopies; i++) mine |= i % NW == wave ? 1u << i : 0u;
+  constexpr int kLoads = 2 * T::kCopies / NW + 1;  // per wave and tile, at least
+  const uint32_t raw = lds_address(&lds.raw[0][0]);
+
+  // This wave's quarter of a tile's conversion: K words wave, wave + 4, .. of
+  // both halves (heads of 64: word wave % 2 of half wave / 2), and the key
+  // pair `wave` of V, a fourth of each of its operands.
+  auto convert = [&](int kt, const uint8_t* y, int to) {
+    if constexpr (T::kKWords == 2) {
+      const int sub = wave >> 1, w = wave & 1;
+      const uint32_t code = *reinterpret_cast<const uint32_t*>(y + sub * T::kHalf + in.k_word(c, g, w));
+      lds.k[to][wave][lane] = convert8<NV>(code, y[in.k_scale(c, g, 0) + sub * 16 * in.row_scales]);
+    } else {
+#pragma unroll
+      for (int sub = 0; sub < 2; sub++) {
+#pragma unroll
+        for (int i = 0; i < T::kKWords / 4; i++) {
+          const int w = wave + 4 * i;
+          const uint32_t code = *reinterpret_cast<const uint32_t*>(y + sub * T::kHalf + in.k_word(c, g, w));
+          const uint32_t scale = y[in.k_scale(c, g, T::k_scale(w)) + sub * 16 * in.row_scales];
+          lds.k[to][sub * T::kKWords + w][lane] = convert8<NV>(code, scale);
+        }
+      }
+    }
+    // keys 16 sub + 4 i + g of the pair, i = 2 (wave % 2) and the next
+    const int sub = wave >> 1, i = 2 * (wave & 1);
+    const uint8_t* yv = y + in.v_code(c, g) + sub * T::kHalf + 4 * i * in.row_codes;
+    const uint8_t* ys = y + in.v_scale(c, g) + (16 * sub + 4 * i) * in.row_scales;
+    uint32_t s0 = ys[0], s1 = ys[4 * in.row_scales];
+    const int key = kt + 16 * sub + 4 * i + g;
+#pragma unroll
+    for (int w = 0; w < T::kVWords; w++) {
+      uint32_t x0 = v_word<DP>(yv, w), x1 = v_word<DP>(yv + 4 * in.row_codes, w);
+      if (kt + kTileKeys > r.len) {
+        // a weight of 0 must meet a number
+        if (key >= r.len) s0 = x0 = 0u;
+        if (key + 4 >= r.len) s1 = x1 = 0u;
+      }
+      uint32_t vt[2 * T::kPairs];
+      convert_key_pair<NV, T::kPairs>(x0, x1, s0, s1, vt);
+#pragma unroll
+      for (int j = 0; j < 2 * T::kPairs; j++)
+        reinterpret_cast<uint32_t*>(&lds.v[to][8 * w + j][lane])[wave] = vt[j];
+    }
+  };
+  auto slot_of = [](int n) { return n % Space::kRing * T::kSlot; };
+
+  if (first < end) {
+#pragma unroll
+    for (int i = 0; i < 3; i++) {
+      const int kt = min(first + i * kTileKeys, last);
+      in.copy(kt, in.pages(kt), raw + slot_of(i), lane, mine);
+    }
+  }
+  int2 ahead = make_int2(0, 0);
+  if (first < end) ahead = in.pages(min(first + 3 * kTileKeys, last));
+
+  r.row0 += 16 * RT * wave;
+  const bool idle = r.row0 >= r.n * a.group;  // no rows for this wave: it only helps
+  if (idle) r.row0 = 0;
+  tile_keys(a, 16 * RT, r);
+  Rows<DP, NV, true, FULL, RT> rows;
+  rows.start(a, r, h, c, g);
+  if (first < end) {
+    wait_copies<2 * kLoads>();
+    __syncthreads();
+    convert(first, &lds.raw[0][0], 0);
+    wait_copies<kLoads>();
+    wait_lds();
+    __syncthreads();
+  }
+  int n = 0;
+  for (int kt = first; kt < end; kt += kTileKeys, n++) {
+    // the tile after the next two begins its way, the next one is converted
+    in.copy(min(kt + 3 * kTileKeys, last), ahead, raw + slot_of(n + 3), lane, mine);
+    ahead = in.pages(min(kt + 4 * kTileKeys, last));
+    convert(min(kt + kTileKeys, last), &lds.raw[0][0] + slot_of(n + 1), (n + 1) & 1);
+    if (!idle && kt < r.hi && kt + kTileKeys > r.lo) {
+      float s[RT][8];
+#pragma unroll
+      for (int sub = 0; sub < 2; sub++) {
+        f32x4 acc[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; rt++) acc[rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int w = 0; w < T::kKWords; w++) rows.times_k(lds.k[n & 1][sub * T::kKWords + w][lane], w, acc);
+#pragma unroll
+        for (int rt = 0; rt < RT; rt++) {
+#pragma unroll
+          for (int i = 0; i < 4; i++) s[rt][4 * sub + i] = acc[rt][i];
+        }
+      }
+      u32x4 pw[RT][1];
+      rows.weigh(a, kt, g, s, pw);
+#pragma unroll
+      for (int j = 0; j < T::kChunkV; j++) rows.times_v(lds.v[n & 1][j][lane], j, pw);
+    }
+    // the tile after next and what the waves wrote is there for all
+    wait_copies<kLoads>();
+    wait_lds();
+    __syncthreads();
+  }
+  wait_copies<0>();
+  if (idle) return;
+  rows.sum_denominators();
+#pragma unroll
+  for (int rt = 0; rt < RT; rt++) {
+    const float f = row_factor<NV>(a, h, rows.l[rt]);
+    if (!rows.live[rt]) continue;
+    // a lane has 4 kChunkV elements in a row
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      float y[T::kChunkV];
+#pragma unroll
+      for (int j = 0; j < T::kChunkV; j++) y[j] = rows.o[rt][j][i] * f;
+      const int d = T::kChunkV * (4 * g + i);
+      if (d < D) store_row<true, T::kChunkV>(a, rows.token[rt], rows.head[rt], d, y);
+    }
+    if (g == 0 && a.lse) a.lse[(int64_t)rows.token[rt] * a.q_heads + rows.head[rt]] = row_lse<NV>(rows.m[rt], rows.l[rt]);
+  }
+}
+
+// Joins the partial results of one row of one item, if it has any: DP / 4
+// lanes take four elements each, and the rest of the workgroup every
+// kGroups-th partial result.
 template <int DP, bool NV, bool BF16, int THREADS>
-__global__ __launch_bounds__(THREADS) void kv_attn_join_kernel(KvAttnArgs a, int splits, int64_t chunk) {
+__global__ __launch_bounds__(THREADS) void kv_attn_join_kernel(KvAttnArgs a, int runs, int least, int rows_each) {
   constexpr int kRows = 16;
   constexpr int kLanes = DP / 4, kGroups = THREADS / kLanes;
   __shared__ float s_acc[kGroups][DP + 4];
   __shared__ float s_m[kGroups], s_l[kGroups];
-  const int jr = blockIdx.x % kRows, th = blockIdx.x / kRows;
-  const int h = th % a.c.heads, tile = th / a.c.heads;
-  RowTile r;
-  if (!find_tile<kRows>(a, tile, r)) return;
+  const int jr = blockIdx.x % rows_each;
+  int item = blockIdx.x / rows_each, before;
+  SeqWork w;
+  if (!find_work<kRows, true>(a, item, w, before)) return;
+  const int per = run_length(total_work<kRows>(a), runs, least);
+  const int begin = before + item * w.span;
+  const int run0 = begin / per, n = (begin + w.span - 1) / per - run0 + 1;
+  if (n == 1) return;
+  const int h = item % a.c.heads;
   const int D = a.c.dim, G = a.group;
-  const int row = r.row0 + jr;
-  if (row >= r.n * G) return;
-  const int n = tile_chunks(r, chunk);
+  const int row = item / a.c.heads * kRows + jr;
+  if (row >= w.n * G) return;
   const int t = row / G, head = h * G + row - t * G;
   const int64_t step = kRows * (D + 2);
-  const float* part = a.ws + (int64_t)th * splits * step;
   const int grp = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
   float top = kNoMax, sum = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (d < D) {
 #pragma unroll 4
     for (int k = grp; k < n; k += kGroups) {
-      const float* p = part + k * step;
+      const float* p = a.ws + (int64_t)(2 * (run0 + k) + (k == 0 ? 1 : 0)) * step;
       const float pm = p[kRows * D + jr], pl = p[kRows * (D + 1) + jr];
       const float4 v = *reinterpret_cast<const float4*>(p + jr * D + d);
       const float raised = __builtin_fmaxf(top, pm);
@@ -668,81 +1151,103 @@ __global__ __launch_bounds__(THREADS) void kv_attn_join_kernel(KvAttnArgs a, int
   const float f = row_factor<NV>(a, h, sum);
 #pragma unroll
   for (int j = 0; j < 4; j++) y[j] *= f;
-  store_row<BF16, 4>(a, r.q0 + t, head, d, y);
-  if (d == 0 && a.lse) a.lse[(int64_t)(r.q0 + t) * a.q_heads + head] = row_lse<NV>(all, sum);
+  store_row<BF16, 4>(a, w.q0 + t, head, d, y);
+  if (d == 0 && a.lse) a.lse[(int64_t)(w.q0 + t) * a.q_heads + head] = row_lse<NV>(all, sum);
 }
 
 namespace {
 constexpr int kWaves = 4;
 // waves of the wide form: as many as its registers allow (heads past 128: no wide form)
 constexpr int wide_waves(int dp) { return dp <= 128 ? 8 : kWaves; }
+// most 16-row tiles of a wave in the form for many rows, as its registers allow
+constexpr int most_tiles(int dp) { return dp <= 64 ? 4 : dp <= 128 ? 3 : 1; }
 }  // namespace
 
 KvAttnPlan plan_kv_attention(const KvAttnArgs& a) {
   KvAttnPlan p{};
-  p.rows = 16;
-  p.waves = kWaves;
   const int64_t rows = a.tokens * a.group;
-  p.tiles = a.offs ? rows / p.rows + a.batch : a.batch * ((a.group + p.rows - 1) / p.rows);
+  const int64_t cus = device_cu_count();
+  // Many rows a sequence.
+  if (a.bf16 && a.offs && rows >= 128 * a.batch) {
+    p.row_tiles = most_tiles(a.c.dim);
+    // fewer rows a wave while that leaves CUs without a second workgroup
+    while (p.row_tiles > 1 && (rows / (16 * kWaves * p.row_tiles) + a.batch / 2) * a.c.heads < 2 * cus) p.row_tiles--;
+    if (p.row_tiles == 3 && a.c.dim <= 64) p.row_tiles = 2;
+    p.tiles = rows / (16 * kWaves * p.row_tiles) + a.batch;
+    return p;
+  }
+  p.tiles = a.offs ? rows / 16 + a.batch : a.batch * ((a.group + 15) / 16);
   // keys a tile can see at most: all, or the windows of its queries
   int64_t keys = a.max_len;
   if (a.window > 0) {
-    const int64_t w = a.window + p.rows + kTileKeys;
+    const int64_t w = a.window + 16 + kTileKeys;
     keys = keys < w ? keys : w;
   }
-  const int64_t work = p.tiles * a.c.heads;
+  const int64_t items = p.tiles * a.c.heads;
+  p.waves = kWaves;
   // Little work: one launch whose workgroups have many waves, rather than
-  // chunks and a second launch to join them.
+  // runs and a second launch to join them.
   const int wide = wide_waves(a.c.dim);
-  if (work <= 256 && keys <= 4 * wide * kTileKeys) {
+  if (items <= cus && keys <= 8 * wide * kTileKeys) {
     p.waves = wide;
-    p.chunk = keys > 0 ? keys : 1;
-    p.splits = 1;
     return p;
   }
-  const int64_t per_pass = kTileKeys * kWaves;
-  const int64_t want = 4096;
-  int64_t splits = work >= want ? 1 : (want + work - 1) / work;
-  int64_t chunk = ((keys + splits - 1) / splits + per_pass - 1) / per_pass * per_pass;
-  if (chunk < 4 * per_pass) chunk = 4 * per_pass;
-  p.chunk = chunk;
-  p.splits = keys <= chunk ? 1 : (keys + chunk - 1) / chunk;
-  p.ws = p.splits > 1 ? (size_t)(work * p.splits) * (size_t)(p.rows * (a.c.dim + 2)) * sizeof(float) : 0;
+  // Enough items of few keys: the order in which workgroups end evens them out.
+  // (Key tiles are counted in 32 bits, whatever the offsets are on the device.)
+  const int64_t span = (a.max_len + kTileKeys - 1) / kTileKeys + 1;
+  const int64_t most = (a.offs ? a.batch * (rows / 16 + 1) : p.tiles) * a.c.heads;
+  if (items >= 4 * cus || keys <= 8 * kWaves * kTileKeys || most >= (int64_t(1) << 31) / span) return p;
+  p.runs = 2 * cus;
+  p.least = 2 * kWaves;
+  p.ws = (size_t)(2 * p.runs) * (size_t)(16 * (a.c.dim + 2)) * sizeof(float);
   return p;
 }
 
-template <int DP, bool NV, bool BF16>
+template <int DP, bool NV, bool FULL>
+static void launch_many(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t s) {
+  const dim3 grid((unsigned)(p.tiles * a.c.heads));
+  if (p.row_tiles == 1) hipLaunchKernelGGL((kv_attn_many_kernel<DP, NV, FULL, 1>), grid, dim3(256), 0, s, a);
+  if constexpr (most_tiles(DP) > 1) {
+    if (p.row_tiles == 2) hipLaunchKernelGGL((kv_attn_many_kernel<DP, NV, FULL, 2>), grid, dim3(256), 0, s, a);
+    if (p.row_tiles > 2)
+      hipLaunchKernelGGL((kv_attn_many_kernel<DP, NV, FULL, most_tiles(DP)>), grid, dim3(256), 0, s, a);
+  }
+}
+
+template <int DP, bool NV, bool BF16, bool FULL>
 static hipError_t launch_rows(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t s) {
   constexpr int kWide = wide_waves(DP);
-  const int64_t work = p.tiles * a.c.heads;
-  const dim3 grid((unsigned)(work * p.splits));
-  const int n = (int)p.splits;
-  if (p.waves == kWaves) {
-    if (a.c.dim == DP)
-      hipLaunchKernelGGL((kv_attn_kernel<DP, NV, BF16, true, kWaves>), grid, dim3(64 * kWaves), 0, s, a, n, p.chunk);
+  const int64_t items = p.tiles * a.c.heads;
+  if (p.row_tiles > 0) {
+    if constexpr (BF16) launch_many<DP, NV, FULL>(a, p, s);
+  } else if (p.runs > 0) {
+    const int runs = (int)p.runs, least = (int)p.least;
+    hipLaunchKernelGGL((kv_attn_runs_kernel<DP, NV, BF16, FULL, kWaves>), dim3(runs), dim3(64 * kWaves), 0, s, a, least);
+    const int each = !a.offs && a.group < 16 ? a.group : 16;
+    // few partial results each: more threads would have nothing to do
+    if (runs <= 8 * items)
+      hipLaunchKernelGGL((kv_attn_join_kernel<DP, NV, BF16, 128>), dim3((unsigned)(items * each)), dim3(128), 0, s, a,
+                         runs, least, each);
     else
-      hipLaunchKernelGGL((kv_attn_kernel<DP, NV, BF16, false, kWaves>), grid, dim3(64 * kWaves), 0, s, a, n, p.chunk);
+      hipLaunchKernelGGL((kv_attn_join_kernel<DP, NV, BF16, 1024>), dim3((unsigned)(items * each)), dim3(1024), 0, s,
+                         a, runs, least, each);
+  } else if (p.waves == kWaves) {
+    hipLaunchKernelGGL((kv_attn_kernel<DP, NV, BF16, FULL, kWaves>), dim3((unsigned)items), dim3(64 * kWaves), 0, s, a);
   } else {
-    if (a.c.dim == DP)
-      hipLaunchKernelGGL((kv_attn_kernel<DP, NV, BF16, true, kWide>), grid, dim3(64 * kWide), 0, s, a, n, p.chunk);
-    else
-      hipLaunchKernelGGL((kv_attn_kernel<DP, NV, BF16, false, kWide>), grid, dim3(64 * kWide), 0, s, a, n, p.chunk);
-  }
-  if (n > 1) {
-    const dim3 rows((unsigned)(work * p.rows));
-    // few chunks: more threads would have nothing to do
-    if (n <= 16)
-      hipLaunchKernelGGL((kv_attn_join_kernel<DP, NV, BF16, 128>), rows, dim3(128), 0, s, a, n, p.chunk);
-    else
-      hipLaunchKernelGGL((kv_attn_join_kernel<DP, NV, BF16, 1024>), rows, dim3(1024), 0, s, a, n, p.chunk);
+    hipLaunchKernelGGL((kv_attn_kernel<DP, NV, BF16, FULL, kWide>), dim3((unsigned)items), dim3(64 * kWide), 0, s, a);
   }
   return hipGetLastError();
 }
 
+template <int DP, bool NV, bool BF16>
+static hipError_t launch_full(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t s) {
+  return a.c.dim == DP ? launch_rows<DP, NV, BF16, true>(a, p, s) : launch_rows<DP, NV, BF16, false>(a, p, s);
+}
+
 template <int DP>
 static hipError_t launch_dim(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t s) {
-  if (a.c.nvfp4) return a.bf16 ? launch_rows<DP, true, true>(a, p, s) : launch_rows<DP, true, false>(a, p, s);
-  return a.bf16 ? launch_rows<DP, false, true>(a, p, s) : launch_rows<DP, false, false>(a, p, s);
+  if (a.c.nvfp4) return a.bf16 ? launch_full<DP, true, true>(a, p, s) : launch_full<DP, true, false>(a, p, s);
+  return a.bf16 ? launch_full<DP, false, true>(a, p, s) : launch_full<DP, false, false>(a, p, s);
 }
 
 hipError_t launch_kv_attention(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t s) {

@@ -158,16 +158,14 @@ struct KvAttnArgs {
   float* ws;
 };
 
-// How a call's work is cut: row tiles (16 rows of one sequence and kv head,
-// or more), and each tile's visible keys into chunks of chunk_keys, at most
-// `splits` of them.
+// How a call's work is cut.
 struct KvAttnPlan {
-  int rows;        // rows of a tile
-  int waves;       // of a workgroup
-  int64_t tiles;   // upper bound over the batch, per kv head
-  int64_t chunk;   // keys
-  int64_t splits;
-  size_t ws;       // bytes of partial results
+  int row_tiles;  // > 0: the form for many rows, this many 16-row tiles a wave; 0: the form for few
+  int waves;      // few rows: of a workgroup
+  int64_t tiles;  // row tiles of the batch per kv head, an upper bound
+  int64_t runs;   // few rows, 0: a workgroup for each row tile and kv head; else equal runs of key tiles
+  int64_t least;  // key tiles of a run, at least
+  size_t ws;      // bytes of partial results
 };
 
 KvAttnPlan plan_kv_attention(const KvAttnArgs& a);
