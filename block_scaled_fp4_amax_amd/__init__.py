@@ -149,6 +149,10 @@ class fp4_kv_attention_args(ctypes.Structure):
     ]
 
 
+_APPEND_SIZE = ctypes.sizeof(fp4_kv_append_args)
+_ATTENTION_SIZE = ctypes.sizeof(fp4_kv_attention_args)
+
+
 class Fp4Error(RuntimeError):
     def __init__(self, status: int, where: str):
         super().__init__(f"{where}: {fp4_status_str(status)} ({status})")
@@ -619,6 +623,8 @@ class KVCache:
         return cls(fmt, *bufs, *scales)
 
 
+# A decode step calls these functions for every layer, and a launch costs less
+# host time than careless Python: the checks below are written to be cheap.
 def _kv_dtype(t, what):
     import torch
     d = t.dtype
@@ -629,11 +635,11 @@ def _kv_dtype(t, what):
     raise ValueError(f"{what} must be bfloat16 or float32")
 
 
-def _kv_rows(t, cache, tokens, what):
+def _kv_rows(t, cache, what):
     """Check a [tokens, heads, head_dim] operand (rows dense, any strides);
     returns its shape and strides."""
     shape, strides = t.shape, t.stride()
-    if len(shape) != 3 or shape[2] != cache.head_dim or (tokens is not None and shape[0] != tokens):
+    if len(shape) != 3 or shape[2] != cache.head_dim:
         raise ValueError(f"{what} must be [tokens, heads, head_dim]")
     if strides[2] != 1:
         raise ValueError(f"{what} rows must be contiguous")
@@ -642,9 +648,11 @@ def _kv_rows(t, cache, tokens, what):
     return shape, strides
 
 
-def _kv_index(t, cache, shape, dtype, what):
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != cache.index or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} on the cache's GPU")
+def _kv_vector(t, cache, n, dtype, what):
+    """Check a contiguous device vector of n elements; returns its address."""
+    if t.dtype is not dtype or t.dim() != 1 or t.numel() != n or t.get_device() != cache.index or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} vector of {n} elements on the cache's GPU")
+    return t.data_ptr()
 
 
 def _kv_stream(cache, stream, *made):
@@ -662,22 +670,13 @@ def _kv_stream(cache, stream, *made):
     return stream
 
 
-def _on_cache_gpu(call):
-    """Make the cache's GPU current for the call (outputs and the launch)."""
-    import functools
-
-    @functools.wraps(call)
-    def wrapped(*args, **kw):
-        import torch
-        cache = kw.get("cache") or (args[0] if isinstance(args[0], KVCache) else args[1])
-        if torch.cuda.current_device() == cache.index:
-            return call(*args, **kw)
-        with torch.cuda.device(cache.index):
-            return call(*args, **kw)
-    return wrapped
+def _on_cache_gpu(call, cache, *args, **kw):
+    """The call again, with the cache's GPU current (outputs and the launch)."""
+    import torch
+    with torch.cuda.device(cache.index):
+        return call(*args, **kw)
 
 
-@_on_cache_gpu
 def kv_append(cache: KVCache, k, v, slots, *, q=None, positions=None, cos=None, sin=None, interleaved=False,
               four_over_six=False, q_out=None, stream=None):
     """Rotate, quantize and store the keys and values [tokens, kv_heads,
@@ -691,73 +690,78 @@ def kv_append(cache: KVCache, k, v, slots, *, q=None, positions=None, cos=None, 
     or (2i, 2i + 1) if `interleaved`; positions: int64 [tokens]. Without
     tables nothing is rotated."""
     import torch
-    kshape, ks = _kv_rows(k, cache, None, "k")
-    tokens = kshape[0]
-    vshape, vs = _kv_rows(v, cache, tokens, "v")
+    if torch._C._cuda_getDevice() != cache.index:
+        return _on_cache_gpu(kv_append, cache, cache, k, v, slots, q=q, positions=positions, cos=cos, sin=sin,
+                             interleaved=interleaved, four_over_six=four_over_six, q_out=q_out, stream=stream)
+    (tokens, kh, _), ks = _kv_rows(k, cache, "k")
+    vshape, vs = _kv_rows(v, cache, "v")
     dt = _kv_dtype(k, "k")
-    if v.dtype is not k.dtype or kshape[1] != cache.kv_heads or vshape[1] != cache.kv_heads:
+    if v.dtype is not k.dtype or kh != cache.kv_heads or vshape != k.shape:
         raise ValueError("k and v must be [tokens, kv_heads, head_dim] of one dtype")
-    _kv_index(slots, cache, (tokens,), torch.int64, "slots")
+    at_slots = _kv_vector(slots, cache, tokens, torch.int64, "slots")
     rotary = max_position = heads = 0
     at_pos = at_cos = at_sin = at_q = at_out = made = None
-    qs = os_ = (0, 0)
+    q0 = q1 = o0 = o1 = 0
     if cos is not None:
         if sin is None or positions is None:
             raise ValueError("rotation needs cos, sin and positions")
         max_position, half = cos.shape
+        for t in (cos, sin):
+            if (t.dtype is not torch.float32 or t.shape != cos.shape or t.get_device() != cache.index
+                    or not t.is_contiguous()):
+                raise ValueError("cos and sin must be contiguous float32 tensors of one shape on the cache's GPU")
+        at_pos = _kv_vector(positions, cache, tokens, torch.int64, "positions")
         rotary = 2 * half
-        _kv_index(cos, cache, (max_position, half), torch.float32, "cos")
-        _kv_index(sin, cache, (max_position, half), torch.float32, "sin")
-        _kv_index(positions, cache, (tokens,), torch.int64, "positions")
-        if rotary:
-            at_pos, at_cos, at_sin = positions.data_ptr(), cos.data_ptr(), sin.data_ptr()
+        at_cos, at_sin = cos.data_ptr(), sin.data_ptr()
     elif sin is not None:
         raise ValueError("rotation needs cos, sin and positions")
     if q is not None:
-        qshape, qs = _kv_rows(q, cache, tokens, "q")
-        if q.dtype is not k.dtype:
-            raise ValueError("q, k and v must have one dtype")
+        qshape, (q0, q1, _) = _kv_rows(q, cache, "q")
         heads = qshape[1]
+        if q.dtype is not k.dtype or qshape[0] != tokens:
+            raise ValueError("q, k and v must have one dtype and as many tokens")
         if q_out is None:
-            q_out = made = torch.empty(qshape, dtype=q.dtype, device=cache.device)
-        elif q_out.dtype is not q.dtype or q_out.shape != qshape:
-            raise ValueError("q_out must be like q")
-        os_ = _kv_rows(q_out, cache, tokens, "q_out")[1]
+            q_out = made = q.new_empty(qshape)
+            o0, o1 = heads * cache.head_dim, cache.head_dim
+        else:
+            oshape, (o0, o1, _) = _kv_rows(q_out, cache, "q_out")
+            if q_out.dtype is not q.dtype or oshape != qshape:
+                raise ValueError("q_out must be like q")
         at_q, at_out = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
     args = fp4_kv_append_args(
-        ctypes.sizeof(fp4_kv_append_args), dt,
+        _APPEND_SIZE, dt,
         (FP4_FOUR_OVER_SIX if four_over_six else 0) | (FP4_KV_INTERLEAVED if interleaved else 0), heads, tokens,
-        k.data_ptr(), v.data_ptr(), at_q, at_out, ks[0], ks[1], vs[0], vs[1], qs[0], qs[1], os_[0], os_[1],
-        slots.data_ptr(), at_pos, at_cos, at_sin, max_position, rotary, 0)
+        k.data_ptr(), v.data_ptr(), at_q, at_out, ks[0], ks[1], vs[0], vs[1], q0, q1, o0, o1, at_slots, at_pos,
+        at_cos, at_sin, max_position, rotary, 0)
     st = lib().fp4_kv_append(cache._ref, ctypes.byref(args), _kv_stream(cache, stream, made))
     if st != FP4_OK:
         raise Fp4Error(st, "fp4_kv_append")
     return q_out
 
 
-@_on_cache_gpu
 def kv_read(cache: KVCache, slots, dtype=None, stream=None):
     """The keys and values of the given slots (int64 [tokens]) as plain
     numbers: two [tokens, kv_heads, head_dim] tensors of `dtype` (bf16 unless
     given, or fp32). A slot outside the cache reads as zeros."""
     import torch
+    if torch._C._cuda_getDevice() != cache.index:
+        return _on_cache_gpu(kv_read, cache, cache, slots, dtype, stream)
     tokens = slots.numel()
-    _kv_index(slots, cache, (tokens,), torch.int64, "slots")
+    at_slots = _kv_vector(slots, cache, tokens, torch.int64, "slots")
     # one allocation: keys, then values
     both = torch.empty((2, tokens, cache.kv_heads, cache.head_dim), dtype=dtype or torch.bfloat16,
                        device=cache.device)
     dt = _kv_dtype(both, "dtype")
-    k, v = both.unbind(0)
-    st = lib().fp4_kv_read(cache._ref, tokens, slots.data_ptr(), k.data_ptr(), v.data_ptr(), dt,
+    at = both.data_ptr()
+    st = lib().fp4_kv_read(cache._ref, tokens, at_slots, at, at + both.nbytes // 2, dt,
                            _kv_stream(cache, stream, both))
     if st != FP4_OK:
         raise Fp4Error(st, "fp4_kv_read")
-    return k, v
+    return both.unbind()
 
 
-@_on_cache_gpu
 def kv_attention(q, cache: KVCache, block_table, kv_lens, *, q_offsets=None, max_kv_len=None, causal=True, window=0,
                  softcap=0.0, scale=None, return_lse=False, out=None, stream=None):
     """Softmax attention of queries [tokens, heads, head_dim] (bf16 or fp32)
@@ -778,40 +782,46 @@ def kv_attention(q, cache: KVCache, block_table, kv_lens, *, q_offsets=None, max
     logarithm of each row's sum of exponentials; rows that see nothing are 0
     and -inf."""
     import torch
-    qshape, qs = _kv_rows(q, cache, None, "q")
+    if torch._C._cuda_getDevice() != cache.index:
+        return _on_cache_gpu(kv_attention, cache, q, cache, block_table, kv_lens, q_offsets=q_offsets,
+                             max_kv_len=max_kv_len, causal=causal, window=window, softcap=softcap, scale=scale,
+                             return_lse=return_lse, out=out, stream=stream)
+    qshape, (q0, q1, _) = _kv_rows(q, cache, "q")
     dt = _kv_dtype(q, "q")
     tokens, heads, dim = qshape
     if block_table.dim() != 2 or block_table.dtype is not torch.int32 or block_table.get_device() != cache.index:
         raise ValueError("block_table must be an int32 [batch, width] tensor on the cache's GPU")
     batch, width = block_table.shape
-    tstride = block_table.stride()
-    if width > 1 and tstride[1] != 1:
+    t0, t1 = block_table.stride()
+    if width > 1 and t1 != 1:
         raise ValueError("block_table rows must be contiguous")
-    _kv_index(kv_lens, cache, (batch,), torch.int32, "kv_lens")
+    at_lens = _kv_vector(kv_lens, cache, batch, torch.int32, "kv_lens")
     at_offs = None
     if q_offsets is not None:
-        _kv_index(q_offsets, cache, (batch + 1,), torch.int32, "q_offsets")
-        at_offs = q_offsets.data_ptr()
+        at_offs = _kv_vector(q_offsets, cache, batch + 1, torch.int32, "q_offsets")
     made = lse = ws = at_lse = at_ws = None
     if out is None:
-        out = made = torch.empty(qshape, dtype=q.dtype, device=cache.device)
-    elif out.dtype is not q.dtype or out.shape != qshape:
-        raise ValueError("out must be like q")
-    os_ = _kv_rows(out, cache, tokens, "out")[1]
+        # (empty_like and new_empty cost a third less than empty)
+        out = made = torch.empty_like(q) if q.is_contiguous() else q.new_empty(qshape)
+        o0, o1 = heads * dim, dim
+    else:
+        oshape, (o0, o1, _) = _kv_rows(out, cache, "out")
+        if out.dtype is not q.dtype or oshape != qshape:
+            raise ValueError("out must be like q")
     if return_lse:
-        lse = torch.empty((tokens, heads), dtype=torch.float32, device=cache.device)
+        lse = q.new_empty((tokens, heads), dtype=torch.float32)
         at_lse = lse.data_ptr()
     capacity = width * cache.page_size
     args = fp4_kv_attention_args(
-        ctypes.sizeof(fp4_kv_attention_args), dt, FP4_KV_CAUSAL if causal else 0, heads, batch, tokens, at_offs,
-        kv_lens.data_ptr(), block_table.data_ptr(), tstride[0] if batch > 1 else width, width,
-        capacity if max_kv_len is None else min(max_kv_len, capacity), q.data_ptr(), out.data_ptr(), at_lse, qs[0],
-        qs[1], os_[0], os_[1], dim ** -0.5 if scale is None else scale, softcap, window)
+        _ATTENTION_SIZE, dt, FP4_KV_CAUSAL if causal else 0, heads, batch, tokens, at_offs, at_lens,
+        block_table.data_ptr(), t0 if batch > 1 else width, width,
+        capacity if max_kv_len is None or max_kv_len > capacity else max_kv_len, q.data_ptr(), out.data_ptr(), at_lse,
+        q0, q1, o0, o1, dim ** -0.5 if scale is None else scale, softcap, window)
     ref = ctypes.byref(args)
     L = lib()
     need = L.fp4_kv_attention_workspace(cache._ref, ref)
     if need:
-        ws = torch.empty((need,), dtype=torch.uint8, device=cache.device)
+        ws = q.new_empty((need,), dtype=torch.uint8)
         at_ws = ws.data_ptr()
     st = L.fp4_kv_attention(cache._ref, ref, at_ws, need, _kv_stream(cache, stream, made, lse, ws))
     if st != FP4_OK:

@@ -177,48 +177,72 @@ __device__ __forceinline__ SeqWork seq_work(const KvAttnArgs& a, int b) {
   return w;
 }
 
-// Key tiles of the whole batch.
-template <int ROWS>
-__device__ __forceinline__ int total_work(const KvAttnArgs& a) {
-  const int lane = threadIdx.x & 63, B = (int)a.batch;
-  int sum = 0;
-  for (int b = lane; b < B; b += 64) {
-    const SeqWork w = seq_work<ROWS>(a, b);
-    sum += w.row_tiles * a.c.heads * w.span;
-  }
-  return __builtin_amdgcn_readlane(wave_prefix(sum), 63);
-}
 __device__ __forceinline__ int run_length(int total, int runs, int least) {
   return max((total + runs - 1) / runs, least);
 }
 
-// The sequence that holds key tile `at` (ITEM: item `at`) of the batch;
-// `before` are the key tiles of the sequences before it, and `at` becomes
-// the place within the sequence.
+// 64 sequences' work, one a lane, and its running sums.
+template <int ROWS>
+struct WorkScan {
+  SeqWork mine;
+  int tiles, items;            // of this lane's sequence
+  int upto_tiles, upto_items;  // of the 64 up to it
+
+  __device__ __forceinline__ WorkScan(const KvAttnArgs& a, int b0) {
+    const int b = b0 + (threadIdx.x & 63);
+    mine = seq_work<ROWS>(a, min(b, (int)a.batch - 1));
+    items = b < a.batch ? mine.row_tiles * a.c.heads : 0;
+    tiles = items * mine.span;
+    upto_tiles = wave_prefix(tiles);
+    upto_items = wave_prefix(items);
+  }
+  __device__ __forceinline__ int all_tiles() const { return __builtin_amdgcn_readlane(upto_tiles, 63); }
+  __device__ __forceinline__ int all_items() const { return __builtin_amdgcn_readlane(upto_items, 63); }
+
+  // The sequence that holds key tile `at` (ITEM: item `at`) of these 64;
+  // `before` are the key tiles of those before it, and `at` becomes the place
+  // within the sequence.
+  template <bool ITEM>
+  __device__ __forceinline__ bool find(int& at, SeqWork& w, int& before) const {
+    const uint64_t hit = __ballot((ITEM ? upto_items : upto_tiles) > at);
+    if (!hit) return false;
+    const int src = __builtin_ctzll(hit);
+    w.b = __builtin_amdgcn_readlane(mine.b, src);
+    w.q0 = __builtin_amdgcn_readlane(mine.q0, src);
+    w.n = __builtin_amdgcn_readlane(mine.n, src);
+    w.len = __builtin_amdgcn_readlane(mine.len, src);
+    w.lo = __builtin_amdgcn_readlane(mine.lo, src);
+    w.span = __builtin_amdgcn_readlane(mine.span, src);
+    w.row_tiles = __builtin_amdgcn_readlane(mine.row_tiles, src);
+    before = __builtin_amdgcn_readlane(upto_tiles - tiles, src);
+    at -= ITEM ? __builtin_amdgcn_readlane(upto_items - items, src) : before;
+    return true;
+  }
+};
+
+// Key tiles of the whole batch, of which `first` holds the first 64 sequences.
+template <int ROWS>
+__device__ __forceinline__ int total_work(const KvAttnArgs& a, const WorkScan<ROWS>& first) {
+  int sum = first.all_tiles();
+  for (int b0 = 64; b0 < a.batch; b0 += 64) sum += WorkScan<ROWS>(a, b0).all_tiles();
+  return sum;
+}
+
+// The sequence that holds key tile (ITEM: item) `at` of the batch.
 template <int ROWS, bool ITEM>
-__device__ __forceinline__ bool find_work(const KvAttnArgs& a, int& at, SeqWork& w, int& before) {
-  const int lane = threadIdx.x & 63, B = (int)a.batch;
-  int tiles = 0, items = 0;
-  for (int b0 = 0; b0 < B; b0 += 64) {
-    const SeqWork mine = seq_work<ROWS>(a, min(b0 + lane, B - 1));
-    const int my_items = b0 + lane < B ? mine.row_tiles * a.c.heads : 0, my_tiles = my_items * mine.span;
-    const int upto_tiles = wave_prefix(my_tiles), upto_items = ITEM ? wave_prefix(my_items) : 0;
-    const uint64_t hit = __ballot((ITEM ? items + upto_items : tiles + upto_tiles) > at);
-    if (hit) {
-      const int src = __builtin_ctzll(hit);
-      w.b = b0 + src;
-      w.q0 = __builtin_amdgcn_readlane(mine.q0, src);
-      w.n = __builtin_amdgcn_readlane(mine.n, src);
-      w.len = __builtin_amdgcn_readlane(mine.len, src);
-      w.lo = __builtin_amdgcn_readlane(mine.lo, src);
-      w.span = __builtin_amdgcn_readlane(mine.span, src);
-      w.row_tiles = __builtin_amdgcn_readlane(mine.row_tiles, src);
-      before = tiles + __builtin_amdgcn_readlane(upto_tiles - my_tiles, src);
-      at -= ITEM ? items + __builtin_amdgcn_readlane(upto_items - my_items, src) : before;
+__device__ __forceinline__ bool find_work(const KvAttnArgs& a, const WorkScan<ROWS>& first, int& at, SeqWork& w,
+                                          int& before) {
+  if (first.template find<ITEM>(at, w, before)) return true;
+  int tiles = first.all_tiles();
+  at -= ITEM ? first.all_items() : tiles;
+  for (int b0 = 64; b0 < a.batch; b0 += 64) {
+    const WorkScan<ROWS> next(a, b0);
+    if (next.template find<ITEM>(at, w, before)) {
+      before += tiles;
       return true;
     }
-    tiles += __builtin_amdgcn_readlane(upto_tiles, 63);
-    if (ITEM) items += __builtin_amdgcn_readlane(upto_items, 63);
+    tiles += next.all_tiles();
+    at -= ITEM ? next.all_items() : next.all_tiles();
   }
   return false;
 }
@@ -896,14 +920,15 @@ template <int DP, bool NV, bool BF16, bool FULL, int NW>
 __global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 3) void kv_attn_runs_kernel(KvAttnArgs a, int least) {
   constexpr int kRows = 16;
   __shared__ __attribute__((aligned(16))) FewSpace<DP, NV, NW> lds;
-  const int total = total_work<kRows>(a);
+  const WorkScan<kRows> scan(a, 0);
+  const int total = total_work<kRows>(a, scan);
   const int per = run_length(total, gridDim.x, least);
   int at = (int)min((int64_t)blockIdx.x * per, (int64_t)total);
   int left = min(per, total - at);
   if (left <= 0) return;
   SeqWork w;
   int before;
-  if (!find_work<kRows, false>(a, at, w, before)) return;
+  if (!find_work<kRows, false>(a, scan, at, w, before)) return;
   int item = at / w.span, k = at - item * w.span;
   while (true) {
     const int take = min(w.span - k, left);
@@ -1097,8 +1122,9 @@ __global__ __launch_bounds__(THREADS) void kv_attn_join_kernel(KvAttnArgs a, int
   const int jr = blockIdx.x % rows_each;
   int item = blockIdx.x / rows_each, before;
   SeqWork w;
-  if (!find_work<kRows, true>(a, item, w, before)) return;
-  const int per = run_length(total_work<kRows>(a), runs, least);
+  const WorkScan<kRows> scan(a, 0);
+  if (!find_work<kRows, true>(a, scan, item, w, before)) return;
+  const int per = run_length(total_work<kRows>(a, scan), runs, least);
   const int begin = before + item * w.span;
   const int run0 = begin / per, n = (begin + w.span - 1) / per - run0 + 1;
   if (n == 1) return;
@@ -1185,10 +1211,13 @@ KvAttnPlan plan_kv_attention(const KvAttnArgs& a) {
   }
   const int64_t items = p.tiles * a.c.heads;
   p.waves = kWaves;
-  // Little work: one launch whose workgroups have many waves, rather than
-  // runs and a second launch to join them.
+  // Little work, or at most a few tiles more for some workgroups than for
+  // others: one launch whose workgroups have many waves, rather than runs and
+  // a second launch to join them (24 sequences of 5 queries over 3000 keys:
+  // 20 against 28 us; 32 to 4096 keys: 27 against 32).
   const int wide = wide_waves(a.c.dim);
-  if (items <= cus && keys <= 8 * wide * kTileKeys) {
+  const int64_t each = keys / (wide * kTileKeys);  // key tiles of a wave
+  if (items <= 4 * cus && each <= (2 * items >= cus ? 24 : 8)) {
     p.waves = wide;
     return p;
   }
@@ -1229,7 +1258,7 @@ static hipError_t launch_rows(const KvAttnArgs& a, const KvAttnPlan& p, hipStrea
       hipLaunchKernelGGL((kv_attn_join_kernel<DP, NV, BF16, 128>), dim3((unsigned)(items * each)), dim3(128), 0, s, a,
                          runs, least, each);
     else
-      hipLaunchKernelGGL((kv_attn_join_kernel<DP, NV, BF16, 1024>), dim3((unsigned)(items * each)), dim3(1024), 0, s,
+      hipLaunchKernelGGL((kv_attn_join_kernel<DP, NV, BF16, 512>), dim3((unsigned)(items * each)), dim3(512), 0, s,
                          a, runs, least, each);
   } else if (p.waves == kWaves) {
     hipLaunchKernelGGL((kv_attn_kernel<DP, NV, BF16, FULL, kWaves>), dim3((unsigned)items), dim3(64 * kWaves), 0, s, a);

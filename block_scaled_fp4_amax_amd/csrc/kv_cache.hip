@@ -41,6 +41,17 @@ __device__ __forceinline__ void store8<float>(float* p, const float v[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
+// Eight fp32 of 4-byte alignment.
+__device__ __forceinline__ void load8_any(const float* p, float v[8]) {
+  typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+  const f32x4_any a = *reinterpret_cast<const f32x4_any*>(p), b = *reinterpret_cast<const f32x4_any*>(p + 4);
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    v[i] = a[i];
+    v[4 + i] = b[i];
+  }
+}
+
 // Cosines and signed sines of a unit's 16 elements: element e becomes
 // x[e] * c[e] + x[partner(e)] * s[e] (s negative for a pair's first
 // element), the rounding of a c - b s and b c + a s step by step.
@@ -49,6 +60,27 @@ __device__ __forceinline__ void load_turn(const KvAppendArgs& a, int64_t pos, in
   const int half = a.rotary >> 1;
   const float* ct = a.cos_t + pos * half;
   const float* st = a.sin_t + pos * half;
+  if constexpr (ROT == kHalves) {
+    // half % 8 == 0: 8 elements use 8 entries in a row
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+      const int e = e0 + 8 * k;
+      if (e >= a.rotary) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          c[8 * k + i] = 1.0f;
+          s[8 * k + i] = 0.0f;
+        }
+        continue;
+      }
+      const int j = e < half ? e : e - half;
+      load8_any(ct + j, c + 8 * k);
+      load8_any(st + j, s + 8 * k);
+#pragma unroll
+      for (int i = 0; i < 8; i++) s[8 * k + i] = e < half ? -s[8 * k + i] : s[8 * k + i];
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 16; i++) {
     const int e = e0 + i;
@@ -153,6 +185,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, int pass
       store8<T>(o, v);
       store8<T>(o + 8, v + 8);
     }
+    if (base + rpp <= a.q_heads) continue;  // queries only
     NvConsts nc{};
     if constexpr (NV) {
       nc.St = live && !is_q ? sane_scale(is_k ? a.c.k_ts : a.c.v_ts, h) : 1.0f;
