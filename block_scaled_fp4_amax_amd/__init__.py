@@ -750,16 +750,14 @@ def kv_read(cache: KVCache, slots, dtype=None, stream=None):
         return _on_cache_gpu(kv_read, cache, cache, slots, dtype, stream)
     tokens = slots.numel()
     at_slots = _kv_vector(slots, cache, tokens, torch.int64, "slots")
-    # one allocation: keys, then values
-    both = torch.empty((2, tokens, cache.kv_heads, cache.head_dim), dtype=dtype or torch.bfloat16,
-                       device=cache.device)
-    dt = _kv_dtype(both, "dtype")
-    at = both.data_ptr()
-    st = lib().fp4_kv_read(cache._ref, tokens, at_slots, at, at + both.nbytes // 2, dt,
-                           _kv_stream(cache, stream, both))
+    k = slots.new_empty((tokens, cache.kv_heads, cache.head_dim), dtype=dtype or torch.bfloat16)
+    dt = _kv_dtype(k, "dtype")
+    v = torch.empty_like(k)
+    st = lib().fp4_kv_read(cache._ref, tokens, at_slots, k.data_ptr(), v.data_ptr(), dt,
+                           _kv_stream(cache, stream, k, v))
     if st != FP4_OK:
         raise Fp4Error(st, "fp4_kv_read")
-    return both.unbind()
+    return k, v
 
 
 def kv_attention(q, cache: KVCache, block_table, kv_lens, *, q_offsets=None, max_kv_len=None, causal=True, window=0,

@@ -35,8 +35,8 @@
 // elements times their E4M3 scale in fp16; the NVFP4 tensor scales multiply
 // the scores and the result. fp16 queries are brought to a common power of
 // two per row first, so that no bf16 or fp32 query leaves fp16's range.
-// fp32 calls split the queries (3 bf16 or 2 fp16 terms) and the weights (2
-// terms) and multiply every term.
+// fp32 calls split the queries and the weights into 3 bf16 or 2 fp16 terms
+// (24 and 22 bits) and multiply every term.
 // (The block-scaled matrix instruction could take MXFP4 codes as they are,
 // against queries split into two E4M3 terms. It was tried and left: it sums
 // products of an 8-bit operand in groups of eight with about 16 bits, and
@@ -583,7 +583,7 @@ template <int DP, bool NV, bool BF16, bool FULL, int RT>
 struct Rows {
   static constexpr int kChunkV = DP / 16;
   static constexpr int kQTerms = BF16 ? 1 : NV ? 2 : 3;
-  static constexpr int kPTerms = BF16 ? 1 : 2;
+  static constexpr int kPTerms = BF16 ? 1 : NV ? 2 : 3;
   bool live[RT];
   int token[RT], head[RT];
   int my_lo[RT], my_hi[RT];  // the keys this lane's rows see
@@ -1193,14 +1193,18 @@ KvAttnPlan plan_kv_attention(const KvAttnArgs& a) {
   KvAttnPlan p{};
   const int64_t rows = a.tokens * a.group;
   const int64_t cus = device_cu_count();
-  // Many rows a sequence.
+  // Many rows a sequence, and enough of them that two workgroups a CU have
+  // two row tiles a wave (heads past 128: one) or more: the form for many.
+  // Fewer rows: each key tile's conversion and barrier serve too few (8 x 448
+  // queries of 20 heads of 64 over 1500 keys: 58 us in that form, 46 in the other).
   if (a.bf16 && a.offs && rows >= 128 * a.batch) {
-    p.row_tiles = most_tiles(a.c.dim);
-    // fewer rows a wave while that leaves CUs without a second workgroup
-    while (p.row_tiles > 1 && (rows / (16 * kWaves * p.row_tiles) + a.batch / 2) * a.c.heads < 2 * cus) p.row_tiles--;
-    if (p.row_tiles == 3 && a.c.dim <= 64) p.row_tiles = 2;
-    p.tiles = rows / (16 * kWaves * p.row_tiles) + a.batch;
-    return p;
+    const int least = a.c.dim <= 128 ? 2 : 1;
+    for (int n = most_tiles(a.c.dim); n >= least; n -= n == 4 ? 2 : 1) {
+      if ((rows / (16 * kWaves * n) + a.batch / 2) * a.c.heads < 2 * cus) continue;
+      p.row_tiles = n;
+      p.tiles = rows / (16 * kWaves * n) + a.batch;
+      return p;
+    }
   }
   p.tiles = a.offs ? rows / 16 + a.batch : a.batch * ((a.group + 15) / 16);
   // keys a tile can see at most: all, or the windows of its queries
@@ -1235,12 +1239,13 @@ KvAttnPlan plan_kv_attention(const KvAttnArgs& a) {
 template <int DP, bool NV, bool FULL>
 static void launch_many(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t s) {
   const dim3 grid((unsigned)(p.tiles * a.c.heads));
-  if (p.row_tiles == 1) hipLaunchKernelGGL((kv_attn_many_kernel<DP, NV, FULL, 1>), grid, dim3(256), 0, s, a);
-  if constexpr (most_tiles(DP) > 1) {
-    if (p.row_tiles == 2) hipLaunchKernelGGL((kv_attn_many_kernel<DP, NV, FULL, 2>), grid, dim3(256), 0, s, a);
-    if (p.row_tiles > 2)
-      hipLaunchKernelGGL((kv_attn_many_kernel<DP, NV, FULL, most_tiles(DP)>), grid, dim3(256), 0, s, a);
+  if constexpr (most_tiles(DP) > 2) {
+    if (p.row_tiles == 2) {
+      hipLaunchKernelGGL((kv_attn_many_kernel<DP, NV, FULL, 2>), grid, dim3(256), 0, s, a);
+      return;
+    }
   }
+  hipLaunchKernelGGL((kv_attn_many_kernel<DP, NV, FULL, most_tiles(DP)>), grid, dim3(256), 0, s, a);
 }
 
 template <int DP, bool NV, bool BF16, bool FULL>

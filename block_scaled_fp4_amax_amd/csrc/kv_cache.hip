@@ -2,8 +2,10 @@
 //
 // Append: for each token, rotate the keys (and the step's queries) to the
 // token's position, quantize keys and values in blocks along the head and
-// store them at the token's slot. One lane takes a unit of 16 elements of a
-// row, the unit of quantize_unit, so codes and scales are those of
+// store them at the token's slot. One lane takes 8 elements of a row, so that
+// a wave's loads and stores are whole lines; the lanes of a block (2 for
+// NVFP4, 4 for MXFP4) exchange its maximum and squared errors. Every step is
+// that of quant_common.h's 16-element unit, so codes and scales are those of
 // fp4_quantize under the same S_t, bit for bit (no rounding between the
 // rotation and the quantizer).
 //
@@ -15,31 +17,50 @@ namespace fp4impl {
 
 enum Rotation {
   kNoRotation = 0,
-  kHalves = 1,       // pairs (i, i + R/2), R % 16 == 0: the partners of 8 elements are 8 whole elements
-  kInterleaved = 2,  // pairs (2i, 2i + 1): partners lie in the same unit
+  kHalves = 1,       // pairs (i, i + R/2), R % 16 == 0: the partners of 8 elements are another lane's 8
+  kInterleaved = 2,  // pairs (2i, 2i + 1): partners lie in the same lane
   kHalvesAny = 3,    // pairs (i, i + R/2), any even R: partners one by one
 };
 
+// Eight elements as they lie in memory.
+template <typename T>
+struct Raw8 {
+  static constexpr int kWords = 8 * sizeof(T) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < kWords; i += 4) {
+      const u32x4 x = reinterpret_cast<const u32x4*>(p)[i / 4];
+#pragma unroll
+      for (int j = 0; j < 4; j++) w[i + j] = x[j];
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int i = 0; i < kWords; i += 4)
+      reinterpret_cast<u32x4*>(p)[i / 4] = u32x4{w[i], w[i + 1], w[i + 2], w[i + 3]};
+  }
+  __device__ __forceinline__ void get(float v[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      if constexpr (sizeof(T) == 4) v[i] = __builtin_bit_cast(float, w[i]);
+      else v[i] = i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+    }
+  }
+  __device__ __forceinline__ void set(const float v[8]) {
+#pragma unroll
+    for (int i = 0; i < kWords; i++) {
+      if constexpr (sizeof(T) == 4) {
+        w[i] = __builtin_bit_cast(uint32_t, v[i]);
+      } else {
+        const bf16x2 pr = {(__bf16)v[2 * i], (__bf16)v[2 * i + 1]};
+        w[i] = __builtin_bit_cast(uint32_t, pr);
+      }
+    }
+  }
+};
 __device__ __forceinline__ float load1(const uint16_t* p) { return __builtin_bit_cast(float, (uint32_t)*p << 16); }
 __device__ __forceinline__ float load1(const float* p) { return *p; }
-
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const float v[8]);
-template <>
-__device__ __forceinline__ void store8<uint16_t>(uint16_t* p, const float v[8]) {
-  uint32_t o[4];
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const bf16x2 pr = {(__bf16)v[2 * i], (__bf16)v[2 * i + 1]};
-    o[i] = __builtin_bit_cast(uint32_t, pr);
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
-}
-template <>
-__device__ __forceinline__ void store8<float>(float* p, const float v[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
 
 // Eight fp32 of 4-byte alignment.
 __device__ __forceinline__ void load8_any(const float* p, float v[8]) {
@@ -52,82 +73,99 @@ __device__ __forceinline__ void load8_any(const float* p, float v[8]) {
   }
 }
 
-// Cosines and signed sines of a unit's 16 elements: element e becomes
+// Cosines and signed sines of 8 elements from e0 on: element e becomes
 // x[e] * c[e] + x[partner(e)] * s[e] (s negative for a pair's first
 // element), the rounding of a c - b s and b c + a s step by step.
 template <int ROT>
-__device__ __forceinline__ void load_turn(const KvAppendArgs& a, int64_t pos, int e0, float c[16], float s[16]) {
+__device__ __forceinline__ void load_turn(const KvAppendArgs& a, int64_t pos, int e0, float c[8], float s[8]) {
   const int half = a.rotary >> 1;
   const float* ct = a.cos_t + pos * half;
   const float* st = a.sin_t + pos * half;
   if constexpr (ROT == kHalves) {
-    // half % 8 == 0: 8 elements use 8 entries in a row
+    if (e0 < a.rotary) {
+      const int j = e0 < half ? e0 : e0 - half;
+      load8_any(ct + j, c);
+      load8_any(st + j, s);
 #pragma unroll
-    for (int k = 0; k < 2; k++) {
-      const int e = e0 + 8 * k;
-      if (e >= a.rotary) {
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-          c[8 * k + i] = 1.0f;
-          s[8 * k + i] = 0.0f;
-        }
-        continue;
-      }
-      const int j = e < half ? e : e - half;
-      load8_any(ct + j, c + 8 * k);
-      load8_any(st + j, s + 8 * k);
-#pragma unroll
-      for (int i = 0; i < 8; i++) s[8 * k + i] = e < half ? -s[8 * k + i] : s[8 * k + i];
+      for (int i = 0; i < 8; i++) s[i] = e0 < half ? -s[i] : s[i];
     }
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int i = 0; i < 16; i++) {
-    const int e = e0 + i;
-    if (e < a.rotary) {
+    for (int i = 0; i < 8; i++) {
+      const int e = e0 + i;
+      if (e >= a.rotary) continue;
       const int j = ROT == kInterleaved ? e >> 1 : (e < half ? e : e - half);
       const bool first = ROT == kInterleaved ? (i & 1) == 0 : e < half;
       c[i] = ct[j];
       s[i] = first ? -st[j] : st[j];
-    } else {
-      c[i] = 1.0f;
-      s[i] = 0.0f;
     }
   }
 }
 
-// 16 elements of a row from e0 on, rotated.
-template <typename T, int ROT>
-__device__ __forceinline__ void load_turned(const KvAppendArgs& a, const T* row, int e0, const float c[16],
-                                            const float s[16], float v[16]) {
-  load8<T>(row + e0, v);
-  load8<T>(row + e0 + 8, v + 8);
-  if constexpr (ROT == kNoRotation) return;
-  const int half = a.rotary >> 1;
-  float w[16];
-  if constexpr (ROT == kInterleaved) {
+// Codes of 8 scaled values, and a block's codes and scale byte from 8 of its
+// values in each of its lanes (see quantize_unit).
+__device__ __forceinline__ uint32_t pack8(const float q[8]) {
+  uint32_t w = e2m1_pack2<0>(0u, q[0], q[1]);
+  w = e2m1_pack2<1>(w, q[2], q[3]);
+  w = e2m1_pack2<2>(w, q[4], q[5]);
+  return e2m1_pack2<3>(w, q[6], q[7]);
+}
+template <bool NV, int SEL>
+__device__ __forceinline__ uint32_t quantize8(const float v[8], const NvConsts& nc, uint32_t& sbyte) {
+  float amax = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; i++) w[i] = v[i ^ 1];
-  } else if constexpr (ROT == kHalves) {
+  for (int i = 0; i < 8; i++) amax = __builtin_fmaxf(amax, __builtin_fabsf(v[i]));
+  amax = __builtin_fmaxf(amax, xor_shfl<1>(amax));
+  float q[8];
+  if constexpr (NV) {
+    const NvCand c = nv_candidate<false>(amax, nc.k6, nc);
 #pragma unroll
-    for (int k = 0; k < 2; k++) {
-      const int e = e0 + 8 * k;
-      const int from = e < half ? e + half : e < a.rotary ? e - half : e;
-      load8<T>(row + from, w + 8 * k);
+    for (int i = 0; i < 8; i++) q[i] = v[i] * c.r;
+    uint32_t w = pack8(q);
+    sbyte = c.code;
+    if constexpr (SEL == 1) {
+      const NvCand c4 = nv_candidate<false>(amax, nc.k4, nc);
+      float q4[8];
+#pragma unroll
+      for (int i = 0; i < 8; i++) q4[i] = v[i] * c4.r;
+      const uint32_t w4 = pack8(q4);
+      float s6 = sq_chain8(q, w), s4 = sq_chain8(q4, w4);
+      s6 += xor_shfl<1>(s6);
+      s4 += xor_shfl<1>(s4);
+      if (cand_error(c4, s4) < cand_error(c, s6)) {
+        w = w4;
+        sbyte = c4.code;
+      }
     }
+    return w;
   } else {
-#pragma unroll
-    for (int i = 0; i < 16; i++) {
-      const int e = e0 + i;
-      w[i] = load1(row + (e < half ? e + half : e < a.rotary ? e - half : e));
+    amax = __builtin_fmaxf(amax, xor_shfl<2>(amax));
+    sbyte = e8m0_from_amax(amax);
+    if constexpr (SEL == 0) {
+      const float sc = e8m0_scale_operand(sbyte);
+      uint32_t w = e2m1_pack2_scaled<0>(0u, v[0], v[1], sc);
+      w = e2m1_pack2_scaled<1>(w, v[2], v[3], sc);
+      w = e2m1_pack2_scaled<2>(w, v[4], v[5], sc);
+      return e2m1_pack2_scaled<3>(w, v[6], v[7], sc);
     }
-  }
+    const int e = (int)sbyte - 127;
 #pragma unroll
-  for (int i = 0; i < 16; i++) {
-    // elements past the rotary part pass unchanged (also infinities, which a
-    // product with 0 would turn into NaN)
-    const float y = v[i] * c[i] + w[i] * s[i];
-    v[i] = e0 + i < a.rotary ? y : v[i];
+    for (int i = 0; i < 8; i++) q[i] = __builtin_ldexpf(v[i], -e);
+    const uint32_t w = pack8(q);
+    float q1[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) q1[i] = __builtin_ldexpf(v[i], -e - 1);
+    const uint32_t w1 = pack8(q1);
+    float s0 = sq_chain8(q, w), s1 = sq_chain8(q1, w1);
+    s0 += xor_shfl<1>(s0);
+    s1 += xor_shfl<1>(s1);
+    s0 += xor_shfl<2>(s0);
+    s1 += xor_shfl<2>(s1);
+    if (e < 127 && 4.0f * s1 < s0) {
+      sbyte += 1;
+      return w1;
+    }
+    return w;
   }
 }
 
@@ -136,82 +174,152 @@ __device__ __forceinline__ float sane_scale(const float* ts, int h) {
   return s >= kFltMin && s <= 3.40282347e38f ? s : 1.0f;
 }
 
-// One wave per (token, group of row passes): 64 / (D / 16) rows at a time,
-// the rows being q heads, then keys, then values. A lane keeps the same unit
-// of every row it visits, so the token's cosines and sines stay in registers.
+// One wave per (token, group of passes): a pass takes 64 / (D / 8) rows, first
+// the query rows', then the keys', then the values'. A lane keeps the same 8
+// elements of every row it visits, so the token's cosines and sines stay in
+// registers; the next pass's elements are on their way during a pass.
 template <typename T, bool NV, int SEL, int ROT>
 __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, int passes_per_wave) {
   const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t t = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (t >= a.tokens) return;  // whole waves only: the lanes below exchange data
-  const int upr = a.c.dim >> 4;
-  const int rpp = 64 / upr;
-  const int r_in = lane / upr, u = lane - r_in * upr;
-  const int e0 = u << 4;
-  const int rows = a.q_heads + 2 * a.c.heads;
+  const int lpr = a.c.dim >> 3;  // lanes of a row
+  const int rpp = 64 / lpr;
+  const int r_in = lane / lpr, u = lane - r_in * lpr;
+  const int e0 = u << 3, half = a.rotary >> 1;
   const int64_t slot = a.slots[t];
   const bool stored = slot >= 0 && slot < (a.c.pages << a.c.page_shift);
   bool placed = true;
-  float c[16], s[16];
+  float c[8], s[8];
   if constexpr (ROT != kNoRotation) {
     const int64_t pos = a.positions[t];
     placed = pos >= 0 && pos < a.max_position;
     if (placed) load_turn<ROT>(a, pos, e0, c, s);
   }
-  const int64_t page = slot >> a.c.page_shift;
-  const int64_t in_page = slot & ((1 << a.c.page_shift) - 1);
-  const int blk_units = NV ? 1 : 2;
-  for (int pass = 0; pass < passes_per_wave; pass++) {
-    const int base = (blockIdx.y * passes_per_wave + pass) * rpp;
-    if (base >= rows) return;
-    const int r = base + r_in;
-    const bool live = r_in < rpp && r < rows;
-    const bool is_q = r < a.q_heads, is_k = !is_q && r < a.q_heads + a.c.heads;
-    const int h = is_q ? r : is_k ? r - a.q_heads : r - a.q_heads - a.c.heads;
-    float v[16];
+  // the lane with this lane's partners
+  const int partner = e0 < half ? lane + (half >> 3) : e0 < a.rotary ? lane - (half >> 3) : lane;
+
+  // 8 elements of a rotated row
+  auto turn = [&](const Raw8<T>& now, const T* row, float v[8]) {
+    now.get(v);
+    if constexpr (ROT == kHalves) {
+      Raw8<T> other;
 #pragma unroll
-    for (int i = 0; i < 16; i++) v[i] = 0.0f;
-    if (live && placed) {
-      if (is_q) load_turned<T, ROT>(a, static_cast<const T*>(a.q) + t * a.q_ts_ + h * a.q_hs, e0, c, s, v);
-      else if (is_k) load_turned<T, ROT>(a, static_cast<const T*>(a.k) + t * a.k_ts_ + h * a.k_hs, e0, c, s, v);
-      else load_turned<T, kNoRotation>(a, static_cast<const T*>(a.v) + t * a.v_ts_ + h * a.v_hs, e0, c, s, v);
+      for (int i = 0; i < Raw8<T>::kWords; i++) other.w[i] = __builtin_amdgcn_ds_bpermute(4 * partner, now.w[i]);
+      if (e0 < a.rotary) {  // all 8 or none
+        float w[8];
+        other.get(w);
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = v[i] * c[i] + w[i] * s[i];
+      }
+    } else if constexpr (ROT != kNoRotation) {
+      float w[8];
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        const int e = e0 + i;
+        if constexpr (ROT == kInterleaved) w[i] = v[i ^ 1];
+        else w[i] = e < a.rotary ? load1(row + (e < half ? e + half : e - half)) : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        const float y = v[i] * c[i] + w[i] * s[i];
+        v[i] = e0 + i < a.rotary ? y : v[i];
+      }
     }
-    if (live && is_q) {
+  };
+
+  const int q_passes = (a.q_heads + rpp - 1) / rpp, c_passes = (a.c.heads + rpp - 1) / rpp;
+  const int first = blockIdx.y * passes_per_wave, end = first + passes_per_wave;
+  const bool lane_on = r_in < rpp;
+
+  // queries
+  {
+    const int p1 = min(end, q_passes);
+    int r = first * rpp + r_in;
+    const T* in = static_cast<const T*>(a.q) + t * a.q_ts_ + (int64_t)r * a.q_hs + e0;
+    T* out = static_cast<T*>(a.q_out) + t * a.o_ts_ + (int64_t)r * a.o_hs + e0;
+    const int64_t in_step = rpp * a.q_hs, out_step = rpp * a.o_hs;
+    Raw8<T> raw{};
+    if (first < p1 && lane_on && r < a.q_heads) raw.load(in);
+    for (int p = first; p < p1; p++) {
+      const Raw8<T> now = raw;
+      const bool live = lane_on && r < a.q_heads;
+      const T* row = live ? in - e0 : static_cast<const T*>(a.q);
+      r += rpp;
+      in += in_step;
+      if (p + 1 < p1 && lane_on && r < a.q_heads) raw.load(in);
+      float v[8];
+      turn(now, row, v);
       if (!placed) {
 #pragma unroll
-        for (int i = 0; i < 16; i++) v[i] = __builtin_nanf("");
+        for (int i = 0; i < 8; i++) v[i] = __builtin_nanf("");
       }
-      T* o = static_cast<T*>(a.q_out) + t * a.o_ts_ + h * a.o_hs + e0;
-      store8<T>(o, v);
-      store8<T>(o + 8, v + 8);
+      if (live) {
+        Raw8<T> y;
+        y.set(v);
+        y.store(out);
+      }
+      out += out_step;
     }
-    if (base + rpp <= a.q_heads) continue;  // queries only
-    NvConsts nc{};
-    if constexpr (NV) {
-      nc.St = live && !is_q ? sane_scale(is_k ? a.c.k_ts : a.c.v_ts, h) : 1.0f;
-      nc.k6 = 1.0f / (6.0f * nc.St);
-      nc.k4 = 1.0f / (4.0f * nc.St);
-    }
-    uint32_t w0, w1, sbyte;
-    quantize_unit<NV, SEL, false, false, false>(v, nc, 0, 0, 0, w0, w1, sbyte);
-    if (live && !is_q && stored && placed) {
-      const int64_t row = ((int64_t)h << a.c.page_shift) + in_page;
-      uint8_t* codes = (is_k ? a.c.kc : a.c.vc) + page * a.c.codes_ps + row * (a.c.dim >> 1) + (e0 >> 1);
-      *reinterpret_cast<uint2*>(codes) = make_uint2(w0, w1);
-      uint8_t* scales = (is_k ? a.c.ks : a.c.vs) + page * a.c.scales_ps + row * (upr / blk_units);
-      if (NV || (u & 1) == 0) scales[u / blk_units] = (uint8_t)sbyte;
+  }
+
+  // keys, then values
+  const int64_t page = slot >> a.c.page_shift;
+  const int64_t in_page = slot & ((1 << a.c.page_shift) - 1);
+  constexpr int kLanes = NV ? 2 : 4;  // of a block
+#pragma unroll
+  for (int kv = 0; kv < 2; kv++) {
+    const int before = q_passes + kv * c_passes;
+    const int p0 = max(first - before, 0), p1 = min(end - before, c_passes);
+    if (p0 >= p1) continue;
+    int h = p0 * rpp + r_in;
+    const int64_t hs = kv ? a.v_hs : a.k_hs;
+    const T* in = static_cast<const T*>(kv ? a.v : a.k) + t * (kv ? a.v_ts_ : a.k_ts_) + (int64_t)h * hs + e0;
+    const int64_t row0 = ((int64_t)h << a.c.page_shift) + in_page;
+    uint8_t* codes_to = (kv ? a.c.vc : a.c.kc) + page * a.c.codes_ps + row0 * (a.c.dim >> 1) + (e0 >> 1);
+    uint8_t* scale_to = (kv ? a.c.vs : a.c.ks) + page * a.c.scales_ps + row0 * (lpr / kLanes) + u / kLanes;
+    const int64_t rows_step = (int64_t)rpp << a.c.page_shift;
+    Raw8<T> raw{};
+    if (lane_on && h < a.c.heads) raw.load(in);
+    for (int p = p0; p < p1; p++) {
+      const Raw8<T> now = raw;
+      const bool live = lane_on && h < a.c.heads;
+      const int head = live ? h : 0;
+      const T* row = live ? in - e0 : static_cast<const T*>(a.k);
+      h += rpp;
+      in += rpp * hs;
+      if (p + 1 < p1 && lane_on && h < a.c.heads) raw.load(in);
+      float v[8];
+      if (kv) now.get(v);
+      else turn(now, row, v);
+      NvConsts nc{};
+      if constexpr (NV) {
+        nc.St = sane_scale(kv ? a.c.v_ts : a.c.k_ts, head);
+        nc.k6 = 1.0f / (6.0f * nc.St);
+        nc.k4 = 1.0f / (4.0f * nc.St);
+      }
+      uint32_t sbyte;
+      const uint32_t codes = quantize8<NV, SEL>(v, nc, sbyte);
+      if (live && stored && placed) {
+        *reinterpret_cast<uint32_t*>(codes_to) = codes;
+        if (u % kLanes == 0) *scale_to = (uint8_t)sbyte;
+      }
+      codes_to += rows_step * (a.c.dim >> 1);
+      scale_to += rows_step * (lpr / kLanes);
     }
   }
 }
 
 template <typename T, bool NV, int SEL>
 static hipError_t append_rot(const KvAppendArgs& a, hipStream_t s) {
-  const int rows = a.q_heads + 2 * a.c.heads, rpp = 64 / (a.c.dim >> 4);
-  const int passes = (rows + rpp - 1) / rpp;
+  const int rpp = 64 / (a.c.dim >> 3);
+  const int passes = (a.q_heads + rpp - 1) / rpp + 2 * ((a.c.heads + rpp - 1) / rpp);
   // few tokens: a wave takes one pass, so that the rows of a token spread
-  // over the GPU; many: a wave takes them all and reads the tables once
+  // over the GPU; many: four, of which each but the first is loaded during
+  // the one before (16384 tokens of 32 + 2 x 8 rows of 128: 83 us; six 87,
+  // all twelve 85)
   const int64_t waves = 4 * 2048;
-  const int per_wave = a.tokens * passes <= waves ? 1 : passes;
+  const int per_wave = a.tokens * passes <= waves ? 1 : passes < 4 ? passes : 4;
   const dim3 grid((unsigned)((a.tokens + 3) / 4), (unsigned)((passes + per_wave - 1) / per_wave));
   if (a.rotary == 0) hipLaunchKernelGGL((kv_append_kernel<T, NV, SEL, kNoRotation>), grid, dim3(256), 0, s, a, per_wave);
   else if (a.interleaved)
@@ -266,8 +374,11 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvReadArgs a) {
     }
   }
   T* y = static_cast<T*>(is_k ? a.k : a.v) + th * a.c.dim + u * 16;
-  store8<T>(y, v);
-  store8<T>(y + 8, v + 8);
+  Raw8<T> lo, hi;
+  lo.set(v);
+  hi.set(v + 8);
+  lo.store(y);
+  hi.store(y + 8);
 }
 
 hipError_t launch_kv_read(const KvReadArgs& a, hipStream_t s) {

@@ -120,8 +120,8 @@ def attention_bounds(ref, fmt_nv, bf16, D, max_len, softcap):
     Scores: fp32 accumulation over D, a few roundings and the hardware's exp2;
     fp32 queries are held to 2^-22 (NVFP4: two fp16 terms) or 2^-24. A score
     off by e scales its weight by 1 + e, in the numerator and the sum alike.
-    Weights: 16-bit rounding (bf16 2^-8, fp16 2^-11), squared where two terms
-    are kept; fp16 loses at most 2^-25 of the lifted scale 2^-6 per key.
+    Weights: 16-bit rounding (bf16 2^-8, fp16 2^-11), to the third power and
+    squared where three and two terms are kept; fp16 loses at most 2^-25 of the lifted scale 2^-6 per key.
     Sums: fp32 over max_len keys. Result: one rounding."""
     out, lse, absv, mag, vmax = ref
     e = (D + 8) * 2.0 ** -24 * mag + 2.0 ** -20
@@ -129,7 +129,7 @@ def attention_bounds(ref, fmt_nv, bf16, D, max_len, softcap):
         e = e + 2.0 ** -21 * mag
     if softcap:
         e = e + softcap * 2.0 ** -20
-    u_p = (2.0 ** -11 if fmt_nv else 2.0 ** -8) if bf16 else (2.0 ** -22 if fmt_nv else 2.0 ** -16)
+    u_p = (2.0 ** -11 if fmt_nv else 2.0 ** -8) if bf16 else (2.0 ** -22 if fmt_nv else 2.0 ** -24)
     sums = (max_len + 64) * 2.0 ** -24
     tol = (u_p + 2 * e[..., None] + 2 * sums) * absv + (2.0 ** -8 if bf16 else 2.0 ** -23) * np.abs(out)
     if fmt_nv:

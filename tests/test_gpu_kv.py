@@ -153,7 +153,7 @@ def test_append_passes_infinities_past_the_rotary_part(fp4):
 # attention
 # ---------------------------------------------------------------------------
 def attention_case(F, O, fmt, dtype, lens, q_lens, heads, kv_heads, dim, page, causal=True, window=0, softcap=0.0,
-                   scale=None, seed=0, q_scale=1.5, max_kv_len=None):
+                   scale=None, seed=0, q_scale=1.5, max_kv_len=None, ref_of=attention_f64):
     need = sum(-(-n // page) for n in lens)
     cache, k, v = random_cache(F, O, fmt, need + 2, page, kv_heads, dim, seed)
     table = lay_out(cache, lens, seed)
@@ -169,7 +169,7 @@ def attention_case(F, O, fmt, dtype, lens, q_lens, heads, kv_heads, dim, page, c
     out, lse = F.kv_attention(q.cuda(), cache, td, ld, **kw)
     torch.cuda.synchronize()
     sc = dim ** -0.5 if scale is None else scale
-    ref = attention_f64(q.double().numpy(), k, v, table, page, lens, q_lens, causal, window, softcap, sc)
+    ref = ref_of(q.double().numpy(), k, v, table, page, lens, q_lens, causal, window, softcap, sc)
     tol, tol_lse = attention_bounds(ref, fmt == NV, dtype == BF, dim, max(lens + [1]), softcap)
     check_attention(out, lse, ref, tol, tol_lse, f"fmt {fmt} {dtype} lens {lens[:4]} q {list(q_lens)[:4]}")
     again, lse2 = F.kv_attention(q.cuda(), cache, td, ld, **kw)
@@ -207,6 +207,22 @@ def test_long_sequences_cut_into_chunks(fp4, oracle, fmt, dtype, page):
 
 
 @pytest.mark.parametrize("fmt,dtype", FD, ids=FD_IDS)
+def test_uneven_batches(fp4, oracle, fmt, dtype):
+    """Batches whose key tiles are cut into equal runs: items that end, begin
+    and lie within runs, more than 64 sequences, sequences without rows or
+    queries between them, heads past 128."""
+    print(f"[uneven] {fmt} {dtype}", flush=True)
+    rng = np.random.RandomState(40)
+    lens = [int(x) for x in rng.randint(0, 60, 90)]
+    lens[3], lens[40], lens[77] = 12000, 9000, 7001
+    attention_case(fp4, oracle, fmt, dtype, lens, [1] * 90, 4, 2, 64, 16, seed=41)
+    q_lens = [int(x) for x in rng.randint(0, 4, 90)]
+    attention_case(fp4, oracle, fmt, dtype, lens, q_lens, 4, 1, 64, 64, seed=42)
+    attention_case(fp4, oracle, fmt, dtype, [7000, 0, 100, 4000], [1] * 4, 6, 2, 256, 32, seed=43)
+    attention_case(fp4, oracle, fmt, dtype, [9000, 30, 6000], [1] * 3, 20, 1, 96, 32, seed=44, window=5000)
+
+
+@pytest.mark.parametrize("fmt,dtype", FD, ids=FD_IDS)
 @pytest.mark.parametrize("causal", [True, False])
 def test_ragged_queries(fp4, oracle, fmt, dtype, causal):
     """Sequences without queries, without rows, with more queries than rows
@@ -225,6 +241,65 @@ def test_many_queries(fp4, oracle, fmt, dtype):
     attention_case(fp4, oracle, fmt, dtype, [390], [333], 5, 5, 64, 16, seed=11)
     attention_case(fp4, oracle, fmt, dtype, [300], [290], 2, 1, 256, 32, seed=12)
     attention_case(fp4, oracle, fmt, dtype, [300], [140], 3, 1, 96, 32, seed=13, causal=False)
+
+
+def prompt_f64(q, k, v, table, page, lens, q_lens, causal, window, softcap, scale):
+    """attention_f64's results for large cases: float64 on the GPU, a kv head
+    and sequence at a time."""
+    T, H, D = q.shape
+    Hkv = k.shape[1]
+    G = H // Hkv
+    q, k, v = (torch.from_numpy(x).cuda() for x in (q, k, v))
+    out, absv = torch.zeros(T, H, D, dtype=torch.float64), torch.zeros(T, H, D, dtype=torch.float64)
+    lse, mag = torch.full((T, H), -np.inf, dtype=torch.float64), torch.zeros(T, H, dtype=torch.float64)
+    vmax = torch.zeros(T, H, 1, dtype=torch.float64)
+    start = 0
+    for b, n in enumerate(q_lens):
+        L = int(lens[b])
+        j = np.arange(L)
+        at = (torch.from_numpy(table[b][j // page]).long(), torch.from_numpy(j % page))
+        back = (L - n + torch.arange(n, device="cuda"))[:, None] - torch.arange(L, device="cuda")
+        hidden = torch.zeros_like(back, dtype=torch.bool) if not causal else (back < 0) | (window > 0) & (back >= window)
+        for h in range(Hkv if L else 0):
+            kk, vv = k[at[0].cuda(), h, at[1].cuda()], v[at[0].cuda(), h, at[1].cuda()]
+            for head in range(h * G, h * G + G):
+                qq = q[start:start + n, head]
+                s = qq @ kk.T * scale
+                if softcap:
+                    s = softcap * torch.tanh(s / softcap)
+                s = s.masked_fill(hidden, -np.inf)
+                l = torch.logsumexp(s, 1)
+                w = torch.exp(s - l[:, None]).nan_to_num(0.0)
+                sl = slice(start, start + n)
+                out[sl, head], absv[sl, head] = (w @ vv).cpu(), (w @ vv.abs()).cpu()
+                lse[sl, head] = l.cpu()
+                mag[sl, head] = ((qq.abs() @ kk.abs().T).amax(1) * abs(scale)).cpu()
+                vmax[sl, head, 0] = vv.abs().max().cpu()
+        start += n
+    return tuple(x.numpy() for x in (out, lse, absv, mag, vmax))
+
+
+LARGE = [
+    # (heads, kv_heads, dim, page, lens, q_lens, causal, window, softcap)
+    (16, 16, 128, 64, [900, 1500, 70], [900, 700, 70], True, 0, 0.0),       # three row tiles a wave
+    (12, 12, 128, 16, [1100, 640], [500, 640], True, 0, 0.0),               # two
+    (40, 20, 64, 16, [1000, 750, 0, 33], [1000, 500, 5, 33], True, 0, 0.0), # four
+    (20, 20, 64, 32, [640, 400], [600, 400], True, 90, 20.0),               # two
+    (16, 8, 96, 32, [777, 1300], [777, 1031], True, 0, 0.0),
+    (32, 4, 128, 128, [700, 900], [500, 800], False, 0, 0.0),
+    (24, 24, 256, 32, [500, 700], [500, 650], True, 0, 0.0),
+    (24, 12, 192, 64, [500, 700], [500, 650], True, 333, 0.0),
+]
+
+
+@pytest.mark.parametrize("fmt", BOTH)
+@pytest.mark.parametrize("case", LARGE, ids=[f"{c[0]}x{c[2]}-{len(c[4])}" for c in LARGE])
+def test_prompts_of_many_rows(fp4, oracle, fmt, case):
+    """Prompts large enough for every count of row tiles a wave takes."""
+    heads, kv_heads, dim, page, lens, q_lens, causal, window, softcap = case
+    print(f"[large] {fmt} {case}", flush=True)
+    attention_case(fp4, oracle, fmt, BF, lens, q_lens, heads, kv_heads, dim, page, causal=causal, window=window,
+                   softcap=softcap, seed=30, ref_of=prompt_f64)
 
 
 @pytest.mark.parametrize("fmt,dtype", FD, ids=FD_IDS)
