@@ -15,7 +15,7 @@
 // workspace and are joined by a second kernel.
 //
 // Many rows (prompts; bound by arithmetic): a workgroup's four waves have rows
-// of their own, 16 to 64 each, and go through the key tiles together. Each
+// of their own, 32 or 48 each, and go through the key tiles together. Each
 // wave converts a quarter of the next tile and leaves it in LDS as the matrix
 // instructions' operands, while all of them use the present one.
 //
@@ -968,7 +968,7 @@ struct ManySpace {
 };
 
 template <int DP, bool NV, bool FULL, int RT>
-__global__ __launch_bounds__(256, 2) void kv_attn_many_kernel(KvAttnArgs a) {
+__global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 64 ? 4 : RT == 2 ? 3 : 2) void kv_attn_many_kernel(KvAttnArgs a) {
   using T = Tile<DP, NV>;
   using Space = ManySpace<DP, NV>;
   constexpr int NW = 4;
@@ -1185,22 +1185,27 @@ namespace {
 constexpr int kWaves = 4;
 // waves of the wide form: as many as its registers allow (heads past 128: no wide form)
 constexpr int wide_waves(int dp) { return dp <= 128 ? 8 : kWaves; }
-// most 16-row tiles of a wave in the form for many rows, as its registers allow
-constexpr int most_tiles(int dp) { return dp <= 64 ? 4 : dp <= 128 ? 3 : 1; }
+// Most 16-row tiles of a wave in the form for many rows. Three rather than
+// two share a tile's conversion among more rows but leave registers for two
+// waves a SIMD instead of three: even at heads of 128 (a prompt of 8192:
+// 646 against 660 us), slower at 64 (three or four against two: 327 against
+// 314 us); past 128 three do not fit, and one is a third slower (1226 against
+// 820 us, 4096 queries over 8192).
+constexpr int most_tiles(int dp) { return dp > 64 && dp <= 128 ? 3 : 2; }
 }  // namespace
 
 KvAttnPlan plan_kv_attention(const KvAttnArgs& a) {
   KvAttnPlan p{};
   const int64_t rows = a.tokens * a.group;
   const int64_t cus = device_cu_count();
-  // Many rows a sequence, and enough of them that two workgroups a CU have
-  // two row tiles a wave (heads past 128: one) or more: the form for many.
+  // Many rows a sequence, and enough of them to fill the GPU (two workgroups a
+  // CU, heads past 128 one) with two row tiles a wave or more: the form for many.
   // Fewer rows: each key tile's conversion and barrier serve too few (8 x 448
-  // queries of 20 heads of 64 over 1500 keys: 58 us in that form, 46 in the other).
+  // queries of 20 heads of 64 over 1500 keys: 58 us in that form, 43 in the other).
   if (a.bf16 && a.offs && rows >= 128 * a.batch) {
-    const int least = a.c.dim <= 128 ? 2 : 1;
-    for (int n = most_tiles(a.c.dim); n >= least; n -= n == 4 ? 2 : 1) {
-      if ((rows / (16 * kWaves * n) + a.batch / 2) * a.c.heads < 2 * cus) continue;
+    const int64_t fill = a.c.dim <= 128 ? 2 * cus : cus;
+    for (int n = most_tiles(a.c.dim); n >= 2; n--) {
+      if ((rows / (16 * kWaves * n) + a.batch / 2) * a.c.heads < fill) continue;
       p.row_tiles = n;
       p.tiles = rows / (16 * kWaves * n) + a.batch;
       return p;

@@ -282,9 +282,9 @@ def prompt_f64(q, k, v, table, page, lens, q_lens, causal, window, softcap, scal
 LARGE = [
     # (heads, kv_heads, dim, page, lens, q_lens, causal, window, softcap)
     (16, 16, 128, 64, [900, 1500, 70], [900, 700, 70], True, 0, 0.0),       # three row tiles a wave
-    (12, 12, 128, 16, [1100, 640], [500, 640], True, 0, 0.0),               # two
-    (40, 20, 64, 16, [1000, 750, 0, 33], [1000, 500, 5, 33], True, 0, 0.0), # four
-    (20, 20, 64, 32, [640, 400], [600, 400], True, 90, 20.0),               # two
+    (12, 12, 128, 16, [1100, 640], [500, 640], True, 0, 0.0),               # two row tiles
+    (40, 20, 64, 16, [1000, 750, 0, 33], [1000, 500, 5, 33], True, 0, 0.0), # two, short head
+    (20, 20, 64, 32, [640, 400], [600, 400], True, 90, 20.0),
     (16, 8, 96, 32, [777, 1300], [777, 1031], True, 0, 0.0),
     (32, 4, 128, 128, [700, 900], [500, 800], False, 0, 0.0),
     (24, 24, 256, 32, [500, 700], [500, 650], True, 0, 0.0),
