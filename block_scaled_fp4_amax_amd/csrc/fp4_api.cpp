@@ -683,8 +683,8 @@ static fp4_status plan_kv_attention_call(const fp4_kv_cache* cache, const fp4_kv
   *p = KvAttnPlan{};
   if (args->batch > 0 && args->tokens > 0) {
     *p = plan_kv_attention(*a);
-    // the join has a workgroup for each of an item's 16 rows
-    if (p->tiles * cache->kv_heads * 16 > kMaxGridX) return FP4_ERR_UNSUPPORTED;
+    // the join has a workgroup for each of an item's rows, 32 at most
+    if (p->tiles * cache->kv_heads * 32 > kMaxGridX) return FP4_ERR_UNSUPPORTED;
   }
   return FP4_OK;
 }

@@ -767,14 +767,14 @@ union FewSpace {
   } join;
 };
 
-// 16 rows of kv head h over their keys from c_lo (a multiple of kTileKeys) to
-// c_hi, each wave every NW-th tile; the result to `out`, or (part) the
-// partial result to a slot.
-template <int DP, bool NV, bool BF16, bool FULL, int NW>
+// RT * 16 rows of kv head h over their keys from c_lo (a multiple of
+// kTileKeys) to c_hi, each wave every NW-th tile; the result to `out`, or
+// (part) the partial result to a slot.
+template <int DP, bool NV, bool BF16, bool FULL, int NW, int RT>
 __device__ __forceinline__ void attend_few(const KvAttnArgs& a, const RowTile& r, int h, int c_lo, int c_hi,
                                            float* part, FewSpace<DP, NV, NW>& lds) {
   using T = Tile<DP, NV>;
-  constexpr int kRows = 16;
+  constexpr int kRows = 16 * RT;
   constexpr int kStep = kTileKeys * NW;
   constexpr int kDepth = FewSpace<DP, NV, NW>::kDepth;
   constexpr uint32_t kAllCopies = (1u << 2 * T::kCopies) - 1;
@@ -797,17 +797,19 @@ __device__ __forceinline__ void attend_few(const KvAttnArgs& a, const RowTile& r
       in.copy(min(kt + i * kStep, last), in.pages(min(kt + i * kStep, last)), ring + i * T::kSlot, lane, kAllCopies);
     ahead = in.pages(min(kt + kDepth * kStep, last));
   }
-  Rows<DP, NV, BF16, FULL, 1> rows;
+  Rows<DP, NV, BF16, FULL, RT> rows;
   rows.start(a, r, h, c, g);
 
   uint32_t slot = 0;
   for (; kt < c_hi; kt += kStep) {
     wait_copies<(kDepth - 1) * T::kLoads>();
     const uint8_t* y = &lds.tiles[wave][0][0] + slot;
-    float s[1][8];
+    float s[RT][8];
 #pragma unroll
     for (int sub = 0; sub < 2; sub++) {
-      f32x4 acc[1] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
+      f32x4 acc[RT];
+#pragma unroll
+      for (int rt = 0; rt < RT; rt++) acc[rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int w = 0; w < T::kKWords; w++) {
         const uint32_t code = *reinterpret_cast<const uint32_t*>(y + sub * T::kHalf + in.k_word(c, g, w));
@@ -815,7 +817,10 @@ __device__ __forceinline__ void attend_few(const KvAttnArgs& a, const RowTile& r
         rows.times_k(convert8<NV>(code, scale), w, acc);
       }
 #pragma unroll
-      for (int i = 0; i < 4; i++) s[0][4 * sub + i] = acc[0][i];
+      for (int rt = 0; rt < RT; rt++) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) s[rt][4 * sub + i] = acc[rt][i];
+      }
     }
     uint32_t v[8][T::kVWords], vs[8];
 #pragma unroll
@@ -838,7 +843,7 @@ __device__ __forceinline__ void attend_few(const KvAttnArgs& a, const RowTile& r
         }
       }
     }
-    u32x4 pw[1][Rows<DP, NV, BF16, FULL, 1>::kPTerms];
+    u32x4 pw[RT][Rows<DP, NV, BF16, FULL, RT>::kPTerms];
     rows.weigh(a, kt, g, s, pw);
 #pragma unroll
     for (int w = 0; w < T::kVWords; w++) {
@@ -860,65 +865,73 @@ __device__ __forceinline__ void attend_few(const KvAttnArgs& a, const RowTile& r
   __syncthreads();
 
   // O tile j holds of row c the elements kChunkV * (4g + i) + j
-  if (g == 0) {
-    lds.join.m[wave][c] = rows.m[0];
-    lds.join.l[wave][c] = rows.l[0];
-  }
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
-#pragma unroll
-    for (int j = 0; j < T::kChunkV; j++) lds.join.o[wave][c][(4 * g + i) * T::kChunkV + j] = rows.o[0][j][i];
-  }
-  __syncthreads();
-  constexpr int kEach = kRows * DP / (64 * NW);  // elements a thread joins
-  constexpr int kPerRow = DP / kEach;
-  const int jr = threadIdx.x / kPerRow, d = threadIdx.x % kPerRow * kEach;
-  const int jrow = r.row0 + jr;
-  if (jrow >= r.n * G || d >= D) return;
-  const int jt = jrow / G, jhead = h * G + jrow - jt * G;
-  float top = lds.join.m[0][jr];
-#pragma unroll
-  for (int w = 1; w < NW; w++) top = __builtin_fmaxf(top, lds.join.m[w][jr]);
-  float sum = 0.0f, acc[kEach];
-#pragma unroll
-  for (int j = 0; j < kEach; j++) acc[j] = 0.0f;
-#pragma unroll
-  for (int w = 0; w < NW; w++) {
-    const float f = __builtin_amdgcn_exp2f(lds.join.m[w][jr] - top);
-    sum += f * lds.join.l[w][jr];
-#pragma unroll
-    for (int j = 0; j < kEach; j++) acc[j] += f * lds.join.o[w][jr][d + j];
-  }
-  if (part) {
-#pragma unroll
-    for (int j = 0; j < kEach; j++) part[jr * D + d + j] = acc[j];
-    if (d == 0) {
-      part[kRows * D + jr] = top;
-      part[kRows * (D + 1) + jr] = sum;
+  for (int rt = 0; rt < RT; rt++) {
+    if (rt) __syncthreads();
+    if (g == 0) {
+      lds.join.m[wave][c] = rows.m[rt];
+      lds.join.l[wave][c] = rows.l[rt];
     }
-  } else {
-    const float f = row_factor<NV>(a, h, sum);
 #pragma unroll
-    for (int j = 0; j < kEach; j++) acc[j] *= f;
-    store_row<BF16, kEach>(a, r.q0 + jt, jhead, d, acc);
-    if (d == 0 && a.lse) a.lse[(int64_t)(r.q0 + jt) * a.q_heads + jhead] = row_lse<NV>(top, sum);
+    for (int i = 0; i < 4; i++) {
+#pragma unroll
+      for (int j = 0; j < T::kChunkV; j++) lds.join.o[wave][c][(4 * g + i) * T::kChunkV + j] = rows.o[rt][j][i];
+    }
+    __syncthreads();
+    constexpr int kEach = 16 * DP / (64 * NW);  // elements a thread joins
+    constexpr int kPerRow = DP / kEach;
+    const int jr = threadIdx.x / kPerRow, d = threadIdx.x % kPerRow * kEach;
+    const int jrow = r.row0 + 16 * rt + jr;
+    if (jrow >= r.n * G || d >= D) continue;
+    const int jt = jrow / G, jhead = h * G + jrow - jt * G;
+    float top = lds.join.m[0][jr];
+#pragma unroll
+    for (int w = 1; w < NW; w++) top = __builtin_fmaxf(top, lds.join.m[w][jr]);
+    float sum = 0.0f, acc[kEach];
+#pragma unroll
+    for (int j = 0; j < kEach; j++) acc[j] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; w++) {
+      const float f = __builtin_amdgcn_exp2f(lds.join.m[w][jr] - top);
+      sum += f * lds.join.l[w][jr];
+#pragma unroll
+      for (int j = 0; j < kEach; j++) acc[j] += f * lds.join.o[w][jr][d + j];
+    }
+    if (part) {
+      const int pr = 16 * rt + jr;
+#pragma unroll
+      for (int j = 0; j < kEach; j++) part[pr * D + d + j] = acc[j];
+      if (d == 0) {
+        part[kRows * D + pr] = top;
+        part[kRows * (D + 1) + pr] = sum;
+      }
+    } else {
+      const float f = row_factor<NV>(a, h, sum);
+#pragma unroll
+      for (int j = 0; j < kEach; j++) acc[j] *= f;
+      store_row<BF16, kEach>(a, r.q0 + jt, jhead, d, acc);
+      if (d == 0 && a.lse) a.lse[(int64_t)(r.q0 + jt) * a.q_heads + jhead] = row_lse<NV>(top, sum);
+    }
   }
 }
 
+// Waves a SIMD that the registers of the form for few rows allow.
+constexpr int few_waves(int dp, int rt) { return dp == 256 ? 1 : dp == 128 && rt > 1 ? 2 : 3; }
+
 // One workgroup for each row tile and kv head.
-template <int DP, bool NV, bool BF16, bool FULL, int NW>
-__global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 3) void kv_attn_kernel(KvAttnArgs a) {
+template <int DP, bool NV, bool BF16, bool FULL, int NW, int RT>
+__global__ __launch_bounds__(64 * NW, few_waves(DP, RT)) void kv_attn_kernel(KvAttnArgs a) {
   __shared__ __attribute__((aligned(16))) FewSpace<DP, NV, NW> lds;
   const int h = blockIdx.x % a.c.heads, tile = blockIdx.x / a.c.heads;
   RowTile r;
-  if (!find_tile<16>(a, tile, r)) return;
-  attend_few<DP, NV, BF16, FULL, NW>(a, r, h, r.lo, r.hi, nullptr, lds);
+  if (!find_tile<16 * RT>(a, tile, r)) return;
+  attend_few<DP, NV, BF16, FULL, NW, RT>(a, r, h, r.lo, r.hi, nullptr, lds);
 }
 
 // The balanced form: one workgroup for each run of key tiles.
-template <int DP, bool NV, bool BF16, bool FULL, int NW>
-__global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 3) void kv_attn_runs_kernel(KvAttnArgs a, int least) {
-  constexpr int kRows = 16;
+template <int DP, bool NV, bool BF16, bool FULL, int NW, int RT>
+__global__ __launch_bounds__(64 * NW, few_waves(DP, RT)) void kv_attn_runs_kernel(KvAttnArgs a, int least) {
+  constexpr int kRows = 16 * RT;
   __shared__ __attribute__((aligned(16))) FewSpace<DP, NV, NW> lds;
   const WorkScan<kRows> scan(a, 0);
   const int total = total_work<kRows>(a, scan);
@@ -942,7 +955,7 @@ __global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 3) void kv_attn_runs_kerne
     const int c_lo = max(w.lo + k * kTileKeys, r.lo), c_hi = min(w.lo + (k + take) * kTileKeys, r.hi);
     float* part =
         take == w.span ? nullptr : a.ws + (int64_t)(2 * blockIdx.x + (k == 0 ? 1 : 0)) * (kRows * (a.c.dim + 2));
-    attend_few<DP, NV, BF16, FULL, NW>(a, r, item % a.c.heads, c_lo, c_hi, part, lds);
+    attend_few<DP, NV, BF16, FULL, NW, RT>(a, r, item % a.c.heads, c_lo, c_hi, part, lds);
     left -= take;
     if (left == 0) return;
     k = 0;
@@ -1113,9 +1126,9 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 64 ? 4 : RT == 2 ? 3 : 2
 // Joins the partial results of one row of one item, if it has any: DP / 4
 // lanes take four elements each, and the rest of the workgroup every
 // kGroups-th partial result.
-template <int DP, bool NV, bool BF16, int THREADS>
+template <int DP, bool NV, bool BF16, int RT, int THREADS>
 __global__ __launch_bounds__(THREADS) void kv_attn_join_kernel(KvAttnArgs a, int runs, int least, int rows_each) {
-  constexpr int kRows = 16;
+  constexpr int kRows = 16 * RT;
   constexpr int kLanes = DP / 4, kGroups = THREADS / kLanes;
   __shared__ float s_acc[kGroups][DP + 4];
   __shared__ float s_m[kGroups], s_l[kGroups];
@@ -1185,6 +1198,8 @@ namespace {
 constexpr int kWaves = 4;
 // waves of the wide form: as many as its registers allow (heads past 128: no wide form)
 constexpr int wide_waves(int dp) { return dp <= 128 ? 8 : kWaves; }
+// Most 16-row tiles of a wave in the form for few rows.
+constexpr int few_tiles(int dp, bool bf16) { return bf16 && dp <= 128 ? 2 : 1; }
 // Most 16-row tiles of a wave in the form for many rows. Three rather than
 // two share a tile's conversion among more rows but leave registers for two
 // waves a SIMD instead of three: even at heads of 128 (a prompt of 8192:
@@ -1211,21 +1226,34 @@ KvAttnPlan plan_kv_attention(const KvAttnArgs& a) {
       return p;
     }
   }
-  p.tiles = a.offs ? rows / 16 + a.batch : a.batch * ((a.group + 15) / 16);
-  // keys a tile can see at most: all, or the windows of its queries
+  // Few. Keys a tile can see at most: all, or the windows of its queries.
   int64_t keys = a.max_len;
   if (a.window > 0) {
-    const int64_t w = a.window + 16 + kTileKeys;
+    const int64_t w = a.window + 32 + kTileKeys;
     keys = keys < w ? keys : w;
   }
+  const int wide = wide_waves(a.c.dim);
+  const int64_t each = keys / (wide * kTileKeys);  // key tiles of a wave of the wide form
+  // Two row tiles share the conversion of their keys, but make half as many
+  // workgroups and leave fewer waves a SIMD. They are taken where enough
+  // workgroups are left (8 x 448 queries over 1500 keys, 20 heads of 64: 40
+  // against 46 us), where one row tile each would need a second round of the
+  // wide form (24 x 5 queries over 3000, heads of 128: 28 against 39; but 16 x 5
+  // over 6000 of 4 kv heads, one round: 42 against 34), and for the runs of long
+  // keys where there is work for them all (60 queries over 20000: 53 against 58;
+  // but 16 over 8192: 23 against 21).
+  auto tiles = [&](int64_t per) { return a.batch * ((rows / a.batch + per - 1) / per) * a.c.heads; };
+  p.few_tiles = 1;
+  if (rows > 16 * a.batch && (tiles(32) >= 4 * cus || (tiles(16) <= 2 * cus && (tiles(16) > cus || (each > 24 && tiles(16) >= cus / 4)))))
+    p.few_tiles = few_tiles(a.c.dim, a.bf16);
+  const int per = 16 * p.few_tiles;
+  p.tiles = a.offs ? rows / per + a.batch : a.batch * ((a.group + per - 1) / per);
   const int64_t items = p.tiles * a.c.heads;
   p.waves = kWaves;
   // Little work, or at most a few tiles more for some workgroups than for
   // others: one launch whose workgroups have many waves, rather than runs and
   // a second launch to join them (24 sequences of 5 queries over 3000 keys:
   // 20 against 28 us; 32 to 4096 keys: 27 against 32).
-  const int wide = wide_waves(a.c.dim);
-  const int64_t each = keys / (wide * kTileKeys);  // key tiles of a wave
   if (items <= 4 * cus && each <= (2 * items >= cus ? 24 : 8)) {
     p.waves = wide;
     return p;
@@ -1233,11 +1261,11 @@ KvAttnPlan plan_kv_attention(const KvAttnArgs& a) {
   // Enough items of few keys: the order in which workgroups end evens them out.
   // (Key tiles are counted in 32 bits, whatever the offsets are on the device.)
   const int64_t span = (a.max_len + kTileKeys - 1) / kTileKeys + 1;
-  const int64_t most = (a.offs ? a.batch * (rows / 16 + 1) : p.tiles) * a.c.heads;
+  const int64_t most = (a.offs ? a.batch * (rows / per + 1) : p.tiles) * a.c.heads;
   if (items >= 4 * cus || keys <= 8 * kWaves * kTileKeys || most >= (int64_t(1) << 31) / span) return p;
   p.runs = 2 * cus;
   p.least = 2 * kWaves;
-  p.ws = (size_t)(2 * p.runs) * (size_t)(16 * (a.c.dim + 2)) * sizeof(float);
+  p.ws = (size_t)(2 * p.runs) * (size_t)(per * (a.c.dim + 2)) * sizeof(float);
   return p;
 }
 
@@ -1253,27 +1281,37 @@ static void launch_many(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t s)
   hipLaunchKernelGGL((kv_attn_many_kernel<DP, NV, FULL, most_tiles(DP)>), grid, dim3(256), 0, s, a);
 }
 
-template <int DP, bool NV, bool BF16, bool FULL>
-static hipError_t launch_rows(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t s) {
+template <int DP, bool NV, bool BF16, bool FULL, int RT>
+static void launch_few(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t s) {
   constexpr int kWide = wide_waves(DP);
   const int64_t items = p.tiles * a.c.heads;
-  if (p.row_tiles > 0) {
-    if constexpr (BF16) launch_many<DP, NV, FULL>(a, p, s);
-  } else if (p.runs > 0) {
+  const dim3 grid((unsigned)items);
+  if (p.runs > 0) {
     const int runs = (int)p.runs, least = (int)p.least;
-    hipLaunchKernelGGL((kv_attn_runs_kernel<DP, NV, BF16, FULL, kWaves>), dim3(runs), dim3(64 * kWaves), 0, s, a, least);
-    const int each = !a.offs && a.group < 16 ? a.group : 16;
+    hipLaunchKernelGGL((kv_attn_runs_kernel<DP, NV, BF16, FULL, kWaves, RT>), dim3(runs), dim3(64 * kWaves), 0, s, a,
+                       least);
+    const int each = !a.offs && a.group < 16 * RT ? a.group : 16 * RT;
+    const dim3 rows((unsigned)(items * each));
     // few partial results each: more threads would have nothing to do
     if (runs <= 8 * items)
-      hipLaunchKernelGGL((kv_attn_join_kernel<DP, NV, BF16, 128>), dim3((unsigned)(items * each)), dim3(128), 0, s, a,
-                         runs, least, each);
+      hipLaunchKernelGGL((kv_attn_join_kernel<DP, NV, BF16, RT, 128>), rows, dim3(128), 0, s, a, runs, least, each);
     else
-      hipLaunchKernelGGL((kv_attn_join_kernel<DP, NV, BF16, 512>), dim3((unsigned)(items * each)), dim3(512), 0, s,
-                         a, runs, least, each);
+      hipLaunchKernelGGL((kv_attn_join_kernel<DP, NV, BF16, RT, 512>), rows, dim3(512), 0, s, a, runs, least, each);
   } else if (p.waves == kWaves) {
-    hipLaunchKernelGGL((kv_attn_kernel<DP, NV, BF16, FULL, kWaves>), dim3((unsigned)items), dim3(64 * kWaves), 0, s, a);
+    hipLaunchKernelGGL((kv_attn_kernel<DP, NV, BF16, FULL, kWaves, RT>), grid, dim3(64 * kWaves), 0, s, a);
   } else {
-    hipLaunchKernelGGL((kv_attn_kernel<DP, NV, BF16, FULL, kWide>), dim3((unsigned)items), dim3(64 * kWide), 0, s, a);
+    hipLaunchKernelGGL((kv_attn_kernel<DP, NV, BF16, FULL, kWide, RT>), grid, dim3(64 * kWide), 0, s, a);
+  }
+}
+
+template <int DP, bool NV, bool BF16, bool FULL>
+static hipError_t launch_rows(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t s) {
+  if (p.row_tiles > 0) {
+    if constexpr (BF16) launch_many<DP, NV, FULL>(a, p, s);
+  } else if (p.few_tiles == 1) {
+    launch_few<DP, NV, BF16, FULL, 1>(a, p, s);
+  } else {
+    launch_few<DP, NV, BF16, FULL, few_tiles(DP, BF16)>(a, p, s);
   }
   return hipGetLastError();
 }

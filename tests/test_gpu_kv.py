@@ -302,6 +302,27 @@ def test_prompts_of_many_rows(fp4, oracle, fmt, case):
                    softcap=softcap, seed=30, ref_of=prompt_f64)
 
 
+MIDDLE = [
+    # some queries of each sequence: two row tiles in each of the launches for few rows
+    (128, 16, 128, 64, [300, 77, 901, 0, 120], [7, 9, 5, 2, 12], True, 0, 0.0),           # one round, wide workgroups
+    (128, 16, 96, 16, [300, 77, 901, 33, 120], [7, 0, 11, 2, 12], False, 0, 15.0),
+    (128, 16, 128, 32, [500, 700, 450, 300, 120], [9, 7, 8, 9, 6], True, 61, 0.0),
+    (64, 16, 64, 16, [100, 130, 31, 64] * 4, [30, 34, 31, 40] * 4, True, 0, 0.0),          # many workgroups
+    (64, 16, 96, 16, [100, 130, 31, 64] * 4, [30, 33, 31, 40] * 4, False, 0, 0.0),
+    (64, 8, 128, 64, [6700, 300, 41], [10, 12, 3], True, 0, 0.0),                         # runs of long keys
+    (64, 8, 32, 16, [6311, 6550], [11, 10], False, 0, 0.0),
+]
+
+
+@pytest.mark.parametrize("fmt", BOTH)
+@pytest.mark.parametrize("case", MIDDLE, ids=[f"{c[0]}x{c[2]}-{c[4][0]}" for c in MIDDLE])
+def test_some_queries_of_each_sequence(fp4, oracle, fmt, case):
+    heads, kv_heads, dim, page, lens, q_lens, causal, window, softcap = case
+    print(f"[middle] {fmt} {case}", flush=True)
+    attention_case(fp4, oracle, fmt, BF, lens, q_lens, heads, kv_heads, dim, page, causal=causal, window=window,
+                   softcap=softcap, seed=31)
+
+
 @pytest.mark.parametrize("fmt,dtype", FD, ids=FD_IDS)
 @pytest.mark.parametrize("window", [1, 17, 100])
 def test_window(fp4, oracle, fmt, dtype, window):
