@@ -1123,14 +1123,14 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 64 ? 4 : RT == 2 ? 3 : 2
   }
 }
 
-// Joins the partial results of one row of one item, if it has any: DP / 4
-// lanes take four elements each, and the rest of the workgroup every
-// kGroups-th partial result.
-template <int DP, bool NV, bool BF16, int RT, int THREADS>
+// Joins COLS columns of the partial results of one row of one item, if it has
+// any: COLS / 4 lanes take four elements each, and the rest of the workgroup
+// every kGroups-th partial result.
+template <int DP, bool NV, bool BF16, int RT, int THREADS, int COLS>
 __global__ __launch_bounds__(THREADS) void kv_attn_join_kernel(KvAttnArgs a, int runs, int least, int rows_each) {
   constexpr int kRows = 16 * RT;
-  constexpr int kLanes = DP / 4, kGroups = THREADS / kLanes;
-  __shared__ float s_acc[kGroups][DP + 4];
+  constexpr int kLanes = COLS / 4, kGroups = THREADS / kLanes;
+  __shared__ float s_acc[kGroups][COLS + 4];
   __shared__ float s_m[kGroups], s_l[kGroups];
   const int jr = blockIdx.x % rows_each;
   int item = blockIdx.x / rows_each, before;
@@ -1147,7 +1147,7 @@ __global__ __launch_bounds__(THREADS) void kv_attn_join_kernel(KvAttnArgs a, int
   if (row >= w.n * G) return;
   const int t = row / G, head = h * G + row - t * G;
   const int64_t step = kRows * (D + 2);
-  const int grp = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
+  const int grp = threadIdx.x / kLanes, dl = threadIdx.x % kLanes * 4, d = blockIdx.y * COLS + dl;
   float top = kNoMax, sum = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (d < D) {
@@ -1166,11 +1166,11 @@ __global__ __launch_bounds__(THREADS) void kv_attn_join_kernel(KvAttnArgs a, int
       acc.w = acc.w * fo + v.w * fn;
     }
   }
-  if (d == 0) {
+  if (dl == 0) {
     s_m[grp] = top;
     s_l[grp] = sum;
   }
-  *reinterpret_cast<float4*>(&s_acc[grp][d]) = acc;
+  *reinterpret_cast<float4*>(&s_acc[grp][dl]) = acc;
   __syncthreads();
   if (grp != 0 || d >= D) return;
   const int used = n < kGroups ? n : kGroups;
@@ -1181,7 +1181,7 @@ __global__ __launch_bounds__(THREADS) void kv_attn_join_kernel(KvAttnArgs a, int
   for (int k = 0; k < used; k++) {
     const float f = __builtin_amdgcn_exp2f(s_m[k] - all);
     sum += f * s_l[k];
-    const float4 v = *reinterpret_cast<const float4*>(&s_acc[k][d]);
+    const float4 v = *reinterpret_cast<const float4*>(&s_acc[k][dl]);
     y[0] += f * v.x;
     y[1] += f * v.y;
     y[2] += f * v.z;
@@ -1292,11 +1292,14 @@ static void launch_few(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t s) 
                        least);
     const int each = !a.offs && a.group < 16 * RT ? a.group : 16 * RT;
     const dim3 rows((unsigned)(items * each));
-    // few partial results each: more threads would have nothing to do
+    // few partial results each: more threads would have nothing to do; many
+    // (256 of a row of 128): 32 columns a workgroup (512 threads for all of
+    // them: 22.3 against 21.8 us, 130001 keys)
     if (runs <= 8 * items)
-      hipLaunchKernelGGL((kv_attn_join_kernel<DP, NV, BF16, RT, 128>), rows, dim3(128), 0, s, a, runs, least, each);
+      hipLaunchKernelGGL((kv_attn_join_kernel<DP, NV, BF16, RT, 128, DP>), rows, dim3(128), 0, s, a, runs, least, each);
     else
-      hipLaunchKernelGGL((kv_attn_join_kernel<DP, NV, BF16, RT, 512>), rows, dim3(512), 0, s, a, runs, least, each);
+      hipLaunchKernelGGL((kv_attn_join_kernel<DP, NV, BF16, RT, 256, 32>), dim3(rows.x, (a.c.dim + 31) / 32),
+                         dim3(256), 0, s, a, runs, least, each);
   } else if (p.waves == kWaves) {
     hipLaunchKernelGGL((kv_attn_kernel<DP, NV, BF16, FULL, kWaves, RT>), grid, dim3(64 * kWaves), 0, s, a);
   } else {
