@@ -632,7 +632,7 @@ fp4_status fp4_kv_read(const fp4_kv_cache* cache, int64_t tokens, const int64_t*
   if (y_dtype != FP4_F32 && y_dtype != FP4_BF16) return FP4_ERR_INVALID;
   if (tokens < 0) return FP4_ERR_INVALID;
   if (tokens > (int64_t(1) << 30) ||
-      (tokens * cache->kv_heads * (cache->head_dim / 16) + 255) / 256 > kMaxGridX)
+      (tokens * cache->kv_heads * (cache->head_dim / 8) + 255) / 256 > kMaxGridX)
     return FP4_ERR_UNSUPPORTED;
   if (tokens == 0) return FP4_OK;
   if (!slots || !k_out || !v_out) return FP4_ERR_INVALID;

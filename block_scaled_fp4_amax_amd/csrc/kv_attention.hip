@@ -5,10 +5,10 @@
 // in one pass over the keys with a running maximum and sum, in tiles of 32
 // keys. A row is (query, head of the kv head's group). Two forms:
 //
-// Few rows (a token or a few per sequence; bound by reading the cache): a
-// workgroup takes 16 rows of one sequence and kv head; each of its waves takes
-// every n-th key tile on its own, with no barrier until the waves' results
-// are joined through LDS. Where that alone would leave the GPU unevenly
+// Few rows (a token or some per sequence; bound by reading the cache): a
+// workgroup takes 16 or 32 rows of one sequence and kv head; each of its waves
+// takes every n-th key tile on its own, with no barrier until the waves'
+// results are joined through LDS. Where that alone would leave the GPU unevenly
 // loaded, the key tiles of the whole batch are cut into equal runs, one for
 // each workgroup that fits on the GPU at once; partial results (fp32 sum,
 // maximum, denominator) of rows whose keys lie in several runs go to the
@@ -919,6 +919,16 @@ __device__ __forceinline__ void attend_few(const KvAttnArgs& a, const RowTile& r
 constexpr int few_waves(int dp, int rt) { return dp == 256 ? 1 : dp == 128 && rt > 1 ? 2 : 3; }
 
 // One workgroup for each row tile and kv head.
+//
+// A tile of 32 keys of 128 elements in MXFP4 costs a wave about 190 vector
+// instructions, 64 of them conversions (3.7 ns each, others 2 to 2.4), and 16
+// matrix instructions: 0.57 us with two waves a SIMD. So little work is bound
+// by the launch, the chain of first loads (lengths, page, tile: 6 us with one
+// key) and the tiles one wave goes through: one sequence of 997 keys, 4 tiles
+// a wave, 10 us. 32 sequences to 4096 keys (98 MB, 32 heads over 8 of 128):
+// 27 us, 4.6 TB/s after the first 6 us, where a copy of that size reaches 4.8.
+// Sixteen waves a workgroup: 31 us; a ring of three or four tiles a wave, or
+// all of a tile's LDS reads ahead of its first use: no faster.
 template <int DP, bool NV, bool BF16, bool FULL, int NW, int RT>
 __global__ __launch_bounds__(64 * NW, few_waves(DP, RT)) void kv_attn_kernel(KvAttnArgs a) {
   __shared__ __attribute__((aligned(16))) FewSpace<DP, NV, NW> lds;
@@ -928,7 +938,9 @@ __global__ __launch_bounds__(64 * NW, few_waves(DP, RT)) void kv_attn_kernel(KvA
   attend_few<DP, NV, BF16, FULL, NW, RT>(a, r, h, r.lo, r.hi, nullptr, lds);
 }
 
-// The balanced form: one workgroup for each run of key tiles.
+// The balanced form: one workgroup for each run of key tiles, two a CU. 64
+// sequences to 16384 keys (699 MB, 64 heads over 8 of 128): 135 us, 5.2 TB/s,
+// and 6 to join; reads of 4 to 8 KB from anywhere reach 5.7 to 5.9 here.
 template <int DP, bool NV, bool BF16, bool FULL, int NW, int RT>
 __global__ __launch_bounds__(64 * NW, few_waves(DP, RT)) void kv_attn_runs_kernel(KvAttnArgs a, int least) {
   constexpr int kRows = 16 * RT;
@@ -971,6 +983,16 @@ __global__ __launch_bounds__(64 * NW, few_waves(DP, RT)) void kv_attn_runs_kerne
 }
 
 // Many rows: NW waves with RT tiles of 16 rows each.
+//
+// Bound by the vector unit, beside which the matrix instructions of other waves
+// run: a weight costs an fma, an exponential (9.9 ns a wave's 64) and its parts
+// of a maximum, a sum and a conversion, and each tile's conversion comes on top,
+// which is why waves share it through LDS (each on its own: 737 us with two row
+// tiles, this form: 620, for a prompt of 8192 of 32 heads over 8 of 128). That is
+// 885 TFLOP/s of the pairs seen; a large library product of bf16 runs at 1140.
+// The next scores beside this tile's softmax within a wave: 695 us. 4 x 1024
+// queries over 6000 keys (8 heads a kv head): 312 us, 654 TFLOP/s, as their
+// equal workgroups fill the GPU one and a third times.
 template <int DP, bool NV>
 struct ManySpace {
   static constexpr int kRing = 4;  // raw tiles: one being converted, two on their way, one being started
@@ -1125,7 +1147,8 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 64 ? 4 : RT == 2 ? 3 : 2
 
 // Joins COLS columns of the partial results of one row of one item, if it has
 // any: COLS / 4 lanes take four elements each, and the rest of the workgroup
-// every kGroups-th partial result.
+// every kGroups-th partial result. Bound by latency: 6 to 7 us, 4 of them what
+// any second launch takes.
 template <int DP, bool NV, bool BF16, int RT, int THREADS, int COLS>
 __global__ __launch_bounds__(THREADS) void kv_attn_join_kernel(KvAttnArgs a, int runs, int least, int rows_each) {
   constexpr int kRows = 16 * RT;
@@ -1244,7 +1267,9 @@ KvAttnPlan plan_kv_attention(const KvAttnArgs& a) {
   // but 16 over 8192: 23 against 21).
   auto tiles = [&](int64_t per) { return a.batch * ((rows / a.batch + per - 1) / per) * a.c.heads; };
   p.few_tiles = 1;
-  if (rows > 16 * a.batch && (tiles(32) >= 4 * cus || (tiles(16) <= 2 * cus && (tiles(16) > cus || (each > 24 && tiles(16) >= cus / 4)))))
+  if (rows > 16 * a.batch &&
+      (tiles(32) >= 4 * cus ||
+       (tiles(16) <= 2 * cus && (tiles(16) > cus || (each > 24 && tiles(16) >= cus / 4)))))
     p.few_tiles = few_tiles(a.c.dim, a.bf16);
   const int per = 16 * p.few_tiles;
   p.tiles = a.offs ? rows / per + a.batch : a.batch * ((a.group + per - 1) / per);
@@ -1253,7 +1278,8 @@ KvAttnPlan plan_kv_attention(const KvAttnArgs& a) {
   // Little work, or at most a few tiles more for some workgroups than for
   // others: one launch whose workgroups have many waves, rather than runs and
   // a second launch to join them (24 sequences of 5 queries over 3000 keys:
-  // 20 against 28 us; 32 to 4096 keys: 27 against 32).
+  // 20 against 28 us; 32 to 4096 keys: 27 against 32). Where most CUs would
+  // have no workgroup, only up to 8 tiles a wave.
   if (items <= 4 * cus && each <= (2 * items >= cus ? 24 : 8)) {
     p.waves = wide;
     return p;
