@@ -15,7 +15,7 @@
 // workspace and are joined by a second kernel.
 //
 // Many rows (prompts; bound by arithmetic): a workgroup's four waves have rows
-// of their own, 32 or 48 each, and go through the key tiles together. Each
+// of their own, 32 each, and go through the key tiles together. Each
 // wave converts a quarter of the next tile and leaves it in LDS as the matrix
 // instructions' operands, while all of them use the present one.
 //
@@ -982,17 +982,12 @@ __global__ __launch_bounds__(64 * NW, few_waves(DP, RT)) void kv_attn_runs_kerne
   }
 }
 
-// Many rows: NW waves with RT tiles of 16 rows each.
-//
-// Bound by the vector unit, beside which the matrix instructions of other waves
-// run: a weight costs an fma, an exponential (9.9 ns a wave's 64) and its parts
-// of a maximum, a sum and a conversion, and each tile's conversion comes on top,
-// which is why waves share it through LDS (each on its own: 737 us with two row
-// tiles, this form: 620, for a prompt of 8192 of 32 heads over 8 of 128). That is
-// 885 TFLOP/s of the pairs seen; a large library product of bf16 runs at 1140.
-// The next scores beside this tile's softmax within a wave: 695 us. 4 x 1024
-// queries over 6000 keys (8 heads a kv head): 312 us, 654 TFLOP/s, as their
-// equal workgroups fill the GPU one and a third times.
+// 16-row tiles of a wave in the form for many rows. Three leave registers for
+// two waves a SIMD instead of three: 644 against 612 us (the prompt of 8192
+// below), and at heads of 64 327 against 314; past 128 three do not fit, and one
+// is a third slower (1226 against 820 us, 4096 queries over 8192).
+constexpr int kManyTiles = 2;
+
 template <int DP, bool NV>
 struct ManySpace {
   static constexpr int kRing = 4;  // raw tiles: one being converted, two on their way, one being started
@@ -1002,11 +997,23 @@ struct ManySpace {
   u32x4 v[2][kVParts][64];
 };
 
-template <int DP, bool NV, bool FULL, int RT>
-__global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 64 ? 4 : RT == 2 ? 3 : 2) void kv_attn_many_kernel(KvAttnArgs a) {
+// Many rows: NW waves with RT tiles of 16 rows each.
+//
+// Bound by the vector unit, beside which the matrix instructions of other waves
+// run: a weight costs an fma, an exponential (9.9 ns a wave's 64) and its parts
+// of a maximum, a sum and a conversion, and each tile's conversion comes on top,
+// which is why waves share it through LDS (each on its own: 737 us with two row
+// tiles, this form: 612, for a prompt of 8192 of 32 heads over 8 of 128). That is
+// 900 TFLOP/s of the pairs seen; a large library product of bf16 runs at 1140.
+// The next scores beside this tile's softmax within a wave: 695 us. Conversion
+// and the product with V go before other waves' work: without, 622 us, and
+// 4 x 1024 queries over 6000 keys (8 heads a kv head) 312 instead of 286.
+// Those are 713 TFLOP/s: their equal workgroups fill the GPU one and a third times.
+template <int DP, bool NV, bool FULL>
+__global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 64 ? 4 : 3) void kv_attn_many_kernel(KvAttnArgs a) {
   using T = Tile<DP, NV>;
   using Space = ManySpace<DP, NV>;
-  constexpr int NW = 4;
+  constexpr int NW = 4, RT = kManyTiles;
   constexpr int kRows = 16 * RT * NW;
   __shared__ __attribute__((aligned(16))) Space lds;
   // The last rows have the most keys under a causal order: they begin first.
@@ -1099,7 +1106,9 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 64 ? 4 : RT == 2 ? 3 : 2
     // the tile after the next two begins its way, the next one is converted
     in.copy(min(kt + 3 * kTileKeys, last), ahead, raw + slot_of(n + 3), lane, mine);
     ahead = in.pages(min(kt + 4 * kTileKeys, last));
+    __builtin_amdgcn_s_setprio(1);
     convert(min(kt + kTileKeys, last), &lds.raw[0][0] + slot_of(n + 1), (n + 1) & 1);
+    __builtin_amdgcn_s_setprio(0);
     if (!idle && kt < r.hi && kt + kTileKeys > r.lo) {
       float s[RT][8];
 #pragma unroll
@@ -1117,8 +1126,10 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 64 ? 4 : RT == 2 ? 3 : 2
       }
       u32x4 pw[RT][1];
       rows.weigh(a, kt, g, s, pw);
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int j = 0; j < T::kChunkV; j++) rows.times_v(lds.v[n & 1][j][lane], j, pw);
+      __builtin_amdgcn_s_setprio(0);
     }
     // the tile after next and what the waves wrote is there for all
     wait_copies<kLoads>();
@@ -1223,13 +1234,6 @@ constexpr int kWaves = 4;
 constexpr int wide_waves(int dp) { return dp <= 128 ? 8 : kWaves; }
 // Most 16-row tiles of a wave in the form for few rows.
 constexpr int few_tiles(int dp, bool bf16) { return bf16 && dp <= 128 ? 2 : 1; }
-// Most 16-row tiles of a wave in the form for many rows. Three rather than
-// two share a tile's conversion among more rows but leave registers for two
-// waves a SIMD instead of three: even at heads of 128 (a prompt of 8192:
-// 646 against 660 us), slower at 64 (three or four against two: 327 against
-// 314 us); past 128 three do not fit, and one is a third slower (1226 against
-// 820 us, 4096 queries over 8192).
-constexpr int most_tiles(int dp) { return dp > 64 && dp <= 128 ? 3 : 2; }
 }  // namespace
 
 KvAttnPlan plan_kv_attention(const KvAttnArgs& a) {
@@ -1237,17 +1241,15 @@ KvAttnPlan plan_kv_attention(const KvAttnArgs& a) {
   const int64_t rows = a.tokens * a.group;
   const int64_t cus = device_cu_count();
   // Many rows a sequence, and enough of them to fill the GPU (two workgroups a
-  // CU, heads past 128 one) with two row tiles a wave or more: the form for many.
+  // CU, heads past 128 one): the form for many.
   // Fewer rows: each key tile's conversion and barrier serve too few (8 x 448
   // queries of 20 heads of 64 over 1500 keys: 58 us in that form, 43 in the other).
-  if (a.bf16 && a.offs && rows >= 128 * a.batch) {
-    const int64_t fill = a.c.dim <= 128 ? 2 * cus : cus;
-    for (int n = most_tiles(a.c.dim); n >= 2; n--) {
-      if ((rows / (16 * kWaves * n) + a.batch / 2) * a.c.heads < fill) continue;
-      p.row_tiles = n;
-      p.tiles = rows / (16 * kWaves * n) + a.batch;
-      return p;
-    }
+  constexpr int kManyRows = 16 * kWaves * kManyTiles;
+  const int64_t fill = a.c.dim <= 128 ? 2 * cus : cus;
+  if (a.bf16 && a.offs && rows >= 128 * a.batch && (rows / kManyRows + a.batch / 2) * a.c.heads >= fill) {
+    p.many = true;
+    p.tiles = rows / kManyRows + a.batch;
+    return p;
   }
   // Few. Keys a tile can see at most: all, or the windows of its queries.
   int64_t keys = a.max_len;
@@ -1295,18 +1297,6 @@ KvAttnPlan plan_kv_attention(const KvAttnArgs& a) {
   return p;
 }
 
-template <int DP, bool NV, bool FULL>
-static void launch_many(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t s) {
-  const dim3 grid((unsigned)(p.tiles * a.c.heads));
-  if constexpr (most_tiles(DP) > 2) {
-    if (p.row_tiles == 2) {
-      hipLaunchKernelGGL((kv_attn_many_kernel<DP, NV, FULL, 2>), grid, dim3(256), 0, s, a);
-      return;
-    }
-  }
-  hipLaunchKernelGGL((kv_attn_many_kernel<DP, NV, FULL, most_tiles(DP)>), grid, dim3(256), 0, s, a);
-}
-
 template <int DP, bool NV, bool BF16, bool FULL, int RT>
 static void launch_few(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t s) {
   constexpr int kWide = wide_waves(DP);
@@ -1335,8 +1325,10 @@ static void launch_few(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t s) 
 
 template <int DP, bool NV, bool BF16, bool FULL>
 static hipError_t launch_rows(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t s) {
-  if (p.row_tiles > 0) {
-    if constexpr (BF16) launch_many<DP, NV, FULL>(a, p, s);
+  if (p.many) {
+    if constexpr (BF16)
+      hipLaunchKernelGGL((kv_attn_many_kernel<DP, NV, FULL>), dim3((unsigned)(p.tiles * a.c.heads)),
+                         dim3(64 * kWaves), 0, s, a);
   } else if (p.few_tiles == 1) {
     launch_few<DP, NV, BF16, FULL, 1>(a, p, s);
   } else {

@@ -160,7 +160,7 @@ struct KvAttnArgs {
 
 // How a call's work is cut.
 struct KvAttnPlan {
-  int row_tiles;  // > 0: the form for many rows, this many 16-row tiles a wave; 0: the form for few
+  bool many;      // the form for many rows
   int few_tiles;  // few rows: 16-row tiles a wave
   int waves;      // few rows: of a workgroup
   int64_t tiles;  // row tiles of the batch per kv head, an upper bound

@@ -281,9 +281,9 @@ def prompt_f64(q, k, v, table, page, lens, q_lens, causal, window, softcap, scal
 
 LARGE = [
     # (heads, kv_heads, dim, page, lens, q_lens, causal, window, softcap)
-    (16, 16, 128, 64, [900, 1500, 70], [900, 700, 70], True, 0, 0.0),       # three row tiles a wave
-    (12, 12, 128, 16, [1100, 640], [500, 640], True, 0, 0.0),               # two row tiles
-    (40, 20, 64, 16, [1000, 750, 0, 33], [1000, 500, 5, 33], True, 0, 0.0), # two, short head
+    (16, 16, 128, 64, [900, 1500, 70], [900, 700, 70], True, 0, 0.0),
+    (12, 12, 128, 16, [1100, 640], [500, 640], True, 0, 0.0),
+    (40, 20, 64, 16, [1000, 750, 0, 33], [1000, 500, 5, 33], True, 0, 0.0),
     (20, 20, 64, 32, [640, 400], [600, 400], True, 90, 20.0),
     (16, 8, 96, 32, [777, 1300], [777, 1031], True, 0, 0.0),
     (32, 4, 128, 128, [700, 900], [500, 800], False, 0, 0.0),
@@ -295,7 +295,7 @@ LARGE = [
 @pytest.mark.parametrize("fmt", BOTH)
 @pytest.mark.parametrize("case", LARGE, ids=[f"{c[0]}x{c[2]}-{len(c[4])}" for c in LARGE])
 def test_prompts_of_many_rows(fp4, oracle, fmt, case):
-    """Prompts large enough for every count of row tiles a wave takes."""
+    """Prompts large enough for the form for many rows, at every size of head."""
     heads, kv_heads, dim, page, lens, q_lens, causal, window, softcap = case
     print(f"[large] {fmt} {case}", flush=True)
     attention_case(fp4, oracle, fmt, BF, lens, q_lens, heads, kv_heads, dim, page, causal=causal, window=window,
