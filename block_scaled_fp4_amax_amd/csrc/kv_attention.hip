@@ -666,8 +666,10 @@ struct Rows {
     }
   }
 
-  // The products s[rt][4 sub + i] (key kt + 16 sub + 4 i + g) to weights in
-  // 16 bits, in the order of V's operand; the statistics and sums follow.
+  // The products s[rt][i] (key kt + 4 i + g, or TURNED: its pairs of keys begun g
+  // pairs earlier, round the four) to weights in 16 bits, in the order of V's
+  // operand; the statistics and sums follow.
+  template <bool TURNED>
   __device__ __forceinline__ void weigh(const KvAttnArgs& a, int kt, int g, float s[RT][8], u32x4 pw[RT][kPTerms]) {
     float factor[RT];  // of s, to scores in powers of two
 #pragma unroll
@@ -684,7 +686,7 @@ struct Rows {
     if (kt + kTileKeys > all_hi || kt < all_lo) {
 #pragma unroll
       for (int i = 0; i < 8; i++) {
-        const int key = kt + 16 * (i >> 2) + 4 * (i & 3) + g;
+        const int key = kt + 8 * (TURNED ? ((i >> 1) - g) & 3 : i >> 1) + 4 * (i & 1) + g;
 #pragma unroll
         for (int rt = 0; rt < RT; rt++)
           s[rt][i] = key < my_hi[rt] && key >= my_lo[rt] ? s[rt][i] * factor[rt] : -__builtin_huge_valf();
@@ -844,7 +846,7 @@ __device__ __forceinline__ void attend_few(const KvAttnArgs& a, const RowTile& r
       }
     }
     u32x4 pw[RT][Rows<DP, NV, BF16, FULL, RT>::kPTerms];
-    rows.weigh(a, kt, g, s, pw);
+    rows.template weigh<false>(a, kt, g, s, pw);
 #pragma unroll
     for (int w = 0; w < T::kVWords; w++) {
       uint32_t vt[4][2 * T::kPairs];
@@ -1036,12 +1038,20 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 64 ? 4 : 3) void kv_attn
 
   // This wave's quarter of a tile's conversion: K words wave, wave + 4, .. of
   // both halves (heads of 64: word wave % 2 of half wave / 2), and the key
-  // pair `wave` of V, a fourth of each of its operands.
+  // pair `wave` of V, a fourth of each of its operands. That fourth lies g
+  // further on, round the four: always the same one would meet 16 of the 64
+  // banks only. K's rows lie in the order that this gives the weights.
+  uint32_t k_to[2];
+#pragma unroll
+  for (int sub = 0; sub < 2; sub++) {
+    const int pair = (2 * sub + (c >> 1 & 1) + (c >> 2)) & 3;
+    k_to[sub] = (pair >> 1) * T::kKWords * 64 + 16 * g + (c & 12) + 2 * (pair & 1) + (c & 1);
+  }
   auto convert = [&](int kt, const uint8_t* y, int to) {
     if constexpr (T::kKWords == 2) {
       const int sub = wave >> 1, w = wave & 1;
       const uint32_t code = *reinterpret_cast<const uint32_t*>(y + sub * T::kHalf + in.k_word(c, g, w));
-      lds.k[to][wave][lane] = convert8<NV>(code, y[in.k_scale(c, g, 0) + sub * 16 * in.row_scales]);
+      (&lds.k[to][w][0])[k_to[sub]] = convert8<NV>(code, y[in.k_scale(c, g, 0) + sub * 16 * in.row_scales]);
     } else {
 #pragma unroll
       for (int sub = 0; sub < 2; sub++) {
@@ -1050,7 +1060,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 64 ? 4 : 3) void kv_attn
           const int w = wave + 4 * i;
           const uint32_t code = *reinterpret_cast<const uint32_t*>(y + sub * T::kHalf + in.k_word(c, g, w));
           const uint32_t scale = y[in.k_scale(c, g, T::k_scale(w)) + sub * 16 * in.row_scales];
-          lds.k[to][sub * T::kKWords + w][lane] = convert8<NV>(code, scale);
+          (&lds.k[to][w][0])[k_to[sub]] = convert8<NV>(code, scale);
         }
       }
     }
@@ -1072,7 +1082,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 64 ? 4 : 3) void kv_attn
       convert_key_pair<NV, T::kPairs>(x0, x1, s0, s1, vt);
 #pragma unroll
       for (int j = 0; j < 2 * T::kPairs; j++)
-        reinterpret_cast<uint32_t*>(&lds.v[to][8 * w + j][lane])[wave] = vt[j];
+        reinterpret_cast<uint32_t*>(&lds.v[to][8 * w + j][lane])[(wave + g) & 3] = vt[j];
     }
   };
   auto slot_of = [](int n) { return n % Space::kRing * T::kSlot; };
@@ -1125,7 +1135,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 64 ? 4 : 3) void kv_attn
         }
       }
       u32x4 pw[RT][1];
-      rows.weigh(a, kt, g, s, pw);
+      rows.template weigh<true>(a, kt, g, s, pw);
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int j = 0; j < T::kChunkV; j++) rows.times_v(lds.v[n & 1][j][lane], j, pw);
