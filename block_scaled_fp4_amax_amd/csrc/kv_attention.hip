@@ -1049,7 +1049,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 64 ? 4 : 3) void kv_attn
   }
   auto convert = [&](int kt, const uint8_t* y, int to) {
     if constexpr (T::kKWords == 2) {
-      const int sub = wave >> 1, w = wave & 1;
+      const int sub = wave >> 1, w = (wave + (g >> 1)) & 1;
       const uint32_t code = *reinterpret_cast<const uint32_t*>(y + sub * T::kHalf + in.k_word(c, g, w));
       (&lds.k[to][w][0])[k_to[sub]] = convert8<NV>(code, y[in.k_scale(c, g, 0) + sub * 16 * in.row_scales]);
     } else {
@@ -1057,7 +1057,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 64 ? 4 : 3) void kv_attn
       for (int sub = 0; sub < 2; sub++) {
 #pragma unroll
         for (int i = 0; i < T::kKWords / 4; i++) {
-          const int w = wave + 4 * i;
+          const int w = ((wave + g) & 3) + 4 * i;
           const uint32_t code = *reinterpret_cast<const uint32_t*>(y + sub * T::kHalf + in.k_word(c, g, w));
           const uint32_t scale = y[in.k_scale(c, g, T::k_scale(w)) + sub * 16 * in.row_scales];
           (&lds.k[to][w][0])[k_to[sub]] = convert8<NV>(code, scale);
