@@ -985,7 +985,7 @@ __global__ __launch_bounds__(64 * NW, few_waves(DP, RT)) void kv_attn_runs_kerne
 }
 
 // 16-row tiles of a wave in the form for many rows. Three leave registers for
-// two waves a SIMD instead of three: 644 against 612 us (the prompt of 8192
+// two waves a SIMD instead of three: 590 against 559 us (the prompt of 8192
 // below), and at heads of 64 327 against 314; past 128 three do not fit, and one
 // is a third slower (1226 against 820 us, 4096 queries over 8192).
 constexpr int kManyTiles = 2;
@@ -1005,12 +1005,14 @@ struct ManySpace {
 // run: a weight costs an fma, an exponential (9.9 ns a wave's 64) and its parts
 // of a maximum, a sum and a conversion, and each tile's conversion comes on top,
 // which is why waves share it through LDS (each on its own: 737 us with two row
-// tiles, this form: 612, for a prompt of 8192 of 32 heads over 8 of 128). That is
-// 900 TFLOP/s of the pairs seen; a large library product of bf16 runs at 1140.
-// The next scores beside this tile's softmax within a wave: 695 us. Conversion
-// and the product with V go before other waves' work: without, 622 us, and
-// 4 x 1024 queries over 6000 keys (8 heads a kv head) 312 instead of 286.
-// Those are 713 TFLOP/s: their equal workgroups fill the GPU one and a third times.
+// tiles, then 620 in this form, for a prompt of 8192 of 32 heads over 8 of 128).
+// LDS comes next: four waves read 64 KB of operands a tile. With every access on
+// all of its banks 563 us, 976 TFLOP/s of the pairs seen; a large library product
+// of bf16 runs at 1140. The next scores beside this tile's softmax within a wave
+// were slower (620 to 695 us). Conversion and the product with V go before other waves'
+// work: 4 x 1024 queries over 6000 keys (8 heads a kv head) took 312 us without
+// and 286 with that, 266 now, 766 TFLOP/s: equal workgroups that fill the GPU
+// one and a third times.
 template <int DP, bool NV, bool FULL>
 __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 64 ? 4 : 3) void kv_attn_many_kernel(KvAttnArgs a) {
   using T = Tile<DP, NV>;
@@ -1036,11 +1038,12 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 64 ? 4 : 3) void kv_attn
   constexpr int kLoads = 2 * T::kCopies / NW + 1;  // per wave and tile, at least
   const uint32_t raw = lds_address(&lds.raw[0][0]);
 
-  // This wave's quarter of a tile's conversion: K words wave, wave + 4, .. of
-  // both halves (heads of 64: word wave % 2 of half wave / 2), and the key
-  // pair `wave` of V, a fourth of each of its operands. That fourth lies g
-  // further on, round the four: always the same one would meet 16 of the 64
-  // banks only. K's rows lie in the order that this gives the weights.
+  // This wave's quarter of a tile's conversion: a fourth of the K words of both
+  // halves (heads of 64: one of the two words of half wave / 2), and the key
+  // pair `wave` of V, a fourth of each of its operands. Which word, and which
+  // fourth, moves on with g: lanes lie 16 bytes apart, and one and the same word
+  // of each would meet 16 of the 64 banks only (prompt of 8192: 612 against 563
+  // us). K's rows lie in the order that this gives the weights.
   uint32_t k_to[2];
 #pragma unroll
   for (int sub = 0; sub < 2; sub++) {
@@ -1250,12 +1253,18 @@ KvAttnPlan plan_kv_attention(const KvAttnArgs& a) {
   KvAttnPlan p{};
   const int64_t rows = a.tokens * a.group;
   const int64_t cus = device_cu_count();
-  // Many rows a sequence, and enough of them to fill the GPU (two workgroups a
-  // CU, heads past 128 one): the form for many.
-  // Fewer rows: each key tile's conversion and barrier serve too few (8 x 448
-  // queries of 20 heads of 64 over 1500 keys: 58 us in that form, 43 in the other).
+  // Many rows a sequence, and enough of them for two workgroups a CU (heads of
+  // up to 64 and more than a few tiles of keys: three): the form for many. Fewer
+  // rows: each key tile's conversion and barrier serve too few (8 x 448 queries
+  // of 20 heads of 64 over 1500 keys: 58 us in that form, 43 in the other); fewer
+  // workgroups: the longest of them, whose keys nobody shares, set the time.
+  // That form against the other, 32 heads over 8, at 512 workgroups and more:
+  // heads of 128, prompts of 2 x 1024 58 against 63 us, 8 x 256 27 against 44, 2 x 2048
+  // 118 against 159 (2048 alone: 92 against 86); heads of 64, 8 x 256 18 against 27, but 2048
+  // 67 against 54; heads of 256, 2048 164 against 182. Below that: heads of 128, 1024
+  // queries over 6000 225 against 145; heads of 256, 1536 over 8192 894 against 628.
   constexpr int kManyRows = 16 * kWaves * kManyTiles;
-  const int64_t fill = a.c.dim <= 128 ? 2 * cus : cus;
+  const int64_t fill = (a.c.dim <= 64 && a.max_len > 512 ? 3 : 2) * cus;
   if (a.bf16 && a.offs && rows >= 128 * a.batch && (rows / kManyRows + a.batch / 2) * a.c.heads >= fill) {
     p.many = true;
     p.tiles = rows / kManyRows + a.batch;

@@ -295,11 +295,33 @@ LARGE = [
 @pytest.mark.parametrize("fmt", BOTH)
 @pytest.mark.parametrize("case", LARGE, ids=[f"{c[0]}x{c[2]}-{len(c[4])}" for c in LARGE])
 def test_prompts_of_many_rows(fp4, oracle, fmt, case):
-    """Prompts large enough for the form for many rows, at every size of head."""
+    """Prompts of some hundred rows a sequence, at every size of head."""
     heads, kv_heads, dim, page, lens, q_lens, causal, window, softcap = case
     print(f"[large] {fmt} {case}", flush=True)
     attention_case(fp4, oracle, fmt, BF, lens, q_lens, heads, kv_heads, dim, page, causal=causal, window=window,
                    softcap=softcap, seed=30, ref_of=prompt_f64)
+
+
+FILLING = [
+    # rows and heads enough for the form for many rows: two workgroups of 128 rows a CU (heads of 64, long keys: three)
+    (64, 64, 128, 64, [300, 760], [300, 720], True, 0, 0.0),
+    (96, 16, 128, 32, [700, 90], [650, 90], True, 0, 0.0),
+    (64, 32, 96, 16, [500, 640, 0, 40], [480, 640, 3, 45], True, 90, 20.0),
+    (128, 64, 64, 32, [500, 300, 33], [470, 300, 33], True, 0, 0.0),
+    (128, 64, 64, 16, [560, 420], [560, 420], False, 0, 0.0),
+    (128, 64, 32, 16, [400, 260], [400, 260], True, 0, 0.0),
+    (64, 64, 256, 32, [300, 760], [300, 740], True, 0, 0.0),
+    (64, 64, 192, 64, [300, 760], [280, 740], True, 333, 0.0),
+]
+
+
+@pytest.mark.parametrize("fmt", BOTH)
+@pytest.mark.parametrize("case", FILLING, ids=[f"{c[0]}x{c[2]}-{c[4][0]}" for c in FILLING])
+def test_prompts_that_fill_the_gpu(fp4, oracle, fmt, case):
+    heads, kv_heads, dim, page, lens, q_lens, causal, window, softcap = case
+    print(f"[filling] {fmt} {case}", flush=True)
+    attention_case(fp4, oracle, fmt, BF, lens, q_lens, heads, kv_heads, dim, page, causal=causal, window=window,
+                   softcap=softcap, seed=32, ref_of=prompt_f64)
 
 
 MIDDLE = [
