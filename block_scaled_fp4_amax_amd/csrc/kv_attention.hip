@@ -1001,13 +1001,13 @@ struct ManySpace {
 
 // Many rows: NW waves with RT tiles of 16 rows each.
 //
-// Bound by the vector unit, beside which the matrix instructions of other waves
-// run: a weight costs an fma, an exponential (9.9 ns a wave's 64) and its parts
+// Bound by vector and matrix instructions together (57 and 41 % of the SIMDs'
+// cycles by the counters): a weight costs an fma, an exponential (9.9 ns a wave's 64) and its parts
 // of a maximum, a sum and a conversion, and each tile's conversion comes on top,
 // which is why waves share it through LDS (each on its own: 737 us with two row
 // tiles, then 620 in this form, for a prompt of 8192 of 32 heads over 8 of 128).
-// LDS comes next: four waves read 64 KB of operands a tile. With every access on
-// all of its banks 563 us, 976 TFLOP/s of the pairs seen; a large library product
+// LDS comes next (42 %): four waves read 64 KB of operands a tile. With every
+// conversion's access on all of its banks 561 us, 980 TFLOP/s of the pairs seen; a large library product
 // of bf16 runs at 1140. The next scores beside this tile's softmax within a wave
 // were slower (620 to 695 us). Conversion and the product with V go before other waves'
 // work: 4 x 1024 queries over 6000 keys (8 heads a kv head) took 312 us without
