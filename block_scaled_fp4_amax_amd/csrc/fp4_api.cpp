@@ -3,6 +3,7 @@
 // and dispatch to the kernels.
 #include "fp4.h"
 
+#include <float.h>
 #include <hip/hip_runtime.h>
 
 #include <atomic>
@@ -733,7 +734,14 @@ fp4_status fp4_kv_attention(const fp4_kv_cache* cache, const fp4_kv_attention_ar
   a.o_ts_ = args->out_token_stride;
   a.o_hs = args->out_head_stride;
   a.scale = args->scale;
-  a.softcap = args->softcap;
+  if (args->softcap > 0.0f) {
+    // scores are held in powers of two; both numbers stay finite (the largest
+    // caps differ from FLT_MAX only where scores pass 1e37, the smallest make
+    // every score 0)
+    const double cap = args->softcap * 1.4426950408889634;
+    a.cap = (float)(cap < FLT_MAX ? cap : FLT_MAX);
+    a.inv_cap = (float)(1.0 / cap < FLT_MAX ? 1.0 / cap : FLT_MAX);
+  }
   a.ws = static_cast<float*>(workspace);
   (void)hipGetLastError();
   return launch_kv_attention(a, p, static_cast<hipStream_t>(stream)) == hipSuccess ? FP4_OK : FP4_ERR_HIP;

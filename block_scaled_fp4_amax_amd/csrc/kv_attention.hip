@@ -343,9 +343,25 @@ __device__ __forceinline__ void convert_key_pair(uint32_t x, uint32_t y, uint32_
   }
 }
 
-// tanh by one exponential; 1 and -1 where it over- and underflows.
-__device__ __forceinline__ float tanh_exp(float x) {
-  return 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * (2.0f * kLog2e)));
+// cap tanh(s / cap), with 1 / cap given. Below |x| = 0.6 (SMALL: known to be
+// below) the score times tanh(x) / x = 1 + x^2 P(x^2), P of least relative
+// error there (2^-28, found by reweighted least squares): small scores under a
+// large cap keep all their bits, where 1 - 2 / (1 + e^2x) would be off by 2^-24
+// of the cap. Above, that form, 1 where the exponential overflows.
+constexpr float kSmallTanh = 0.6f;
+template <bool SMALL>
+__device__ __forceinline__ float soft_cap(float s, float cap, float inv_cap) {
+  const float x = s * inv_cap, u = x * x;
+  float p = -0.00589515548f;
+  p = __builtin_fmaf(p, u, 0.0207959693f);
+  p = __builtin_fmaf(p, u, -0.0537838303f);
+  p = __builtin_fmaf(p, u, 0.133319244f);
+  p = __builtin_fmaf(p, u, -0.333332986f);
+  const float small = __builtin_fmaf(s * u, p, s);
+  if constexpr (SMALL) return small;
+  const float ax = __builtin_fabsf(x);
+  const float t = 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(ax * (2.0f * kLog2e)));
+  return ax < kSmallTanh ? small : __builtin_copysignf(cap * t, s);
 }
 
 __device__ __forceinline__ float tensor_scale_of(const float* ts, int h) {
@@ -662,25 +678,43 @@ struct Rows {
           for (int i = 0; i < 4; i++) q[rt][k][w][i] = split16bit<NV>(x[8 * w + 2 * i], x[8 * w + 2 * i + 1]);
         }
       }
-      score_scale[rt] = a.softcap > 0.0f ? f / a.softcap : f * kLog2e;
+      score_scale[rt] = f * kLog2e;
     }
   }
 
   // The products s[rt][i] (key kt + 4 i + g, or TURNED: its pairs of keys begun g
   // pairs earlier, round the four) to weights in 16 bits, in the order of V's
   // operand; the statistics and sums follow.
-  template <bool TURNED>
+  template <bool TURNED, bool CAP>
   __device__ __forceinline__ void weigh(const KvAttnArgs& a, int kt, int g, float s[RT][8], u32x4 pw[RT][kPTerms]) {
     float factor[RT];  // of s, to scores in powers of two
 #pragma unroll
     for (int rt = 0; rt < RT; rt++) factor[rt] = score_scale[rt];
-    if (a.softcap > 0.0f) {
-      const float cap2 = a.softcap * kLog2e;
+    if (CAP && a.cap > 0.0f) {
+      float top = 0.0f;
 #pragma unroll
       for (int rt = 0; rt < RT; rt++) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) s[rt][i] = cap2 * tanh_exp(s[rt][i] * score_scale[rt]);
+        for (int i = 0; i < 8; i++) {
+          s[rt][i] *= score_scale[rt];
+          top = __builtin_fmaxf(top, __builtin_fabsf(s[rt][i]));
+        }
         factor[rt] = 1.0f;
+      }
+      // mostly all small (prompt of 4096 under a cap of 30: 221 us; both forms
+      // for every score: 250)
+      if (__any(top * a.inv_cap >= kSmallTanh)) {
+#pragma unroll
+        for (int rt = 0; rt < RT; rt++) {
+#pragma unroll
+          for (int i = 0; i < 8; i++) s[rt][i] = soft_cap<false>(s[rt][i], a.cap, a.inv_cap);
+        }
+      } else {
+#pragma unroll
+        for (int rt = 0; rt < RT; rt++) {
+#pragma unroll
+          for (int i = 0; i < 8; i++) s[rt][i] = soft_cap<true>(s[rt][i], a.cap, a.inv_cap);
+        }
       }
     }
     if (kt + kTileKeys > all_hi || kt < all_lo) {
@@ -846,7 +880,7 @@ __device__ __forceinline__ void attend_few(const KvAttnArgs& a, const RowTile& r
       }
     }
     u32x4 pw[RT][Rows<DP, NV, BF16, FULL, RT>::kPTerms];
-    rows.template weigh<false>(a, kt, g, s, pw);
+    rows.template weigh<false, true>(a, kt, g, s, pw);
 #pragma unroll
     for (int w = 0; w < T::kVWords; w++) {
       uint32_t vt[4][2 * T::kPairs];
@@ -999,7 +1033,9 @@ struct ManySpace {
   u32x4 v[2][kVParts][64];
 };
 
-// Many rows: NW waves with RT tiles of 16 rows each.
+// Many rows: NW waves with RT tiles of 16 rows each. CAP: under a softcap. (Its
+// registers beside the loop's own, asked for in one kernel by a.cap: prompts of
+// 4096 without one, heads of 96 197 against 184 us, of 256 340 against 306.)
 //
 // Bound by vector and matrix instructions together (57 and 41 % of the SIMDs'
 // cycles by the counters): a weight costs an fma, an exponential (9.9 ns a wave's 64) and its parts
@@ -1013,7 +1049,7 @@ struct ManySpace {
 // work: 4 x 1024 queries over 6000 keys (8 heads a kv head) took 312 us without
 // and 286 with that, 266 now, 766 TFLOP/s: equal workgroups that fill the GPU
 // one and a third times.
-template <int DP, bool NV, bool FULL>
+template <int DP, bool NV, bool FULL, bool CAP>
 __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 64 ? 4 : 3) void kv_attn_many_kernel(KvAttnArgs a) {
   using T = Tile<DP, NV>;
   using Space = ManySpace<DP, NV>;
@@ -1138,7 +1174,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 64 ? 4 : 3) void kv_attn
         }
       }
       u32x4 pw[RT][1];
-      rows.template weigh<true>(a, kt, g, s, pw);
+      rows.template weigh<true, CAP>(a, kt, g, s, pw);
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int j = 0; j < T::kChunkV; j++) rows.times_v(lds.v[n & 1][j][lane], j, pw);
@@ -1345,9 +1381,11 @@ static void launch_few(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t s) 
 template <int DP, bool NV, bool BF16, bool FULL>
 static hipError_t launch_rows(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t s) {
   if (p.many) {
-    if constexpr (BF16)
-      hipLaunchKernelGGL((kv_attn_many_kernel<DP, NV, FULL>), dim3((unsigned)(p.tiles * a.c.heads)),
-                         dim3(64 * kWaves), 0, s, a);
+    if constexpr (BF16) {
+      const dim3 grid((unsigned)(p.tiles * a.c.heads)), block(64 * kWaves);
+      if (a.cap > 0.0f) hipLaunchKernelGGL((kv_attn_many_kernel<DP, NV, FULL, true>), grid, block, 0, s, a);
+      else hipLaunchKernelGGL((kv_attn_many_kernel<DP, NV, FULL, false>), grid, block, 0, s, a);
+    }
   } else if (p.few_tiles == 1) {
     launch_few<DP, NV, BF16, FULL, 1>(a, p, s);
   } else {

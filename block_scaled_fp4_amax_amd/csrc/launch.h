@@ -153,7 +153,8 @@ struct KvAttnArgs {
   void* out;
   float* lse;
   int64_t q_ts_, q_hs, o_ts_, o_hs;
-  float scale, softcap;
+  float scale;
+  float cap, inv_cap;  // the softcap in powers of two (0: off), and its inverse
   int64_t window;
   float* ws;
 };

@@ -1,0 +1,49 @@
+"""Attention over the 4-bit cache where its arithmetic is strained: softcaps of
+every size."""
+import numpy as np
+import pytest
+import torch
+
+from kv_util import attention_bounds, attention_f64, check_attention, lay_out, random_cache
+
+pytestmark = pytest.mark.gpu
+
+MX, NV = 0, 1
+BF, F32 = torch.bfloat16, torch.float32
+FD = [(f, d) for f in (MX, NV) for d in (BF, F32)]
+FD_IDS = ["mx-bf16", "mx-f32", "nv-bf16", "nv-f32"]
+
+
+def attend(F, cache, q, table, lens, q_lens, **kw):
+    """out, lse of one call over sequences of `lens` rows."""
+    offs = torch.tensor(np.cumsum([0] + list(q_lens)), dtype=torch.int32, device="cuda")
+    out, lse = F.kv_attention(q.cuda(), cache, torch.from_numpy(table).cuda(),
+                              torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                              q_offsets=None if all(n == 1 for n in q_lens) else offs, max_kv_len=max(lens),
+                              return_lse=True, **kw)
+    torch.cuda.synchronize()
+    return out, lse
+
+
+# ---------------------------------------------------------------------------
+# softcap
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("fmt,dtype", FD, ids=FD_IDS)
+@pytest.mark.parametrize("softcap", [1e-45, 1e-38, 1e-3, 0.5, 30.0, 1e3, 1e6, 1e9, 3e38])
+@pytest.mark.parametrize("q_scale", [0.05, 2.0])
+def test_softcap_of_any_size(fp4, oracle, fmt, dtype, softcap, q_scale):
+    """The capped score is as exact as the score itself, whatever the cap:
+    16 roundings more (products with the cap and its inverse, and tanh within
+    10 units of 2^-24 of its own size), as if 16 elements of a head more were
+    summed. A cap below the normal numbers leaves scores of 0."""
+    print(f"[softcap] {fmt} {dtype} {softcap} {q_scale}", flush=True)
+    lens, q_lens, heads, kv_heads, dim, page = [90, 33, 161], [1, 20, 7], 4, 2, 32, 16
+    cache, k, v = random_cache(fp4, oracle, fmt, 23, page, kv_heads, dim, 50)
+    table = lay_out(cache, lens, 51)
+    g = torch.Generator().manual_seed(52)
+    q = (q_scale * torch.randn(sum(q_lens), heads, dim, generator=g)).to(dtype)
+    out, lse = attend(fp4, cache, q, table, lens, q_lens, softcap=softcap)
+    cap = float(np.float32(softcap))
+    ref = attention_f64(q.double().numpy(), k, v, table, page, lens, q_lens, True, 0, cap, float(np.float32(dim ** -0.5)))
+    tol, tol_lse = attention_bounds(ref, fmt == NV, dtype == BF, dim + 16, max(lens), 0.0)
+    check_attention(out, lse, ref, tol, tol_lse, f"softcap {softcap}")
