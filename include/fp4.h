@@ -448,8 +448,9 @@ size_t fp4_kv_attention_workspace(const fp4_kv_cache* cache, const fp4_kv_attent
  * with k_j and v_j the values the cache stands for, products accumulated and
  * the softmax's statistics held in fp32. A query that sees no row gets
  * out = 0 and lse = -inf. bf16: the weights are rounded to 16 bits (bf16 for
- * MXFP4, fp16 for NVFP4) for the product with V, out is rounded once. fp32: queries and weights are split
- * into 16-bit terms, so that the result has fp32 accuracy.
+ * MXFP4, whose values leave fp16's range; fp16 for NVFP4) for the product with
+ * V, out is rounded once. fp32: queries and weights are split into three bf16
+ * terms, 24 bits together, so that the result has fp32 accuracy.
  *   kv_lens are cut to [0, max_kv_len], q_offsets clamped into [0, tokens],
  *   each end to at least its start, and page numbers into [0, num_pages), so
  *   no device value makes the kernel access memory outside the operands. Table

@@ -1,5 +1,5 @@
 """Attention over the 4-bit cache where its arithmetic is strained: softcaps of
-every size."""
+every size, weights far below the largest."""
 import numpy as np
 import pytest
 import torch
@@ -47,3 +47,47 @@ def test_softcap_of_any_size(fp4, oracle, fmt, dtype, softcap, q_scale):
     ref = attention_f64(q.double().numpy(), k, v, table, page, lens, q_lens, True, 0, cap, float(np.float32(dim ** -0.5)))
     tol, tol_lse = attention_bounds(ref, fmt == NV, dtype == BF, dim + 16, max(lens), 0.0)
     check_attention(out, lse, ref, tol, tol_lse, f"softcap {softcap}")
+
+
+# ---------------------------------------------------------------------------
+# weights far below the largest
+# ---------------------------------------------------------------------------
+def cache_of(F, O, fmt, x, page):
+    """A cache of one kv head whose rows are x = (k, v), each [rows, dim] fp32
+    (whole pages), quantized by the oracle; and their values."""
+    out, vals = [], []
+    for t in x:
+        r = O.quantize(np.ascontiguousarray(t, np.float32), fmt, amax=float(np.abs(t).max()) if fmt == NV else None)
+        vals.append(np.asarray(O.dequantize(fmt, r["codes"], r["scales"], r["tensor_scale"]), np.float64)
+                    .reshape(-1, 1, page, t.shape[1]))
+        out += [torch.from_numpy(r[n].reshape(-1, 1, page, r[n].shape[-1]).copy()).cuda() for n in ("codes", "scales")]
+        out.append(torch.full((1,), float(r["tensor_scale"])).cuda() if fmt == NV else None)
+    kc, ks, kt, vc, vs, vt = out
+    return F.KVCache("nvfp4" if fmt == NV else "mxfp4", kc, ks, vc, vs, kt, vt), *vals
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("queries", [1, 3])
+@pytest.mark.parametrize("keys,bits", [(41, 20.0), (900, 26.0), (130001, 31.5), (4000, 45.0), (60, 80.0)])
+def test_small_weights_of_fp32_calls(fp4, oracle, fmt, queries, keys, bits):
+    """One key takes nearly all the weight and has values of 0; the result is
+    what the others, each 2^-bits of it, leave: fp32 calls keep them all."""
+    print(f"[sink] {fmt} {queries} {keys} {bits}", flush=True)
+    dim, page = 32, 16
+    rows = -(-keys // page) * page
+    rng = np.random.RandomState(60)
+    k = np.zeros((rows, dim), np.float32)
+    sink = keys // 2
+    k[sink] = rng.uniform(1, 4, dim)
+    v = rng.uniform(0.5, 6.0, (rows, dim)).astype(np.float32)
+    v[sink] = 0
+    cache, kv, vv = cache_of(fp4, oracle, fmt, (k, v), page)
+    q = torch.from_numpy(rng.uniform(0.5, 1.5, (queries, 1, dim)).astype(np.float32))
+    dots = q.double().numpy()[:, 0] @ kv[sink // page, 0, sink % page]
+    scale = float(np.float32(bits * np.log(2) / dots.max()))
+    table = np.arange(rows // page, dtype=np.int32)[None]
+    out, lse = attend(fp4, cache, q, table, [keys], [queries], scale=scale, causal=False)
+    ref = attention_f64(q.double().numpy(), kv, vv, table, page, [keys], [queries], False, 0, 0.0, scale)
+    # every term of attention_bounds but NVFP4's loss of small weights
+    tol, tol_lse = attention_bounds(ref, False, False, dim, keys, 0.0)
+    check_attention(out, lse, ref, tol, tol_lse, f"sink {keys} {bits}")
