@@ -741,10 +741,10 @@ struct Rows {
         }
       }
     }
-    if (kt + kTileKeys > all_hi || kt < all_lo) {
+    if (partly_seen(kt)) {
 #pragma unroll
       for (int i = 0; i < 8; i++) {
-        const int key = kt + 8 * (TURNED ? ((i >> 1) - g) & 3 : i >> 1) + 4 * (i & 1) + g;
+        const int key = key_of<TURNED>(kt, g, i >> 1, i & 1);
 #pragma unroll
         for (int rt = 0; rt < RT; rt++)
           s[rt][i] = key < my_hi[rt] && key >= my_lo[rt] ? s[rt][i] * factor[rt] : -__builtin_huge_valf();
@@ -806,6 +806,14 @@ struct Rows {
     }
   }
 
+  // The key of the tile at kt that half `odd` of operand word i stands for.
+  template <bool TURNED>
+  static __device__ __forceinline__ int key_of(int kt, int g, int i, int odd) {
+    return kt + 8 * (TURNED ? (i - g) & 3 : i) + 4 * odd + g;
+  }
+  // Whether some row does not see some key of the tile at kt.
+  __device__ __forceinline__ bool partly_seen(int kt) const { return kt + kTileKeys > all_hi || kt < all_lo; }
+
   __device__ __forceinline__ void sum_denominators() {
 #pragma unroll
     for (int rt = 0; rt < RT; rt++) {
@@ -814,6 +822,58 @@ struct Rows {
     }
   }
 };
+
+// A weight of 0 hides a value only if that is a number: an infinity or NaN that
+// some rows see would reach the sums of those that do not. So in a tile that
+// not every row sees whole, a key with such a value (a block whose scale is
+// NaN, or 2^126 and more, which passes bf16 and fp32) gets values of 0 and a key
+// of NaN, which makes NaN of the rows that see it and is masked for the others;
+// keys past the sequence's end, which may hold anything, get values of 0.
+//
+// The bytes of four such scales, by their highest bits.
+template <bool NV>
+__device__ __forceinline__ uint32_t no_numbers(uint32_t scales) {
+  const uint32_t low = scales & 0x7f7f7f7fu;
+  return (NV ? low + 0x01010101u : (low + 0x03030303u) & scales) & 0x80808080u;
+}
+// Whether the tile at kt, in a wave's LDS slot y, has keys past the end or with
+// such values.
+template <int DP, bool NV, bool FULL>
+__device__ __forceinline__ bool unsettled(const CacheReader<DP, NV, FULL>& in, const uint8_t* y, int kt, int lane) {
+  using T = Tile<DP, NV>;
+  if (kt + kTileKeys > in.len) return true;
+  asm volatile("" : "+v"(lane));  // its addresses are not kept through the loop over tiles
+  const uint32_t* vs = reinterpret_cast<const uint32_t*>(y + T::kScalesAt + 2 * 16 * in.row_scales);
+  uint32_t found = 0u;
+#pragma unroll
+  for (int i = 0; i < (8 * DP / T::kBlk + 63) / 64; i++) {
+    const int at = 64 * i + lane;
+    if (at < 8 * in.row_scales) found |= no_numbers<NV>(vs[at]);
+  }
+  return __any(found != 0u);
+}
+// Lanes 0 to 31 settle a key each.
+template <int DP, bool NV, bool FULL>
+__device__ __forceinline__ void settle(const CacheReader<DP, NV, FULL>& in, uint8_t* y, int kt, int lane) {
+  using T = Tile<DP, NV>;
+  asm volatile("" : "+v"(lane));
+  if (lane < kTileKeys) {
+    uint8_t* ks = y + T::kScalesAt + lane * in.row_scales;
+    uint8_t* vs = ks + 2 * 16 * in.row_scales;
+    const bool past = kt + lane >= in.len;
+    uint32_t found = 0u;
+#pragma unroll 1
+    for (int i = 0; i < in.row_scales; i++) found |= no_numbers<NV>(vs[i]);
+    if (past || found) {
+#pragma unroll 1
+      for (int i = 0; i < in.row_scales; i++) {
+        vs[i] = 0;
+        if (!past) ks[i] = 255;
+      }
+    }
+  }
+  asm volatile("" ::: "memory");  // a wave's LDS accesses keep their order
+}
 
 // Few rows: a workgroup's LDS, its waves' tiles and afterwards their results.
 template <int DP, bool NV, int NW>
@@ -863,7 +923,8 @@ __device__ __forceinline__ void attend_few(const KvAttnArgs& a, const RowTile& r
   uint32_t slot = 0;
   for (; kt < c_hi; kt += kStep) {
     wait_copies<(kDepth - 1) * T::kLoads>();
-    const uint8_t* y = &lds.tiles[wave][0][0] + slot;
+    uint8_t* y = &lds.tiles[wave][0][0] + slot;
+    if (rows.partly_seen(kt) && unsettled(in, y, kt, lane)) settle(in, y, kt, lane);
     float s[RT][8];
 #pragma unroll
     for (int sub = 0; sub < 2; sub++) {
@@ -890,18 +951,6 @@ __device__ __forceinline__ void attend_few(const KvAttnArgs& a, const RowTile& r
 #pragma unroll
       for (int w = 0; w < T::kVWords; w++)
         v[i][w] = v_word<DP>(y + in.v_code(c, g) + (i >> 2) * T::kHalf + 4 * (i & 3) * in.row_codes, w);
-    }
-    if (kt + kTileKeys > r.len) {
-      asm volatile("");  // a branch, not selects on every tile
-      // a weight of 0 must meet a number
-#pragma unroll
-      for (int i = 0; i < 8; i++) {
-        if (kt + 16 * (i >> 2) + 4 * (i & 3) + g >= r.len) {
-          vs[i] = 0u;
-#pragma unroll
-          for (int w = 0; w < T::kVWords; w++) v[i][w] = 0u;
-        }
-      }
     }
     u32x4 pw[RT][Rows<DP, NV, BF16, FULL, RT>::kTerms];
     rows.template weigh<false, true>(a, kt, g, s, pw);
@@ -975,12 +1024,14 @@ __device__ __forceinline__ void attend_few(const KvAttnArgs& a, const RowTile& r
   }
 }
 
-// Waves a SIMD that the registers of the form for few rows allow. TWO: the
-// launch has no more than two anyway (runs, or eight waves a workgroup past
-// heads of 64), which fp32's terms need there (300 sequences to 700 in four
-// waves: 67 us with two, 57 with three).
+// Waves a SIMD that the registers of the form for few rows allow: past heads of
+// 128 two for bf16, so that two workgroups stay on a CU (8 sequences to 30000 of
+// heads of 256: 49 us, 65 with one; of 192: 43 against 67). TWO: the launch has
+// no more than two anyway (runs, or eight waves a workgroup past heads of 64),
+// which fp32's terms need there (130001 keys: 24.8 us, 27.6 with registers for
+// three; 300 sequences to 700 in four waves: 67 with two, 57 with three).
 constexpr int few_waves(int dp, int rt, bool bf16, bool two) {
-  return dp == 256 ? 1 : dp == 128 && (rt > 1 || (!bf16 && two)) ? 2 : 3;
+  return dp == 256 ? (bf16 ? 2 : 1) : dp == 128 && (rt > 1 || (!bf16 && two)) ? 2 : 3;
 }
 
 // One workgroup for each row tile and kv head.
@@ -1115,7 +1166,18 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 64 ? 4 : 3) void kv_attn
     const int pair = (2 * sub + (c >> 1 & 1) + (c >> 2)) & 3;
     k_to[sub] = (pair >> 1) * T::kKWords * 64 + 16 * g + (c & 12) + 2 * (pair & 1) + (c & 1);
   }
-  auto convert = [&](int kt, const uint8_t* y, int to) {
+  // Whether some row of the workgroup does not see some key of a tile.
+  const int all_hi = end_key(a, r.len, r.n, r.row0 / a.group);
+  const int all_lo = first_key(a, r.len, r.n, min((r.row0 + kRows - 1) / a.group, r.n - 1));
+  auto partly_seen = [=](int kt) { return kt + kTileKeys > all_hi || kt < all_lo; };
+  auto convert = [&](int kt, uint8_t* y, int to) {
+    if (partly_seen(kt) && unsettled(in, y, kt, lane)) {  // all waves or none
+      wait_lds();
+      __syncthreads();
+      if (wave == 0) settle(in, y, kt, lane);
+      wait_lds();
+      __syncthreads();
+    }
     if constexpr (T::kKWords == 2) {
       const int sub = wave >> 1, w = (wave + (g >> 1)) & 1;
       const uint32_t code = *reinterpret_cast<const uint32_t*>(y + sub * T::kHalf + in.k_word(c, g, w));
@@ -1136,16 +1198,10 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 64 ? 4 : 3) void kv_attn
     const int sub = wave >> 1, i = 2 * (wave & 1);
     const uint8_t* yv = y + in.v_code(c, g) + sub * T::kHalf + 4 * i * in.row_codes;
     const uint8_t* ys = y + in.v_scale(c, g) + (16 * sub + 4 * i) * in.row_scales;
-    uint32_t s0 = ys[0], s1 = ys[4 * in.row_scales];
-    const int key = kt + 16 * sub + 4 * i + g;
+    const uint32_t s0 = ys[0], s1 = ys[4 * in.row_scales];
 #pragma unroll
     for (int w = 0; w < T::kVWords; w++) {
-      uint32_t x0 = v_word<DP>(yv, w), x1 = v_word<DP>(yv + 4 * in.row_codes, w);
-      if (kt + kTileKeys > r.len) {
-        // a weight of 0 must meet a number
-        if (key >= r.len) s0 = x0 = 0u;
-        if (key + 4 >= r.len) s1 = x1 = 0u;
-      }
+      const uint32_t x0 = v_word<DP>(yv, w), x1 = v_word<DP>(yv + 4 * in.row_codes, w);
       uint32_t vt[2 * T::kPairs];
       convert_key_pair<NV, NV, T::kPairs>(x0, x1, s0, s1, vt);
 #pragma unroll

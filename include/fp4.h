@@ -454,8 +454,12 @@ size_t fp4_kv_attention_workspace(const fp4_kv_cache* cache, const fp4_kv_attent
  *   kv_lens are cut to [0, max_kv_len], q_offsets clamped into [0, tokens],
  *   each end to at least its start, and page numbers into [0, num_pages), so
  *   no device value makes the kernel access memory outside the operands. Table
- *   entries past a sequence's last page are not used; the rows of its last
- *   page past its end may hold anything. Rows of out and lse outside every
+ *   entries past a sequence's last page are not used, and pages before every
+ *   query's window may be given back. Rows that a query does not see (past the
+ *   end, later tokens, before its window) have no part in its result whatever
+ *   they hold, infinities and NaN included. A query that sees an infinite or NaN
+ *   value is infinite or NaN in those elements, and may be NaN in all (also from
+ *   MXFP4 blocks of scales 2^126 and more). Rows of out and lse outside every
  *   sequence are not written.
  *   q and out 16-byte aligned with strides multiples of 16 bytes.
  *   workspace: at least fp4_kv_attention_workspace() bytes, 16-byte aligned;
