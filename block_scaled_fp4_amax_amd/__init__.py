@@ -674,19 +674,11 @@ def _kv_vector(t, cache, n, dtype, what):
     return t.data_ptr()
 
 
-def _kv_stream(cache, stream, *made):
-    """The stream to launch on, the current device being the cache's. Tensors
-    made by this call (`made`) for a stream other than torch's current one
-    must not have their memory reused before that stream has passed the call."""
+def _kv_stream(cache):
+    """torch's current stream on the cache's GPU."""
     import torch
     # the handle torch.cuda.current_stream() wraps, without making the object
-    current = torch._C._cuda_getCurrentRawStream(cache.index)
-    if stream is None or stream == current:
-        return current
-    for t in made:
-        if t is not None:
-            t.record_stream(torch.cuda.ExternalStream(stream, device=cache.device))
-    return stream
+    return torch._C._cuda_getCurrentRawStream(cache.index)
 
 
 def _on_cache_gpu(call, cache, *args, **kw):
@@ -694,6 +686,21 @@ def _on_cache_gpu(call, cache, *args, **kw):
     import torch
     with torch.cuda.device(cache.index):
         return call(*args, **kw)
+
+
+def _on_stream(call, cache, stream, given, *args, **kw):
+    """The call again, with `stream` current: outputs and workspace then come
+    from its own memory, which nothing queued on another stream still uses.
+    The outputs it makes (not `given`) may be used on the caller's stream too,
+    and are not reused before that has passed their last use."""
+    import torch
+    caller = torch.cuda.current_stream(cache.device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=cache.device)):
+        result = call(*args, **kw)
+    for t in result if isinstance(result, tuple) else (result,):
+        if t is not None and t is not given:
+            t.record_stream(caller)
+    return result
 
 
 def kv_append(cache: KVCache, k, v, slots, *, q=None, positions=None, cos=None, sin=None, interleaved=False,
@@ -712,6 +719,9 @@ def kv_append(cache: KVCache, k, v, slots, *, q=None, positions=None, cos=None, 
     if torch._C._cuda_getDevice() != cache.index:
         return _on_cache_gpu(kv_append, cache, cache, k, v, slots, q=q, positions=positions, cos=cos, sin=sin,
                              interleaved=interleaved, four_over_six=four_over_six, q_out=q_out, stream=stream)
+    if stream is not None and stream != _kv_stream(cache):
+        return _on_stream(kv_append, cache, stream, q_out, cache, k, v, slots, q=q, positions=positions, cos=cos, sin=sin,
+                          interleaved=interleaved, four_over_six=four_over_six, q_out=q_out)
     (tokens, kh, _), ks = _kv_rows(k, cache, "k")
     vshape, vs = _kv_rows(v, cache, "v")
     dt = _kv_dtype(k, "k")
@@ -719,7 +729,6 @@ def kv_append(cache: KVCache, k, v, slots, *, q=None, positions=None, cos=None, 
         raise ValueError("k and v must be [tokens, kv_heads, head_dim] of one dtype")
     at_slots = _kv_vector(slots, cache, tokens, torch.int64, "slots")
     rotary = max_position = heads = 0
-    made = None
     at_pos = at_cos = at_sin = at_q = at_out = q0 = q1 = o0 = o1 = 0
     if cos is not None:
         if sin is None or positions is None:
@@ -740,7 +749,7 @@ def kv_append(cache: KVCache, k, v, slots, *, q=None, positions=None, cos=None, 
         if q.dtype is not k.dtype or qshape[0] != tokens:
             raise ValueError("q, k and v must have one dtype and as many tokens")
         if q_out is None:
-            q_out = made = torch.empty_like(q, memory_format=torch.contiguous_format)
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
             o0, o1 = heads * cache.head_dim, cache.head_dim
         else:
             oshape, (o0, o1, _) = _kv_rows(q_out, cache, "q_out")
@@ -754,7 +763,7 @@ def kv_append(cache: KVCache, k, v, slots, *, q=None, positions=None, cos=None, 
         (FP4_FOUR_OVER_SIX if four_over_six else 0) | (FP4_KV_INTERLEAVED if interleaved else 0), heads, tokens,
         k.data_ptr(), v.data_ptr(), at_q, at_out, ks[0], ks[1], vs[0], vs[1], q0, q1, o0, o1, at_slots, at_pos,
         at_cos, at_sin, max_position, rotary, 0)
-    st = lib().fp4_kv_append(cache._ref, args, _kv_stream(cache, stream, made))
+    st = lib().fp4_kv_append(cache._ref, args, _kv_stream(cache))
     if st != FP4_OK:
         raise Fp4Error(st, "fp4_kv_append")
     return q_out
@@ -767,13 +776,14 @@ def kv_read(cache: KVCache, slots, dtype=None, stream=None):
     import torch
     if torch._C._cuda_getDevice() != cache.index:
         return _on_cache_gpu(kv_read, cache, cache, slots, dtype, stream)
+    if stream is not None and stream != _kv_stream(cache):
+        return _on_stream(kv_read, cache, stream, None, cache, slots, dtype)
     tokens = slots.numel()
     at_slots = _kv_vector(slots, cache, tokens, torch.int64, "slots")
     k = slots.new_empty((tokens, cache.kv_heads, cache.head_dim), dtype=dtype or torch.bfloat16)
     dt = _kv_dtype(k, "dtype")
     v = torch.empty_like(k)
-    st = lib().fp4_kv_read(cache._ref, tokens, at_slots, k.data_ptr(), v.data_ptr(), dt,
-                           _kv_stream(cache, stream, k, v))
+    st = lib().fp4_kv_read(cache._ref, tokens, at_slots, k.data_ptr(), v.data_ptr(), dt, _kv_stream(cache))
     if st != FP4_OK:
         raise Fp4Error(st, "fp4_kv_read")
     return k, v
@@ -803,6 +813,10 @@ def kv_attention(q, cache: KVCache, block_table, kv_lens, *, q_offsets=None, max
         return _on_cache_gpu(kv_attention, cache, q, cache, block_table, kv_lens, q_offsets=q_offsets,
                              max_kv_len=max_kv_len, causal=causal, window=window, softcap=softcap, scale=scale,
                              return_lse=return_lse, out=out, stream=stream)
+    if stream is not None and stream != _kv_stream(cache):
+        return _on_stream(kv_attention, cache, stream, out, q, cache, block_table, kv_lens, q_offsets=q_offsets,
+                          max_kv_len=max_kv_len, causal=causal, window=window, softcap=softcap, scale=scale,
+                          return_lse=return_lse, out=out)
     qshape, (q0, q1, _) = _kv_rows(q, cache, "q")
     dt = _kv_dtype(q, "q")
     tokens, heads, dim = qshape
@@ -816,10 +830,10 @@ def kv_attention(q, cache: KVCache, block_table, kv_lens, *, q_offsets=None, max
     at_offs = at_lse = 0
     if q_offsets is not None:
         at_offs = _kv_vector(q_offsets, cache, batch + 1, torch.int32, "q_offsets")
-    made = lse = ws = at_ws = None
+    lse = at_ws = None
     if out is None:
         # (empty_like costs half of empty)
-        out = made = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
         o0, o1 = heads * dim, dim
     else:
         oshape, (o0, o1, _) = _kv_rows(out, cache, "out")
@@ -839,7 +853,7 @@ def kv_attention(q, cache: KVCache, block_table, kv_lens, *, q_offsets=None, max
     if need:
         ws = q.new_empty((need,), dtype=torch.uint8)
         at_ws = ws.data_ptr()
-    st = L.fp4_kv_attention(cache._ref, args, at_ws, need, _kv_stream(cache, stream, made, lse, ws))
+    st = L.fp4_kv_attention(cache._ref, args, at_ws, need, _kv_stream(cache))
     if st != FP4_OK:
         raise Fp4Error(st, "fp4_kv_attention")
     return (out, lse) if return_lse else out
