@@ -506,6 +506,9 @@ namespace {
 
 bool finite(float x) { return x - x == 0.0f; }
 
+// A launch holds fewer than 2^32 work items along x.
+constexpr int64_t kMaxItemsX = (int64_t(1) << 32) - 1;
+
 // Checks of a cache handle, and its form for the kernels.
 fp4_status plan_kv_cache(const fp4_kv_cache* c, KvCache* k) {
   if (!c || c->size != sizeof(fp4_kv_cache) || c->reserved != 0) return FP4_ERR_INVALID;
@@ -578,7 +581,7 @@ fp4_status fp4_kv_append(const fp4_kv_cache* cache, const fp4_kv_append_args* ar
   if (args->tokens < 0 || args->q_heads < 0) return FP4_ERR_INVALID;
   if (args->rotary < 0 || args->rotary > cache->head_dim || args->rotary % 2 != 0 || args->max_position < 0)
     return FP4_ERR_INVALID;
-  if (args->q_heads > kMaxGridYZ || args->tokens > (int64_t(1) << 30)) return FP4_ERR_UNSUPPORTED;
+  if (args->q_heads > kMaxGridYZ || args->tokens > kMaxItemsX / 256 * 4) return FP4_ERR_UNSUPPORTED;
   if (args->tokens == 0) return FP4_OK;
   const int64_t es = args->dtype == FP4_BF16 ? 2 : 4, T = args->tokens, D = cache->head_dim;
   if (!args->slots) return FP4_ERR_INVALID;
@@ -632,8 +635,7 @@ fp4_status fp4_kv_read(const fp4_kv_cache* cache, int64_t tokens, const int64_t*
   if (st != FP4_OK) return st;
   if (y_dtype != FP4_F32 && y_dtype != FP4_BF16) return FP4_ERR_INVALID;
   if (tokens < 0) return FP4_ERR_INVALID;
-  if (tokens > (int64_t(1) << 30) ||
-      (tokens * cache->kv_heads * (cache->head_dim / 8) + 255) / 256 > kMaxGridX)
+  if (tokens > (int64_t(1) << 30) || tokens * cache->kv_heads * (cache->head_dim / 8) > kMaxItemsX / 256 * 256)
     return FP4_ERR_UNSUPPORTED;
   if (tokens == 0) return FP4_OK;
   if (!slots || !k_out || !v_out) return FP4_ERR_INVALID;
@@ -680,12 +682,13 @@ static fp4_status plan_kv_attention_call(const fp4_kv_cache* cache, const fp4_kv
   a->table_stride = args->table_stride;
   a->table_width = args->table_width;
   a->max_len = args->max_kv_len;
-  a->window = args->window;
+  // a window of all the rows there may be is none
+  a->window = args->window < args->max_kv_len ? args->window : 0;
   *p = KvAttnPlan{};
   if (args->batch > 0 && args->tokens > 0) {
     *p = plan_kv_attention(*a);
-    // the join has a workgroup for each of an item's rows, 32 at most
-    if (p->tiles * cache->kv_heads * 32 > kMaxGridX) return FP4_ERR_UNSUPPORTED;
+    // (runs, and the rows that they join, are few)
+    if (p->runs == 0 && p->tiles * cache->kv_heads > kMaxItemsX / (64 * p->waves)) return FP4_ERR_UNSUPPORTED;
   }
   return FP4_OK;
 }

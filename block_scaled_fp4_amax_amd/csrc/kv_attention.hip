@@ -1388,6 +1388,7 @@ KvAttnPlan plan_kv_attention(const KvAttnArgs& a) {
   const int64_t fill = (a.c.dim <= 64 && a.max_len > 512 ? 3 : 2) * cus;
   if (a.bf16 && a.offs && rows >= 128 * a.batch && (rows / kManyRows + a.batch / 2) * a.c.heads >= fill) {
     p.many = true;
+    p.waves = kWaves;
     p.tiles = rows / kManyRows + a.batch;
     return p;
   }

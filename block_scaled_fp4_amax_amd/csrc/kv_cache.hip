@@ -319,9 +319,10 @@ static hipError_t append_rot(const KvAppendArgs& a, hipStream_t s) {
   // few tokens: a wave takes one pass, so that the rows of a token spread
   // over the GPU; many: four, of which each but the first is loaded during
   // the one before (16384 tokens of 32 + 2 x 8 rows of 128: 83 us; six 87,
-  // all twelve 85)
+  // all twelve 85). A launch has up to 65535 workgroups along y; four passes
+  // a wave need fewer for any number of heads.
   const int64_t waves = 4 * 2048;
-  const int per_wave = a.tokens * passes <= waves ? 1 : passes < 4 ? passes : 4;
+  const int per_wave = a.tokens * passes <= waves && passes <= 65535 ? 1 : passes < 4 ? passes : 4;
   const dim3 grid((unsigned)((a.tokens + 3) / 4), (unsigned)((passes + per_wave - 1) / per_wave));
   if (a.rotary == 0) hipLaunchKernelGGL((kv_append_kernel<T, NV, SEL, kNoRotation>), grid, dim3(256), 0, s, a, per_wave);
   else if (a.interleaved)

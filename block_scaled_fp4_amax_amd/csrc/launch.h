@@ -163,7 +163,7 @@ struct KvAttnArgs {
 struct KvAttnPlan {
   bool many;      // the form for many rows
   int few_tiles;  // few rows: 16-row tiles a wave
-  int waves;      // few rows: of a workgroup
+  int waves;      // of a workgroup
   int64_t tiles;  // row tiles of the batch per kv head, an upper bound
   int64_t runs;   // few rows, 0: a workgroup for each row tile and kv head; else equal runs of key tiles
   int64_t least;  // key tiles of a run, at least

@@ -391,7 +391,7 @@ typedef struct fp4_kv_append_args {
  * Pointers of k, v, q and q_out 16-byte aligned, strides multiples of 16
  * bytes; q_out either is q with q's strides or does not overlap it.
  * Errors: FP4_ERR_INVALID (sizes, strides, NULLs), FP4_ERR_UNSUPPORTED (too
- * many tokens or heads for one launch), FP4_ERR_ALIGN, FP4_ERR_DEVICE,
+ * many tokens or heads for one launch: 2^26 - 3 tokens), FP4_ERR_ALIGN, FP4_ERR_DEVICE,
  * FP4_ERR_HIP. tokens = 0 is a valid empty call.
  */
 fp4_status fp4_kv_append(const fp4_kv_cache* cache, const fp4_kv_append_args* args, void* stream);
@@ -432,7 +432,7 @@ typedef struct fp4_kv_attention_args {
   int64_t out_token_stride, out_head_stride;
   float scale;              /* multiplies q . k */
   float softcap;            /* > 0: scores become softcap * tanh(score / softcap); 0: off */
-  int64_t window;           /* > 0 (causal only): the last `window` of the rows a query sees; 0: off */
+  int64_t window;           /* > 0 (causal only): the last `window` of the rows a query sees; 0, or max_kv_len and more: all */
 } fp4_kv_attention_args;
 
 /* Bytes of device workspace fp4_kv_attention needs for these sizes (0 when
