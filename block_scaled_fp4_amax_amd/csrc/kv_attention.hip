@@ -69,6 +69,11 @@ constexpr float kSlack = 8.0f;
 // sum.
 constexpr float kF16Lift = 6.0f;
 
+// A weight is 2 to the exact product of score and factor, less the maximum,
+// which is a rounded one: at 2^20 that rounding alone makes it 2^(1/16), and far
+// past it would leave fp16 and fp32. From here on products are rounded alike.
+constexpr float kLargeScore = 1048576.0f;
+
 // What one row tile of one kv head has to do.
 struct RowTile {
   int b;        // sequence
@@ -628,6 +633,7 @@ struct Rows {
   int token[RT], head[RT];
   int my_lo[RT], my_hi[RT];  // the keys this lane's rows see
   int all_lo, all_hi;        // keys that every row sees
+  bool large = false;        // a maximum of these rows passed kLargeScore
   u32x4 q[RT][kTerms][DP / 32];
   float score_scale[RT];
   f32x4 o[RT][kChunkV];
@@ -741,7 +747,7 @@ struct Rows {
         }
       }
     }
-    if (partly_seen(kt)) {
+    if (partly_seen(kt) || large) {
 #pragma unroll
       for (int i = 0; i < 8; i++) {
         const int key = key_of<TURNED>(kt, g, i >> 1, i & 1);
@@ -773,6 +779,18 @@ struct Rows {
 #pragma unroll
         for (int j = 0; j < kChunkV; j++) o[rt][j] *= down;
         m[rt] = raised;
+      }
+      bool passed = false;
+#pragma unroll
+      for (int rt = 0; rt < RT; rt++) passed |= __builtin_fabsf(m[rt]) > kLargeScore && m[rt] != kNoMax;
+      large = __any(passed);
+      if (large) {
+#pragma unroll
+        for (int rt = 0; rt < RT; rt++) {
+#pragma unroll
+          for (int i = 0; i < 8; i++) s[rt][i] *= factor[rt];
+          factor[rt] = 1.0f;
+        }
       }
     }
 #pragma unroll

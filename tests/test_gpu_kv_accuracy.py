@@ -91,3 +91,38 @@ def test_small_weights_of_fp32_calls(fp4, oracle, fmt, queries, keys, bits):
     # every term of attention_bounds but NVFP4's loss of small weights
     tol, tol_lse = attention_bounds(ref, False, False, dim, keys, 0.0)
     check_attention(out, lse, ref, tol, tol_lse, f"sink {keys} {bits}")
+
+
+# ---------------------------------------------------------------------------
+# scores of any finite size
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("fmt,dtype", FD, ids=FD_IDS)
+@pytest.mark.parametrize("queries", [1, 40])
+@pytest.mark.parametrize("scale", [3e5, 7e8, 1.1e20, -9e7])
+def test_large_scores(fp4, oracle, fmt, dtype, queries, scale):
+    """Scores so large that the largest of a row takes all the weight, and
+    equal ones share it: k has one element that counts, -6 to 6 in exact
+    values, and the query is a one there."""
+    print(f"[large scores] {fmt} {dtype} {queries} {scale}", flush=True)
+    dim, page, keys = 32, 16, 200
+    rng = np.random.RandomState(61)
+    k, v = np.zeros((208, dim), np.float32), rng.choice([-4, -3, -2, 1, 2, 3, 6], (208, dim)).astype(np.float32)
+    k[:, 0] = rng.choice([-4, -3, -2, -1, 0, 1, 2, 3], 208)
+    k[:, 16] = v[:, 31] = 6                # one scale for all blocks of a row
+    best = 6 if scale > 0 else -6
+    k[[70, 130, 131, 150], 0] = best       # four rows with the largest score
+    cache, kv, vv = cache_of(fp4, oracle, fmt, (k, v), page)
+    assert np.array_equal(kv.reshape(208, dim)[:, 0], k[:, 0]) or fmt == NV
+    q = torch.zeros(queries, 1, dim, dtype=dtype)
+    q[..., 0] = 1
+    table = np.arange(13, dtype=np.int32)[None]
+    out, lse = attend(fp4, cache, q, table, [keys], [queries], scale=scale, causal=False)
+    vals, keyv = vv.reshape(208, dim), kv.reshape(208, dim)[:keys, 0]
+    top = np.flatnonzero(keyv * np.sign(scale) == (keyv * np.sign(scale)).max())
+    assert list(top) == [70, 130, 131, 150]
+    want = vals[top].mean(0)
+    got = out.double().cpu().numpy()[:, 0]
+    # equal weights: a quarter of an exact sum, and one rounding
+    assert (np.abs(got - want) <= np.abs(vals[top]).mean(0) * 2.0 ** (-8 if dtype == BF else -22)).all()
+    score = keyv[top[0]] * float(np.float32(scale))
+    assert np.allclose(lse.double().cpu().numpy(), score + np.log(4), rtol=2.0 ** -21)
