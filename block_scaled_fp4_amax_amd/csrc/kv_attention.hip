@@ -57,9 +57,10 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 constexpr int kTileKeys = 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// The running maximum starts below every score that is not -inf; a masked
-// score (-inf) then weighs exp2(-inf) = 0 also before the first visible key.
-constexpr float kNoMax = -1e30f;
+// The running maximum starts at the lowest number, so that a masked score
+// (-inf) weighs exp2(-inf) = 0 also before the first visible key, and every
+// finite one counts.
+constexpr float kNoMax = -3.40282347e38f;
 // A row's maximum is only raised when a score passes it by more than 2^8
 // (weights may grow to that without harm in fp32), so that most tiles need
 // neither the exchange across lanes nor the rescaling.

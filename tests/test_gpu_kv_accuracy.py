@@ -1,5 +1,5 @@
 """Attention over the 4-bit cache where its arithmetic is strained: softcaps of
-every size, weights far below the largest."""
+every size, weights far below the largest, scores far from 0."""
 import numpy as np
 import pytest
 import torch
@@ -126,3 +126,28 @@ def test_large_scores(fp4, oracle, fmt, dtype, queries, scale):
     assert (np.abs(got - want) <= np.abs(vals[top]).mean(0) * 2.0 ** (-8 if dtype == BF else -22)).all()
     score = keyv[top[0]] * float(np.float32(scale))
     assert np.allclose(lse.double().cpu().numpy(), score + np.log(4), rtol=2.0 ** -21)
+
+
+@pytest.mark.parametrize("fmt,dtype", FD, ids=FD_IDS)
+@pytest.mark.parametrize("queries,keys", [(1, 200), (40, 200), (1, 9000)])
+@pytest.mark.parametrize("scale", [-2e29, -1e37])
+def test_scores_far_below_zero(fp4, oracle, fmt, dtype, queries, keys, scale):
+    """Scores of -6e29 and less are scores still: a row whose keys all have
+    them is their mean, not a row that sees nothing."""
+    print(f"[low scores] {fmt} {dtype} {queries} {keys} {scale}", flush=True)
+    dim, page = 32, 16
+    rows = -(-keys // page) * page
+    k = np.full((rows, dim), 6, np.float32)
+    v = np.random.RandomState(62).choice([1, 2, 3, 4, 6], (rows, dim)).astype(np.float32)
+    v[:, 31] = 6
+    v[:, 15] = 6
+    cache, kv, vv = cache_of(fp4, oracle, fmt, (k, v), page)
+    q = torch.zeros(queries, 1, dim, dtype=dtype)
+    q[..., 0] = 1
+    table = np.arange(rows // page, dtype=np.int32)[None]
+    out, lse = attend(fp4, cache, q, table, [keys], [queries], scale=scale, causal=False)
+    want = vv.reshape(rows, dim)[:keys].mean(0)
+    got = out.double().cpu().numpy()[:, 0]
+    # equal weights: fp32 sums of `keys` terms, and one rounding
+    assert (np.abs(got - want) <= want * (2.0 ** (-8 if dtype == BF else -23) + (keys + 64) * 2.0 ** -23)).all()
+    assert np.allclose(lse.double().cpu().numpy(), kv.reshape(-1)[0] * float(np.float32(scale)), rtol=2.0 ** -21)
