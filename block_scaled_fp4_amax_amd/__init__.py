@@ -371,9 +371,29 @@ def _fmt(fmt) -> int:
     return int(fmt)
 
 
-def _stream(stream):
+def _stream():
     import torch
-    return stream if stream is not None else torch.cuda.current_stream().cuda_stream
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _on_stream(call, device, stream, given, *args, **kw):
+    """The call again, with `stream` current: copies, outputs and workspace are
+    then that stream's own, and nothing queued on another still uses their
+    memory. The outputs it makes (not `given`) may be used on the caller's
+    stream too, and are not reused before that has passed their last use."""
+    import torch
+    caller = torch.cuda.current_stream(device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+        result = call(*args, **kw)
+    made = (result.codes, result.scales, result.tensor_scale) if isinstance(result, Quantized) else result
+    for t in made if isinstance(made, tuple) else (made,):
+        if t is not None and t is not given:
+            t.record_stream(caller)
+    return result
+
+
+def _elsewhere(stream) -> bool:
+    return stream is not None and stream != _stream()
 
 
 def _check(status: int, where: str):
@@ -387,6 +407,10 @@ def quantize(x, fmt="nvfp4", *, four_over_six=False, block2d=False, transpose=Fa
     """Quantize a [rows, cols] or [batch, rows, cols] bf16/fp32 device tensor
     (tensor_scale: the NVFP4 whole-tensor mode, FP4_TENSOR_SCALE)."""
     import torch
+    if _elsewhere(stream):
+        return _on_stream(quantize, x.device, stream, None, x, fmt, four_over_six=four_over_six, block2d=block2d,
+                          transpose=transpose, stochastic=stochastic, hadamard=hadamard, scale_search=scale_search,
+                          tensor_scale=tensor_scale, rht_signs=rht_signs, seed=seed, offset=offset, amax=amax)
     fmt = _fmt(fmt)
     squeeze = x.dim() == 2
     x3 = x.unsqueeze(0) if squeeze else x
@@ -417,7 +441,7 @@ def quantize(x, fmt="nvfp4", *, four_over_six=False, block2d=False, transpose=Fa
     st = fp4_quantize(x3.data_ptr(), dt, batch, rows, cols, cols, rows * cols, opts, codes.data_ptr(), ldc,
                       R * ldc, scales_buf.data_ptr(), lds, R * lds,
                       ts.data_ptr() if ts is not None else None, ws.data_ptr() if ws is not None else None,
-                      ws_bytes, _stream(stream))
+                      ws_bytes, _stream())
     _check(st, "fp4_quantize")
     if squeeze:
         codes, scales = codes[0], scales[0]
@@ -439,6 +463,8 @@ def _check_codes(codes):
 
 def dequantize(q: Quantized, dtype=None, stream=None):
     import torch
+    if _elsewhere(stream):
+        return _on_stream(dequantize, q.codes.device, stream, None, q, dtype)
     dtype = dtype or torch.float32
     codes = q.codes if q.codes.dim() == 3 else q.codes.unsqueeze(0)
     scales = q.scales if q.scales.dim() == 3 else q.scales.unsqueeze(0)
@@ -452,7 +478,7 @@ def dequantize(q: Quantized, dtype=None, stream=None):
                         scales.data_ptr(),
                         scales.stride(1), scales.stride(0),
                         q.tensor_scale.data_ptr() if q.tensor_scale is not None else None, y.data_ptr(), dt, cols,
-                        rows * cols, _stream(stream))
+                        rows * cols, _stream())
     _check(st, "fp4_dequantize")
     return y if q.codes.dim() == 3 else y[0]
 
@@ -460,6 +486,8 @@ def dequantize(q: Quantized, dtype=None, stream=None):
 def gemm(a: Quantized, b: Quantized, out_dtype=None, stream=None):
     """C[g] = deq(A[g]) @ deq(B[g])^T with A [.., M, K] and B [.., N, K]."""
     import torch
+    if _elsewhere(stream):
+        return _on_stream(gemm, a.codes.device, stream, None, a, b, out_dtype)
     out_dtype = out_dtype or torch.float32
     if a.fmt != b.fmt:
         raise ValueError("operands must share a format")
@@ -482,7 +510,7 @@ def gemm(a: Quantized, b: Quantized, out_dtype=None, stream=None):
                   asc.stride(0), a.tensor_scale.data_ptr() if a.tensor_scale is not None else None,
                   bc.data_ptr(), bc.stride(1), bc.stride(0), bsc.data_ptr(), bsc.stride(1), bsc.stride(0),
                   b.tensor_scale.data_ptr() if b.tensor_scale is not None else None, c.data_ptr(), ct, N, M * N,
-                  _stream(stream))
+                  _stream())
     _check(st, "fp4_gemm")
     return c if a.codes.dim() == 3 else c[0]
 
@@ -494,6 +522,10 @@ def gemm_quantize_output(a: Quantized, b: Quantized, fmt="nvfp4", *, four_over_s
     (format `fmt`, options as for quantize); NVFP4 needs `amax`, the tensor
     amax per group that S_t derives from."""
     import torch
+    if _elsewhere(stream):
+        return _on_stream(gemm_quantize_output, a.codes.device, stream, None, a, b, fmt, four_over_six=four_over_six,
+                          stochastic=stochastic, hadamard=hadamard, scale_search=scale_search, rht_signs=rht_signs,
+                          seed=seed, offset=offset, amax=amax)
     if a.fmt != b.fmt:
         raise ValueError("operands must share a format")
     ac = a.codes if a.codes.dim() == 3 else a.codes.unsqueeze(0)
@@ -528,7 +560,7 @@ def gemm_quantize_output(a: Quantized, b: Quantized, fmt="nvfp4", *, four_over_s
                                   bc.data_ptr(), bc.stride(1), bc.stride(0), bsc.data_ptr(), bsc.stride(1),
                                   bsc.stride(0), b.tensor_scale.data_ptr() if b.tensor_scale is not None else None,
                                   opts, codes.data_ptr(), ldq, M * ldq, scales_buf.data_ptr(), lds, M * lds,
-                                  ts.data_ptr() if ts is not None else None, _stream(stream))
+                                  ts.data_ptr() if ts is not None else None, _stream())
     _check(st, "fp4_gemm_quantize_output")
     scales = scales_buf[:, :, : N // blk]
     if a.codes.dim() == 2:
@@ -541,6 +573,8 @@ def gemm_grouped(a: Quantized, b: Quantized, offsets, out_dtype=None, stream=Non
     A [M, K] times B[g] [N, K]^T, into C [M, N]. `offsets` is a device int32
     tensor of groups + 1 entries (e.g. a router's cumulative counts)."""
     import torch
+    if _elsewhere(stream):
+        return _on_stream(gemm_grouped, a.codes.device, stream, None, a, b, offsets, out_dtype)
     out_dtype = out_dtype or torch.float32
     if a.fmt != b.fmt:
         raise ValueError("operands must share a format")
@@ -566,7 +600,7 @@ def gemm_grouped(a: Quantized, b: Quantized, offsets, out_dtype=None, stream=Non
                           a.tensor_scale.data_ptr() if a.tensor_scale is not None else None,
                           bc.data_ptr(), bc.stride(1), bc.stride(0), bsc.data_ptr(), bsc.stride(1), bsc.stride(0),
                           b.tensor_scale.data_ptr() if b.tensor_scale is not None else None, c.data_ptr(), ct, N,
-                          _stream(stream))
+                          _stream())
     _check(st, "fp4_gemm_grouped")
     return c
 
@@ -688,21 +722,6 @@ def _on_cache_gpu(call, cache, *args, **kw):
         return call(*args, **kw)
 
 
-def _on_stream(call, cache, stream, given, *args, **kw):
-    """The call again, with `stream` current: outputs and workspace then come
-    from its own memory, which nothing queued on another stream still uses.
-    The outputs it makes (not `given`) may be used on the caller's stream too,
-    and are not reused before that has passed their last use."""
-    import torch
-    caller = torch.cuda.current_stream(cache.device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=cache.device)):
-        result = call(*args, **kw)
-    for t in result if isinstance(result, tuple) else (result,):
-        if t is not None and t is not given:
-            t.record_stream(caller)
-    return result
-
-
 def kv_append(cache: KVCache, k, v, slots, *, q=None, positions=None, cos=None, sin=None, interleaved=False,
               four_over_six=False, q_out=None, stream=None):
     """Rotate, quantize and store the keys and values [tokens, kv_heads,
@@ -720,8 +739,8 @@ def kv_append(cache: KVCache, k, v, slots, *, q=None, positions=None, cos=None, 
         return _on_cache_gpu(kv_append, cache, cache, k, v, slots, q=q, positions=positions, cos=cos, sin=sin,
                              interleaved=interleaved, four_over_six=four_over_six, q_out=q_out, stream=stream)
     if stream is not None and stream != _kv_stream(cache):
-        return _on_stream(kv_append, cache, stream, q_out, cache, k, v, slots, q=q, positions=positions, cos=cos, sin=sin,
-                          interleaved=interleaved, four_over_six=four_over_six, q_out=q_out)
+        return _on_stream(kv_append, cache.device, stream, q_out, cache, k, v, slots, q=q, positions=positions, cos=cos,
+                          sin=sin, interleaved=interleaved, four_over_six=four_over_six, q_out=q_out)
     (tokens, kh, _), ks = _kv_rows(k, cache, "k")
     vshape, vs = _kv_rows(v, cache, "v")
     dt = _kv_dtype(k, "k")
@@ -777,7 +796,7 @@ def kv_read(cache: KVCache, slots, dtype=None, stream=None):
     if torch._C._cuda_getDevice() != cache.index:
         return _on_cache_gpu(kv_read, cache, cache, slots, dtype, stream)
     if stream is not None and stream != _kv_stream(cache):
-        return _on_stream(kv_read, cache, stream, None, cache, slots, dtype)
+        return _on_stream(kv_read, cache.device, stream, None, cache, slots, dtype)
     tokens = slots.numel()
     at_slots = _kv_vector(slots, cache, tokens, torch.int64, "slots")
     k = slots.new_empty((tokens, cache.kv_heads, cache.head_dim), dtype=dtype or torch.bfloat16)
@@ -814,8 +833,8 @@ def kv_attention(q, cache: KVCache, block_table, kv_lens, *, q_offsets=None, max
                              max_kv_len=max_kv_len, causal=causal, window=window, softcap=softcap, scale=scale,
                              return_lse=return_lse, out=out, stream=stream)
     if stream is not None and stream != _kv_stream(cache):
-        return _on_stream(kv_attention, cache, stream, out, q, cache, block_table, kv_lens, q_offsets=q_offsets,
-                          max_kv_len=max_kv_len, causal=causal, window=window, softcap=softcap, scale=scale,
+        return _on_stream(kv_attention, cache.device, stream, out, q, cache, block_table, kv_lens,
+                          q_offsets=q_offsets, max_kv_len=max_kv_len, causal=causal, window=window, softcap=softcap, scale=scale,
                           return_lse=return_lse, out=out)
     qshape, (q0, q1, _) = _kv_rows(q, cache, "q")
     dt = _kv_dtype(q, "q")

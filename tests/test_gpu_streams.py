@@ -107,3 +107,30 @@ def test_the_default_stream_from_another(fp4):
         got = fp4.kv_attention(q, cache, table, lens, stream=torch.cuda.default_stream().cuda_stream)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+def test_quantize_and_gemm_on_another_stream(fp4):
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(256, 512, generator=g, device="cuda").to(BF).t()  # copied by the call
+    w = torch.randn(512, 256, generator=g, device="cuda").to(BF)
+    offsets = torch.tensor([0, 200, 512], dtype=torch.int32, device="cuda")
+    qx, qw = fp4.quantize(x), fp4.quantize(w)
+    pair = fp4.quantize(w.view(2, 256, 256), "mxfp4")
+    qm = fp4.quantize(x, "mxfp4")
+    calls = {
+        "quantize": lambda s: fp4.quantize(x, four_over_six=True, stream=s),
+        "dequantize": lambda s: fp4.dequantize(qx, stream=s),
+        "gemm": lambda s: fp4.gemm(qx, qw, stream=s),
+        "gemm_quantize_output": lambda s: fp4.gemm_quantize_output(qx, qw, amax=300.0, stream=s),
+        "gemm_grouped": lambda s: fp4.gemm_grouped(qm, pair, offsets, stream=s),
+    }
+    parts = lambda y: (y.codes, y.scales, y.tensor_scale) if isinstance(y, fp4.Quantized) else (y,)
+    side = torch.cuda.Stream()
+    for name, call in calls.items():
+        print(f"[streams] {name}", flush=True)
+        want = [t.cpu() for t in parts(call(None))]
+        torch.cuda.synchronize()
+        late_writes([4, 512, 512 * 16, 512 * 128, 512 * 256 * 2, 512 * 512 * 2, 512 * 256 * 4, 512 * 512 * 4])
+        got = ordered(side, lambda s: parts(call(s)))
+        for y, z in zip(got, want):
+            assert torch.equal(y, z), name
