@@ -632,7 +632,9 @@ class KVCache:
                 raise ValueError("cache buffers must be uint8 tensors on one GPU")
             if tuple(t.shape) != (pages, heads, page_size, width):
                 raise ValueError(f"cache buffer of shape {tuple(t.shape)}, expected {(pages, heads, page_size, width)}")
-            if pages and tuple(t.stride()[1:]) != (page_size * width, width, 1):
+            # (a single kv head, or a row of one scale, may have any stride)
+            if pages and any(n > 1 and have != want for n, have, want in
+                             zip(t.shape[1:], t.stride()[1:], (page_size * width, width, 1))):
                 raise ValueError("the pages of a cache buffer must be dense")
         for a, b in ((k_codes, v_codes), (k_scales, v_scales)):
             if pages > 1 and a.stride(0) != b.stride(0):
