@@ -680,7 +680,6 @@ static fp4_status plan_kv_attention_call(const fp4_kv_cache* cache, const fp4_kv
   a->tokens = args->tokens;
   a->offs = args->q_offsets;
   a->table_stride = args->table_stride;
-  a->table_width = args->table_width;
   a->max_len = args->max_kv_len;
   // a window of all the rows there may be is none
   a->window = args->window < args->max_kv_len ? args->window : 0;

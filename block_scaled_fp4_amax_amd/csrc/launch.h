@@ -148,7 +148,7 @@ struct KvAttnArgs {
   int q_heads, group;  // group = q_heads / kv heads
   int64_t batch, tokens;
   const int32_t *offs, *lens, *table;  // offs NULL: one query per sequence
-  int64_t table_stride, table_width, max_len;
+  int64_t table_stride, max_len;
   const void* q;
   void* out;
   float* lse;
