@@ -13,8 +13,9 @@ of ``include/fp4.h``). This module only marshals arguments:
 * ``quantize``, ``dequantize``, ``gemm``, ``gemm_grouped``,
   ``gemm_quantize_output``, and ``KVCache`` with ``kv_append``, ``kv_read``,
   ``kv_attention`` -- conveniences over torch device
-  tensors that allocate outputs with torch, pass the current HIP stream and
-  raise ``Fp4Error`` on a non-OK status.
+  tensors that allocate outputs with torch, pass the current HIP stream (or
+  allocate and launch on the one whose handle is given as ``stream``; inputs
+  have to be ready there) and raise ``Fp4Error`` on a non-OK status.
 
 There is no fallback: if ``libfp4.so`` is missing or a call fails, an error is
 raised.

@@ -1075,7 +1075,7 @@ __global__ __launch_bounds__(64 * NW, few_waves(DP, RT, BF16, NW > 4)) void kv_a
 
 // The balanced form: one workgroup for each run of key tiles, two a CU. 64
 // sequences to 16384 keys (699 MB, 64 heads over 8 of 128): 135 us, 5.2 TB/s,
-// and 6 to join; reads of 4 to 8 KB from anywhere reach 5.7 to 5.9 here.
+// and 7 to join; reads of 4 to 8 KB from anywhere reach 5.7 to 5.9 here.
 template <int DP, bool NV, bool BF16, bool FULL, int NW, int RT>
 __global__ __launch_bounds__(64 * NW, few_waves(DP, RT, BF16, true)) void kv_attn_runs_kernel(KvAttnArgs a, int least) {
   constexpr int kRows = 16 * RT;
@@ -1136,18 +1136,20 @@ struct ManySpace {
 // registers beside the loop's own, asked for in one kernel by a.cap: prompts of
 // 4096 without one, heads of 96 197 against 184 us, of 256 340 against 306.)
 //
-// Bound by vector and matrix instructions together (57 and 41 % of the SIMDs'
-// cycles by the counters): a weight costs an fma, an exponential (9.9 ns a wave's 64) and its parts
-// of a maximum, a sum and a conversion, and each tile's conversion comes on top,
+// Bound by vector and matrix instructions together (issuing 56 and 40 % of the
+// SIMDs' cycles by the counters, one or the other waiting for the rest): a
+// weight costs an fma, an exponential (9.9 ns a wave's 64) and its parts of a
+// maximum, a sum and a conversion, and each tile's conversion comes on top,
 // which is why waves share it through LDS (each on its own: 737 us with two row
 // tiles, then 620 in this form, for a prompt of 8192 of 32 heads over 8 of 128).
 // LDS comes next (42 %): four waves read 64 KB of operands a tile. With every
-// conversion's access on all of its banks 561 us, 980 TFLOP/s of the pairs seen; a large library product
-// of bf16 runs at 1140. The next scores beside this tile's softmax within a wave
-// were slower (620 to 695 us). Conversion and the product with V go before other waves'
-// work: 4 x 1024 queries over 6000 keys (8 heads a kv head) took 312 us without
-// and 286 with that, 266 now, 766 TFLOP/s: equal workgroups that fill the GPU
-// one and a third times.
+// conversion's access on all of its banks 573 us, 960 TFLOP/s of the pairs seen;
+// a large library product of bf16 runs at 1140. The next scores beside this
+// tile's softmax within a wave were slower (620 to 695 us). Conversion and the
+// product with V go before other waves' work: 4 x up to 1024 queries over up to
+// 6000 keys (8 heads a kv head) took 312 us without and 286 with that, 272 now,
+// 750 TFLOP/s: all 752 workgroups are on the GPU from the start, of 51 to 188
+// key tiles each, and the fullest CU has 446 where the mean is 385.
 template <int DP, bool NV, bool FULL, bool CAP>
 __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 64 ? 4 : 3) void kv_attn_many_kernel(KvAttnArgs a) {
   using T = Tile<DP, NV>;
@@ -1389,6 +1391,10 @@ constexpr int wide_waves(int dp) { return dp <= 128 ? 8 : kWaves; }
 constexpr int few_tiles(int dp, bool bf16) { return bf16 && dp <= 128 ? 2 : 1; }
 }  // namespace
 
+// Lengths and offsets are on the device: max_len stands for every length, the
+// mean rows for every sequence's. A bound of 131072 in place of the lengths: one
+// sequence of 997 keys 11.0 us instead of 10.1, 32 to 4096 31.3 instead of 28.6.
+// A prompt of 4096 beside forty tokens over 16384 keys: 634 us, 319 in two calls.
 KvAttnPlan plan_kv_attention(const KvAttnArgs& a) {
   KvAttnPlan p{};
   const int64_t rows = a.tokens * a.group;
