@@ -432,7 +432,8 @@ typedef struct fp4_kv_attention_args {
   int64_t out_token_stride, out_head_stride;
   float scale;              /* multiplies q . k */
   float softcap;            /* > 0: scores become softcap * tanh(score / softcap); 0: off */
-  int64_t window;           /* > 0 (causal only): the last `window` of the rows a query sees; 0, or max_kv_len and more: all */
+  int64_t window;           /* > 0 (causal only): the last `window` of the rows a query sees; 0, or max_kv_len and
+                             * more: all of them */
 } fp4_kv_attention_args;
 
 /* Bytes of device workspace fp4_kv_attention needs for these sizes (0 when
