@@ -7,12 +7,17 @@ of ``include/fp4.h``). This module only marshals arguments:
 * ``fp4_quantize``, ``fp4_quantize_noalloc``, ``fp4_dequantize``,
   ``fp4_gemm``, ``fp4_gemm_grouped``, ``fp4_gemm_quantize_output``,
   ``fp4_kv_append``, ``fp4_kv_read``, ``fp4_kv_attention``,
-  ``fp4_kv_attention_workspace``, ``fp4_quantize_workspace``,
+  ``fp4_kv_attention_workspace``, ``fp4_moe_route``, ``fp4_moe_route_backward``,
+  ``fp4_moe_group``, ``fp4_moe_group_workspace``, ``fp4_moe_dispatch``,
+  ``fp4_moe_combine``, ``fp4_moe_combine_backward``, ``fp4_matvec``,
+  ``fp4_quantize_workspace``,
   ``fp4_status_str`` -- the C entry points with
   the same names and argument order (integers for device pointers);
 * ``quantize``, ``dequantize``, ``gemm``, ``gemm_grouped``,
-  ``gemm_quantize_output``, and ``KVCache`` with ``kv_append``, ``kv_read``,
-  ``kv_attention`` -- conveniences over torch device
+  ``gemm_quantize_output``, ``matvec``, ``KVCache`` with ``kv_append``,
+  ``kv_read``, ``kv_attention``, and ``moe_route``, ``moe_route_backward``,
+  ``moe_group``, ``moe_dispatch``, ``moe_combine``, ``moe_combine_backward``
+  -- conveniences over torch device
   tensors that allocate outputs with torch, pass the current HIP stream (or
   allocate and launch on the one whose handle is given as ``stream``; inputs
   have to be ready there) and raise ``Fp4Error`` on a non-OK status.
@@ -57,10 +62,15 @@ FP4_TENSOR_SCALE = 64
 # fp4_kv_append_args.flags, fp4_kv_attention_args.flags
 FP4_KV_INTERLEAVED = 256
 FP4_KV_CAUSAL = 1
+# fp4_moe_route_args.flags
+FP4_MOE_SIGMOID = 1
+FP4_MOE_RENORMALIZE = 2
 
 EXPORTED_SYMBOLS = ("fp4_quantize_workspace", "fp4_quantize", "fp4_quantize_noalloc", "fp4_dequantize", "fp4_gemm",
                     "fp4_gemm_grouped", "fp4_gemm_quantize_output", "fp4_kv_append", "fp4_kv_read",
-                    "fp4_kv_attention_workspace", "fp4_kv_attention", "fp4_status_str")
+                    "fp4_kv_attention_workspace", "fp4_kv_attention", "fp4_moe_route", "fp4_moe_route_backward",
+                    "fp4_moe_group_workspace", "fp4_moe_group", "fp4_moe_dispatch", "fp4_moe_combine",
+                    "fp4_moe_combine_backward", "fp4_matvec", "fp4_status_str")
 
 
 class fp4_quant_opts(ctypes.Structure):
@@ -151,8 +161,57 @@ class fp4_kv_attention_args(ctypes.Structure):
     ]
 
 
+class fp4_moe_route_args(ctypes.Structure):
+    _fields_ = [
+        ("size", c_uint32),
+        ("dtype", c_int32),
+        ("flags", c_uint32),
+        ("experts", c_int32),
+        ("top_k", c_int32),
+        ("groups", c_int32),
+        ("top_groups", c_int32),
+        ("group_best", c_int32),
+        ("tokens", c_int64),
+        ("logits", c_void_p),
+        ("ld_logits", c_int64),
+        ("bias", c_void_p),
+        ("weights", c_void_p),
+        ("ids", c_void_p),
+        ("scale", c_float),
+        ("reserved", c_int32),
+    ]
+
+
+class fp4_matvec_args(ctypes.Structure):
+    _fields_ = [
+        ("size", c_uint32),
+        ("format", c_int32),
+        ("x_dtype", c_int32),
+        ("y_dtype", c_int32),
+        ("pairs", c_int64),
+        ("repeat", c_int64),
+        ("N", c_int64),
+        ("K", c_int64),
+        ("x", c_void_p),
+        ("ld_x", c_int64),
+        ("codes", c_void_p),
+        ("ld_codes", c_int64),
+        ("codes_expert_stride", c_int64),
+        ("scales", c_void_p),
+        ("ld_scales", c_int64),
+        ("scales_expert_stride", c_int64),
+        ("tensor_scale", c_void_p),
+        ("experts", c_int64),
+        ("ids", c_void_p),
+        ("y", c_void_p),
+        ("ld_y", c_int64),
+    ]
+
+
 _APPEND_SIZE = ctypes.sizeof(fp4_kv_append_args)
 _ATTENTION_SIZE = ctypes.sizeof(fp4_kv_attention_args)
+_ROUTE_SIZE = ctypes.sizeof(fp4_moe_route_args)
+_MATVEC_SIZE = ctypes.sizeof(fp4_matvec_args)
 
 
 def _packer(args):
@@ -172,6 +231,8 @@ def _packer(args):
 
 _pack_append = _packer(fp4_kv_append_args)
 _pack_attention = _packer(fp4_kv_attention_args)
+_pack_route = _packer(fp4_moe_route_args)
+_pack_matvec = _packer(fp4_matvec_args)
 
 
 class Fp4Error(RuntimeError):
@@ -234,6 +295,29 @@ def lib() -> ctypes.CDLL:
         L.fp4_kv_attention_workspace.argtypes = [ctypes.POINTER(fp4_kv_cache), c_void_p]
         L.fp4_kv_attention.restype = c_int32
         L.fp4_kv_attention.argtypes = [ctypes.POINTER(fp4_kv_cache), c_void_p, c_void_p, c_size_t, c_void_p]
+        L.fp4_moe_route.restype = c_int32
+        L.fp4_moe_route.argtypes = [c_void_p, c_void_p]
+        L.fp4_moe_route_backward.restype = c_int32
+        L.fp4_moe_route_backward.argtypes = [c_void_p, c_void_p, c_void_p, c_int64, c_void_p]
+        L.fp4_moe_group_workspace.restype = c_size_t
+        L.fp4_moe_group_workspace.argtypes = [c_int64, c_int32]
+        L.fp4_moe_group.restype = c_int32
+        L.fp4_moe_group.argtypes = [c_int64, c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
+                                    c_void_p]
+        L.fp4_moe_dispatch.restype = c_int32
+        L.fp4_moe_dispatch.argtypes = [
+            c_int64, c_int32, c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int64, c_void_p,
+            c_int64, c_void_p, c_int64, c_void_p]
+        L.fp4_moe_combine.restype = c_int32
+        L.fp4_moe_combine.argtypes = [
+            c_int32, c_int64, c_int32, c_int64, c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_void_p,
+            c_int64, c_void_p]
+        L.fp4_moe_combine_backward.restype = c_int32
+        L.fp4_moe_combine_backward.argtypes = [
+            c_int32, c_int64, c_int32, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int64, c_void_p, c_void_p,
+            c_void_p, c_void_p, c_int64, c_void_p, c_void_p]
+        L.fp4_matvec.restype = c_int32
+        L.fp4_matvec.argtypes = [c_void_p, c_void_p]
         L.fp4_status_str.restype = c_char_p
         L.fp4_status_str.argtypes = [c_int32]
         _lib = L
@@ -330,6 +414,44 @@ def fp4_kv_attention(cache: fp4_kv_cache, args: fp4_kv_attention_args, workspace
     return lib().fp4_kv_attention(ctypes.byref(cache), ctypes.byref(args), workspace, workspace_bytes, stream)
 
 
+def fp4_moe_route(args: fp4_moe_route_args, stream) -> int:
+    return lib().fp4_moe_route(ctypes.byref(args), stream)
+
+
+def fp4_moe_route_backward(args: fp4_moe_route_args, grad_weights, grad_logits, ld_grad, stream) -> int:
+    return lib().fp4_moe_route_backward(ctypes.byref(args), grad_weights, grad_logits, ld_grad, stream)
+
+
+def fp4_moe_group_workspace(pairs, experts) -> int:
+    return lib().fp4_moe_group_workspace(pairs, experts)
+
+
+def fp4_moe_group(pairs, ids, experts, offsets, order, place, workspace, workspace_bytes, stream) -> int:
+    return lib().fp4_moe_group(pairs, ids, experts, offsets, order, place, workspace, workspace_bytes, stream)
+
+
+def fp4_moe_dispatch(tokens, top_k, place, kept, row_bytes, x, ld_x, rows, ld_rows, row_bytes2, x2, ld_x2, rows2,
+                     ld_rows2, stream) -> int:
+    return lib().fp4_moe_dispatch(tokens, top_k, place, kept, row_bytes, x, ld_x, rows, ld_rows, row_bytes2, x2, ld_x2,
+                                  rows2, ld_rows2, stream)
+
+
+def fp4_moe_combine(dtype, tokens, top_k, width, rows, ld_rows, num_rows, place, kept, weights, out, ld_out,
+                    stream) -> int:
+    return lib().fp4_moe_combine(dtype, tokens, top_k, width, rows, ld_rows, num_rows, place, kept, weights, out,
+                                 ld_out, stream)
+
+
+def fp4_moe_combine_backward(dtype, tokens, top_k, width, grad_out, ld_grad, rows, ld_rows, num_rows, place, kept,
+                             weights, grad_rows, ld_grad_rows, grad_weights, stream) -> int:
+    return lib().fp4_moe_combine_backward(dtype, tokens, top_k, width, grad_out, ld_grad, rows, ld_rows, num_rows,
+                                          place, kept, weights, grad_rows, ld_grad_rows, grad_weights, stream)
+
+
+def fp4_matvec(args: fp4_matvec_args, stream) -> int:
+    return lib().fp4_matvec(ctypes.byref(args), stream)
+
+
 # ---------------------------------------------------------------------------
 # torch conveniences (allocation + current stream only)
 # ---------------------------------------------------------------------------
@@ -386,7 +508,12 @@ def _on_stream(call, device, stream, given, *args, **kw):
     caller = torch.cuda.current_stream(device)
     with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
         result = call(*args, **kw)
-    made = (result.codes, result.scales, result.tensor_scale) if isinstance(result, Quantized) else result
+    if isinstance(result, Quantized):
+        made = (result.codes, result.scales, result.tensor_scale)
+    elif isinstance(result, MoeGroups):
+        made = (result.offsets, result.order, result.place)
+    else:
+        made = result
     for t in made if isinstance(made, tuple) else (made,):
         if t is not None and t is not given:
             t.record_stream(caller)
@@ -879,3 +1006,355 @@ def kv_attention(q, cache: KVCache, block_table, kv_lens, *, q_offsets=None, max
     if st != FP4_OK:
         raise Fp4Error(st, "fp4_kv_attention")
     return (out, lse) if return_lse else out
+
+
+# ---------------------------------------------------------------------------
+# mixture of experts, and products of a few rows
+# ---------------------------------------------------------------------------
+@dataclass
+class MoeGroups:
+    """The (token, expert) pairs of a step sorted by expert, as moe_group
+    makes them: offsets int32 [experts + 1] (what gemm_grouped takes; the last
+    is the number of pairs that have an expert), order int32 [pairs] (the pair,
+    token * top_k + slot, at each row) and place int32 like the ids (the row of
+    each pair). Rows from offsets[-1] on belong to pairs without an expert."""
+    offsets: "torch.Tensor"
+    order: "torch.Tensor"
+    place: "torch.Tensor"
+
+
+def _gpu(t, what):
+    """The index of a tensor's GPU."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{what} must be on a GPU")
+    return index
+
+
+def _raw_stream(index):
+    """torch's current stream on a GPU, as a handle."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _away(index, stream):
+    """Is this GPU, or the stream asked for, not the current one?"""
+    import torch
+    return torch._C._cuda_getDevice() != index or (stream is not None and stream != _raw_stream(index))
+
+
+def _there(call, index, stream, given, *args, **kw):
+    """The call again, with that GPU and stream current."""
+    import torch
+    with torch.cuda.device(index):
+        if stream is None or stream == _raw_stream(index):
+            return call(*args, **kw)
+        return _on_stream(call, torch.device("cuda", index), stream, given, *args, **kw)
+
+
+def _dense(t, index, dtype, shape, what):
+    """Check a contiguous device tensor; returns its address."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor {tuple(shape)} on the same GPU")
+    return t.data_ptr()
+
+
+def _matrix(t, index, what, like=None):
+    """Check a [rows, width] tensor with dense rows; returns its row pitch."""
+    if t.dim() != 2 or t.get_device() != index or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be a [rows, width] tensor with contiguous rows on the same GPU")
+    if like is not None and t.dtype is not like:
+        raise ValueError(f"{what} must be {like}")
+    rows, width = t.shape
+    return t.stride(0) if rows > 1 else width
+
+
+def _route_flags(score, renormalize):
+    if score not in ("softmax", "sigmoid"):
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    return (FP4_MOE_SIGMOID if score == "sigmoid" else 0) | (FP4_MOE_RENORMALIZE if renormalize else 0)
+
+
+def moe_route(logits, top_k, *, score="softmax", bias=None, groups=1, top_groups=None, group_best=1, renormalize=True,
+              scale=1.0, stream=None):
+    """Each token's top_k experts by a router's logits [tokens, experts] (bf16
+    or fp32, any row pitch): (weights fp32, ids int32), both [tokens, top_k],
+    best expert first.
+
+    score: softmax over all experts, or sigmoid. bias (fp32 [experts]) is added
+    to the scores for the choice, not to the weights. groups > 1: experts are
+    chosen from the top_groups of that many groups of consecutive experts,
+    ranked by the sum of their group_best (1 or 2) best choice values.
+    renormalize: weights over their sum; scale multiplies them. Equal values go
+    to the lowest index; an expert whose logit or bias is -inf or NaN is never
+    chosen, slots left over are id -1 with weight 0."""
+    import torch
+    index = _gpu(logits, "logits")
+    if _away(index, stream):
+        return _there(moe_route, index, stream, None, logits, top_k, score=score, bias=bias, groups=groups,
+                      top_groups=top_groups, group_best=group_best, renormalize=renormalize, scale=scale)
+    ld = _matrix(logits, index, "logits")
+    dt = _kv_dtype(logits, "logits")
+    tokens, experts = logits.shape
+    at_bias = 0 if bias is None else _dense(bias, index, torch.float32, (experts,), "bias")
+    weights = logits.new_empty((tokens, top_k), dtype=torch.float32)
+    ids = logits.new_empty((tokens, top_k), dtype=torch.int32)
+    args = _pack_route(_ROUTE_SIZE, dt, _route_flags(score, renormalize), experts, top_k, groups,
+                       groups if top_groups is None else top_groups, group_best, tokens, logits.data_ptr(), ld,
+                       at_bias, weights.data_ptr(), ids.data_ptr(), scale, 0)
+    st = lib().fp4_moe_route(args, _raw_stream(index))
+    if st != FP4_OK:
+        raise Fp4Error(st, "fp4_moe_route")
+    return weights, ids
+
+
+def moe_route_backward(grad_weights, logits, ids, *, score="softmax", renormalize=True, scale=1.0, stream=None):
+    """The gradient of the logits (like logits) from that of moe_route's
+    weights (fp32 [tokens, top_k]), for the ids it chose and the same score,
+    renormalize and scale."""
+    import torch
+    index = _gpu(logits, "logits")
+    if _away(index, stream):
+        return _there(moe_route_backward, index, stream, None, grad_weights, logits, ids, score=score,
+                      renormalize=renormalize, scale=scale)
+    ld = _matrix(logits, index, "logits")
+    dt = _kv_dtype(logits, "logits")
+    tokens, experts = logits.shape
+    if ids.dim() != 2 or ids.shape[0] != tokens:
+        raise ValueError("ids must be [tokens, top_k]")
+    at_ids = _dense(ids, index, torch.int32, ids.shape, "ids")
+    at_grad = _dense(grad_weights, index, torch.float32, ids.shape, "grad_weights")
+    out = torch.empty_like(logits, memory_format=torch.contiguous_format)
+    args = _pack_route(_ROUTE_SIZE, dt, _route_flags(score, renormalize), experts, ids.shape[1], 1, 1, 1, tokens,
+                       logits.data_ptr(), ld, 0, 0, at_ids, scale, 0)
+    st = lib().fp4_moe_route_backward(args, at_grad, out.data_ptr(), experts, _raw_stream(index))
+    if st != FP4_OK:
+        raise Fp4Error(st, "fp4_moe_route_backward")
+    return out
+
+
+def moe_group(ids, experts, *, stream=None) -> MoeGroups:
+    """Sort the pairs of ids (int32 [tokens, top_k] or [pairs], as moe_route
+    gives them) by expert; ids outside [0, experts) belong to none (a GPU that
+    holds experts a to b - 1 passes ids - a and b - a)."""
+    import torch
+    index = _gpu(ids, "ids")
+    if _away(index, stream):
+        return _there(moe_group, index, stream, None, ids, experts)
+    at_ids = _dense(ids, index, torch.int32, ids.shape, "ids")
+    pairs = ids.numel()
+    L = lib()
+    offsets = ids.new_empty((experts + 1 if experts > 0 else 1,))
+    order = ids.new_empty((pairs,))
+    place = torch.empty_like(ids)
+    need = L.fp4_moe_group_workspace(pairs, experts)
+    ws = ids.new_empty((need,), dtype=torch.uint8) if need else None
+    st = L.fp4_moe_group(pairs, at_ids, experts, offsets.data_ptr(), order.data_ptr(), place.data_ptr(),
+                         ws.data_ptr() if need else None, need, _raw_stream(index))
+    if st != FP4_OK:
+        raise Fp4Error(st, "fp4_moe_group")
+    return MoeGroups(offsets, order, place)
+
+
+def _places(groups, tokens, top_k, index):
+    """Addresses of place and of the number of pairs that have an expert."""
+    import torch
+    place, offsets = groups.place, groups.offsets
+    if place.numel() != tokens * top_k:
+        raise ValueError(f"groups of {place.numel()} pairs for {tokens} tokens of {top_k}")
+    at = _dense(place, index, torch.int32, place.shape, "groups.place")
+    _dense(offsets, index, torch.int32, offsets.shape, "groups.offsets")
+    return at, offsets.data_ptr() + 4 * (offsets.numel() - 1)
+
+
+def moe_dispatch(x, groups: MoeGroups, *, stream=None):
+    """The tokens' rows, sorted by expert: row groups.place[t, j] of the result
+    is row t of x [tokens, width] (bf16, fp32, or a Quantized matrix, whose
+    codes and scales are carried as they are). Rows of pairs without an expert
+    are zeros."""
+    import torch
+    packed = isinstance(x, Quantized)
+    first = x.codes if packed else x
+    index = _gpu(first, "x")
+    if _away(index, stream):
+        return _there(moe_dispatch, index, stream, x.tensor_scale if packed else None, x, groups)
+    ld = _matrix(first, index, "x.codes" if packed else "x")
+    tokens, width = first.shape
+    pairs = groups.place.numel()
+    if tokens == 0 or pairs % tokens:
+        if tokens or pairs:
+            raise ValueError(f"groups of {pairs} pairs for {tokens} tokens")
+    top_k = pairs // tokens if tokens else 1
+    at_place, at_kept = _places(groups, tokens, top_k, index)
+    stream = _raw_stream(index)
+    if packed:
+        blocks = x.scales.shape[-1]
+        ld2 = _matrix(x.scales, index, "x.scales", torch.uint8)
+        if x.scales.shape[0] != tokens:
+            raise ValueError("codes and scales do not match")
+        ld_out, ld_out2 = code_pitch(width), scale_pitch(blocks)
+        rows = first.new_empty((pairs, ld_out))[:, :width]
+        scales = first.new_empty((pairs, ld_out2))[:, :blocks]
+        st = fp4_moe_dispatch(tokens, max(top_k, 1), at_place, at_kept, width, first.data_ptr(), ld, rows.data_ptr(),
+                              ld_out, blocks, x.scales.data_ptr(), ld2, scales.data_ptr(), ld_out2, stream)
+    else:
+        _kv_dtype(x, "x")
+        es = x.element_size()
+        rows = x.new_empty((pairs, width))
+        st = fp4_moe_dispatch(tokens, max(top_k, 1), at_place, at_kept, width * es, x.data_ptr(), ld * es,
+                              rows.data_ptr(), width * es, 0, None, 0, None, 0, stream)
+    _check(st, "fp4_moe_dispatch")
+    return Quantized(x.fmt, rows, scales, x.tensor_scale) if packed else rows
+
+
+def _combine_rows(rows, weights, groups, tokens, index):
+    """Check the operands both directions share: rows as a matrix, its pitch,
+    top_k and the addresses of weights, places and the number kept."""
+    import torch
+    if rows.dim() == 3:
+        rows = rows.flatten(0, 1)
+    ld = _matrix(rows, index, "rows")
+    at_place = at_kept = at_w = 0
+    if weights is not None:
+        if weights.dim() != 2:
+            raise ValueError("weights must be [tokens, top_k]")
+        tokens, top_k = weights.shape
+        at_w = _dense(weights, index, torch.float32, weights.shape, "weights")
+    elif groups is not None and groups.place.dim() == 2:
+        tokens, top_k = groups.place.shape
+    elif tokens is not None:
+        top_k = (rows.shape[0] if groups is None else groups.place.numel()) // max(tokens, 1)
+    else:
+        raise ValueError("weights, or the ids' shape in groups, must give tokens and top_k")
+    if groups is not None:
+        at_place, at_kept = _places(groups, tokens, top_k, index)
+    elif rows.shape[0] != tokens * top_k:
+        raise ValueError(f"{rows.shape[0]} rows for {tokens} tokens of {top_k}")
+    return rows, ld, tokens, top_k, at_w, at_place, at_kept
+
+
+def moe_combine(rows, weights=None, groups: Optional[MoeGroups] = None, *, out=None, stream=None):
+    """The experts' rows (bf16 or fp32) back to their tokens, times weights
+    (fp32 [tokens, top_k]; None: 1) and summed in fp32: [tokens, width].
+    groups: rows are sorted by expert, as moe_dispatch and gemm_grouped leave
+    them; without, they are [tokens, top_k, width] or [pairs, width] in the
+    pairs' order, as matvec leaves them. Rows of pairs without an expert have no
+    part. moe_combine(grad_rows, None, groups) is moe_dispatch's backward."""
+    index = _gpu(rows, "rows")
+    if _away(index, stream):
+        return _there(moe_combine, index, stream, out, rows, weights, groups, out=out)
+    dt = _kv_dtype(rows, "rows")
+    tokens = rows.shape[0] if rows.dim() == 3 and groups is None else None
+    rows, ld, tokens, top_k, at_w, at_place, at_kept = _combine_rows(rows, weights, groups, tokens, index)
+    width = rows.shape[1]
+    if out is None:
+        out = rows.new_empty((tokens, width))
+        ld_out = width
+    else:
+        ld_out = _matrix(out, index, "out", rows.dtype)
+        if out.shape != (tokens, width):
+            raise ValueError(f"out must be [{tokens}, {width}]")
+    st = fp4_moe_combine(dt, tokens, max(top_k, 1), width, rows.data_ptr(), ld, rows.shape[0], at_place, at_kept, at_w,
+                         out.data_ptr(), ld_out, _raw_stream(index))
+    _check(st, "fp4_moe_combine")
+    return out
+
+
+def moe_combine_backward(grad_out, rows, weights=None, groups: Optional[MoeGroups] = None, *, stream=None):
+    """(grad_rows, grad_weights) of moe_combine from the gradient of its result
+    [tokens, width]; grad_rows like rows (zeros where a pair has no expert),
+    grad_weights fp32 like weights, None without weights."""
+    import torch
+    index = _gpu(rows, "rows")
+    if _away(index, stream):
+        return _there(moe_combine_backward, index, stream, None, grad_out, rows, weights, groups)
+    dt = _kv_dtype(rows, "rows")
+    ld_grad = _matrix(grad_out, index, "grad_out", rows.dtype)
+    shape = rows.shape
+    rows, ld, tokens, top_k, at_w, at_place, at_kept = _combine_rows(rows, weights, groups, grad_out.shape[0], index)
+    width = rows.shape[1]
+    if grad_out.shape != (tokens, width):
+        raise ValueError(f"grad_out must be [{tokens}, {width}]")
+    if groups is not None and rows.shape[0] != tokens * top_k:
+        raise ValueError(f"{rows.shape[0]} rows for {tokens} tokens of {top_k}")
+    grad_rows = rows.new_empty(shape)
+    grad_w = None if weights is None else torch.empty_like(weights)
+    st = fp4_moe_combine_backward(dt, tokens, max(top_k, 1), width, grad_out.data_ptr(), ld_grad, rows.data_ptr(), ld,
+                                  rows.shape[0], at_place, at_kept, at_w, grad_rows.data_ptr(), width,
+                                  grad_w.data_ptr() if grad_w is not None else None, _raw_stream(index))
+    _check(st, "fp4_moe_combine_backward")
+    return grad_rows, grad_w
+
+
+def matvec(x, w: Quantized, ids=None, *, out_dtype=None, out=None, stream=None):
+    """A few rows times 4-bit weights, x @ deq(w)^T, with x (bf16 or fp32) as it
+    is: the linear layer of a decoder's step.
+
+    Without ids: x [rows, K] (or [K]) and w [N, K] -> [rows, N] (or [N]). With
+    ids (int32 [tokens, top_k], as moe_route gives them) and w [experts, N, K]:
+    x [tokens, K], each row to all its experts, or [tokens, top_k, K] (or
+    [tokens * top_k, K]), a row for each pair -> [tokens, top_k, N]; an id
+    outside [0, experts) gives zeros.
+    Also ids [rows] with x [rows, K] -> [rows, N]. The result has x's dtype
+    unless out_dtype (or out) says otherwise."""
+    import torch
+    index = _gpu(x, "x")
+    if _away(index, stream):
+        return _there(matvec, index, stream, out, x, w, ids, out_dtype=out_dtype, out=out)
+    xt = _kv_dtype(x, "x")
+    codes, scales = w.codes, w.scales
+    cs, ss = codes.shape, scales.shape
+    K = x.shape[-1]
+    if len(cs) == 2:
+        experts, N, ces, ses = 1, cs[0], 0, 0
+    else:
+        experts, N, ces, ses = cs[0], cs[1], codes.stride(0), scales.stride(0)
+    if cs[-1] * 2 != K or ss[:-1] != cs[:-1] or ss[-1] * w.block != K:
+        raise ValueError(f"weights {tuple(w.shape)} do not match rows of {K}")
+    if codes.get_device() != index or scales.get_device() != index:
+        raise ValueError("weights must be on the same GPU")
+    if codes.stride(-1) != 1 or (scales.stride(-1) != 1 and ss[-1] > 1):
+        raise ValueError("code and scale rows must be contiguous")
+    at_ids, repeat = 0, 1
+    lead = x.shape[:-1]
+    if ids is None:
+        if experts != 1:
+            raise ValueError("ids must say which of the matrices each row takes")
+        if len(lead) > 1:
+            raise ValueError("x must be [rows, K]")
+    else:
+        at_ids = _dense(ids, index, torch.int32, ids.shape, "ids")
+        if ids.dim() == 2 and len(lead) == 1 and ids.shape[0] == lead[0]:
+            repeat = ids.shape[1]
+        elif ids.shape != lead and (len(lead) != 1 or ids.numel() != lead[0]):
+            raise ValueError("x must be [tokens, K] or [tokens, top_k, K] for ids [tokens, top_k]")
+        lead = ids.shape
+    flat = x if x.dim() == 2 else x.reshape(-1, K)
+    ld, es = flat.stride(0) if flat.shape[0] > 1 else K, x.element_size()
+    if (K > 1 and flat.stride(1) != 1) or ld < K or (ld * es) % 16 or flat.data_ptr() % 16:
+        flat = flat.clone(memory_format=torch.contiguous_format)
+        ld = K
+    pairs = 1
+    for n in lead:
+        pairs *= n
+    if out is None:
+        out = x.new_empty((*lead, N), dtype=out_dtype or x.dtype)
+        ld_y = N
+    else:
+        if out.shape != (*lead, N) or out.get_device() != index or (out_dtype or out.dtype) is not out.dtype:
+            raise ValueError(f"out must be {(*lead, N)} on the same GPU")
+        rows = out.view(-1, N)
+        ld_y = rows.stride(0) if pairs > 1 else N
+        if N > 1 and rows.stride(1) != 1:
+            raise ValueError("out rows must be contiguous")
+    ts = w.tensor_scale
+    at_ts = 0
+    if w.fmt == FP4_NVFP4:
+        at_ts = _dense(ts, index, torch.float32, (experts,), "tensor_scale")
+    args = _pack_matvec(_MATVEC_SIZE, w.fmt, xt, _kv_dtype(out, "out"), pairs, max(repeat, 1), N, K, flat.data_ptr(), ld,
+                        codes.data_ptr(), codes.stride(-2), ces, scales.data_ptr(), scales.stride(-2), ses, at_ts,
+                        experts, at_ids, out.data_ptr(), ld_y)
+    st = lib().fp4_matvec(args, _raw_stream(index))
+    if st != FP4_OK:
+        raise Fp4Error(st, "fp4_matvec")
+    return out

@@ -22,7 +22,8 @@ INCLUDE = REPO_DIR / "include"
 BUILD_DIR = REPO_DIR / "_build"
 LIB_PATH = PKG_DIR / "libfp4.so"
 
-SOURCES = ["fp4_api.cpp", "quantize.hip", "dequantize.hip", "gemm.hip", "kv_cache.hip", "kv_attention.hip"]
+SOURCES = ["fp4_api.cpp", "quantize.hip", "dequantize.hip", "gemm.hip", "kv_cache.hip", "kv_attention.hip",
+           "moe_route.hip", "moe_rows.hip", "matvec.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

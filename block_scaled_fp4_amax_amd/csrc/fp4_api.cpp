@@ -750,3 +750,278 @@ fp4_status fp4_kv_attention(const fp4_kv_cache* cache, const fp4_kv_attention_ar
 }
 
 }  // extern "C"
+
+namespace {
+
+// Routed layers: what a launch's first grid dimension and 32-bit places hold.
+constexpr int64_t kMaxRouteTokens = int64_t(1) << 26;
+constexpr int64_t kMaxPairs = int64_t(1) << 24;
+constexpr int kMaxTopK = 1024;
+
+// Sizes and options of a router's call.
+fp4_status plan_moe_route(const fp4_moe_route_args* r, RouteArgs* a) {
+  if (!r || r->size != sizeof(fp4_moe_route_args) || r->reserved != 0) return FP4_ERR_INVALID;
+  if (r->dtype != FP4_F32 && r->dtype != FP4_BF16) return FP4_ERR_INVALID;
+  if (r->flags & ~(uint32_t)(FP4_MOE_SIGMOID | FP4_MOE_RENORMALIZE)) return FP4_ERR_INVALID;
+  if (r->tokens < 0 || r->experts < 1 || r->top_k < 1 || r->top_k > r->experts) return FP4_ERR_INVALID;
+  if (r->experts > 1024 || r->top_k > 32) return FP4_ERR_UNSUPPORTED;
+  if (r->groups < 1 || r->experts % r->groups != 0 || r->top_groups < 1 || r->top_groups > r->groups)
+    return FP4_ERR_INVALID;
+  if (r->groups > 64) return FP4_ERR_UNSUPPORTED;
+  if (r->group_best != 1 && r->group_best != 2) return FP4_ERR_INVALID;
+  if (!finite(r->scale)) return FP4_ERR_INVALID;
+  if (r->tokens >= kMaxRouteTokens) return FP4_ERR_UNSUPPORTED;
+  if (r->tokens > 0) {
+    if (!r->logits || !r->ids || r->ld_logits < r->experts) return FP4_ERR_INVALID;
+    if (!aligned(r->logits, r->dtype == FP4_BF16 ? 2 : 4) || !aligned(r->ids, 4) || !aligned(r->bias, 4))
+      return FP4_ERR_ALIGN;
+  }
+  a->bf16 = r->dtype == FP4_BF16;
+  a->sigmoid = (r->flags & FP4_MOE_SIGMOID) != 0;
+  a->renormalize = (r->flags & FP4_MOE_RENORMALIZE) != 0;
+  a->tokens = r->tokens;
+  a->ld = r->ld_logits;
+  a->experts = r->experts;
+  a->top_k = r->top_k;
+  a->groups = r->groups;
+  a->group_size = r->experts / r->groups;
+  a->top_groups = r->top_groups;
+  a->best = r->group_best;
+  a->scale = r->scale;
+  a->logits = r->logits;
+  a->bias = r->bias;
+  a->weights = r->weights;
+  a->ids = r->ids;
+  return FP4_OK;
+}
+
+fp4_status status_of(hipError_t e) { return e == hipSuccess ? FP4_OK : FP4_ERR_HIP; }
+
+}  // namespace
+
+extern "C" {
+
+fp4_status fp4_moe_route(const fp4_moe_route_args* args, void* stream) {
+  RouteArgs a{};
+  fp4_status st = plan_moe_route(args, &a);
+  if (st != FP4_OK) return st;
+  if (args->tokens == 0) return FP4_OK;
+  if (!args->weights) return FP4_ERR_INVALID;
+  if (!aligned(args->weights, 4)) return FP4_ERR_ALIGN;
+  st = check_device();
+  if (st != FP4_OK) return st;
+  (void)hipGetLastError();
+  return status_of(launch_moe_route(a, static_cast<hipStream_t>(stream)));
+}
+
+fp4_status fp4_moe_route_backward(const fp4_moe_route_args* args, const float* grad_weights, void* grad_logits,
+                                  int64_t ld_grad, void* stream) {
+  RouteBackwardArgs b{};
+  fp4_status st = plan_moe_route(args, &b.a);
+  if (st != FP4_OK) return st;
+  if (args->tokens == 0) return FP4_OK;
+  if (!grad_weights || !grad_logits || ld_grad < args->experts) return FP4_ERR_INVALID;
+  if (!aligned(grad_weights, 4) || !aligned(grad_logits, args->dtype == FP4_BF16 ? 2 : 4)) return FP4_ERR_ALIGN;
+  st = check_device();
+  if (st != FP4_OK) return st;
+  // (the choice is made: only the lanes' share of the row depends on the groups)
+  b.a.groups = b.a.top_groups = 1;
+  b.grad = grad_weights;
+  b.out = grad_logits;
+  b.ld_out = ld_grad;
+  (void)hipGetLastError();
+  return status_of(launch_moe_route_backward(b, static_cast<hipStream_t>(stream)));
+}
+
+size_t fp4_moe_group_workspace(int64_t pairs, int32_t experts) {
+  if (pairs < 0 || pairs > kMaxPairs || experts < 1 || experts > 1024) return 0;
+  const int64_t blocks = moe_group_blocks(pairs);
+  return blocks > 1 ? (size_t)blocks * (size_t)(experts + 1) * sizeof(uint32_t) : 0;
+}
+
+fp4_status fp4_moe_group(int64_t pairs, const int32_t* ids, int32_t experts, int32_t* offsets, int32_t* order,
+                         int32_t* place, void* workspace, size_t workspace_bytes, void* stream) {
+  if (pairs < 0 || experts < 1) return FP4_ERR_INVALID;
+  if (pairs > kMaxPairs || experts > 1024) return FP4_ERR_UNSUPPORTED;
+  if (!offsets || (pairs > 0 && (!ids || !order || !place))) return FP4_ERR_INVALID;
+  if (!aligned(ids, 4) || !aligned(offsets, 4) || !aligned(order, 4) || !aligned(place, 4)) return FP4_ERR_ALIGN;
+  const size_t need = fp4_moe_group_workspace(pairs, experts);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return FP4_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return FP4_ERR_ALIGN;
+  }
+  fp4_status st = check_device();
+  if (st != FP4_OK) return st;
+  GroupArgs a{};
+  a.pairs = pairs;
+  a.experts = experts;
+  a.ids = ids;
+  a.offsets = offsets;
+  a.order = order;
+  a.place = place;
+  a.counts = static_cast<uint32_t*>(workspace);
+  (void)hipGetLastError();
+  return status_of(launch_moe_group(a, static_cast<hipStream_t>(stream)));
+}
+
+fp4_status fp4_moe_dispatch(int64_t tokens, int32_t top_k, const int32_t* place, const int32_t* kept,
+                            int64_t row_bytes, const void* x, int64_t ld_x, void* rows, int64_t ld_rows,
+                            int64_t row_bytes2, const void* x2, int64_t ld_x2, void* rows2, int64_t ld_rows2,
+                            void* stream) {
+  if (tokens < 0 || top_k < 1 || row_bytes < 0 || row_bytes2 < 0) return FP4_ERR_INVALID;
+  if (top_k > kMaxTopK || tokens >= kMaxPairs) return FP4_ERR_UNSUPPORTED;
+  if (tokens == 0 || (row_bytes == 0 && row_bytes2 == 0)) return FP4_OK;
+  if (!place) return FP4_ERR_INVALID;
+  if (row_bytes > 0 && (!x || !rows || ld_x < row_bytes || ld_rows < row_bytes)) return FP4_ERR_INVALID;
+  if (row_bytes2 > 0 && (!x2 || !rows2 || ld_x2 < row_bytes2 || ld_rows2 < row_bytes2)) return FP4_ERR_INVALID;
+  if (!aligned(place, 4) || !aligned(kept, 4)) return FP4_ERR_ALIGN;
+  fp4_status st = check_device();
+  if (st != FP4_OK) return st;
+  DispatchArgs a{};
+  a.tokens = tokens;
+  a.top_k = top_k;
+  a.place = place;
+  a.kept = kept;
+  a.x = static_cast<const uint8_t*>(x);
+  a.rows = static_cast<uint8_t*>(rows);
+  a.bytes = row_bytes;
+  a.ld_x = ld_x;
+  a.ld_rows = ld_rows;
+  a.x2 = static_cast<const uint8_t*>(x2);
+  a.rows2 = static_cast<uint8_t*>(rows2);
+  a.bytes2 = row_bytes2;
+  a.ld_x2 = ld_x2;
+  a.ld_rows2 = ld_rows2;
+  (void)hipGetLastError();
+  return status_of(launch_moe_dispatch(a, static_cast<hipStream_t>(stream)));
+}
+
+// Checks of the combining calls that both share.
+static fp4_status plan_moe_combine(int32_t dtype, int64_t tokens, int32_t top_k, int64_t width, const void* rows,
+                                   int64_t ld_rows, int64_t num_rows, const int32_t* place, const int32_t* kept,
+                                   const float* weights, CombineArgs* a) {
+  if (dtype != FP4_F32 && dtype != FP4_BF16) return FP4_ERR_INVALID;
+  if (tokens < 0 || top_k < 1 || width < 0 || num_rows < 0) return FP4_ERR_INVALID;
+  if (top_k > kMaxTopK || tokens >= kMaxPairs || width > kMaxPairs) return FP4_ERR_UNSUPPORTED;
+  if (tokens == 0 || width == 0) return FP4_OK;
+  if (rows && ld_rows < width) return FP4_ERR_INVALID;
+  if (!aligned(rows, dtype == FP4_BF16 ? 2 : 4) || !aligned(place, 4) || !aligned(kept, 4) || !aligned(weights, 4))
+    return FP4_ERR_ALIGN;
+  a->bf16 = dtype == FP4_BF16;
+  a->tokens = tokens;
+  a->top_k = top_k;
+  a->width = width;
+  a->rows = rows;
+  a->ld_rows = ld_rows;
+  a->num_rows = num_rows;
+  a->place = place;
+  a->kept = kept;
+  a->weights = weights;
+  return FP4_OK;
+}
+
+// Rows of whole 16-byte pieces?
+static bool whole_pieces(const void* p, int64_t ld, int64_t width, int64_t esize) {
+  return aligned(p, 16) && (ld * esize) % 16 == 0 && (width * esize) % 16 == 0;
+}
+
+fp4_status fp4_moe_combine(int32_t dtype, int64_t tokens, int32_t top_k, int64_t width, const void* rows,
+                           int64_t ld_rows, int64_t num_rows, const int32_t* place, const int32_t* kept,
+                           const float* weights, void* out, int64_t ld_out, void* stream) {
+  CombineArgs a{};
+  fp4_status st = plan_moe_combine(dtype, tokens, top_k, width, rows, ld_rows, num_rows, place, kept, weights, &a);
+  if (st != FP4_OK) return st;
+  if (tokens == 0 || width == 0) return FP4_OK;
+  if ((!rows && num_rows > 0) || !out || ld_out < width) return FP4_ERR_INVALID;
+  const int64_t es = a.bf16 ? 2 : 4;
+  if (!aligned(out, (uintptr_t)es)) return FP4_ERR_ALIGN;
+  st = check_device();
+  if (st != FP4_OK) return st;
+  a.out = out;
+  a.ld_out = ld_out;
+  a.vec_ok = whole_pieces(rows, ld_rows, width, es) && whole_pieces(out, ld_out, width, es);
+  (void)hipGetLastError();
+  return status_of(launch_moe_combine(a, static_cast<hipStream_t>(stream)));
+}
+
+fp4_status fp4_moe_combine_backward(int32_t dtype, int64_t tokens, int32_t top_k, int64_t width,
+                                    const void* grad_out, int64_t ld_grad, const void* rows, int64_t ld_rows,
+                                    int64_t num_rows, const int32_t* place, const int32_t* kept, const float* weights,
+                                    void* grad_rows, int64_t ld_grad_rows, float* grad_weights, void* stream) {
+  CombineBackwardArgs b{};
+  fp4_status st = plan_moe_combine(dtype, tokens, top_k, width, rows, ld_rows, num_rows, place, kept, weights, &b.a);
+  if (st != FP4_OK) return st;
+  if (tokens == 0 || width == 0) return FP4_OK;
+  if (tokens * top_k >= kMaxPairs) return FP4_ERR_UNSUPPORTED;
+  if (!grad_out || ld_grad < width || (num_rows > 0 && (!grad_rows || ld_grad_rows < width))) return FP4_ERR_INVALID;
+  if (grad_weights && !rows && num_rows > 0) return FP4_ERR_INVALID;
+  const int64_t es = b.a.bf16 ? 2 : 4;
+  if (!aligned(grad_out, (uintptr_t)es) || !aligned(grad_rows, (uintptr_t)es) || !aligned(grad_weights, 4))
+    return FP4_ERR_ALIGN;
+  st = check_device();
+  if (st != FP4_OK) return st;
+  b.grad = grad_out;
+  b.ld_grad = ld_grad;
+  b.grad_rows = grad_rows;
+  b.ld_grad_rows = ld_grad_rows;
+  b.grad_weights = grad_weights;
+  b.a.vec_ok = whole_pieces(grad_out, ld_grad, width, es) && whole_pieces(grad_rows, ld_grad_rows, width, es) &&
+               (!grad_weights || whole_pieces(rows, ld_rows, width, es));
+  (void)hipGetLastError();
+  return status_of(launch_moe_combine_backward(b, static_cast<hipStream_t>(stream)));
+}
+
+fp4_status fp4_matvec(const fp4_matvec_args* m, void* stream) {
+  if (!m || m->size != sizeof(fp4_matvec_args)) return FP4_ERR_INVALID;
+  if (m->format != FP4_MXFP4 && m->format != FP4_NVFP4) return FP4_ERR_INVALID;
+  if ((m->x_dtype != FP4_F32 && m->x_dtype != FP4_BF16) || (m->y_dtype != FP4_F32 && m->y_dtype != FP4_BF16))
+    return FP4_ERR_INVALID;
+  const bool nv = m->format == FP4_NVFP4;
+  const int64_t blk = nv ? 16 : 32;
+  if (m->pairs < 0 || m->repeat < 1 || m->N < 0 || m->K < 0 || m->K % blk != 0 || m->experts < 1) return FP4_ERR_INVALID;
+  if (m->experts > 4096 || m->K > (int64_t(1) << 30) || m->N > (int64_t(1) << 31) - 1) return FP4_ERR_UNSUPPORTED;
+  // (tiles of rows are counted in 32 bits, work items along x in 32 bits too)
+  if (m->pairs > (int64_t(1) << 30) || (m->N + 15) / 16 > kMaxItemsX / 512) return FP4_ERR_UNSUPPORTED;
+  if (m->ids && m->pairs > 4096) return FP4_ERR_UNSUPPORTED;
+  if (m->pairs == 0 || m->N == 0) return FP4_OK;
+  if (!m->y || m->ld_y < m->N) return FP4_ERR_INVALID;
+  if (m->K > 0 && (!m->x || !m->codes || !m->scales)) return FP4_ERR_INVALID;
+  if (nv && !m->tensor_scale) return FP4_ERR_INVALID;
+  if (m->ld_x < m->K || m->ld_codes < m->K / 2 || m->ld_scales < m->K / blk) return FP4_ERR_INVALID;
+  if (m->experts > 1 && (m->codes_expert_stride < 0 || m->scales_expert_stride < 0)) return FP4_ERR_INVALID;
+  const int64_t es = m->x_dtype == FP4_BF16 ? 2 : 4;
+  if (!aligned(m->x, 16) || (m->ld_x * es) % 16 != 0) return FP4_ERR_ALIGN;
+  if (!aligned(m->codes, 16) || m->ld_codes % 16 != 0 || (m->experts > 1 && m->codes_expert_stride % 16 != 0))
+    return FP4_ERR_ALIGN;
+  if (nv && (!aligned(m->scales, 2) || m->ld_scales % 2 != 0 || (m->experts > 1 && m->scales_expert_stride % 2 != 0)))
+    return FP4_ERR_ALIGN;
+  if ((nv && !aligned(m->tensor_scale, 4)) || !aligned(m->ids, 4) || !aligned(m->y, m->y_dtype == FP4_BF16 ? 2 : 4))
+    return FP4_ERR_ALIGN;
+  fp4_status st = check_device();
+  if (st != FP4_OK) return st;
+  MatvecArgs a{};
+  a.nvfp4 = nv;
+  a.x_bf16 = m->x_dtype == FP4_BF16;
+  a.y_bf16 = m->y_dtype == FP4_BF16;
+  a.pairs = m->pairs;
+  a.repeat = m->repeat;
+  a.N = m->N;
+  a.K = m->K;
+  a.x = m->x;
+  a.ld_x = m->ld_x;
+  a.codes = m->codes;
+  a.ld_c = m->ld_codes;
+  a.c_es = m->experts > 1 ? m->codes_expert_stride : 0;
+  a.scales = m->scales;
+  a.ld_s = m->ld_scales;
+  a.s_es = m->experts > 1 ? m->scales_expert_stride : 0;
+  a.ts = m->tensor_scale;
+  a.experts = (int)m->experts;
+  a.ids = m->ids;
+  a.y = m->y;
+  a.ld_y = m->ld_y;
+  (void)hipGetLastError();
+  return status_of(launch_matvec(a, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -173,6 +173,94 @@ struct KvAttnPlan {
 KvAttnPlan plan_kv_attention(const KvAttnArgs& a);
 hipError_t launch_kv_attention(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t stream);
 
+struct RouteArgs {
+  bool bf16, sigmoid, renormalize;
+  int64_t tokens, ld;  // ld: elements
+  int experts, top_k, groups, group_size, top_groups, best;
+  float scale;
+  const void* logits;
+  const float* bias;
+  float* weights;
+  int32_t* ids;  // read by the backward pass
+};
+
+struct RouteBackwardArgs {
+  RouteArgs a;
+  const float* grad;  // [tokens][top_k]
+  void* out;
+  int64_t ld_out;
+};
+
+hipError_t launch_moe_route(const RouteArgs& a, hipStream_t stream);
+hipError_t launch_moe_route_backward(const RouteBackwardArgs& b, hipStream_t stream);
+
+struct GroupArgs {
+  int64_t pairs;
+  int experts, id_bits;  // id_bits: of `experts`, the bucket of pairs without an expert
+  const int32_t* ids;
+  int32_t *offsets, *order, *place;
+  uint32_t* counts;  // workspace [workgroups][experts + 1] where there are several
+};
+
+// Workgroups of the sort, and whether it needs its workspace (more than one).
+int64_t moe_group_blocks(int64_t pairs);
+hipError_t launch_moe_group(GroupArgs a, hipStream_t stream);
+
+struct DispatchArgs {
+  int64_t tokens;
+  int top_k;
+  const int32_t *place, *kept;  // kept NULL: all rows
+  const uint8_t* x;
+  uint8_t* rows;
+  int64_t bytes, ld_x, ld_rows;
+  const uint8_t* x2;  // a second plane of bytes per row (bytes2 = 0: none)
+  uint8_t* rows2;
+  int64_t bytes2, ld_x2, ld_rows2;
+};
+
+hipError_t launch_moe_dispatch(const DispatchArgs& a, hipStream_t stream);
+
+struct CombineArgs {
+  bool bf16, vec_ok;  // vec_ok: every row in whole 16-byte pieces
+  int64_t tokens, width, num_rows;
+  int top_k;
+  const int32_t *place, *kept;  // NULL: row p, all rows
+  const float* weights;         // NULL: 1
+  const void* rows;
+  void* out;
+  int64_t ld_rows, ld_out;  // elements
+};
+
+struct CombineBackwardArgs {
+  CombineArgs a;
+  const void* grad;
+  void* grad_rows;
+  float* grad_weights;  // NULL: not asked for
+  int64_t ld_grad, ld_grad_rows;
+};
+
+hipError_t launch_moe_combine(const CombineArgs& a, hipStream_t stream);
+hipError_t launch_moe_combine_backward(const CombineBackwardArgs& b, hipStream_t stream);
+
+struct MatvecArgs {
+  bool nvfp4, x_bf16, y_bf16;
+  int64_t pairs, repeat;  // row p of y belongs to row p / repeat of x
+  int64_t N, K;
+  const void* x;
+  int64_t ld_x;  // elements
+  const uint8_t* codes;
+  int64_t ld_c, c_es;  // row pitch, and from one expert to the next, bytes
+  const uint8_t* scales;
+  int64_t ld_s, s_es;
+  const float* ts;     // [experts]
+  int experts;
+  const int32_t* ids;  // [pairs], NULL: expert 0 for all
+  void* y;
+  int64_t ld_y;
+};
+
+hipError_t launch_matvec(const MatvecArgs& a, hipStream_t stream);
+
 // Compute units of the current device (cached per device).
 int device_cu_count();
 

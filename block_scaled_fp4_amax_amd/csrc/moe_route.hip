@@ -1,0 +1,528 @@
+// moe_route.hip -- a router's scores to each token's experts and weights, and
+// the gradient of the scores.
+//
+//   s_e = softmax(l)_e or 1 / (1 + exp(-l_e)); choice c_e = s_e + b_e; the k
+//   largest c (within the top groups of consecutive experts, if limited), ties
+//   to the lowest index; w_j = scale * s_ij, over their sum if renormalized.
+//
+// L lanes (a DPP row of 16, or a wave) hold one token's E logits, VPL
+// consecutive ones a lane, so that every reduction stays inside the row and a
+// wave serves 64 / L tokens. A candidate is one double: the fp32 value with
+// its expert's index in the mantissa's lowest bits (a float leaves 29 of them
+// zero), turned so that the larger double is the better candidate and, of
+// equal values, the lower index: one v_max_f64 compares both.
+//
+// The choice is that of the exact numbers. Without a bias the order of the
+// scores is that of the logits, which are compared as they are. With one (or
+// where a group's rank is a sum of two scores) c is computed in fp32 with a
+// known error; where two neighbours of the resulting order lie within it, the
+// row is done again in double (a few rows in a thousand).
+#include <float.h>
+
+#include "fp4_device.h"
+#include "launch.h"
+
+namespace fp4impl {
+using namespace fp4dev;
+
+namespace {
+
+constexpr double kNone = -DBL_MAX;  // key of an expert that may not be chosen
+constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596303e-8f, kLn2 = 0.693147182f;
+
+__device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
+
+// exp(x) to about an ulp for x <= 88: 2^(x log2 e) by the hardware, and a
+// first-order term for what the product's rounding lost.
+__device__ __forceinline__ float exp_near(float x) {
+  x = x < -200.0f ? -200.0f : x;  // (NaN passes)
+  const float hi = x * kLog2e;
+  const float lo = __builtin_fmaf(x, kLog2e, -hi) + x * kLog2eLow;
+  const float r = __builtin_amdgcn_exp2f(hi);
+  return __builtin_fmaf(r * lo, kLn2, r);
+}
+
+// value of lane ^ MASK within rows of 16 lanes (mirrors: the lanes they bring
+// together differ in every lower bit too, which a reduction does not mind)
+template <int STEP>
+__device__ __forceinline__ int row_move(int x) {
+  if constexpr (STEP == 1) return __builtin_amdgcn_mov_dpp(x, 0xB1, 0xF, 0xF, true);        // quad_perm [1, 0, 3, 2]
+  else if constexpr (STEP == 2) return __builtin_amdgcn_mov_dpp(x, 0x4E, 0xF, 0xF, true);   // quad_perm [2, 3, 0, 1]
+  else if constexpr (STEP == 4) return __builtin_amdgcn_mov_dpp(x, 0x141, 0xF, 0xF, true);  // row_half_mirror
+  else if constexpr (STEP == 8) return __builtin_amdgcn_mov_dpp(x, 0x140, 0xF, 0xF, true);  // row_mirror
+  else return __shfl_xor(x, STEP, 64);
+}
+template <int STEP>
+__device__ __forceinline__ float move(float v) {
+  return __builtin_bit_cast(float, row_move<STEP>(__builtin_bit_cast(int, v)));
+}
+template <int STEP>
+__device__ __forceinline__ double move(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)row_move<STEP>((int)(uint32_t)u), hi = (uint32_t)row_move<STEP>((int)(uint32_t)(u >> 32));
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+struct Max {
+  __device__ __forceinline__ float operator()(float a, float b) const { return __builtin_fmaxf(a, b); }
+  __device__ __forceinline__ double operator()(double a, double b) const { return __builtin_fmax(a, b); }
+};
+struct Min {
+  __device__ __forceinline__ float operator()(float a, float b) const { return __builtin_fminf(a, b); }
+  __device__ __forceinline__ double operator()(double a, double b) const { return __builtin_fmin(a, b); }
+};
+struct Add {
+  template <typename T>
+  __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
+};
+
+// over the token's L lanes; every lane gets the result
+template <int L, typename OP, typename T>
+__device__ __forceinline__ T reduce(T v, OP op) {
+  v = op(v, move<1>(v));
+  v = op(v, move<2>(v));
+  v = op(v, move<4>(v));
+  v = op(v, move<8>(v));
+  if constexpr (L == 64) {
+    v = op(v, move<16>(v));
+    v = op(v, move<32>(v));
+  }
+  return v;
+}
+
+template <int L>
+__device__ __forceinline__ float from_lane(float v, int i) { return __shfl(v, i, L); }
+template <int L>
+__device__ __forceinline__ double from_lane(double v, int i) { return __shfl(v, i, L); }
+
+__device__ __forceinline__ double make_key(float v, int e) {
+  // (-0 and +0 are equal logits; +inf and the index would make a NaN)
+  const double d = v == __builtin_inff() ? 0x1p200 : (double)(v + 0.0f);
+  uint64_t u = __builtin_bit_cast(uint64_t, d);
+  const uint32_t turn = (int64_t)u < 0 ? 0u : 1023u;
+  return __builtin_bit_cast(double, u | ((uint32_t)e ^ turn));
+}
+__device__ __forceinline__ int key_index(double k) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, k);
+  return (int)(((uint32_t)u & 1023u) ^ ((int64_t)u < 0 ? 0u : 1023u));
+}
+__device__ __forceinline__ float key_value(double k) {
+  return (float)__builtin_bit_cast(double, __builtin_bit_cast(uint64_t, k) & ~(uint64_t)1023);
+}
+
+__device__ __forceinline__ float load_logit(const RouteArgs& a, const void* row, int e) {
+  return a.bf16 ? bf16_lo(reinterpret_cast<const uint16_t*>(row)[e]) : reinterpret_cast<const float*>(row)[e];
+}
+
+__device__ __forceinline__ const void* logit_row(const RouteArgs& a, int64_t t) {
+  return reinterpret_cast<const char*>(a.logits) + t * a.ld * (a.bf16 ? 2 : 4);
+}
+
+// The kept groups (bit g) of the token, from the choice values c of its
+// experts; `c` of experts that may not be chosen is -inf. `gap`: the
+// difference between the last rank kept and the first left out, `size` the
+// larger magnitude that entered either.
+template <int L, int VPL, typename T>
+__device__ __forceinline__ uint64_t keep_groups(const RouteArgs& a, const T (&c)[VPL], int lane, T* gap, T* size) {
+  const int gs = a.group_size, G = a.groups;
+  const T none = -(T)__builtin_inff();
+  T rank = none, mag = (T)0;  // of group `lane`
+  auto add = [](T& b1, T& b2, T x) {
+    b2 = __builtin_elementwise_max(b2, __builtin_elementwise_min(b1, x));
+    b1 = __builtin_elementwise_max(b1, x);
+  };
+  for (int g = 0; g < G; g++) {
+    T b1 = none, b2 = none;
+    const int first = lane * VPL - g * gs;  // of the lane's experts, counted in the group
+#pragma unroll
+    for (int v = 0; v < VPL; v++) add(b1, b2, (unsigned)(first + v) < (unsigned)gs ? c[v] : none);
+    auto join = [&](T o1, T o2) {
+      b2 = __builtin_elementwise_max(__builtin_elementwise_max(b2, o2), __builtin_elementwise_min(b1, o1));
+      b1 = __builtin_elementwise_max(b1, o1);
+    };
+    join(move<1>(b1), move<1>(b2));
+    join(move<2>(b1), move<2>(b2));
+    join(move<4>(b1), move<4>(b2));
+    join(move<8>(b1), move<8>(b2));
+    if constexpr (L == 64) {
+      join(move<16>(b1), move<16>(b2));
+      join(move<32>(b1), move<32>(b2));
+    }
+    const bool two = a.best == 2 && b2 > none;
+    if (lane == g) {
+      rank = two ? b1 + b2 : b1;
+      mag = __builtin_elementwise_max(__builtin_elementwise_abs(b1), two ? __builtin_elementwise_abs(b2) : (T)0);
+    }
+  }
+  int ahead = 0;
+  for (int g = 0; g < G; g++) {
+    const T r = from_lane<L>(rank, g);
+    ahead += (r > rank || (r == rank && g < lane)) ? 1 : 0;
+  }
+  const bool there = lane < G && rank > none, kept = there && ahead < a.top_groups;
+  const T big = (T)__builtin_inff();
+  *gap = reduce<L>(kept ? rank : big, Min()) - reduce<L>(there && !kept ? rank : none, Max());
+  *size = reduce<L>(there ? mag : (T)0, Max());
+  uint64_t mask = __builtin_amdgcn_ballot_w64(kept);
+  if constexpr (L == 16) mask = (mask >> (threadIdx.x & 48)) & 0xffffu;
+  return mask;
+}
+
+// The experts' groups among those kept: bit v of the result.
+template <int VPL>
+__device__ __forceinline__ uint32_t members(const RouteArgs& a, uint64_t kept, int lane) {
+  int g = lane * VPL / a.group_size, left = a.group_size - (lane * VPL - g * a.group_size);
+  uint32_t m = 0;
+#pragma unroll
+  for (int v = 0; v < VPL; v++) {
+    m |= (uint32_t)((kept >> (g & 63)) & 1) << v;
+    if (--left == 0) {
+      g++;
+      left = a.group_size;
+    }
+  }
+  return m;
+}
+
+// The row's choice in double: slot j's expert goes to lane j (and j - L to
+// its `more`).
+template <int L, int VPL>
+__device__ __forceinline__ void choose_exactly(const RouteArgs& a, int64_t t, int lane, int* mine, int* more) {
+  const void* row = logit_row(a, t);
+  double c[VPL], m = -(double)__builtin_inff();
+  const double none = m;
+#pragma unroll
+  for (int v = 0; v < VPL; v++) {
+    const int e = lane * VPL + v;
+    c[v] = e < a.experts ? (double)load_logit(a, row, e) : none;
+    c[v] = c[v] == c[v] ? c[v] : none;
+    m = __builtin_fmax(m, c[v]);
+  }
+  m = reduce<L>(m, Max());
+  if (a.sigmoid) {
+#pragma unroll
+    for (int v = 0; v < VPL; v++) {
+      const double z = __builtin_fabs(c[v]), small = exp(-z);
+      if (c[v] > none) c[v] = (c[v] >= 0 ? 1.0 : small) / (1.0 + small);
+    }
+  } else {
+    double sum = 0;
+#pragma unroll
+    for (int v = 0; v < VPL; v++) {
+      const double p = c[v] > none ? exp(c[v] - m) : 0;
+      sum += p;
+      if (c[v] > none) c[v] = p;
+    }
+    sum = reduce<L>(sum, Add());
+#pragma unroll
+    for (int v = 0; v < VPL; v++) {
+      if (c[v] > none) c[v] /= sum;
+    }
+  }
+  if (a.bias) {
+#pragma unroll
+    for (int v = 0; v < VPL; v++) {
+      const int e = lane * VPL + v;
+      const double b = e < a.experts ? (double)a.bias[e] : none;
+      c[v] = c[v] > none && b == b ? c[v] + b : none;
+    }
+  }
+  if (a.top_groups < a.groups) {
+    double gap, size;
+    const uint32_t in = members<VPL>(a, keep_groups<L, VPL>(a, c, lane, &gap, &size), lane);
+#pragma unroll
+    for (int v = 0; v < VPL; v++) c[v] = (in >> v) & 1 ? c[v] : none;
+  }
+  if (!a.bias) {  // the logits' order is that of the scores, also where those round to one number
+#pragma unroll
+    for (int v = 0; v < VPL; v++) {
+      if (c[v] > none) c[v] = (double)load_logit(a, row, lane * VPL + v);
+    }
+  }
+  for (int j = 0; j < a.top_k; j++) {
+    double best = none;
+    int at = a.experts;  // (none)
+#pragma unroll
+    for (int v = 0; v < VPL; v++) {
+      if (c[v] > best) {
+        best = c[v];
+        at = lane * VPL + v;
+      }
+    }
+    for (int step = 1; step < L; step <<= 1) {
+      const double o = __shfl_xor(best, step, L);
+      const int oat = __shfl_xor(at, step, L);
+      if (o > best || (o == best && oat < at)) {
+        best = o;
+        at = oat;
+      }
+    }
+    if (lane == (j & (L - 1))) (j < L ? *mine : *more) = best > none ? at : -1;
+#pragma unroll
+    for (int v = 0; v < VPL; v++) c[v] = lane * VPL + v == at ? none : c[v];
+  }
+}
+
+}  // namespace
+
+template <int L, int VPL>
+__global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
+  const int lane = threadIdx.x & (L - 1);
+  const int64_t t = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  if (t >= a.tokens) return;  // (a token's lanes leave together)
+  const void* row = logit_row(a, t);
+  float l[VPL], m = neg_inf();
+#pragma unroll
+  for (int v = 0; v < VPL; v++) {
+    const int e = lane * VPL + v;
+    l[v] = e < a.experts ? load_logit(a, row, e) : neg_inf();
+    m = __builtin_fmaxf(m, l[v]);  // (NaN leaves it)
+  }
+  m = reduce<L>(m, Max());
+  const bool by_score = a.bias != nullptr;
+  const bool limited = a.top_groups < a.groups;
+  const bool group_score = limited && (by_score || a.best == 2);
+  double key[VPL];
+  float sum = 1.0f, unsure = 0.0f;  // unsure: bound on a score's error
+  bool sure = true;
+  if (!a.sigmoid && (!a.renormalize || by_score || group_score)) {
+    sum = 0.0f;
+#pragma unroll
+    for (int v = 0; v < VPL; v++) sum += exp_near(l[v] - m);
+    sum = reduce<L>(sum, Add());
+  }
+  float c[VPL];  // choice value, -inf where there is none
+#pragma unroll
+  for (int v = 0; v < VPL; v++) c[v] = l[v] == l[v] ? l[v] : neg_inf();
+  if (by_score || group_score) {
+    // sigmoid: 2^-23 for exp2 and 2^-23 for the reciprocal, one rounding of
+    // the sum, and 0.23 * 2^-24 for the rounded exponent: below 2^-21.
+    // softmax: (VPL + 6 + 3) 2^-24 relative for the sum, exponent as above:
+    // below 2^-19 of the largest score, 1 / sum.
+    const float inv = __builtin_amdgcn_rcpf(sum);
+    unsure = a.sigmoid ? 0x1p-21f : 0x1p-19f * __builtin_fminf(inv, 1.0f) + 0x1p-24f;
+#pragma unroll
+    for (int v = 0; v < VPL; v++) {
+      const float x = a.sigmoid ? -l[v] : l[v] - m;
+      const float p = __builtin_amdgcn_exp2f(x * kLog2e);
+      float s = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + p) : p * inv;
+      const int e = lane * VPL + v;
+      if (a.bias) s = s + (e < a.experts ? a.bias[e] : neg_inf());
+      c[v] = c[v] > neg_inf() && s == s ? s : neg_inf();
+    }
+  }
+  uint32_t in = ~0u;
+  if (limited) {
+    float gap, size;
+    in = members<VPL>(a, keep_groups<L, VPL>(a, c, lane, &gap, &size), lane);
+    // a rank of two scores: each with its error, and three roundings
+    if (group_score) sure = !(gap <= 4.0f * unsure + 0x1p-21f * size);
+  }
+#pragma unroll
+  for (int v = 0; v < VPL; v++) {
+    const float z = by_score ? c[v] : (l[v] == l[v] ? l[v] : neg_inf());
+    key[v] = z > neg_inf() && ((in >> v) & 1) ? make_key(z, lane * VPL + v) : kNone;
+  }
+  int mine = -1, more = -1;
+  float last = 0.0f;
+  double below = DBL_MAX;
+  for (int j = 0; j < a.top_k + (by_score ? 1 : 0); j++) {
+    double best = kNone;
+#pragma unroll
+    for (int v = 0; v < VPL; v++) best = __builtin_fmax(best, key[v] < below ? key[v] : kNone);
+    best = reduce<L>(best, Max());
+    below = best;
+    if (j < a.top_k && lane == (j & (L - 1))) (j < L ? mine : more) = best > kNone ? key_index(best) : -1;
+    if (by_score) {
+      const float now = key_value(best);
+      if (j > 0 && best > kNone)
+        sure = sure && last - now > 2.0f * unsure + 0x1p-23f * (__builtin_fabsf(last) + __builtin_fabsf(now));
+      last = now;
+    }
+    if (!(best > kNone)) below = kNone;
+  }
+  if (!sure) choose_exactly<L, VPL>(a, t, lane, &mine, &more);
+  // weights: lane j has slot j (and slot j + L)
+  const bool have2 = L < 32 && a.top_k > L;
+  const float z1 = mine >= 0 ? load_logit(a, row, mine) : neg_inf();
+  const float z2 = have2 && more >= 0 ? load_logit(a, row, more) : neg_inf();
+  float w1, w2;
+  if (a.sigmoid) {
+    // exp(min(z, 0)) / (1 + exp(-|z|)); over their sum the largest exponent
+    // is taken out first, so that scores that underflow still have a ratio
+    float top = 0.0f;
+    if (a.renormalize) top = reduce<L>(__builtin_fminf(__builtin_fmaxf(z1, z2), 0.0f), Max());
+    w1 = exp_near(__builtin_fminf(z1, 0.0f) - top) / (1.0f + exp_near(-__builtin_fabsf(z1)));
+    w2 = exp_near(__builtin_fminf(z2, 0.0f) - top) / (1.0f + exp_near(-__builtin_fabsf(z2)));
+  } else {
+    const float top = a.renormalize ? reduce<L>(__builtin_fmaxf(z1, z2), Max()) : m;
+    w1 = exp_near(z1 - top);
+    w2 = exp_near(z2 - top);
+  }
+  w1 = mine >= 0 ? w1 : 0.0f;
+  w2 = have2 && more >= 0 ? w2 : 0.0f;
+  if (a.renormalize) sum = reduce<L>(w1 + w2, Add());
+  const bool divide = a.renormalize || !a.sigmoid;
+  if (lane < a.top_k) {
+    a.ids[t * a.top_k + lane] = mine;
+    a.weights[t * a.top_k + lane] = mine >= 0 ? (divide ? w1 / sum : w1) * a.scale : 0.0f;
+  }
+  if (have2 && lane + L < a.top_k) {
+    a.ids[t * a.top_k + lane + L] = more;
+    a.weights[t * a.top_k + lane + L] = more >= 0 ? (divide ? w2 / sum : w2) * a.scale : 0.0f;
+  }
+}
+
+// dl from dw. Without renormalization softmax gives p_e (g_e - sum p g), g the
+// scaled dw of the chosen and 0 elsewhere, sigmoid g_e s (1 - s); with it, and
+// q_j the chosen scores over their sum, softmax q_j (g_j - sum q g), sigmoid
+// that times (1 - s_j). One pass: the row is read once and written once.
+template <int L, int VPL>
+__global__ __launch_bounds__(256) void route_backward_kernel(RouteBackwardArgs b) {
+  const RouteArgs& a = b.a;
+  const int lane = threadIdx.x & (L - 1);
+  const int64_t t = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  if (t >= a.tokens) return;
+  const void* row = logit_row(a, t);
+  const bool dense = !a.sigmoid && !a.renormalize;
+  float p[VPL], m = neg_inf(), sum = 1.0f;
+  if (dense) {
+#pragma unroll
+    for (int v = 0; v < VPL; v++) {
+      const int e = lane * VPL + v;
+      p[v] = e < a.experts ? load_logit(a, row, e) : neg_inf();
+      m = __builtin_fmaxf(m, p[v]);
+    }
+    m = reduce<L>(m, Max());
+    const float top = m > neg_inf() ? m : 0.0f;  // (a row of -inf has no part)
+    sum = 0.0f;
+#pragma unroll
+    for (int v = 0; v < VPL; v++) {
+      p[v] = exp_near(p[v] - top);
+      sum += p[v];
+    }
+    sum = reduce<L>(sum, Add());
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+    for (int v = 0; v < VPL; v++) p[v] = p[v] * inv;
+    sum = inv;
+  } else {
+#pragma unroll
+    for (int v = 0; v < VPL; v++) p[v] = 0.0f;
+  }
+  // slots j = lane and lane + L
+  int e[2];
+  float z[2], g[2], d[2];
+  float top = neg_inf();
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
+    const int j = lane + i * L;
+    e[i] = j < a.top_k ? a.ids[t * a.top_k + j] : -1;
+    if ((unsigned)e[i] >= (unsigned)a.experts) e[i] = -1;
+    z[i] = e[i] >= 0 ? load_logit(a, row, e[i]) : neg_inf();
+    g[i] = e[i] >= 0 ? b.grad[t * a.top_k + j] * a.scale : 0.0f;
+    top = __builtin_fmaxf(top, a.sigmoid ? __builtin_fminf(z[i], 0.0f) : z[i]);
+  }
+  if (dense) {
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      d[i] = e[i] >= 0 ? exp_near(z[i] - m) * sum * g[i] : 0.0f;
+      dot += d[i];
+    }
+    dot = reduce<L>(dot, Add());
+#pragma unroll
+    for (int v = 0; v < VPL; v++) p[v] = -(p[v] * dot);
+  } else {
+    float q[2], r[2];  // score (times a power of e common to the row), 1 - s
+    top = a.renormalize ? reduce<L>(top, Max()) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      if (a.sigmoid) {
+        const float small = exp_near(-__builtin_fabsf(z[i])), inv = 1.0f / (1.0f + small);
+        q[i] = exp_near(__builtin_fminf(z[i], 0.0f) - top) * inv;
+        r[i] = (z[i] >= 0.0f ? small : 1.0f) * inv;
+      } else {
+        q[i] = exp_near(z[i] - top);
+        r[i] = 1.0f;
+      }
+      if (e[i] < 0) q[i] = 0.0f;
+    }
+    float dot = 0.0f;
+    if (a.renormalize) {
+      const float all = reduce<L>(q[0] + q[1], Add());
+      const float inv = all > 0.0f ? 1.0f / all : 0.0f;
+      q[0] *= inv;
+      q[1] *= inv;
+      dot = reduce<L>(q[0] * g[0] + q[1] * g[1], Add());
+    }
+#pragma unroll
+    for (int i = 0; i < 2; i++) d[i] = e[i] >= 0 ? q[i] * r[i] * (g[i] - dot) : 0.0f;
+  }
+  for (int j = 0; j < a.top_k; j++) {
+    const int at = __shfl(j < L ? e[0] : e[1], j & (L - 1), L) - lane * VPL;
+    const float val = __shfl(j < L ? d[0] : d[1], j & (L - 1), L);
+#pragma unroll
+    for (int v = 0; v < VPL; v++) p[v] += at == v ? val : 0.0f;
+  }
+  char* out = reinterpret_cast<char*>(b.out) + t * b.ld_out * (a.bf16 ? 2 : 4);
+#pragma unroll
+  for (int v = 0; v < VPL; v++) {
+    const int at = lane * VPL + v;
+    if (at < a.experts) {
+      if (a.bf16) reinterpret_cast<__bf16*>(out)[at] = (__bf16)p[v];
+      else reinterpret_cast<float*>(out)[at] = p[v];
+    }
+  }
+}
+
+namespace {
+
+// Lanes for one token: a row of 16 where that fills the GPU, else a wave,
+// which is done sooner (and what more than 16 groups, or more than 256 experts, need).
+bool wide_route(const RouteArgs& a) {
+  return a.experts > 256 || a.groups > 16 || a.tokens <= 4 * device_cu_count();
+}
+
+template <template <int, int> class LAUNCH, typename ARGS>
+hipError_t route_by_size(const RouteArgs& a, const ARGS& args, hipStream_t s) {
+  if (wide_route(a)) {
+    const int per = (a.experts + 63) / 64;
+    if (per <= 1) return LAUNCH<64, 1>::go(args, a.tokens, s);
+    if (per <= 2) return LAUNCH<64, 2>::go(args, a.tokens, s);
+    if (per <= 4) return LAUNCH<64, 4>::go(args, a.tokens, s);
+    if (per <= 8) return LAUNCH<64, 8>::go(args, a.tokens, s);
+    return LAUNCH<64, 16>::go(args, a.tokens, s);
+  }
+  const int per = (a.experts + 15) / 16;
+  if (per <= 1) return LAUNCH<16, 1>::go(args, a.tokens, s);
+  if (per <= 2) return LAUNCH<16, 2>::go(args, a.tokens, s);
+  if (per <= 4) return LAUNCH<16, 4>::go(args, a.tokens, s);
+  if (per <= 8) return LAUNCH<16, 8>::go(args, a.tokens, s);
+  return LAUNCH<16, 16>::go(args, a.tokens, s);
+}
+
+template <int L, int VPL>
+struct Forward {
+  static hipError_t go(const RouteArgs& a, int64_t tokens, hipStream_t s) {
+    hipLaunchKernelGGL((route_kernel<L, VPL>), dim3((unsigned)((tokens + 256 / L - 1) / (256 / L))), dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
+};
+template <int L, int VPL>
+struct Backward {
+  static hipError_t go(const RouteBackwardArgs& b, int64_t tokens, hipStream_t s) {
+    hipLaunchKernelGGL((route_backward_kernel<L, VPL>), dim3((unsigned)((tokens + 256 / L - 1) / (256 / L))), dim3(256),
+                       0, s, b);
+    return hipGetLastError();
+  }
+};
+
+}  // namespace
+
+hipError_t launch_moe_route(const RouteArgs& a, hipStream_t s) { return route_by_size<Forward>(a, a, s); }
+hipError_t launch_moe_route_backward(const RouteBackwardArgs& b, hipStream_t s) {
+  return route_by_size<Backward>(b.a, b, s);
+}
+
+}  // namespace fp4impl

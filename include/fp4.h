@@ -472,6 +472,179 @@ size_t fp4_kv_attention_workspace(const fp4_kv_cache* cache, const fp4_kv_attent
 fp4_status fp4_kv_attention(const fp4_kv_cache* cache, const fp4_kv_attention_args* args, void* workspace,
                             size_t workspace_bytes, void* stream);
 
+/*
+ * A mixture-of-experts layer around the 4-bit products ("FP4", section
+ * "Inferencia e Treinamento FP4": MoE weights in MXFP4): the router's choice,
+ * the sort of its (token, expert) pairs into the row groups of
+ * fp4_gemm_grouped, and the way of rows there and back. Pair p = t * top_k + j
+ * is slot j of token t.
+ */
+
+/* fp4_moe_route_args.flags */
+enum {
+  FP4_MOE_SIGMOID = 1u,     /* scores 1 / (1 + exp(-l)) instead of softmax over all experts */
+  FP4_MOE_RENORMALIZE = 2u  /* weights over the sum of the chosen experts' scores */
+};
+
+typedef struct fp4_moe_route_args {
+  uint32_t size;       /* must equal sizeof(fp4_moe_route_args) */
+  int32_t dtype;       /* fp4_dtype of the logits (and of their gradient) */
+  uint32_t flags;      /* FP4_MOE_*; others -> FP4_ERR_INVALID */
+  int32_t experts;     /* 1 to 1024 */
+  int32_t top_k;       /* 1 to 32, at most experts */
+  int32_t groups;      /* groups of experts / groups consecutive experts; 1 to 64, divides experts */
+  int32_t top_groups;  /* experts are chosen from that many groups: 1 to groups (groups: no limit) */
+  int32_t group_best;  /* a group's rank is the sum of its 1 or 2 best choice values */
+  int64_t tokens;
+  const void* logits;  /* device [tokens][experts], row pitch ld_logits (elements) */
+  int64_t ld_logits;
+  const float* bias;   /* device [experts], added to the scores for the choice only; or NULL */
+  float* weights;      /* device [tokens][top_k] */
+  int32_t* ids;        /* device [tokens][top_k] */
+  float scale;         /* multiplies the weights; finite */
+  int32_t reserved;    /* 0 */
+} fp4_moe_route_args;
+
+/*
+ * fp4_moe_route -- each token's top_k experts and their weights:
+ *   s = softmax(l) or the logistic function of l; choice c_e = s_e + bias_e;
+ *   of the top_groups groups with the largest ranks, the top_k largest c, best
+ *   first; w_j = scale * s_ij, divided by the sum of the chosen s if
+ *   FP4_MOE_RENORMALIZE.
+ * Equal values go to the lowest index (of experts and of groups). Values are
+ * compared as exact numbers: without a bias by the logits themselves, else
+ * by scores whose fp32 rounding does not decide (rows where it could are done
+ * in fp64). Weights are accurate to fp32.
+ *   An expert whose logit or bias is -inf or NaN is never chosen; where fewer
+ *   than top_k can be, the remaining slots get id -1 and weight 0. In a row
+ *   with a logit of NaN or +inf the weights are unspecified, and the ids
+ *   distinct experts or -1.
+ * weights and ids are dense. tokens = 0 is a valid empty call.
+ * Errors: FP4_ERR_INVALID, FP4_ERR_UNSUPPORTED (2^26 tokens and more),
+ * FP4_ERR_ALIGN (pointers below their elements' size), FP4_ERR_DEVICE,
+ * FP4_ERR_HIP.
+ */
+fp4_status fp4_moe_route(const fp4_moe_route_args* args, void* stream);
+
+/*
+ * fp4_moe_route_backward -- the gradient of the logits from that of the
+ * weights (device float [tokens][top_k], dense), for the choice in args->ids
+ * (read here; ids outside [0, experts) have no part, an id twice counts
+ * twice). args as given to fp4_moe_route; weights, bias and the groups are not
+ * used. grad_logits [tokens][experts] of args->dtype, row pitch ld_grad, is
+ * written whole.
+ */
+fp4_status fp4_moe_route_backward(const fp4_moe_route_args* args, const float* grad_weights, void* grad_logits,
+                                  int64_t ld_grad, void* stream);
+
+/* Bytes of device workspace fp4_moe_group needs (0 when none, and for
+ * arguments it would reject). */
+size_t fp4_moe_group_workspace(int64_t pairs, int32_t experts);
+
+/*
+ * fp4_moe_group -- the pairs sorted by expert, stable (a counting sort):
+ *   ids      device [pairs]: expert of each pair; outside [0, experts): none
+ *   offsets  device [experts + 1]: first row of each expert, as
+ *            fp4_gemm_grouped takes them; offsets[experts] = pairs that have one
+ *   order    device [pairs]: the pair at each row; pairs without an expert
+ *            lie behind the others, in order
+ *   place    device [pairs]: the row of each pair (the inverse of order)
+ * experts 1 to 1024, pairs up to 2^24 (more: FP4_ERR_UNSUPPORTED). pairs = 0
+ * writes offsets of 0. workspace: 16-byte aligned, contents on entry do not
+ * matter; not shared by concurrent calls.
+ */
+fp4_status fp4_moe_group(int64_t pairs, const int32_t* ids, int32_t experts, int32_t* offsets, int32_t* order,
+                         int32_t* place, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fp4_moe_dispatch -- each token's row to the rows of its pairs:
+ *   rows[place[t * top_k + j]] = x[t],
+ * for row_bytes bytes of anything (bf16, fp32, or the codes of a quantized
+ * row) and, if row_bytes2 > 0, a second plane with its own pitches (the scales
+ * beside the codes). kept: device int32 (offsets + experts of fp4_moe_group),
+ * or NULL; rows from *kept on are filled with zeros. Places outside
+ * [0, tokens * top_k), the number of rows, are passed over. Pitches in bytes,
+ * any alignment (multiples of 16 are fastest). top_k 1 to 1024, at most 2^24 - 1 tokens.
+ */
+fp4_status fp4_moe_dispatch(int64_t tokens, int32_t top_k, const int32_t* place, const int32_t* kept,
+                            int64_t row_bytes, const void* x, int64_t ld_x, void* rows, int64_t ld_rows,
+                            int64_t row_bytes2, const void* x2, int64_t ld_x2, void* rows2, int64_t ld_rows2,
+                            void* stream);
+
+/*
+ * fp4_moe_combine -- the experts' rows back to their tokens:
+ *   out[t] = sum_j weights[t * top_k + j] * rows[place[t * top_k + j]],
+ * summed in fp32 in order of j, rounded once. rows [num_rows][width] and out
+ * [tokens][width] of dtype, pitches in elements. place NULL: pair p has row p.
+ * weights (dense) NULL: all 1. Pairs whose place lies outside [0, num_rows) or
+ * from *kept on (kept as above, or NULL) have no part. Pointers aligned to
+ * their elements (rows of whole 16-byte pieces are fastest). out does not
+ * overlap rows. With weights NULL this is also the backward pass of
+ * fp4_moe_dispatch. top_k 1 to 1024, at most 2^24 - 1 tokens, width up to 2^24.
+ */
+fp4_status fp4_moe_combine(int32_t dtype, int64_t tokens, int32_t top_k, int64_t width, const void* rows,
+                           int64_t ld_rows, int64_t num_rows, const int32_t* place, const int32_t* kept,
+                           const float* weights, void* out, int64_t ld_out, void* stream);
+
+/*
+ * fp4_moe_combine_backward -- from the gradient of out:
+ *   grad_rows[place[p]] = weights[p] * grad_out[t]   (zeros from *kept on)
+ *   grad_weights[p] = rows[place[p]] . grad_out[t]   (fp32; 0 where p has no part)
+ * Each place is written once if places are distinct, as fp4_moe_group makes
+ * them; rows of no pair are left as they were. grad_weights may be NULL, and
+ * rows then too. At most 2^24 - 1 pairs.
+ */
+fp4_status fp4_moe_combine_backward(int32_t dtype, int64_t tokens, int32_t top_k, int64_t width,
+                                    const void* grad_out, int64_t ld_grad, const void* rows, int64_t ld_rows,
+                                    int64_t num_rows, const int32_t* place, const int32_t* kept, const float* weights,
+                                    void* grad_rows, int64_t ld_grad_rows, float* grad_weights, void* stream);
+
+typedef struct fp4_matvec_args {
+  uint32_t size;        /* must equal sizeof(fp4_matvec_args) */
+  int32_t format;       /* fp4_format of the weights */
+  int32_t x_dtype;      /* fp4_dtype */
+  int32_t y_dtype;
+  int64_t pairs;        /* rows of y */
+  int64_t repeat;       /* row p of y takes row p / repeat of x; at least 1 */
+  int64_t N, K;         /* W_e [N, K]; K a multiple of blk */
+  const void* x;        /* [(pairs - 1) / repeat + 1][K], row pitch ld_x */
+  int64_t ld_x;         /* elements */
+  const uint8_t* codes; /* [experts][N][K / 2] as fp4_quantize writes them */
+  int64_t ld_codes;     /* bytes, as the three below */
+  int64_t codes_expert_stride;
+  const uint8_t* scales; /* [experts][N][K / blk] */
+  int64_t ld_scales;
+  int64_t scales_expert_stride;
+  const float* tensor_scale; /* NVFP4: device [experts] */
+  int64_t experts;           /* matrices; 1 to 4096 */
+  const int32_t* ids;        /* device [pairs]: each row's matrix; NULL: matrix 0 for all */
+  void* y;                   /* [pairs][N], row pitch ld_y */
+  int64_t ld_y;              /* elements */
+} fp4_matvec_args;
+
+/*
+ * fp4_matvec -- a few rows times 4-bit weights ("FP4", section "Inferencia e
+ * Treinamento FP4": FP4 weights, products accumulated in higher precision):
+ *   y[p, n] = sum_k deq(W_e)[n, k] * x[p / repeat, k],  e = ids[p],
+ * for the steps of a decoder that have one token or a few, where the weights'
+ * bytes are all the work: they are read in 4 bits, once, and the activations
+ * are not quantized, nor rounded at all (fp32 as three bf16 terms that hold
+ * its 24 bits). Sums in fp32, y rounded once. Any number of rows is right;
+ * past some dozens (of one matrix) fp4_gemm and fp4_gemm_grouped on quantized
+ * activations are faster.
+ *   ids outside [0, experts) give rows of zeros. With ids at most 4096 pairs
+ *   (more: FP4_ERR_UNSUPPORTED).
+ *   Weights quantized with FP4_HADAMARD stand for rotated ones: x has to be
+ *   rotated by the same signs.
+ * x 16-byte aligned with a row pitch of whole 16 bytes; codes 16-byte aligned,
+ * ld_codes (>= K/2) and expert strides multiples of 16, code rows readable
+ * up to the next multiple of 16 bytes; scales 2-byte aligned (NVFP4), their
+ * pitches even. Errors: FP4_ERR_INVALID, FP4_ERR_UNSUPPORTED, FP4_ERR_ALIGN,
+ * FP4_ERR_DEVICE, FP4_ERR_HIP. pairs = 0 or N = 0 is a valid empty call;
+ * K = 0 gives zeros.
+ */
+fp4_status fp4_matvec(const fp4_matvec_args* args, void* stream);
+
 /* Static string naming a status code; never NULL. */
 const char* fp4_status_str(int32_t status);
 
