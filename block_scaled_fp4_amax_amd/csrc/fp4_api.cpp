@@ -979,10 +979,12 @@ fp4_status fp4_matvec(const fp4_matvec_args* m, void* stream) {
   const bool nv = m->format == FP4_NVFP4;
   const int64_t blk = nv ? 16 : 32;
   if (m->pairs < 0 || m->repeat < 1 || m->N < 0 || m->K < 0 || m->K % blk != 0 || m->experts < 1) return FP4_ERR_INVALID;
-  if (m->experts > 4096 || m->K > (int64_t(1) << 30) || m->N > (int64_t(1) << 31) - 1) return FP4_ERR_UNSUPPORTED;
+  if (m->experts > 4096 || m->K > (int64_t(1) << 24) || m->N > (int64_t(1) << 30)) return FP4_ERR_UNSUPPORTED;
   // (tiles of rows are counted in 32 bits, work items along x in 32 bits too)
   if (m->pairs > (int64_t(1) << 30) || (m->N + 15) / 16 > kMaxItemsX / 512) return FP4_ERR_UNSUPPORTED;
   if (m->ids && m->pairs > 4096) return FP4_ERR_UNSUPPORTED;
+  // (a tile of 32 rows is addressed with 32 bits)
+  if (m->ld_codes >= (int64_t(1) << 23) || m->ld_scales >= (int64_t(1) << 23)) return FP4_ERR_UNSUPPORTED;
   if (m->pairs == 0 || m->N == 0) return FP4_OK;
   if (!m->y || m->ld_y < m->N) return FP4_ERR_INVALID;
   if (m->K > 0 && (!m->x || !m->codes || !m->scales)) return FP4_ERR_INVALID;
@@ -990,10 +992,13 @@ fp4_status fp4_matvec(const fp4_matvec_args* m, void* stream) {
   if (m->ld_x < m->K || m->ld_codes < m->K / 2 || m->ld_scales < m->K / blk) return FP4_ERR_INVALID;
   if (m->experts > 1 && (m->codes_expert_stride < 0 || m->scales_expert_stride < 0)) return FP4_ERR_INVALID;
   const int64_t es = m->x_dtype == FP4_BF16 ? 2 : 4;
-  if (!aligned(m->x, 16) || (m->ld_x * es) % 16 != 0) return FP4_ERR_ALIGN;
-  if (!aligned(m->codes, 16) || m->ld_codes % 16 != 0 || (m->experts > 1 && m->codes_expert_stride % 16 != 0))
+  // (without columns nothing of these is read)
+  if (m->K > 0 && (!aligned(m->x, 16) || (m->ld_x * es) % 16 != 0)) return FP4_ERR_ALIGN;
+  if (m->K > 0 && (!aligned(m->codes, 16) || m->ld_codes % 16 != 0 || (m->experts > 1 && m->codes_expert_stride % 16 != 0)))
     return FP4_ERR_ALIGN;
-  if (nv && (!aligned(m->scales, 2) || m->ld_scales % 2 != 0 || (m->experts > 1 && m->scales_expert_stride % 2 != 0)))
+  // scale rows are read 16 bytes at a time, up to the next multiple of 16
+  if (m->K > 0 &&
+      (!aligned(m->scales, 16) || m->ld_scales % 16 != 0 || (m->experts > 1 && m->scales_expert_stride % 16 != 0)))
     return FP4_ERR_ALIGN;
   if ((nv && !aligned(m->tensor_scale, 4)) || !aligned(m->ids, 4) || !aligned(m->y, m->y_dtype == FP4_BF16 ? 2 : 4))
     return FP4_ERR_ALIGN;
@@ -1004,7 +1009,7 @@ fp4_status fp4_matvec(const fp4_matvec_args* m, void* stream) {
   a.x_bf16 = m->x_dtype == FP4_BF16;
   a.y_bf16 = m->y_dtype == FP4_BF16;
   a.pairs = m->pairs;
-  a.repeat = m->repeat;
+  a.repeat = m->repeat < (int64_t(1) << 30) ? m->repeat : int64_t(1) << 30;
   a.N = m->N;
   a.K = m->K;
   a.x = m->x;

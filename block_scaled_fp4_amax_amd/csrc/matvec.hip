@@ -2,8 +2,6 @@
 //   y[p, n] = sum_k deq(W_e)[n, k] x[p / repeat, k], e = ids[p] (or 0),
 // accumulated in fp32. The weights' bytes are read once; activations are not
 // rounded.
-#include <type_traits>
-
 #include "fp4_device.h"
 #include "launch.h"
 
@@ -13,52 +11,25 @@ using namespace fp4dev;
 namespace {
 
 constexpr int kWaves = 8;
-constexpr int kMaxPairs = 4096;    // of a call by experts
-constexpr int kMaxExperts = 4096;
+constexpr int kUnit = 512;        // K of a wave's unit: four pieces of 128, 256 bytes of each row's codes
 
-struct Bf16Terms {
-  bf16x8 t[3];
+// What the kernels take: sizes in 32 bits, and what only sizes decide.
+struct Call {
+  const void* x;
+  const uint8_t *codes, *scales;
+  const float* ts;
+  const int32_t* ids;
+  void* y;
+  int64_t ld_x, c_es, s_es, ld_y;  // elements, bytes, bytes, elements
+  uint32_t ld_c, ld_s;
+  int pairs, repeat, N, K, experts;
+  int units;                        // of K
+  uint32_t last_code, last_scale;   // where a row's last 16 bytes start
+  int y_bf16;
+  int part_shift;  // few rows: 2^part_shift waves share a tile of W
+  int seg_units;   // few rows: units of x in LDS at once
+  int rounds;      // few rows: tiles of W a wave takes one after another
 };
-
-// Eight numbers of an activation row as bf16 operands: themselves, or three
-// terms that hold all 24 bits of fp32 (each the leading 8 bits of what is
-// left, cut off, so that nothing overflows).
-template <bool XBF>
-__device__ __forceinline__ void load_x(const void* row, int64_t k, bool there, Bf16Terms& o) {
-  if constexpr (XBF) {
-    u32x4 w = {0, 0, 0, 0};
-    if (there) w = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(row) + k);
-    o.t[0] = __builtin_bit_cast(bf16x8, w);
-  } else {
-    f32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
-    if (there) {
-      lo = reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(row) + k)[0];
-      hi = reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(row) + k)[1];
-    }
-    uint32_t w[3][4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      uint32_t part[3][2];
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
-        const int e = 2 * i + h;
-        float v = e < 4 ? lo[e] : hi[e - 4];
-        const uint32_t b0 = __builtin_bit_cast(uint32_t, v);
-        part[0][h] = b0 >> 16;
-        const bool fin = (b0 & 0x7f800000u) != 0x7f800000u;
-        const float r1 = fin ? v - __builtin_bit_cast(float, b0 & 0xffff0000u) : 0.0f;
-        const uint32_t b1 = __builtin_bit_cast(uint32_t, r1);
-        part[1][h] = b1 >> 16;
-        const float r2 = r1 - __builtin_bit_cast(float, b1 & 0xffff0000u);
-        part[2][h] = __builtin_bit_cast(uint32_t, r2) >> 16;
-      }
-#pragma unroll
-      for (int q = 0; q < 3; q++) w[q][i] = part[q][0] | (part[q][1] << 16);
-    }
-#pragma unroll
-    for (int q = 0; q < 3; q++) o.t[q] = __builtin_bit_cast(bf16x8, u32x4{w[q][0], w[q][1], w[q][2], w[q][3]});
-  }
-}
 
 // The eight values of a word of codes, times their block's scale: exact in
 // bf16 (E2M1 has 2 significant bits, E4M3 4).
@@ -79,149 +50,699 @@ __device__ __forceinline__ bf16x8 weights8(uint32_t w, float scale) {
   return __builtin_bit_cast(bf16x8, u32x4{o[0], o[1], o[2], o[3]});
 }
 
-struct Experts {
-  uint32_t seen[kMaxExperts / 32];
-  int expert, count;
-  uint16_t list[kMaxPairs];
+// Eight fp32 numbers as three bf16 terms that hold all their 24 bits: each the
+// leading 8 bits of what is left, cut off, so that nothing overflows.
+__device__ __forceinline__ void split3(const u32x4 lo, const u32x4 hi, u32x4 (&t)[3]) {
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    uint32_t part[3][2];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      const int e = 2 * i + h;
+      const uint32_t b0 = e < 4 ? lo[e] : hi[e - 4];
+      const float v = __builtin_bit_cast(float, b0);
+      // (an infinity is its first term alone)
+      const float r1 = (b0 & 0x7f800000u) != 0x7f800000u ? v - __builtin_bit_cast(float, b0 & 0xffff0000u) : 0.0f;
+      const uint32_t b1 = __builtin_bit_cast(uint32_t, r1);
+      const float r2 = r1 - __builtin_bit_cast(float, b1 & 0xffff0000u);
+      part[0][h] = b0;
+      part[1][h] = b1;
+      part[2][h] = __builtin_bit_cast(uint32_t, r2);
+    }
+#pragma unroll
+    for (int q = 0; q < 3; q++) t[q][i] = (part[q][0] >> 16) | (part[q][1] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+__device__ __forceinline__ f32x4 mfma(u32x4 x, bf16x8 w, f32x4 acc) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), w, acc, 0, 0, 0);
+}
+
+// Where 16 NT rows of W lie: bases of the first (the same for all lanes), and
+// the lane's row, lane % 16 of each tile, from there.
+template <int NT>
+struct Place {
+  const uint8_t *codes, *scales;
+  uint32_t code_row[NT], scale_row[NT];
+  __device__ __forceinline__ Place(const Call& a, int expert, int n0) {
+    const int c16 = threadIdx.x & 15;
+    n0 = n0 < a.N ? n0 : a.N - 1;
+    codes = a.codes + expert * a.c_es + (int64_t)n0 * a.ld_c;
+    scales = a.scales + expert * a.s_es + (int64_t)n0 * a.ld_s;
+    const int rows = a.N - 1 - n0;
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+      const uint32_t row = t * 16 + c16 < rows ? t * 16 + c16 : rows;
+      code_row[t] = row * a.ld_c;
+      scale_row[t] = row * a.ld_s;
+    }
+  }
 };
 
-// The blockIdx.y-th expert among those that the pairs name, and its pairs in
-// order. expert = -1: there are not so many.
-__device__ __forceinline__ void find_expert(const MatvecArgs& a, Experts& s) {
+// One unit of NT tiles of 16 rows of W in a wave's registers: a lane has 32
+// consecutive values of row lane % 16 in each of four pieces of 128, and the
+// rows' scales of all four.
+template <bool NV, int NT>
+struct Weights {
+  u32x4 w[NT][4], s[NT][NV ? 2 : 1];
+  // (past the end: the row's last bytes, for which scale() gives zeros)
+  __device__ __forceinline__ void load(const Call& a, const Place<NT>& p, int k0, int g) {
+    const uint32_t last_code = a.last_code, last_scale = a.last_scale;
+    const uint32_t at = (uint32_t)k0 / 2 + g * 16, sat = (uint32_t)k0 / (NV ? 16 : 32);
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+#pragma unroll
+      for (int i = 0; i < (NV ? 2 : 1); i++) {
+        const uint32_t o = sat + i * 16 < last_scale ? sat + i * 16 : last_scale;
+        s[t][i] = *reinterpret_cast<const u32x4*>(p.scales + (p.scale_row[t] + o));
+      }
+#pragma unroll
+      for (int u = 0; u < 4; u++) {
+        const uint32_t o = at + u * 64 < last_code ? at + u * 64 : last_code;
+        w[t][u] = *reinterpret_cast<const u32x4*>(p.codes + (p.code_row[t] + o));
+      }
+    }
+  }
+  // The scales of the lane's first and second 16 values of piece u, which
+  // starts at k.
+  __device__ __forceinline__ f32x2 scale(int t, int u, int k, int K, int g) const {
+    const bool first = k + g * 32 < K, second = k + g * 32 + 16 < K;
+    if constexpr (NV) {
+      const uint32_t pair = (g & 2 ? s[t][u >> 1][(2 * u + 1) & 3] : s[t][u >> 1][(2 * u) & 3]) >> (16 * (g & 1));
+      const f32x2 f = __builtin_amdgcn_cvt_pk_f32_fp8(pair, false);
+      return f32x2{first ? f.x : 0.0f, second ? f.y : 0.0f};
+    } else {
+      const float f = e8m0_scale_operand(first ? (s[t][0][u] >> (8 * g)) & 0xffu : 0u);
+      return f32x2{f, f};
+    }
+  }
+};
+
+// The words from here on are not known to be the ones loaded: their conversion
+// stays behind this point (else it is moved ahead for a whole unit, before the
+// next unit's loads are issued, and takes 64 registers).
+__device__ __forceinline__ u32x4 pinned(u32x4 v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+__device__ __forceinline__ u32x4 at16(const uint8_t* p) { return *reinterpret_cast<const u32x4*>(p); }
+
+// ---------------------------------------------------------------------------
+// few rows (4 RG of x): the workgroup shares x in LDS
+// ---------------------------------------------------------------------------
+// x lies in LDS as bf16 operand rows, one for each activation row and term,
+// each 16 bytes longer than its values so that the rows' reads meet different
+// banks. Terms of fp32 are rows like others: one matrix instruction multiplies
+// all three, and their sums are added at the end. Behind the rows: zeros, as
+// many as a unit of a row has bytes.
+constexpr int kZeros = kUnit * 2;
+template <bool XBF, int RG>
+constexpr int kOpRows = (XBF ? 1 : 3) * 4 * RG;
+
+// One lane's part of the staging: eight numbers at k of four rows, of which
+// `live` are there (what the others hold meets only results that nobody reads).
+template <bool XBF>
+struct StageX {
+  static constexpr int XR = XBF ? 1 : 2;
+  u32x4 v[4][XR];
+  __device__ __forceinline__ void load(const Call& a, const int64_t* xo, int live, int k) {
+#pragma unroll
+    for (int r = 0; r < 4; r++) {
+      if (r < live) {
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(a.x) + (xo[r] + (k < a.K ? k : 0)) * (XBF ? 2 : 4);
+#pragma unroll
+        for (int h = 0; h < XR; h++) v[r][h] = at16(src + 16 * h);
+      }
+    }
+  }
+  // to: row 0's place; plane: bytes from one term's rows to the next's
+  __device__ __forceinline__ void put(const Call& a, int live, int k, uint8_t* to, int pitch, int plane) {
+#pragma unroll
+    for (int r = 0; r < 4; r++) {
+      if (r < live) {
+        if (k >= a.K) {
+#pragma unroll
+          for (int h = 0; h < XR; h++) v[r][h] = u32x4{0, 0, 0, 0};
+        }
+        if constexpr (XBF) {
+          *reinterpret_cast<u32x4*>(to + r * pitch) = v[r][0];
+        } else {
+          u32x4 t[3];
+          split3(v[r][0], v[r][1], t);
+#pragma unroll
+          for (int q = 0; q < 3; q++) *reinterpret_cast<u32x4*>(to + q * plane + r * pitch) = t[q];
+        }
+      }
+    }
+  }
+};
+
+// 4 RG rows of x, in LDS, times a wave's tile of 16 rows of W.
+//
+// NVFP4 with bf16 rows: instead of scaling every weight, an operand of x
+// holds four rows in operand rows 4 g to 4 g + 3 of lane group g only, zeros in
+// its other rows. Rows 4 g + r of the product, which is what lane group g
+// receives, are then x[r] times this group's own 32 values: a lane has its own
+// partial sums, and its block's scale multiplies four of them instead of
+// sixteen weights.
+template <bool NV, bool XBF, int RG>
+struct FewRows {
+  static constexpr bool DIAG = NV && XBF;
+  static constexpr int ROWS = kOpRows<XBF, RG>, OT = DIAG ? RG : (ROWS + 15) / 16;
+  int from[OT], step[OT];  // of the lane's operands: where those of a segment's first unit lie, and from unit to unit
+  f32x4 acc[OT];
+
+  __device__ __forceinline__ FewRows(int pitch) {
+    const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int o = 0; o < OT; o++) {
+      const int row = DIAG ? o * 4 + (c16 & 3) : (o * 16 + c16) % ROWS;
+      const bool there = !DIAG || (c16 >> 2) == g;
+      from[o] = there ? row * pitch + g * 64 : ROWS * pitch;
+      step[o] = there ? kUnit * 2 : 0;
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int o = 0; o < OT; o++) acc[o] = f32x4{0, 0, 0, 0};
+  }
+  // One unit, which starts at k0 and is unit `at` of x in LDS.
+  __device__ __forceinline__ void multiply(const Weights<NV, 1>& o, int k0, int K, int at, const uint8_t* lds) {
+    const int g = (threadIdx.x & 63) >> 4;
+    const uint8_t* x[OT];
+#pragma unroll
+    for (int i = 0; i < OT; i++) x[i] = lds + (from[i] + at * step[i]);
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+      __builtin_amdgcn_sched_barrier(0);  // (else the operands of all four pieces are read at once)
+      const u32x4 codes = pinned(o.w[0][u]);
+      const f32x2 sc = o.scale(0, u, k0 + u * 128, K, g);
+      if constexpr (DIAG) {
+        bf16x8 w[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) w[j] = weights8<false>(codes[j], 1.0f);
+#pragma unroll
+        for (int i = 0; i < OT; i++) {
+          f32x4 d0 = {0, 0, 0, 0}, d1 = {0, 0, 0, 0};
+          d0 = mfma(at16(x[i] + u * 256), w[0], d0);
+          d1 = mfma(at16(x[i] + u * 256 + 32), w[2], d1);
+          d0 = mfma(at16(x[i] + u * 256 + 16), w[1], d0);
+          d1 = mfma(at16(x[i] + u * 256 + 48), w[3], d1);
+#pragma unroll
+          for (int r = 0; r < 4; r++) acc[i][r] = __builtin_fmaf(sc.y, d1[r], __builtin_fmaf(sc.x, d0[r], acc[i][r]));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          const bf16x8 w = weights8<NV>(codes[j], j < 2 ? sc.x : sc.y);
+#pragma unroll
+          for (int i = 0; i < OT; i++) acc[i] = mfma(at16(x[i] + u * 256 + j * 16), w, acc[i]);
+        }
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  // In lanes of group g < RG: rows 4 g to 4 g + 3 of column lane % 16.
+  __device__ __forceinline__ f32x4 result() {
+    const int g = (threadIdx.x & 63) >> 4;
+    if constexpr (DIAG) {
+#pragma unroll
+      for (int o = 0; o < OT; o++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+          float v = acc[o][r];
+          v += xor_shfl<16>(v);
+          v += xor_shfl<32>(v);
+          acc[o][r] = v;
+        }
+      if constexpr (RG == 2) acc[0] = g == 1 ? acc[1] : acc[0];
+    } else if constexpr (!XBF) {
+      // operand row term * 4 RG + m: group o * 4 + g is term (o * 4 + g) / RG
+#pragma unroll
+      for (int r = 0; r < 4; r++) {
+        float v = acc[0][r];
+        if constexpr (RG == 1) {
+          v = g < 3 ? v : 0.0f;
+          v += xor_shfl<16>(v);
+        } else {
+          v += g < 2 ? acc[1][r] : 0.0f;
+        }
+        v += xor_shfl<32>(v);
+        acc[0][r] = v;
+      }
+    }
+    return acc[0];
+  }
+};
+
+// ---------------------------------------------------------------------------
+// 16 rows: each wave passes x through LDS by itself
+// ---------------------------------------------------------------------------
+// One piece of 128 of 16 activation rows, in planes of [16][16 slots] for each
+// term.
+template <bool XBF>
+constexpr int kStage = (XBF ? 1 : 3) * 16 * 256;
+
+// 16 rows of x (their offsets in elements: xo, rows 4 i + g for lane group g)
+// times NT tiles of 16 rows of W, over this wave's units of K.
+template <bool NV, bool XBF, int NT>
+__device__ __forceinline__ void many_rows(const Call& a, const Place<NT>& at, const int64_t (&xo)[4],
+                                          uint8_t* stage, int wave, int waves, f32x4 (&acc)[NT]) {
+  constexpr int TERMS = XBF ? 1 : 3, XR = XBF ? 4 : 8, XU = XBF ? 2 : 1;  // XU: pieces whose x is loaded at once
+  const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
+  const int K = a.K, units = a.units;
+  auto load_x = [&](int k0, u32x4 (&o)[XR]) {
+    const int k = k0 + c16 * 8;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(a.x) + (xo[i] + (k < K ? k : 0)) * (XBF ? 2 : 4);
+#pragma unroll
+      for (int h = 0; h < XR / 4; h++) {
+        const u32x4 v = at16(src + 16 * h);
+        o[i * (XR / 4) + h] = k < K ? v : u32x4{0, 0, 0, 0};
+      }
+    }
+  };
+  auto put_x = [&](const u32x4 (&v)[XR]) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const int row = i * 4 + g, at = row * 256 + (c16 ^ row) * 16;
+      if constexpr (XBF) {
+        *reinterpret_cast<u32x4*>(stage + at) = v[i];
+      } else {
+        u32x4 t[3];
+        split3(v[2 * i], v[2 * i + 1], t);
+#pragma unroll
+        for (int q = 0; q < 3; q++) *reinterpret_cast<u32x4*>(stage + q * 4096 + at) = t[q];
+      }
+    }
+    wave_sync();
+  };
+  if (wave >= units) return;
+  Weights<NV, NT> now;
+  u32x4 x[XU][XR];
+  now.load(a, at, wave * kUnit, g);
+  for (int unit = wave; unit < units; unit += waves) {
+    Weights<NV, NT> next;
+    const int k0 = unit * kUnit;
+    next.load(a, at, k0 + waves * kUnit, g);
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+      if (u % XU == 0) {
+#pragma unroll
+        for (int v = 0; v < XU; v++) load_x(k0 + (u + v) * 128, x[v]);
+      }
+      put_x(x[u % XU]);
+      u32x4 xv[4][TERMS];
+#pragma unroll
+      for (int j = 0; j < 4; j++)
+#pragma unroll
+        for (int q = 0; q < TERMS; q++) xv[j][q] = at16(stage + q * 4096 + c16 * 256 + ((g * 4 + j) ^ c16) * 16);
+      wave_sync();
+#pragma unroll
+      for (int t = 0; t < NT; t++) {
+        const u32x4 codes = pinned(now.w[t][u]);
+        const f32x2 sc = now.scale(t, u, k0 + u * 128, K, g);
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          const bf16x8 w = weights8<NV>(codes[j], j < 2 ? sc.x : sc.y);
+#pragma unroll
+          for (int q = 0; q < TERMS; q++) acc[t] = mfma(xv[j][q], w, acc[t]);
+        }
+      }
+    }
+    now = next;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the pairs of one expert
+// ---------------------------------------------------------------------------
+// What one workgroup does: `count` of an expert's pairs, in order, whose
+// numbers are in its list. expert = -1: there are not so many slots.
+struct Found {
+  int expert, count;
+};
+
+// The pairs are cut into slots: of each expert that has any, as many as its
+// pairs need at `rows` a slot. This finds the blockIdx.y-th of them. counts:
+// LDS for 16 bits an expert (from 65 pairs on), list: for `rows` numbers.
+__device__ __forceinline__ void find_slot(const Call& a, int rows, Found* s, uint32_t* counts, uint16_t* list) {
   const int lane = threadIdx.x & 63;
-  for (int i = threadIdx.x; i < kMaxExperts / 32; i += blockDim.x) s.seen[i] = 0;
+  if (a.pairs <= 64) {
+    // one load, and an expert's lanes are found by comparison, experts in order of appearance
+    if (threadIdx.x < 64) {
+      const int id = lane < a.pairs ? a.ids[lane] : -1;
+      uint64_t left = __builtin_amdgcn_ballot_w64((unsigned)id < (unsigned)a.experts), same = 0;
+      int slot = blockIdx.y, expert = -1, count = 0;
+      while (left != 0) {
+        expert = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+        same = __builtin_amdgcn_ballot_w64(id == expert);
+        count = __builtin_popcountll(same) - slot * rows;
+        if (count > 0) break;
+        slot -= (__builtin_popcountll(same) + rows - 1) / rows;
+        left &= ~same;
+        expert = -1;
+      }
+      const int at = __builtin_popcountll(same & ((1ull << lane) - 1)) - slot * rows;
+      if (expert >= 0 && id == expert && at >= 0 && at < rows) list[at] = lane;
+      if (lane == 0) *s = Found{expert, count < rows ? count : rows};
+    }
+    __syncthreads();
+    return;
+  }
+  for (int i = threadIdx.x; i < (a.experts + 1) / 2; i += blockDim.x) counts[i] = 0;
   __syncthreads();
   for (int p = threadIdx.x; p < a.pairs; p += blockDim.x) {
     const int e = a.ids[p];
-    if ((unsigned)e < (unsigned)a.experts) atomicOr(&s.seen[e >> 5], 1u << (e & 31));
+    if ((unsigned)e < (unsigned)a.experts) atomicAdd(&counts[e >> 1], e & 1 ? 1u << 16 : 1u);
   }
   __syncthreads();
   if (threadIdx.x < 64) {
-    int left = blockIdx.y, expert = -1;
-    for (int i = 0; i < (a.experts + 31) / 32; i++) {
-      const uint32_t w = s.seen[i];
-      const int n = __builtin_popcount(w);
-      if (left < n) {
-        uint32_t m = w;
-        for (; left > 0; left--) m &= m - 1;
-        expert = i * 32 + __builtin_ctz(m);
-        break;
-      }
-      left -= n;
+    // the lane whose experts hold the slot, then the expert
+    auto pairs_of = [&](int e) { return (int)((counts[e >> 1] >> (e & 1 ? 16 : 0)) & 0xffffu); };
+    const int per = (a.experts + 63) / 64, first = lane * per, end = first + per < a.experts ? first + per : a.experts;
+    int own = 0;
+    for (int e = first; e < end; e++) own += (pairs_of(e) + rows - 1) / rows;
+    int sum = own;
+    for (int step = 1; step < 64; step <<= 1) {
+      const int o = __shfl_up(sum, step, 64);
+      sum += lane >= step ? o : 0;
     }
-    int count = 0;
-    if (expert >= 0) {
-      for (int p0 = 0; p0 < a.pairs; p0 += 64) {
+    int expert = -1, count = 0, slot = (int)blockIdx.y - (sum - own);
+    if (slot >= 0 && slot < own) {
+      for (int e = first; e < end; e++) {
+        count = pairs_of(e);
+        expert = e;
+        const int n = (count + rows - 1) / rows;
+        if (slot < n) break;
+        slot -= n;
+      }
+    }
+    const uint64_t has = __builtin_amdgcn_ballot_w64(expert >= 0);
+    if (has != 0) {
+      const int src = __builtin_ctzll(has);
+      expert = __builtin_amdgcn_readlane(expert, src);
+      count = __builtin_amdgcn_readlane(count, src);
+      slot = __builtin_amdgcn_readlane(slot, src);
+      int at = -slot * rows;
+      for (int p0 = 0; p0 < a.pairs && at < rows; p0 += 64) {
         const bool mine = p0 + lane < a.pairs && a.ids[p0 + lane] == expert;
         const uint64_t m = __builtin_amdgcn_ballot_w64(mine);
-        if (mine) s.list[count + __builtin_popcountll(m & ((1ull << lane) - 1))] = p0 + lane;
-        count += __builtin_popcountll(m);
+        const int i = at + __builtin_popcountll(m & ((1ull << lane) - 1));
+        if (mine && i >= 0 && i < rows) list[i] = p0 + lane;
+        at += __builtin_popcountll(m);
       }
+      count -= slot * rows;
     }
-    if (lane == 0) {
-      s.expert = expert;
-      s.count = count;
-    }
+    if (lane == 0) *s = Found{expert, count < rows ? count : rows};
   }
   __syncthreads();
 }
 
-__device__ __forceinline__ void store_y(const MatvecArgs& a, int64_t p, int64_t n, float v) {
+__device__ __forceinline__ void store_y(const Call& a, int p, int n, float v) {
   if (a.y_bf16) reinterpret_cast<__bf16*>(a.y)[p * a.ld_y + n] = (__bf16)v;
   else reinterpret_cast<float*>(a.y)[p * a.ld_y + n] = v;
 }
 
-}  // namespace
-
-// A workgroup for 16 rows of W (of one expert); its waves take every eighth
-// piece of 128 along K, a lane 32 consecutive values of row lane % 16, which
-// are four operands of v_mfma_f32_16x16x32_bf16 against 16 rows of x.
-template <bool NV, bool XBF, bool BY_EXPERT>
-__global__ __launch_bounds__(64 * kWaves) void matvec_kernel(MatvecArgs a) {
-  __shared__ float red[kWaves][256];
-  __shared__ typename std::conditional<BY_EXPERT, Experts, int>::type found;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, g = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
-  int64_t expert = 0, count = a.pairs;
-  if constexpr (BY_EXPERT) {
-    if (blockIdx.y == 0) {  // pairs without an expert
-      for (int64_t i = threadIdx.x; i < a.pairs * 16; i += blockDim.x) {
-        const int64_t n = n0 + (i & 15);
-        if ((unsigned)a.ids[i >> 4] >= (unsigned)a.experts && n < a.N) store_y(a, i >> 4, n, 0.0f);
-      }
-    }
-    find_expert(a, found);
-    expert = found.expert;
-    count = found.count;
-    if (expert < 0) return;
+// Rows of zeros for pairs without an expert, columns n0 to n0 + cols - 1.
+__device__ __forceinline__ void zero_rows(const Call& a, int n0, int cols) {
+  for (int p = threadIdx.x / 16; p < a.pairs; p += blockDim.x / 16) {
+    if ((unsigned)a.ids[p] < (unsigned)a.experts) continue;
+    for (int n = n0 + (threadIdx.x & 15); n < n0 + cols && n < a.N; n += 16) store_y(a, p, n, 0.0f);
   }
-  const int64_t n = n0 + c16 < a.N ? n0 + c16 : a.N - 1;
-  const uint8_t* codes = a.codes + expert * a.c_es + n * a.ld_c + g * 16;
-  const uint8_t* scales = a.scales + expert * a.s_es + n * a.ld_s + (NV ? 2 * g : g);
+}
+
+__device__ __forceinline__ int64_t x_offset(const Call& a, int pair) {
+  const int row = a.repeat == 1 ? pair : (int)((unsigned)pair / (unsigned)a.repeat);
+  return row * a.ld_x;
+}
+
+// LDS of a few rows' form: x, and zeros where an operand needs them.
+template <bool NV, bool XBF, int RG>
+__host__ __device__ constexpr int few_bytes(int seg_units) {
+  return kOpRows<XBF, RG> * (seg_units * (kUnit * 2) + 16) + (NV && XBF ? kZeros : 0);
+}
+
+// Up to 4 RG pairs of one expert (its list, or else pairs 0 on) against the
+// workgroup's tiles of W: `rounds` times W >> part_shift, one after another,
+// each wave with the next unit's weights on their way while it
+// multiplies, over the ends of tiles too.
+template <bool NV, bool XBF, int RG, int W, bool LIST>
+__device__ __forceinline__ void few_pairs(const Call& a, int expert, const uint16_t* list, int live, uint8_t* lds) {
+  constexpr int MR = 4 * RG, ROWS = kOpRows<XBF, RG>;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c16 = lane & 15, g = lane >> 4;
+  const int per = W >> a.part_shift, parts = 1 << a.part_shift, part = wave & (parts - 1);
+  const int units = a.units, pitch = a.seg_units * (kUnit * 2) + 16;
+  float* red = reinterpret_cast<float*>(lds + few_bytes<NV, XBF, RG>(a.seg_units));  // [W][MR][16], if parts > 1
+  int n0 = (blockIdx.x * a.rounds * per + (wave >> a.part_shift)) * 16;
+  int64_t xo[MR];
+#pragma unroll
+  for (int i = 0; i < MR; i++) {
+    const int r = i < live ? i : live - 1;
+    xo[i] = x_offset(a, LIST ? __builtin_amdgcn_readfirstlane(list[r]) : r);
+  }
+  // item i of a segment's n: octet i of the first four rows, or i - n of the others
+  StageX<XBF> x;
+  int64_t x4[4];
+  int live4 = 0;
+  auto load_x = [&](int i, int n, int k0) {
+    const bool more = RG == 2 && i >= n;
+#pragma unroll
+    for (int r = 0; r < 4; r++) x4[r] = more ? xo[MR - 4 + r] : xo[r];
+    live4 = more ? live - 4 : live;
+    x.load(a, x4, live4, k0 + (more ? i - n : i) * 8);
+  };
+  const int first = (units < a.seg_units ? units : a.seg_units) * 64;
+  if (threadIdx.x < first * RG) load_x(threadIdx.x, first, 0);  // (before the weights, so as not to arrive behind them)
+  Place<1> at(a, expert, n0);
+  Weights<NV, 1> now;
+  now.load(a, at, part * kUnit, g);
+  FewRows<NV, XBF, RG> rows(pitch);
   const float ts = NV ? a.ts[expert] : 1.0f;
-  for (int64_t r0 = 0; r0 < count; r0 += 16) {
-    const int64_t r = r0 + c16 < count ? r0 + c16 : count - 1;
-    int64_t pair = r;
-    if constexpr (BY_EXPERT) pair = found.list[r];
-    const char* x = reinterpret_cast<const char*>(a.x) + (pair / a.repeat) * a.ld_x * (XBF ? 2 : 4);
-    f32x4 acc = {0, 0, 0, 0};
-#pragma unroll 4
-    for (int64_t k0 = wave * 128; k0 < a.K; k0 += 128 * kWaves) {
-      const int64_t k = k0 + g * 32;
-      u32x4 w = {0, 0, 0, 0};
-      uint32_t s = 0;
-      const bool first = k < a.K, second = k + 16 < a.K;
-      if (first) {
-        w = *reinterpret_cast<const u32x4*>(codes + (k0 >> 1));
-        if constexpr (NV) s = *reinterpret_cast<const uint16_t*>(scales + (k0 >> 4));
-        else s = scales[k0 >> 5];
+  for (int round = 0; round < a.rounds; round++) {
+    rows.clear();
+    const bool last_tile = round + 1 == a.rounds;
+    const Place<1> after(a, expert, last_tile ? n0 : n0 + per * 16);
+    int unit = part;
+    for (int u0 = 0; u0 < units; u0 += a.seg_units) {
+      const int here = units - u0 < a.seg_units ? units - u0 : a.seg_units;
+      if (round == 0 || units > a.seg_units) {
+        if (round > 0 || u0 > 0) __syncthreads();
+        if (FewRows<NV, XBF, RG>::DIAG && threadIdx.x < kZeros / 16)
+          *reinterpret_cast<u32x4*>(lds + ROWS * pitch + threadIdx.x * 16) = u32x4{0, 0, 0, 0};
+        for (int i = threadIdx.x; i < here * 64 * RG; i += 64 * W) {
+          if (round > 0 || u0 > 0 || i >= 64 * W) load_x(i, here * 64, u0 * kUnit);
+          const bool more = RG == 2 && i >= here * 64;
+          const int oct = more ? i - here * 64 : i;
+          x.put(a, live4, u0 * kUnit + oct * 8, lds + (more ? 4 * pitch : 0) + oct * 16, pitch, MR * pitch);
+        }
+        __syncthreads();
       }
-      float s0, s1;
-      if constexpr (NV) {
-        s0 = e4m3_decode(s & 0xffu);
-        s1 = second ? e4m3_decode(s >> 8) : 0.0f;
-      } else {
-        s0 = s1 = e8m0_scale_operand(s);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        Bf16Terms xv;
-        load_x<XBF>(x, k + 8 * j, j < 2 ? first : second, xv);
-        const bf16x8 b = weights8<NV>(w[j], j < 2 ? s0 : s1);
-#pragma unroll
-        for (int q = 0; q < (XBF ? 1 : 3); q++) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv.t[q], b, acc, 0, 0, 0);
+      for (; unit < u0 + here; unit += parts) {
+        Weights<NV, 1> next;
+        const bool over = unit + parts >= units;  // (of the last tile: bytes that nobody uses)
+        next.load(a, over ? after : at, over && !last_tile ? part * kUnit : (unit + parts) * kUnit, g);
+        rows.multiply(now, unit * kUnit, a.K, unit - u0, lds);
+        now = next;
       }
     }
+    f32x4 acc = rows.result();
+    if (parts > 1) {
+      if (round > 0) __syncthreads();
+      if (g < RG) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) red[wave][(4 * g + i) * 16 + c16] = acc[i];
-    __syncthreads();
-    if (threadIdx.x < 256) {
-      float sum = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWaves; w++) sum += red[w][threadIdx.x];
-      const int64_t row = r0 + (threadIdx.x >> 4), col = n0 + (threadIdx.x & 15);
-      if (row < count && col < a.N) {
-        int64_t p = row;
-        if constexpr (BY_EXPERT) p = found.list[row];
-        store_y(a, p, col, sum * ts);
+        for (int r = 0; r < 4; r++) red[(wave * MR + 4 * g + r) * 16 + c16] = acc[r];
       }
+      __syncthreads();
+      if (part == 0 && g < RG) {
+        for (int w = 1; w < parts; w++) {
+#pragma unroll
+          for (int r = 0; r < 4; r++) acc[r] += red[((wave + w) * MR + 4 * g + r) * 16 + c16];
+        }
+      }
+    }
+    if (part == 0 && g < RG && n0 + c16 < a.N) {
+#pragma unroll
+      for (int r = 0; r < 4; r++) {
+        const int row = 4 * g + r;
+        if (row < live) store_y(a, LIST ? list[row] : row, n0 + c16, acc[r] * ts);
+      }
+    }
+    at = after;
+    n0 += per * 16;
+  }
+}
+
+// `count` pairs of one expert (list NULL: all pairs) in passes of 16, against
+// the workgroup's 16 NT rows of W, which all its waves share.
+template <bool NV, bool XBF, int NT>
+__device__ __forceinline__ void many_pairs(const Call& a, int expert, const uint16_t* list, int count, uint8_t* lds) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6, c16 = lane & 15, g = lane >> 4;
+  const int n0 = blockIdx.x * (16 * NT);
+  uint8_t* stage = lds + wave * kStage<XBF>;
+  float* red = reinterpret_cast<float*>(lds + waves * kStage<XBF>);  // [waves][NT][16][16]
+  const Place<NT> at(a, expert, n0);
+  const float ts = NV ? a.ts[expert] : 1.0f;
+  for (int r0 = 0; r0 < count; r0 += 16) {
+    int64_t xo[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const int r = r0 + i * 4 + g < count ? r0 + i * 4 + g : count - 1;
+      xo[i] = x_offset(a, list ? list[r] : r);
+    }
+    f32x4 acc[NT];
+#pragma unroll
+    for (int t = 0; t < NT; t++) acc[t] = f32x4{0, 0, 0, 0};
+    many_rows<NV, XBF, NT>(a, at, xo, stage, wave, waves, acc);
+#pragma unroll
+    for (int t = 0; t < NT; t++)
+#pragma unroll
+      for (int r = 0; r < 4; r++) red[((wave * NT + t) * 16 + 4 * g + r) * 16 + c16] = acc[t][r];
+    __syncthreads();
+    for (int i = threadIdx.x; i < NT * 256; i += blockDim.x) {
+      float sum = 0.0f;
+      for (int w = 0; w < waves; w++) sum += red[w * (NT * 256) + i];
+      const int row = r0 + (i >> 4) % 16, col = n0 + (i / 256) * 16 + (i & 15);
+      if (row < count && col < a.N) store_y(a, list ? list[row] : row, col, sum * ts);
     }
     __syncthreads();
   }
 }
 
+}  // namespace
+
+template <bool NV, bool XBF, int RG, int W>
+__global__ __launch_bounds__(64 * W, 4) void matvec_few_kernel(Call a) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  few_pairs<NV, XBF, RG, W, false>(a, 0, nullptr, a.pairs, lds);
+}
+
+template <bool NV, bool XBF, int RG, int W>
+__global__ __launch_bounds__(64 * W, 4) void matvec_experts_few_kernel(Call a) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  __shared__ Found found;
+  __shared__ uint16_t list[4 * RG];
+  const int cols = (W >> a.part_shift) * a.rounds * 16;
+  if (blockIdx.y == 0) zero_rows(a, blockIdx.x * cols, cols);
+  find_slot(a, 4 * RG, &found, reinterpret_cast<uint32_t*>(lds), list);  // (x comes there later)
+  if (found.expert < 0) return;
+  few_pairs<NV, XBF, RG, W, true>(a, __builtin_amdgcn_readfirstlane(found.expert), list,
+                                  __builtin_amdgcn_readfirstlane(found.count), lds);
+}
+
+template <bool NV, bool XBF, int NT>
+__global__ __launch_bounds__(64 * kWaves) void matvec_many_kernel(Call a) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  many_pairs<NV, XBF, NT>(a, 0, nullptr, a.pairs, lds);
+}
+
+template <bool NV, bool XBF>
+__global__ __launch_bounds__(64 * kWaves) void matvec_experts_many_kernel(Call a) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  __shared__ Found found;
+  __shared__ uint16_t list[16];
+  if (blockIdx.y == 0) zero_rows(a, blockIdx.x * 16, 16);
+  find_slot(a, 16, &found, reinterpret_cast<uint32_t*>(lds), list);
+  if (found.expert >= 0) many_pairs<NV, XBF, 1>(a, found.expert, list, found.count, lds);
+}
+
 namespace {
+
+// Waves that share a row of W in the form of 16 rows: as many as have a unit
+// each, in equal rounds.
+int waves_for(int64_t units) {
+  const int64_t rounds = (units + kWaves - 1) / kWaves;
+  return units == 0 ? 1 : (int)((units + rounds - 1) / rounds);
+}
+
+constexpr int kLds = 160 * 1024, kLdsApart = 4 * 1024;  // of a CU; kept for what is not x
+
+template <bool NV, bool XBF, int RG, int W>
+hipError_t launch_few(Call& c, int tiles, int slots, hipStream_t s) {
+  const int cus = device_cu_count(), all = W == 16 ? 1 : 2;  // workgroups a CU
+  // waves for a tile: until there are eight a CU
+  c.part_shift = 0;
+  while ((1 << c.part_shift) < W && (1 << c.part_shift) < c.units && ((int64_t)tiles * slots << c.part_shift) < 8 * cus)
+    c.part_shift++;
+  const int red = c.part_shift > 0 ? W * RG * 256 : 0, room = (kLds / all - kLdsApart - red) / (kOpRows<XBF, RG> * kUnit * 2);
+  c.seg_units = c.units < room ? c.units : room;
+  // tiles one after another: once there are more workgroups than twice what fits at once, unless each would bring x anew
+  c.rounds = 1;
+  int per = W >> c.part_shift;
+  while (c.part_shift == 0 && c.seg_units == c.units && (int64_t)((tiles + per - 1) / per) * slots > 2 * all * cus) {
+    per += W;
+    c.rounds++;
+  }
+  const dim3 grid((tiles + per - 1) / per, slots), block(64 * W);
+  int lds = few_bytes<NV, XBF, RG>(c.seg_units) + red;
+  if (c.ids) {
+    lds = lds > 2 * c.experts + 2 ? lds : 2 * c.experts + 2;
+    hipLaunchKernelGGL((matvec_experts_few_kernel<NV, XBF, RG, W>), grid, block, lds, s, c);
+  } else {
+    hipLaunchKernelGGL((matvec_few_kernel<NV, XBF, RG, W>), grid, block, lds, s, c);
+  }
+  return hipGetLastError();
+}
+
+// Eight waves a workgroup where two have room on a CU with all of x, else 16.
+template <bool NV, bool XBF, int RG>
+hipError_t launch_few_rows(Call& c, int tiles, int slots, hipStream_t s) {
+  if (few_bytes<NV, XBF, RG>(c.units) + 8 * RG * 256 <= kLds / 2 - kLdsApart)
+    return launch_few<NV, XBF, RG, 8>(c, tiles, slots, s);
+  return launch_few<NV, XBF, RG, 16>(c, tiles, slots, s);
+}
 
 template <bool NV, bool XBF>
 hipError_t launch(const MatvecArgs& a, hipStream_t s) {
-  const unsigned tiles = (unsigned)((a.N + 15) / 16);
-  if (a.ids) {
-    const int64_t slots = a.pairs < a.experts ? a.pairs : a.experts;
-    hipLaunchKernelGGL((matvec_kernel<NV, XBF, true>), dim3(tiles, (unsigned)(slots > 0 ? slots : 1)), dim3(64 * kWaves), 0,
-                       s, a);
-  } else {
-    hipLaunchKernelGGL((matvec_kernel<NV, XBF, false>), dim3(tiles), dim3(64 * kWaves), 0, s, a);
+  const int64_t blk = NV ? 16 : 32;
+  auto last16 = [](int64_t bytes) { return (uint32_t)(bytes > 16 ? (bytes + 15) / 16 * 16 - 16 : 0); };
+  Call c{};
+  c.x = a.x;
+  c.codes = a.codes;
+  c.scales = a.scales;
+  c.ts = a.ts;
+  c.ids = a.ids;
+  c.y = a.y;
+  c.ld_x = a.ld_x;
+  c.c_es = a.c_es;
+  c.s_es = a.s_es;
+  c.ld_y = a.ld_y;
+  c.ld_c = (uint32_t)a.ld_c;
+  c.ld_s = (uint32_t)a.ld_s;
+  c.pairs = (int)a.pairs;
+  c.repeat = (int)a.repeat;
+  c.N = (int)a.N;
+  c.K = (int)a.K;
+  c.experts = a.experts;
+  c.units = (int)((a.K + kUnit - 1) / kUnit);
+  c.last_code = last16(a.K / 2);
+  c.last_scale = last16(a.K / blk);
+  c.y_bf16 = a.y_bf16;
+  const int tiles = (c.N + 15) / 16;
+  // experts that may have pairs, and how many slots of `rows` pairs they have at most
+  const int met = a.ids ? (c.pairs < c.experts ? c.pairs : c.experts) : 1;
+  auto slots = [&](int rows) { return a.ids ? (met + c.pairs / rows < c.pairs ? met + c.pairs / rows : c.pairs) : 1; };
+  if (c.units > 0 && c.pairs <= 8 * met) {
+    if (c.pairs <= (a.ids ? 2 : 4) * met) return launch_few_rows<NV, XBF, 1>(c, tiles, slots(4), s);
+    return launch_few_rows<NV, XBF, 2>(c, tiles, slots(8), s);
   }
+  const int waves = waves_for(c.units);
+  const dim3 block(64 * waves);
+  const unsigned one = (unsigned)(waves * (kStage<XBF> + 1024)), two = (unsigned)(waves * (kStage<XBF> + 2048));
+  if (a.ids) {
+    const unsigned lds = one > 2u * c.experts + 2 ? one : 2u * c.experts + 2;
+    hipLaunchKernelGGL((matvec_experts_many_kernel<NV, XBF>), dim3(tiles, slots(16)), block, lds, s, c);
+  }
+  else if (tiles >= 2 * device_cu_count())
+    hipLaunchKernelGGL((matvec_many_kernel<NV, XBF, 2>), dim3((tiles + 1) / 2), block, two, s, c);
+  else hipLaunchKernelGGL((matvec_many_kernel<NV, XBF, 1>), dim3(tiles), block, one, s, c);
   return hipGetLastError();
 }
 

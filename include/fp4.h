@@ -636,10 +636,9 @@ typedef struct fp4_matvec_args {
  *   (more: FP4_ERR_UNSUPPORTED).
  *   Weights quantized with FP4_HADAMARD stand for rotated ones: x has to be
  *   rotated by the same signs.
- * x 16-byte aligned with a row pitch of whole 16 bytes; codes 16-byte aligned,
- * ld_codes (>= K/2) and expert strides multiples of 16, code rows readable
- * up to the next multiple of 16 bytes; scales 2-byte aligned (NVFP4), their
- * pitches even. Errors: FP4_ERR_INVALID, FP4_ERR_UNSUPPORTED, FP4_ERR_ALIGN,
+ * x 16-byte aligned with a row pitch of whole 16 bytes; codes and scales
+ * 16-byte aligned, their pitches and expert strides multiples of 16, their rows
+ * readable up to the next multiple of 16 bytes, as for fp4_gemm. Errors: FP4_ERR_INVALID, FP4_ERR_UNSUPPORTED, FP4_ERR_ALIGN,
  * FP4_ERR_DEVICE, FP4_ERR_HIP. pairs = 0 or N = 0 is a valid empty call;
  * K = 0 gives zeros.
  */

@@ -193,6 +193,43 @@ def test_empty(fp4):
     assert fp4.matvec(torch.empty(0, 64).cuda(), q3, torch.empty(0, 4, dtype=torch.int32).cuda()).shape == (0, 4, 40)
 
 
+def test_no_columns(fp4):
+    """K = 0: a sum of nothing."""
+    q = fp4.Quantized(fp4.FP4_MXFP4, torch.empty(2, 40, 0, dtype=torch.uint8).cuda(), torch.empty(2, 40, 0, dtype=torch.uint8).cuda(), None)
+    ids = torch.tensor([[0], [1], [5]], dtype=torch.int32).cuda()
+    for x in (torch.empty(3, 0).cuda(), torch.empty(3, 0).cuda().bfloat16()):
+        assert fp4.matvec(x, q, ids).abs().sum() == 0
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M_,N,K", [(1, 70000, 96), (3, 33000, 544), (7, 20001, 1504), (2, 9000, 5120), (6, 17000, 5152)])
+def test_many_rows_of_weights(fp4, fmt, dtype, M_, N, K):
+    """Several tiles of W a wave, and x in LDS by parts."""
+    q = weights(fp4, fmt, N, K, 5)
+    x = torch.randn(M_, K, generator=torch.Generator().manual_seed(K)).to(DT[dtype]).cuda()
+    y = fp4.matvec(x, q)
+    cut = torch.cat((torch.arange(0, 200), torch.arange(N // 2, N // 2 + 100), torch.arange(N - 200, N)))
+    part = fp4.Quantized(q.fmt, q.codes.cpu()[cut], q.scales.cpu()[cut], q.tensor_scale)
+    check(y[:, cut.cuda()], x, M.values(part), DT[dtype])
+    same = fp4.matvec(x, fp4.Quantized(q.fmt, q.codes[100:300], q.scales[100:300], q.tensor_scale))
+    # (the waves that share a sum may differ with N: within two such bounds)
+    assert (y[:, 100:300].float() - same.float()).abs().max() <= 2.0 ** -6 * y.float().abs().max()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_tiles_of_many_experts(fp4, fmt, dtype):
+    T, k, E, N, K = 40, 2, 48, 1900, 1088
+    ids = torch.randint(0, E, (T, k), generator=torch.Generator().manual_seed(7), dtype=torch.int32)
+    q = weights(fp4, fmt, N, K, 6, E)
+    x = torch.randn(T, K, generator=torch.Generator().manual_seed(K)).to(DT[dtype]).cuda()
+    y = fp4.matvec(x, q, ids.cuda())
+    W = M.values(q)
+    for t in range(T):
+        check(y[t], x[t][None].expand(k, K), W[ids[t].numpy()], DT[dtype])
+
+
 def test_same_bits_twice_and_whatever_lies_beside(fp4):
     """The order of sums depends on K alone: a row's result does not change
     with the rows beside it, nor from call to call, within one form."""
