@@ -182,6 +182,9 @@ struct RouteArgs {
   const float* bias;
   float* weights;
   int32_t* ids;  // read by the backward pass
+  // set at launch: rows readable four logits at a time; lanes that make a group, 0 if not whole lanes
+  bool vec, vec_bias;
+  int lanes_of_group;
 };
 
 struct RouteBackwardArgs {
@@ -189,10 +192,11 @@ struct RouteBackwardArgs {
   const float* grad;  // [tokens][top_k]
   void* out;
   int64_t ld_out;
+  bool vec_out;
 };
 
-hipError_t launch_moe_route(const RouteArgs& a, hipStream_t stream);
-hipError_t launch_moe_route_backward(const RouteBackwardArgs& b, hipStream_t stream);
+hipError_t launch_moe_route(RouteArgs a, hipStream_t stream);
+hipError_t launch_moe_route_backward(RouteBackwardArgs b, hipStream_t stream);
 
 struct GroupArgs {
   int64_t pairs;

@@ -27,7 +27,9 @@ using namespace fp4dev;
 
 namespace {
 
-constexpr double kNone = -DBL_MAX;  // key of an expert that may not be chosen
+// Keys of experts that may not be chosen: below kNone, where no float lies.
+constexpr uint32_t kNoneHigh = 0xffe00000u;
+constexpr double kNone = -0x1p1000;
 constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596303e-8f, kLn2 = 0.693147182f;
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
@@ -95,12 +97,13 @@ __device__ __forceinline__ float from_lane(float v, int i) { return __shfl(v, i,
 template <int L>
 __device__ __forceinline__ double from_lane(double v, int i) { return __shfl(v, i, L); }
 
+// v of expert e; -inf and NaN make the key of one that may not be chosen.
 __device__ __forceinline__ double make_key(float v, int e) {
-  // (-0 and +0 are equal logits; +inf and the index would make a NaN)
-  const double d = v == __builtin_inff() ? 0x1p200 : (double)(v + 0.0f);
-  uint64_t u = __builtin_bit_cast(uint64_t, d);
-  const uint32_t turn = (int64_t)u < 0 ? 0u : 1023u;
-  return __builtin_bit_cast(double, u | ((uint32_t)e ^ turn));
+  // (-0 and +0 are equal logits; +inf with an index would be a NaN)
+  const uint64_t u = __builtin_bit_cast(uint64_t, (double)(__builtin_fminf(v, FLT_MAX) + 0.0f));
+  const uint32_t hi = (uint32_t)(u >> 32), turn = ~(uint32_t)((int32_t)hi >> 31) & 1023u;
+  const uint32_t lo = (uint32_t)u | ((uint32_t)e ^ turn);
+  return __builtin_bit_cast(double, ((uint64_t)(v > -__builtin_inff() ? hi : kNoneHigh) << 32) | lo);
 }
 __device__ __forceinline__ int key_index(double k) {
   const uint64_t u = __builtin_bit_cast(uint64_t, k);
@@ -108,6 +111,54 @@ __device__ __forceinline__ int key_index(double k) {
 }
 __device__ __forceinline__ float key_value(double k) {
   return (float)__builtin_bit_cast(double, __builtin_bit_cast(uint64_t, k) & ~(uint64_t)1023);
+}
+
+// The lane's VPL numbers of a row (logits, or the bias), `pad` past the last:
+// 16 bytes (8 of bf16) at a time where rows are made of such pieces. No load
+// waits for another: those past the end read the last piece again.
+template <int VPL, bool BF16>
+__device__ __forceinline__ void load_part(const void* row, int n, bool vec, int lane, float pad, float (&l)[VPL]) {
+  if constexpr (VPL >= 4) {
+    if (vec) {
+      uint32_t w[VPL];
+#pragma unroll
+      for (int i = 0; i < VPL; i += 4) {
+        const int e = lane * VPL + i < n ? lane * VPL + i : n - 4;
+        if constexpr (BF16) {
+          const u32x2 h = *reinterpret_cast<const u32x2*>(reinterpret_cast<const uint16_t*>(row) + e);
+          w[i] = h.x;
+          w[i + 1] = h.y;
+        } else {
+          const u32x4 h = *reinterpret_cast<const u32x4*>(reinterpret_cast<const float*>(row) + e);
+          w[i] = h.x;
+          w[i + 1] = h.y;
+          w[i + 2] = h.z;
+          w[i + 3] = h.w;
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < VPL; v++) {
+        const uint32_t word = BF16 ? w[v / 4 * 4 + v % 4 / 2] : w[v];
+        const float f = !BF16 ? __builtin_bit_cast(float, word) : v % 2 ? bf16_hi(word) : bf16_lo(word);
+        l[v] = lane * VPL + v < n ? f : pad;
+      }
+      return;
+    }
+  }
+  uint32_t w[VPL];
+#pragma unroll
+  for (int v = 0; v < VPL; v++) {
+    const int e = lane * VPL + v < n ? lane * VPL + v : n - 1;
+    w[v] = BF16 ? (uint32_t)reinterpret_cast<const uint16_t*>(row)[e] << 16 : reinterpret_cast<const uint32_t*>(row)[e];
+  }
+#pragma unroll
+  for (int v = 0; v < VPL; v++) l[v] = lane * VPL + v < n ? __builtin_bit_cast(float, w[v]) : pad;
+}
+
+template <int VPL>
+__device__ __forceinline__ void load_logits(const RouteArgs& a, const void* row, int lane, float pad, float (&l)[VPL]) {
+  if (a.bf16) load_part<VPL, true>(row, a.experts, a.vec, lane, pad, l);
+  else load_part<VPL, false>(row, a.experts, a.vec, lane, pad, l);
 }
 
 __device__ __forceinline__ float load_logit(const RouteArgs& a, const void* row, int e) {
@@ -118,15 +169,79 @@ __device__ __forceinline__ const void* logit_row(const RouteArgs& a, int64_t t) 
   return reinterpret_cast<const char*>(a.logits) + t * a.ld * (a.bf16 ? 2 : 4);
 }
 
-// The kept groups (bit g) of the token, from the choice values c of its
-// experts; `c` of experts that may not be chosen is -inf. `gap`: the
+// f(value of another lane of the row of 16, that lane) for each of the 15.
+template <int N, typename T, typename F>
+__device__ __forceinline__ void turns(T v, int lane, F f) {
+  if constexpr (N < 16) {
+    auto turn = [](int x) { return __builtin_amdgcn_mov_dpp(x, 0x120 + N, 0xF, 0xF, true); };  // row_ror:N
+    T o;
+    if constexpr (sizeof(T) == 8) {
+      const uint64_t u = __builtin_bit_cast(uint64_t, v);
+      o = __builtin_bit_cast(T, ((uint64_t)(uint32_t)turn((int)(u >> 32)) << 32) | (uint32_t)turn((int)(uint32_t)u));
+    } else {
+      o = __builtin_bit_cast(T, turn(__builtin_bit_cast(int, v)));
+    }
+    f(o, turn(lane));
+    turns<N + 1>(v, lane, f);
+  }
+}
+
+// The lane's keys in descending order (Batcher's odd-even merge sort).
+template <int N>
+__device__ __forceinline__ void sort_down(double (&key)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; i++)
+          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const double x = key[i + j], y = key[i + j + k];
+            key[i + j] = __builtin_fmax(x, y);
+            key[i + j + k] = __builtin_fmin(x, y);
+          }
+}
+
+// Which of the lane's experts belong to the groups kept (bit v), from the
+// choice values c; c of experts that may not be chosen is -inf. `gap`: the
 // difference between the last rank kept and the first left out, `size` the
 // larger magnitude that entered either.
 template <int L, int VPL, typename T>
-__device__ __forceinline__ uint64_t keep_groups(const RouteArgs& a, const T (&c)[VPL], int lane, T* gap, T* size) {
+__device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, const T (&c)[VPL], int lane, T* gap, T* size) {
   const int gs = a.group_size, G = a.groups;
   const T none = -(T)__builtin_inff();
   T rank = none, mag = (T)0;  // of group `lane`
+  if (L == 16 && a.lanes_of_group > 0) {
+    // whole lanes make a group (1, 2, 4 or 8 of them): its best two in each of its lanes
+    T b1 = none, b2 = none;
+#pragma unroll
+    for (int v = 0; v < VPL; v++) {
+      b2 = __builtin_elementwise_max(b2, __builtin_elementwise_min(b1, c[v]));
+      b1 = __builtin_elementwise_max(b1, c[v]);
+    }
+    auto join = [&](T o1, T o2) {
+      b2 = __builtin_elementwise_max(__builtin_elementwise_max(b2, o2), __builtin_elementwise_min(b1, o1));
+      b1 = __builtin_elementwise_max(b1, o1);
+    };
+    const int q = a.lanes_of_group;
+    if (q > 1) join(move<1>(b1), move<1>(b2));
+    if (q > 2) join(move<2>(b1), move<2>(b2));
+    if (q > 4) join(move<4>(b1), move<4>(b2));
+    const bool two = a.best == 2 && b2 > none;
+    rank = two ? b1 + b2 : b1;
+    mag = __builtin_elementwise_max(__builtin_elementwise_abs(b1), two ? __builtin_elementwise_abs(b2) : (T)0);
+    // lanes ahead of this one: those of better groups
+    const int mine = lane & -q;
+    int ahead = 0;
+    turns<1>(rank, lane, [&](T r, int from) { ahead += (int)(r > rank) | ((int)(r == rank) & (int)(from < mine)); });
+    const bool there = rank > none, kept = there && ahead < a.top_groups * q;
+    const T big = (T)__builtin_inff();
+    *gap = reduce<L>(kept ? rank : big, Min()) - reduce<L>(there && !kept ? rank : none, Max());
+    *size = reduce<L>(there ? mag : (T)0, Max());
+    return kept ? ~0u : 0u;
+  }
   auto add = [](T& b1, T& b2, T x) {
     b2 = __builtin_elementwise_max(b2, __builtin_elementwise_min(b1, x));
     b1 = __builtin_elementwise_max(b1, x);
@@ -163,73 +278,81 @@ __device__ __forceinline__ uint64_t keep_groups(const RouteArgs& a, const T (&c)
   const T big = (T)__builtin_inff();
   *gap = reduce<L>(kept ? rank : big, Min()) - reduce<L>(there && !kept ? rank : none, Max());
   *size = reduce<L>(there ? mag : (T)0, Max());
-  uint64_t mask = __builtin_amdgcn_ballot_w64(kept);
+  uint64_t mask = __builtin_amdgcn_ballot_w64(kept);  // bit g for group g
   if constexpr (L == 16) mask = (mask >> (threadIdx.x & 48)) & 0xffffu;
-  return mask;
-}
-
-// The experts' groups among those kept: bit v of the result.
-template <int VPL>
-__device__ __forceinline__ uint32_t members(const RouteArgs& a, uint64_t kept, int lane) {
-  int g = lane * VPL / a.group_size, left = a.group_size - (lane * VPL - g * a.group_size);
-  uint32_t m = 0;
+  int g = lane * VPL / gs, left = gs - (lane * VPL - g * gs);
+  uint32_t in = 0;
 #pragma unroll
   for (int v = 0; v < VPL; v++) {
-    m |= (uint32_t)((kept >> (g & 63)) & 1) << v;
+    in |= (uint32_t)((mask >> (g & 63)) & 1) << v;
     if (--left == 0) {
       g++;
-      left = a.group_size;
+      left = gs;
     }
   }
-  return m;
+  return in;
 }
 
-// The row's choice in double: slot j's expert goes to lane j (and j - L to
-// its `more`).
+// The sum of exp(l - m) over the row in double, and m. spare: LDS for VPL
+// numbers of each thread (four at a time, to keep these rare paths short).
 template <int L, int VPL>
-__device__ __forceinline__ void choose_exactly(const RouteArgs& a, int64_t t, int lane, int* mine, int* more) {
+__device__ __forceinline__ double softmax_sum(const float (&l)[VPL], float m, double* spare) {
+  double sum = 0;
+#pragma unroll
+  for (int v = 0; v < VPL; v++) spare[v * 256 + threadIdx.x] = l[v] > neg_inf() ? (double)l[v] - (double)m : -1e9;
+#pragma unroll 4
+  for (int v = 0; v < VPL; v++) sum += exp(spare[v * 256 + threadIdx.x]);
+  return reduce<L>(sum, Add());
+}
+
+__device__ __forceinline__ double exact_score(const RouteArgs& a, double z, double m, double inv_sum) {
+  const double p = exp(a.sigmoid ? -__builtin_fabs(z) : z - m);
+  return a.sigmoid ? (z >= 0 ? 1.0 : p) / (1.0 + p) : p * inv_sum;
+}
+
+// The first n lanes hold one candidate each, in an order that their scores'
+// errors make unsure; the row's other experts are surely behind them. The
+// exact order: lane j gets the j-th. (Lanes of a row of 16.)
+__device__ __forceinline__ int order_exactly(const RouteArgs& a, const void* row, int lane, int id, int n, double m,
+                                             double inv_sum) {
+  const bool there = lane < n;
+  const double c = there ? exact_score(a, load_logit(a, row, id), m, inv_sum) + (a.bias ? a.bias[id] : 0.0f) : -DBL_MAX;
+  int rank = 0;
+  turns<1>(c, lane, [&](double o, int from) {
+    const int oid = __shfl(id, from, 16);
+    rank += (int)(from < n) & ((int)(o > c) | ((int)(o == c) & (int)(oid < id)));
+  });
+  const int to = (threadIdx.x & 48) | (there ? rank : lane);
+  return __builtin_amdgcn_ds_permute(to * 4, id);
+}
+
+// The whole row's choice in double: slot j's expert goes to lane j (and j - L
+// to its `more`).
+template <int L, int VPL>
+__device__ __forceinline__ void choose_exactly(const RouteArgs& a, int64_t t, int lane, float m, double* spare, int* mine,
+                                               int* more) {
   const void* row = logit_row(a, t);
-  double c[VPL], m = -(double)__builtin_inff();
-  const double none = m;
+  const double none = -(double)__builtin_inff();
+  double c[VPL], inv_sum = 1;
+  {
+    float l[VPL];
+    load_logits<VPL>(a, row, lane, neg_inf(), l);
+    if (!a.sigmoid) inv_sum = 1.0 / softmax_sum<L>(l, m, spare);
 #pragma unroll
+    for (int v = 0; v < VPL; v++) spare[v * 256 + threadIdx.x] = l[v] == l[v] ? (double)l[v] : none;
+  }
+#pragma unroll 4
   for (int v = 0; v < VPL; v++) {
-    const int e = lane * VPL + v;
-    c[v] = e < a.experts ? (double)load_logit(a, row, e) : none;
-    c[v] = c[v] == c[v] ? c[v] : none;
-    m = __builtin_fmax(m, c[v]);
+    const int e = lane * VPL + v < a.experts ? lane * VPL + v : a.experts - 1;
+    const double z = spare[v * 256 + threadIdx.x], b = a.bias ? (double)a.bias[e] : 0.0;
+    const double s = exact_score(a, z, m, inv_sum) + b;
+    spare[v * 256 + threadIdx.x] = z > none && b == b ? s : none;
   }
-  m = reduce<L>(m, Max());
-  if (a.sigmoid) {
 #pragma unroll
-    for (int v = 0; v < VPL; v++) {
-      const double z = __builtin_fabs(c[v]), small = exp(-z);
-      if (c[v] > none) c[v] = (c[v] >= 0 ? 1.0 : small) / (1.0 + small);
-    }
-  } else {
-    double sum = 0;
-#pragma unroll
-    for (int v = 0; v < VPL; v++) {
-      const double p = c[v] > none ? exp(c[v] - m) : 0;
-      sum += p;
-      if (c[v] > none) c[v] = p;
-    }
-    sum = reduce<L>(sum, Add());
-#pragma unroll
-    for (int v = 0; v < VPL; v++) {
-      if (c[v] > none) c[v] /= sum;
-    }
-  }
-  if (a.bias) {
-#pragma unroll
-    for (int v = 0; v < VPL; v++) {
-      const int e = lane * VPL + v;
-      const double b = e < a.experts ? (double)a.bias[e] : none;
-      c[v] = c[v] > none && b == b ? c[v] + b : none;
-    }
-  }
+  for (int v = 0; v < VPL; v++) c[v] = spare[v * 256 + threadIdx.x];
   if (a.top_groups < a.groups) {
     double gap, size;
-    const uint32_t in = members<VPL>(a, keep_groups<L, VPL>(a, c, lane, &gap, &size), lane);
+    const uint32_t in = keep_groups<L, VPL>(a, c, lane, &gap, &size);
 #pragma unroll
     for (int v = 0; v < VPL; v++) c[v] = (in >> v) & 1 ? c[v] : none;
   }
@@ -249,14 +372,9 @@ __device__ __forceinline__ void choose_exactly(const RouteArgs& a, int64_t t, in
         at = lane * VPL + v;
       }
     }
-    for (int step = 1; step < L; step <<= 1) {
-      const double o = __shfl_xor(best, step, L);
-      const int oat = __shfl_xor(at, step, L);
-      if (o > best || (o == best && oat < at)) {
-        best = o;
-        at = oat;
-      }
-    }
+    const double top = reduce<L>(best, Max());
+    at = (int)reduce<L>(best == top ? (float)at : 4096.0f, Min());  // (indices are exact in fp32)
+    best = top;
     if (lane == (j & (L - 1))) (j < L ? *mine : *more) = best > none ? at : -1;
 #pragma unroll
     for (int v = 0; v < VPL; v++) c[v] = lane * VPL + v == at ? none : c[v];
@@ -265,17 +383,19 @@ __device__ __forceinline__ void choose_exactly(const RouteArgs& a, int64_t t, in
 
 }  // namespace
 
-template <int L, int VPL>
-__global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
+// D: keys a lane may give: VPL, or no fewer than the choices, the one after
+// them and what an unsure order may ask for.
+template <int L, int VPL, int D>
+__global__ __launch_bounds__(256, 4) void route_kernel(RouteArgs a) {
+  __shared__ double spare[VPL * 256];
   const int lane = threadIdx.x & (L - 1);
   const int64_t t = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
   if (t >= a.tokens) return;  // (a token's lanes leave together)
   const void* row = logit_row(a, t);
   float l[VPL], m = neg_inf();
+  load_logits<VPL>(a, row, lane, neg_inf(), l);
 #pragma unroll
   for (int v = 0; v < VPL; v++) {
-    const int e = lane * VPL + v;
-    l[v] = e < a.experts ? load_logit(a, row, e) : neg_inf();
     m = __builtin_fmaxf(m, l[v]);  // (NaN leaves it)
   }
   m = reduce<L>(m, Max());
@@ -295,53 +415,97 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
 #pragma unroll
   for (int v = 0; v < VPL; v++) c[v] = l[v] == l[v] ? l[v] : neg_inf();
   if (by_score || group_score) {
-    // sigmoid: 2^-23 for exp2 and 2^-23 for the reciprocal, one rounding of
-    // the sum, and 0.23 * 2^-24 for the rounded exponent: below 2^-21.
+    // sigmoid, p = exp(-l): s (1 - s) times p's relative error, which is 2^-23
+    // for exp2 and 1.5 |l| 2^-24 for its rounded argument, and s times 2^-24
+    // for the sum and 2^-23 for the reciprocal; s (1 - s) is at most 1/4 and
+    // |l| s (1 - s) below 0.23: in all below 2^-22.
     // softmax: (VPL + 6 + 3) 2^-24 relative for the sum, exponent as above:
     // below 2^-19 of the largest score, 1 / sum.
+    float b[VPL];
+    if (a.bias) {
+      load_part<VPL, false>(a.bias, a.experts, a.vec_bias, lane, neg_inf(), b);
+    } else {
+#pragma unroll
+      for (int v = 0; v < VPL; v++) b[v] = 0.0f;
+    }
     const float inv = __builtin_amdgcn_rcpf(sum);
-    unsure = a.sigmoid ? 0x1p-21f : 0x1p-19f * __builtin_fminf(inv, 1.0f) + 0x1p-24f;
+    unsure = a.sigmoid ? 0x1p-22f : 0x1p-19f * __builtin_fminf(inv, 1.0f) + 0x1p-24f;
 #pragma unroll
     for (int v = 0; v < VPL; v++) {
       const float x = a.sigmoid ? -l[v] : l[v] - m;
       const float p = __builtin_amdgcn_exp2f(x * kLog2e);
-      float s = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + p) : p * inv;
-      const int e = lane * VPL + v;
-      if (a.bias) s = s + (e < a.experts ? a.bias[e] : neg_inf());
+      const float s = (a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + p) : p * inv) + b[v];
       c[v] = c[v] > neg_inf() && s == s ? s : neg_inf();
     }
   }
   uint32_t in = ~0u;
   if (limited) {
     float gap, size;
-    in = members<VPL>(a, keep_groups<L, VPL>(a, c, lane, &gap, &size), lane);
+    in = keep_groups<L, VPL>(a, c, lane, &gap, &size);
     // a rank of two scores: each with its error, and three roundings
-    if (group_score) sure = !(gap <= 4.0f * unsure + 0x1p-21f * size);
+    if (group_score) sure = !(gap <= 4.0f * unsure + 0x1p-22f * size);
   }
 #pragma unroll
   for (int v = 0; v < VPL; v++) {
-    const float z = by_score ? c[v] : (l[v] == l[v] ? l[v] : neg_inf());
-    key[v] = z > neg_inf() && ((in >> v) & 1) ? make_key(z, lane * VPL + v) : kNone;
+    key[v] = make_key((in >> v) & 1 ? (by_score ? c[v] : l[v]) : neg_inf(), lane * VPL + v);
   }
-  int mine = -1, more = -1;
+  int mine = -1, more = -1, found = 0;
   float last = 0.0f;
-  double below = DBL_MAX;
-  for (int j = 0; j < a.top_k + (by_score ? 1 : 0); j++) {
-    double best = kNone;
+  // each lane's keys in order: the row's next is the best of their heads
+  sort_down<VPL>(key);
+  auto pop = [&]() {
+    const double best = reduce<L>(key[0], Max());
+    if (key[0] == best) {  // (one lane's, or nothing is left)
 #pragma unroll
-    for (int v = 0; v < VPL; v++) best = __builtin_fmax(best, key[v] < below ? key[v] : kNone);
-    best = reduce<L>(best, Max());
-    below = best;
-    if (j < a.top_k && lane == (j & (L - 1))) (j < L ? mine : more) = best > kNone ? key_index(best) : -1;
+      for (int v = 0; v + 1 < D; v++) key[v] = key[v + 1];
+      key[D - 1] = -DBL_MAX;
+    }
+    return best;
+  };
+  // Could two neighbours of the order be the other way round?
+  auto close = [&](float x, float y) {
+    return !(x - y > 2.0f * unsure + 0x1p-24f * (__builtin_fabsf(x) + __builtin_fabsf(y)));
+  };
+  bool ordered = true, next = false;  // next: lane top_k of a row of 16 holds the one after the chosen
+  for (int j = 0; j < a.top_k + (by_score ? 1 : 0); j++) {
+    const double best = pop();
+    if (lane == (j & (L - 1)) && j < 2 * L) (j < L ? mine : more) = best > kNone ? key_index(best) : -1;
     if (by_score) {
       const float now = key_value(best);
-      if (j > 0 && best > kNone)
-        sure = sure && last - now > 2.0f * unsure + 0x1p-23f * (__builtin_fabsf(last) + __builtin_fabsf(now));
+      if (j > 0 && best > kNone) {
+        next = j == a.top_k && close(last, now);
+        ordered = ordered && !close(last, now);
+      }
       last = now;
+      if (best > kNone) found = j + 1;
     }
-    if (!(best > kNone)) below = kNone;
   }
-  if (!sure) choose_exactly<L, VPL>(a, t, lane, &mine, &more);
+  if (!sure || (!ordered && a.top_k > 14)) {
+    choose_exactly<L, VPL>(a, t, lane, m, spare, &mine, &more);
+  } else if (!ordered) {
+    // more candidates, until one is surely behind (found: those before it)
+    if (!next && found > a.top_k) found = a.top_k;
+    bool enough = !next;
+    for (int j = a.top_k + 1; !enough && j < (D < VPL ? D : 16); j++) {
+      const double best = pop();
+      const float now = key_value(best);
+      enough = !(best > kNone) || !close(last, now);
+      if (!enough) {
+        if (lane == j) mine = key_index(best);
+        found = j + 1;
+        last = now;
+      }
+    }
+    if (enough) {
+      const double inv_sum = a.sigmoid ? 1.0 : 1.0 / softmax_sum<L>(l, m, spare);
+      mine = order_exactly(a, row, lane, mine, found, m, inv_sum);
+      if (lane >= found) mine = -1;
+    } else {
+      choose_exactly<L, VPL>(a, t, lane, m, spare, &mine, &more);
+    }
+  }
+  if (lane >= a.top_k) mine = -1;
+  if (lane + L >= a.top_k) more = -1;
   // weights: lane j has slot j (and slot j + L)
   const bool have2 = L < 32 && a.top_k > L;
   const float z1 = mine >= 0 ? load_logit(a, row, mine) : neg_inf();
@@ -387,12 +551,9 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackwardArgs b
   const bool dense = !a.sigmoid && !a.renormalize;
   float p[VPL], m = neg_inf(), sum = 1.0f;
   if (dense) {
+    load_logits<VPL>(a, row, lane, neg_inf(), p);
 #pragma unroll
-    for (int v = 0; v < VPL; v++) {
-      const int e = lane * VPL + v;
-      p[v] = e < a.experts ? load_logit(a, row, e) : neg_inf();
-      m = __builtin_fmaxf(m, p[v]);
-    }
+    for (int v = 0; v < VPL; v++) m = __builtin_fmaxf(m, p[v]);
     m = reduce<L>(m, Max());
     const float top = m > neg_inf() ? m : 0.0f;  // (a row of -inf has no part)
     sum = 0.0f;
@@ -466,6 +627,22 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackwardArgs b
     for (int v = 0; v < VPL; v++) p[v] += at == v ? val : 0.0f;
   }
   char* out = reinterpret_cast<char*>(b.out) + t * b.ld_out * (a.bf16 ? 2 : 4);
+  if constexpr (VPL >= 4) {
+    if (b.vec_out) {
+#pragma unroll
+      for (int i = 0; i < VPL; i += 4) {
+        const int at = lane * VPL + i;
+        if (at >= a.experts) continue;
+        if (a.bf16) {
+          const bf16x2 lo = {(__bf16)p[i], (__bf16)p[i + 1]}, hi = {(__bf16)p[i + 2], (__bf16)p[i + 3]};
+          *reinterpret_cast<u32x2*>(out + 2 * at) = u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+        } else {
+          *reinterpret_cast<f32x4*>(out + 4 * at) = f32x4{p[i], p[i + 1], p[i + 2], p[i + 3]};
+        }
+      }
+      return;
+    }
+  }
 #pragma unroll
   for (int v = 0; v < VPL; v++) {
     const int at = lane * VPL + v;
@@ -482,6 +659,17 @@ namespace {
 // which is done sooner (and what more than 16 groups, or more than 256 experts, need).
 bool wide_route(const RouteArgs& a) {
   return a.experts > 256 || a.groups > 16 || a.tokens <= 4 * device_cu_count();
+}
+
+// What depends on the lanes' shares: 16-byte rows, and lanes that make a group.
+void set_shares(RouteArgs& a) {
+  const int64_t piece = a.bf16 ? 8 : 16;  // of four logits
+  a.vec = (uintptr_t)a.logits % piece == 0 && (a.ld * (a.bf16 ? 2 : 4)) % piece == 0 && a.experts % 4 == 0;
+  a.vec_bias = (uintptr_t)a.bias % 16 == 0 && a.experts % 4 == 0;
+  int vpl = 1;
+  while (vpl * 16 < a.experts) vpl *= 2;
+  const int q = a.group_size / vpl;
+  a.lanes_of_group = a.group_size % vpl == 0 && (q & (q - 1)) == 0 && q <= 8 ? q : 0;
 }
 
 template <template <int, int> class LAUNCH, typename ARGS>
@@ -505,7 +693,10 @@ hipError_t route_by_size(const RouteArgs& a, const ARGS& args, hipStream_t s) {
 template <int L, int VPL>
 struct Forward {
   static hipError_t go(const RouteArgs& a, int64_t tokens, hipStream_t s) {
-    hipLaunchKernelGGL((route_kernel<L, VPL>), dim3((unsigned)((tokens + 256 / L - 1) / (256 / L))), dim3(256), 0, s, a);
+    const dim3 grid((unsigned)((tokens + 256 / L - 1) / (256 / L))), block(256);
+    constexpr int D = VPL < 12 ? VPL : 12;
+    if (a.top_k < D) hipLaunchKernelGGL((route_kernel<L, VPL, D>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((route_kernel<L, VPL, VPL>), grid, block, 0, s, a);
     return hipGetLastError();
   }
 };
@@ -520,8 +711,14 @@ struct Backward {
 
 }  // namespace
 
-hipError_t launch_moe_route(const RouteArgs& a, hipStream_t s) { return route_by_size<Forward>(a, a, s); }
-hipError_t launch_moe_route_backward(const RouteBackwardArgs& b, hipStream_t s) {
+hipError_t launch_moe_route(RouteArgs a, hipStream_t s) {
+  set_shares(a);
+  return route_by_size<Forward>(a, a, s);
+}
+hipError_t launch_moe_route_backward(RouteBackwardArgs b, hipStream_t s) {
+  set_shares(b.a);
+  const int64_t piece = b.a.bf16 ? 8 : 16;
+  b.vec_out = (uintptr_t)b.out % piece == 0 && (b.ld_out * (b.a.bf16 ? 2 : 4)) % piece == 0 && b.a.experts % 4 == 0;
   return route_by_size<Backward>(b.a, b, s);
 }
 
