@@ -10,7 +10,6 @@ using namespace fp4dev;
 
 namespace {
 
-constexpr int kWaves = 8;
 constexpr int kUnit = 512;        // K of a wave's unit: four pieces of 128, 256 bytes of each row's codes
 
 // What the kernels take: sizes in 32 bits, and what only sizes decide.
@@ -72,11 +71,6 @@ __device__ __forceinline__ void split3(const u32x4 lo, const u32x4 hi, u32x4 (&t
 #pragma unroll
     for (int q = 0; q < 3; q++) t[q][i] = (part[q][0] >> 16) | (part[q][1] & 0xffff0000u);
   }
-}
-
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
 }
 
 __device__ __forceinline__ f32x4 mfma(u32x4 x, bf16x8 w, f32x4 acc) {
@@ -211,9 +205,14 @@ struct StageX {
 // receives, are then x[r] times this group's own 32 values: a lane has its own
 // partial sums, and its block's scale multiplies four of them instead of
 // sixteen weights.
+// (With 16 rows that would take four such products, and scaling the weights
+// costs no more.)
+template <bool NV, bool XBF, int RG>
+constexpr bool diagonal = NV && XBF && RG <= 2;
+
 template <bool NV, bool XBF, int RG>
 struct FewRows {
-  static constexpr bool DIAG = NV && XBF;
+  static constexpr bool DIAG = diagonal<NV, XBF, RG>;
   static constexpr int ROWS = kOpRows<XBF, RG>, OT = DIAG ? RG : (ROWS + 15) / 16;
   int from[OT], step[OT];  // of the lane's operands: where those of a segment's first unit lie, and from unit to unit
   f32x4 acc[OT];
@@ -287,10 +286,14 @@ struct FewRows {
 #pragma unroll
       for (int r = 0; r < 4; r++) {
         float v = acc[0][r];
+        if constexpr (RG == 4) {
+          acc[0][r] = v + acc[1][r] + acc[2][r];
+          continue;
+        }
         if constexpr (RG == 1) {
           v = g < 3 ? v : 0.0f;
           v += xor_shfl<16>(v);
-        } else {
+        } else if constexpr (RG == 2) {
           v += g < 2 ? acc[1][r] : 0.0f;
         }
         v += xor_shfl<32>(v);
@@ -300,86 +303,6 @@ struct FewRows {
     return acc[0];
   }
 };
-
-// ---------------------------------------------------------------------------
-// 16 rows: each wave passes x through LDS by itself
-// ---------------------------------------------------------------------------
-// One piece of 128 of 16 activation rows, in planes of [16][16 slots] for each
-// term.
-template <bool XBF>
-constexpr int kStage = (XBF ? 1 : 3) * 16 * 256;
-
-// 16 rows of x (their offsets in elements: xo, rows 4 i + g for lane group g)
-// times NT tiles of 16 rows of W, over this wave's units of K.
-template <bool NV, bool XBF, int NT>
-__device__ __forceinline__ void many_rows(const Call& a, const Place<NT>& at, const int64_t (&xo)[4],
-                                          uint8_t* stage, int wave, int waves, f32x4 (&acc)[NT]) {
-  constexpr int TERMS = XBF ? 1 : 3, XR = XBF ? 4 : 8, XU = XBF ? 2 : 1;  // XU: pieces whose x is loaded at once
-  const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
-  const int K = a.K, units = a.units;
-  auto load_x = [&](int k0, u32x4 (&o)[XR]) {
-    const int k = k0 + c16 * 8;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(a.x) + (xo[i] + (k < K ? k : 0)) * (XBF ? 2 : 4);
-#pragma unroll
-      for (int h = 0; h < XR / 4; h++) {
-        const u32x4 v = at16(src + 16 * h);
-        o[i * (XR / 4) + h] = k < K ? v : u32x4{0, 0, 0, 0};
-      }
-    }
-  };
-  auto put_x = [&](const u32x4 (&v)[XR]) {
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const int row = i * 4 + g, at = row * 256 + (c16 ^ row) * 16;
-      if constexpr (XBF) {
-        *reinterpret_cast<u32x4*>(stage + at) = v[i];
-      } else {
-        u32x4 t[3];
-        split3(v[2 * i], v[2 * i + 1], t);
-#pragma unroll
-        for (int q = 0; q < 3; q++) *reinterpret_cast<u32x4*>(stage + q * 4096 + at) = t[q];
-      }
-    }
-    wave_sync();
-  };
-  if (wave >= units) return;
-  Weights<NV, NT> now;
-  u32x4 x[XU][XR];
-  now.load(a, at, wave * kUnit, g);
-  for (int unit = wave; unit < units; unit += waves) {
-    Weights<NV, NT> next;
-    const int k0 = unit * kUnit;
-    next.load(a, at, k0 + waves * kUnit, g);
-#pragma unroll
-    for (int u = 0; u < 4; u++) {
-      if (u % XU == 0) {
-#pragma unroll
-        for (int v = 0; v < XU; v++) load_x(k0 + (u + v) * 128, x[v]);
-      }
-      put_x(x[u % XU]);
-      u32x4 xv[4][TERMS];
-#pragma unroll
-      for (int j = 0; j < 4; j++)
-#pragma unroll
-        for (int q = 0; q < TERMS; q++) xv[j][q] = at16(stage + q * 4096 + c16 * 256 + ((g * 4 + j) ^ c16) * 16);
-      wave_sync();
-#pragma unroll
-      for (int t = 0; t < NT; t++) {
-        const u32x4 codes = pinned(now.w[t][u]);
-        const f32x2 sc = now.scale(t, u, k0 + u * 128, K, g);
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-          const bf16x8 w = weights8<NV>(codes[j], j < 2 ? sc.x : sc.y);
-#pragma unroll
-          for (int q = 0; q < TERMS; q++) acc[t] = mfma(xv[j][q], w, acc[t]);
-        }
-      }
-    }
-    now = next;
-  }
-}
 
 // ---------------------------------------------------------------------------
 // the pairs of one expert
@@ -487,43 +410,47 @@ __device__ __forceinline__ int64_t x_offset(const Call& a, int pair) {
 // LDS of a few rows' form: x, and zeros where an operand needs them.
 template <bool NV, bool XBF, int RG>
 __host__ __device__ constexpr int few_bytes(int seg_units) {
-  return kOpRows<XBF, RG> * (seg_units * (kUnit * 2) + 16) + (NV && XBF ? kZeros : 0);
+  return kOpRows<XBF, RG> * (seg_units * (kUnit * 2) + 16) + (diagonal<NV, XBF, RG> ? kZeros : 0);
 }
 
-// Up to 4 RG pairs of one expert (its list, or else pairs 0 on) against the
-// workgroup's tiles of W: `rounds` times W >> part_shift, one after another,
-// each wave with the next unit's weights on their way while it
-// multiplies, over the ends of tiles too.
+// Up to 4 RG pairs of one expert (its list, or else pairs `first` on) against
+// the workgroup's tiles of W: `rounds` times W >> part_shift, one after another,
+// each wave with the next unit's weights on their way while it multiplies, over
+// the ends of tiles too.
 template <bool NV, bool XBF, int RG, int W, bool LIST>
-__device__ __forceinline__ void few_pairs(const Call& a, int expert, const uint16_t* list, int live, uint8_t* lds) {
+__device__ __forceinline__ void few_pairs(const Call& a, int expert, const uint16_t* list, int first, int live,
+                                          uint8_t* lds) {
   constexpr int MR = 4 * RG, ROWS = kOpRows<XBF, RG>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c16 = lane & 15, g = lane >> 4;
   const int per = W >> a.part_shift, parts = 1 << a.part_shift, part = wave & (parts - 1);
   const int units = a.units, pitch = a.seg_units * (kUnit * 2) + 16;
   float* red = reinterpret_cast<float*>(lds + few_bytes<NV, XBF, RG>(a.seg_units));  // [W][MR][16], if parts > 1
   int n0 = (blockIdx.x * a.rounds * per + (wave >> a.part_shift)) * 16;
-  int64_t xo[MR];
-#pragma unroll
-  for (int i = 0; i < MR; i++) {
-    const int r = i < live ? i : live - 1;
-    xo[i] = x_offset(a, LIST ? __builtin_amdgcn_readfirstlane(list[r]) : r);
-  }
-  // item i of a segment's n: octet i of the first four rows, or i - n of the others
+  // item i of a segment's n * RG: octet i % n of row group i / n
   StageX<XBF> x;
-  int64_t x4[4];
-  int live4 = 0;
+  int group = 0, oct = 0;
   auto load_x = [&](int i, int n, int k0) {
-    const bool more = RG == 2 && i >= n;
+    group = 0;
+    oct = i;
 #pragma unroll
-    for (int r = 0; r < 4; r++) x4[r] = more ? xo[MR - 4 + r] : xo[r];
-    live4 = more ? live - 4 : live;
-    x.load(a, x4, live4, k0 + (more ? i - n : i) * 8);
+    for (int h = 1; h < RG; h++) {
+      group += i >= h * n ? 1 : 0;
+      oct -= i >= h * n ? n : 0;
+    }
+    int64_t xo[4];
+#pragma unroll
+    for (int r = 0; r < 4; r++) {
+      const int row = group * 4 + r < live ? group * 4 + r : live - 1;
+      const int pair = LIST ? (int)list[row] : first + row;
+      xo[r] = x_offset(a, RG == 1 ? __builtin_amdgcn_readfirstlane(pair) : pair);
+    }
+    x.load(a, xo, live - 4 * group, k0 + oct * 8);
   };
-  const int first = (units < a.seg_units ? units : a.seg_units) * 64;
-  if (threadIdx.x < first * RG) load_x(threadIdx.x, first, 0);  // (before the weights, so as not to arrive behind them)
+  const int n1 = (units < a.seg_units ? units : a.seg_units) * 64;
+  if (threadIdx.x < n1 * RG) load_x(threadIdx.x, n1, 0);  // (before the weights, so as not to arrive behind them)
   Place<1> at(a, expert, n0);
   Weights<NV, 1> now;
-  now.load(a, at, part * kUnit, g);
+  if (units > 0) now.load(a, at, part * kUnit, g);
   FewRows<NV, XBF, RG> rows(pitch);
   const float ts = NV ? a.ts[expert] : 1.0f;
   for (int round = 0; round < a.rounds; round++) {
@@ -539,9 +466,7 @@ __device__ __forceinline__ void few_pairs(const Call& a, int expert, const uint1
           *reinterpret_cast<u32x4*>(lds + ROWS * pitch + threadIdx.x * 16) = u32x4{0, 0, 0, 0};
         for (int i = threadIdx.x; i < here * 64 * RG; i += 64 * W) {
           if (round > 0 || u0 > 0 || i >= 64 * W) load_x(i, here * 64, u0 * kUnit);
-          const bool more = RG == 2 && i >= here * 64;
-          const int oct = more ? i - here * 64 : i;
-          x.put(a, live4, u0 * kUnit + oct * 8, lds + (more ? 4 * pitch : 0) + oct * 16, pitch, MR * pitch);
+          x.put(a, live - 4 * group, u0 * kUnit + oct * 8, lds + 4 * group * pitch + oct * 16, pitch, MR * pitch);
         }
         __syncthreads();
       }
@@ -572,47 +497,11 @@ __device__ __forceinline__ void few_pairs(const Call& a, int expert, const uint1
 #pragma unroll
       for (int r = 0; r < 4; r++) {
         const int row = 4 * g + r;
-        if (row < live) store_y(a, LIST ? list[row] : row, n0 + c16, acc[r] * ts);
+        if (row < live) store_y(a, LIST ? list[row] : first + row, n0 + c16, acc[r] * ts);
       }
     }
     at = after;
     n0 += per * 16;
-  }
-}
-
-// `count` pairs of one expert (list NULL: all pairs) in passes of 16, against
-// the workgroup's 16 NT rows of W, which all its waves share.
-template <bool NV, bool XBF, int NT>
-__device__ __forceinline__ void many_pairs(const Call& a, int expert, const uint16_t* list, int count, uint8_t* lds) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6, c16 = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * (16 * NT);
-  uint8_t* stage = lds + wave * kStage<XBF>;
-  float* red = reinterpret_cast<float*>(lds + waves * kStage<XBF>);  // [waves][NT][16][16]
-  const Place<NT> at(a, expert, n0);
-  const float ts = NV ? a.ts[expert] : 1.0f;
-  for (int r0 = 0; r0 < count; r0 += 16) {
-    int64_t xo[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const int r = r0 + i * 4 + g < count ? r0 + i * 4 + g : count - 1;
-      xo[i] = x_offset(a, list ? list[r] : r);
-    }
-    f32x4 acc[NT];
-#pragma unroll
-    for (int t = 0; t < NT; t++) acc[t] = f32x4{0, 0, 0, 0};
-    many_rows<NV, XBF, NT>(a, at, xo, stage, wave, waves, acc);
-#pragma unroll
-    for (int t = 0; t < NT; t++)
-#pragma unroll
-      for (int r = 0; r < 4; r++) red[((wave * NT + t) * 16 + 4 * g + r) * 16 + c16] = acc[t][r];
-    __syncthreads();
-    for (int i = threadIdx.x; i < NT * 256; i += blockDim.x) {
-      float sum = 0.0f;
-      for (int w = 0; w < waves; w++) sum += red[w * (NT * 256) + i];
-      const int row = r0 + (i >> 4) % 16, col = n0 + (i / 256) * 16 + (i & 15);
-      if (row < count && col < a.N) store_y(a, list ? list[row] : row, col, sum * ts);
-    }
-    __syncthreads();
   }
 }
 
@@ -621,7 +510,8 @@ __device__ __forceinline__ void many_pairs(const Call& a, int expert, const uint
 template <bool NV, bool XBF, int RG, int W>
 __global__ __launch_bounds__(64 * W, 4) void matvec_few_kernel(Call a) {
   extern __shared__ __align__(16) uint8_t lds[];
-  few_pairs<NV, XBF, RG, W, false>(a, 0, nullptr, a.pairs, lds);
+  const int first = blockIdx.y * (4 * RG), left = a.pairs - first;
+  few_pairs<NV, XBF, RG, W, false>(a, 0, nullptr, first, left < 4 * RG ? left : 4 * RG, lds);
 }
 
 template <bool NV, bool XBF, int RG, int W>
@@ -633,43 +523,20 @@ __global__ __launch_bounds__(64 * W, 4) void matvec_experts_few_kernel(Call a) {
   if (blockIdx.y == 0) zero_rows(a, blockIdx.x * cols, cols);
   find_slot(a, 4 * RG, &found, reinterpret_cast<uint32_t*>(lds), list);  // (x comes there later)
   if (found.expert < 0) return;
-  few_pairs<NV, XBF, RG, W, true>(a, __builtin_amdgcn_readfirstlane(found.expert), list,
+  few_pairs<NV, XBF, RG, W, true>(a, __builtin_amdgcn_readfirstlane(found.expert), list, 0,
                                   __builtin_amdgcn_readfirstlane(found.count), lds);
 }
 
-template <bool NV, bool XBF, int NT>
-__global__ __launch_bounds__(64 * kWaves) void matvec_many_kernel(Call a) {
-  extern __shared__ __align__(16) uint8_t lds[];
-  many_pairs<NV, XBF, NT>(a, 0, nullptr, a.pairs, lds);
-}
-
-template <bool NV, bool XBF>
-__global__ __launch_bounds__(64 * kWaves) void matvec_experts_many_kernel(Call a) {
-  extern __shared__ __align__(16) uint8_t lds[];
-  __shared__ Found found;
-  __shared__ uint16_t list[16];
-  if (blockIdx.y == 0) zero_rows(a, blockIdx.x * 16, 16);
-  find_slot(a, 16, &found, reinterpret_cast<uint32_t*>(lds), list);
-  if (found.expert >= 0) many_pairs<NV, XBF, 1>(a, found.expert, list, found.count, lds);
-}
-
 namespace {
-
-// Waves that share a row of W in the form of 16 rows: as many as have a unit
-// each, in equal rounds.
-int waves_for(int64_t units) {
-  const int64_t rounds = (units + kWaves - 1) / kWaves;
-  return units == 0 ? 1 : (int)((units + rounds - 1) / rounds);
-}
 
 constexpr int kLds = 160 * 1024, kLdsApart = 4 * 1024;  // of a CU; kept for what is not x
 
 template <bool NV, bool XBF, int RG, int W>
 hipError_t launch_few(Call& c, int tiles, int slots, hipStream_t s) {
   const int cus = device_cu_count(), all = W == 16 ? 1 : 2;  // workgroups a CU
-  // waves for a tile: until there are eight a CU
+  // waves for a tile: until each CU has a workgroup
   c.part_shift = 0;
-  while ((1 << c.part_shift) < W && (1 << c.part_shift) < c.units && ((int64_t)tiles * slots << c.part_shift) < 8 * cus)
+  while ((1 << c.part_shift) < W && (1 << c.part_shift) < c.units && ((int64_t)tiles * slots << c.part_shift) < W * cus)
     c.part_shift++;
   const int red = c.part_shift > 0 ? W * RG * 256 : 0, room = (kLds / all - kLdsApart - red) / (kOpRows<XBF, RG> * kUnit * 2);
   c.seg_units = c.units < room ? c.units : room;
@@ -694,8 +561,10 @@ hipError_t launch_few(Call& c, int tiles, int slots, hipStream_t s) {
 // Eight waves a workgroup where two have room on a CU with all of x, else 16.
 template <bool NV, bool XBF, int RG>
 hipError_t launch_few_rows(Call& c, int tiles, int slots, hipStream_t s) {
-  if (few_bytes<NV, XBF, RG>(c.units) + 8 * RG * 256 <= kLds / 2 - kLdsApart)
-    return launch_few<NV, XBF, RG, 8>(c, tiles, slots, s);
+  if constexpr (RG < 4) {
+    if (few_bytes<NV, XBF, RG>(c.units) + 8 * RG * 256 <= kLds / 2 - kLdsApart)
+      return launch_few<NV, XBF, RG, 8>(c, tiles, slots, s);
+  }
   return launch_few<NV, XBF, RG, 16>(c, tiles, slots, s);
 }
 
@@ -726,24 +595,15 @@ hipError_t launch(const MatvecArgs& a, hipStream_t s) {
   c.last_scale = last16(a.K / blk);
   c.y_bf16 = a.y_bf16;
   const int tiles = (c.N + 15) / 16;
-  // experts that may have pairs, and how many slots of `rows` pairs they have at most
+  // experts that may have pairs, and how many slots of `rows` pairs there are at most
   const int met = a.ids ? (c.pairs < c.experts ? c.pairs : c.experts) : 1;
-  auto slots = [&](int rows) { return a.ids ? (met + c.pairs / rows < c.pairs ? met + c.pairs / rows : c.pairs) : 1; };
-  if (c.units > 0 && c.pairs <= 8 * met) {
-    if (c.pairs <= (a.ids ? 2 : 4) * met) return launch_few_rows<NV, XBF, 1>(c, tiles, slots(4), s);
-    return launch_few_rows<NV, XBF, 2>(c, tiles, slots(8), s);
-  }
-  const int waves = waves_for(c.units);
-  const dim3 block(64 * waves);
-  const unsigned one = (unsigned)(waves * (kStage<XBF> + 1024)), two = (unsigned)(waves * (kStage<XBF> + 2048));
-  if (a.ids) {
-    const unsigned lds = one > 2u * c.experts + 2 ? one : 2u * c.experts + 2;
-    hipLaunchKernelGGL((matvec_experts_many_kernel<NV, XBF>), dim3(tiles, slots(16)), block, lds, s, c);
-  }
-  else if (tiles >= 2 * device_cu_count())
-    hipLaunchKernelGGL((matvec_many_kernel<NV, XBF, 2>), dim3((tiles + 1) / 2), block, two, s, c);
-  else hipLaunchKernelGGL((matvec_many_kernel<NV, XBF, 1>), dim3(tiles), block, one, s, c);
-  return hipGetLastError();
+  auto slots = [&](int rows) {
+    if (!a.ids) return (c.pairs + rows - 1) / rows;
+    return met + c.pairs / rows < c.pairs ? met + c.pairs / rows : c.pairs;
+  };
+  if (c.pairs <= (a.ids ? 2 : 4) * met) return launch_few_rows<NV, XBF, 1>(c, tiles, slots(4), s);
+  if (c.pairs <= 8 * met) return launch_few_rows<NV, XBF, 2>(c, tiles, slots(8), s);
+  return launch_few_rows<NV, XBF, 4>(c, tiles, slots(16), s);
 }
 
 }  // namespace

@@ -629,11 +629,12 @@ typedef struct fp4_matvec_args {
  * for the steps of a decoder that have one token or a few, where the weights'
  * bytes are all the work: they are read in 4 bits, once, and the activations
  * are not quantized, nor rounded at all (fp32 as three bf16 terms that hold
- * its 24 bits). Sums in fp32, y rounded once. Any number of rows is right;
- * past some dozens (of one matrix) fp4_gemm and fp4_gemm_grouped on quantized
- * activations are faster.
- *   ids outside [0, experts) give rows of zeros. With ids at most 4096 pairs
- *   (more: FP4_ERR_UNSUPPORTED).
+ * its 24 bits). Sums in fp32, y rounded once. The work grows with every 16
+ * rows; past some dozens (of one matrix) fp4_gemm and fp4_gemm_grouped on
+ * quantized activations are faster.
+ *   ids outside [0, experts) give rows of zeros. Limits (beyond:
+ *   FP4_ERR_UNSUPPORTED): 2^20 - 16 pairs, with ids 4096; N 2^26 - 64; K 2^24;
+ *   row pitches of codes and scales below 8 MiB.
  *   Weights quantized with FP4_HADAMARD stand for rotated ones: x has to be
  *   rotated by the same signs.
  * x 16-byte aligned with a row pitch of whole 16 bytes; codes and scales
