@@ -159,19 +159,18 @@ constexpr int kZeros = kUnit * 2;
 template <bool XBF, int RG>
 constexpr int kOpRows = (XBF ? 1 : 3) * 4 * RG;
 
-// One lane's part of the staging: eight numbers at k of four rows, of which
-// `live` are there (what the others hold meets only results that nobody reads).
-template <bool XBF>
+// fp32 rows on their way to LDS: a lane's eight numbers at k of four rows, of
+// which `live` are there (what the others hold meets only results that nobody
+// reads), cut into three terms.
 struct StageX {
-  static constexpr int XR = XBF ? 1 : 2;
-  u32x4 v[4][XR];
-  __device__ __forceinline__ void load(const Call& a, const int64_t* xo, int live, int k) {
+  u32x4 v[4][2];
+  __device__ __forceinline__ void load(const Call& a, const int64_t (&xo)[4], int live, int k) {
 #pragma unroll
     for (int r = 0; r < 4; r++) {
       if (r < live) {
-        const uint8_t* src = reinterpret_cast<const uint8_t*>(a.x) + (xo[r] + (k < a.K ? k : 0)) * (XBF ? 2 : 4);
-#pragma unroll
-        for (int h = 0; h < XR; h++) v[r][h] = at16(src + 16 * h);
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(a.x) + (xo[r] + (k < a.K ? k : 0)) * 4;
+        v[r][0] = at16(src);
+        v[r][1] = at16(src + 16);
       }
     }
   }
@@ -180,22 +179,35 @@ struct StageX {
 #pragma unroll
     for (int r = 0; r < 4; r++) {
       if (r < live) {
-        if (k >= a.K) {
+        if (k >= a.K) v[r][0] = v[r][1] = u32x4{0, 0, 0, 0};
+        u32x4 t[3];
+        split3(v[r][0], v[r][1], t);
 #pragma unroll
-          for (int h = 0; h < XR; h++) v[r][h] = u32x4{0, 0, 0, 0};
-        }
-        if constexpr (XBF) {
-          *reinterpret_cast<u32x4*>(to + r * pitch) = v[r][0];
-        } else {
-          u32x4 t[3];
-          split3(v[r][0], v[r][1], t);
-#pragma unroll
-          for (int q = 0; q < 3; q++) *reinterpret_cast<u32x4*>(to + q * plane + r * pitch) = t[q];
-        }
+        for (int q = 0; q < 3; q++) *reinterpret_cast<u32x4*>(to + q * plane + r * pitch) = t[q];
       }
     }
   }
 };
+
+// bf16 rows need no work on their way to LDS and are copied there directly: a
+// wave copies units of the rows, 1 KB each, lane i the 16 bytes 16 i of it. (No
+// lane waits, and no register is taken.) Past K: zeros.
+template <int W>
+__device__ __forceinline__ void copy_x(const Call& a, int64_t xo, int row, int u0, int here, int wave, uint8_t* lds,
+                                       int pitch) {
+  const int lane = threadIdx.x & 63;
+  for (int u = (wave - row) & (W - 1); u < here; u += W) {
+    const int k = (u0 + u) * kUnit + lane * 8;
+    uint8_t* to = lds + row * pitch + u * (kUnit * 2);
+    if (k < a.K) {
+      const uint8_t* from = reinterpret_cast<const uint8_t*>(a.x) + (xo + k) * 2;
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint8_t*)from,
+                                       (__attribute__((address_space(3))) uint8_t*)to, 16, 0, 0);
+    } else {
+      *reinterpret_cast<u32x4*>(to + lane * 16) = u32x4{0, 0, 0, 0};
+    }
+  }
+}
 
 // 4 RG rows of x, in LDS, times a wave's tile of 16 rows of W.
 //
@@ -426,8 +438,13 @@ __device__ __forceinline__ void few_pairs(const Call& a, int expert, const uint1
   const int units = a.units, pitch = a.seg_units * (kUnit * 2) + 16;
   float* red = reinterpret_cast<float*>(lds + few_bytes<NV, XBF, RG>(a.seg_units));  // [W][MR][16], if parts > 1
   int n0 = (blockIdx.x * a.rounds * per + (wave >> a.part_shift)) * 16;
-  // item i of a segment's n * RG: octet i % n of row group i / n
-  StageX<XBF> x;
+  auto offset_of = [&](int row) {
+    const int pair = LIST ? (int)list[row] : first + row;
+    return x_offset(a, pair);
+  };
+  // x for a segment: bf16 rows straight to LDS; fp32 as items i of n * RG in
+  // registers, octet i % n of row group i / n
+  StageX x;
   int group = 0, oct = 0;
   auto load_x = [&](int i, int n, int k0) {
     group = 0;
@@ -439,15 +456,17 @@ __device__ __forceinline__ void few_pairs(const Call& a, int expert, const uint1
     }
     int64_t xo[4];
 #pragma unroll
-    for (int r = 0; r < 4; r++) {
-      const int row = group * 4 + r < live ? group * 4 + r : live - 1;
-      const int pair = LIST ? (int)list[row] : first + row;
-      xo[r] = x_offset(a, RG == 1 ? __builtin_amdgcn_readfirstlane(pair) : pair);
-    }
+    for (int r = 0; r < 4; r++) xo[r] = offset_of(group * 4 + r < live ? group * 4 + r : live - 1);
     x.load(a, xo, live - 4 * group, k0 + oct * 8);
   };
-  const int n1 = (units < a.seg_units ? units : a.seg_units) * 64;
-  if (threadIdx.x < n1 * RG) load_x(threadIdx.x, n1, 0);  // (before the weights, so as not to arrive behind them)
+  auto copy_all = [&](int u0, int here) {
+    for (int row = 0; row < live; row++)
+      copy_x<W>(a, offset_of(__builtin_amdgcn_readfirstlane(row)), row, u0, here, wave, lds, pitch);
+  };
+  // (before the weights, so as not to arrive behind them)
+  const int in_lds = units < a.seg_units ? units : a.seg_units, n1 = in_lds * 64;
+  if constexpr (XBF) copy_all(0, in_lds);
+  else if (threadIdx.x < n1 * RG) load_x(threadIdx.x, n1, 0);
   Place<1> at(a, expert, n0);
   Weights<NV, 1> now;
   if (units > 0) now.load(a, at, part * kUnit, g);
@@ -464,9 +483,14 @@ __device__ __forceinline__ void few_pairs(const Call& a, int expert, const uint1
         if (round > 0 || u0 > 0) __syncthreads();
         if (FewRows<NV, XBF, RG>::DIAG && threadIdx.x < kZeros / 16)
           *reinterpret_cast<u32x4*>(lds + ROWS * pitch + threadIdx.x * 16) = u32x4{0, 0, 0, 0};
-        for (int i = threadIdx.x; i < here * 64 * RG; i += 64 * W) {
-          if (round > 0 || u0 > 0 || i >= 64 * W) load_x(i, here * 64, u0 * kUnit);
-          x.put(a, live - 4 * group, u0 * kUnit + oct * 8, lds + 4 * group * pitch + oct * 16, pitch, MR * pitch);
+        if constexpr (XBF) {
+          if (round > 0 || u0 > 0) copy_all(u0, here);
+          asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (the copies to LDS are counted there)
+        } else {
+          for (int i = threadIdx.x; i < here * 64 * RG; i += 64 * W) {
+            if (round > 0 || u0 > 0 || i >= 64 * W) load_x(i, here * 64, u0 * kUnit);
+            x.put(a, live - 4 * group, u0 * kUnit + oct * 8, lds + 4 * group * pitch + oct * 16, pitch, MR * pitch);
+          }
         }
         __syncthreads();
       }
@@ -539,7 +563,8 @@ hipError_t launch_few(Call& c, int tiles, int slots, hipStream_t s) {
   while ((1 << c.part_shift) < W && (1 << c.part_shift) < c.units && ((int64_t)tiles * slots << c.part_shift) < W * cus)
     c.part_shift++;
   const int red = c.part_shift > 0 ? W * RG * 256 : 0, room = (kLds / all - kLdsApart - red) / (kOpRows<XBF, RG> * kUnit * 2);
-  c.seg_units = c.units < room ? c.units : room;
+  // (all of x, or else whole turns of the waves)
+  c.seg_units = c.units < room ? c.units : room >> c.part_shift > 0 ? room >> c.part_shift << c.part_shift : room;
   // tiles one after another: once there are more workgroups than twice what fits at once, unless each would bring x anew
   c.rounds = 1;
   int per = W >> c.part_shift;
