@@ -920,11 +920,6 @@ static fp4_status plan_moe_combine(int32_t dtype, int64_t tokens, int32_t top_k,
   return FP4_OK;
 }
 
-// Rows of whole 16-byte pieces?
-static bool whole_pieces(const void* p, int64_t ld, int64_t width, int64_t esize) {
-  return aligned(p, 16) && (ld * esize) % 16 == 0 && (width * esize) % 16 == 0;
-}
-
 fp4_status fp4_moe_combine(int32_t dtype, int64_t tokens, int32_t top_k, int64_t width, const void* rows,
                            int64_t ld_rows, int64_t num_rows, const int32_t* place, const int32_t* kept,
                            const float* weights, void* out, int64_t ld_out, void* stream) {
@@ -939,7 +934,6 @@ fp4_status fp4_moe_combine(int32_t dtype, int64_t tokens, int32_t top_k, int64_t
   if (st != FP4_OK) return st;
   a.out = out;
   a.ld_out = ld_out;
-  a.vec_ok = whole_pieces(rows, ld_rows, width, es) && whole_pieces(out, ld_out, width, es);
   (void)hipGetLastError();
   return status_of(launch_moe_combine(a, static_cast<hipStream_t>(stream)));
 }
@@ -965,8 +959,6 @@ fp4_status fp4_moe_combine_backward(int32_t dtype, int64_t tokens, int32_t top_k
   b.grad_rows = grad_rows;
   b.ld_grad_rows = ld_grad_rows;
   b.grad_weights = grad_weights;
-  b.a.vec_ok = whole_pieces(grad_out, ld_grad, width, es) && whole_pieces(grad_rows, ld_grad_rows, width, es) &&
-               (!grad_weights || whole_pieces(rows, ld_rows, width, es));
   (void)hipGetLastError();
   return status_of(launch_moe_combine_backward(b, static_cast<hipStream_t>(stream)));
 }

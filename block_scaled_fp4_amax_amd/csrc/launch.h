@@ -225,7 +225,7 @@ struct DispatchArgs {
 hipError_t launch_moe_dispatch(const DispatchArgs& a, hipStream_t stream);
 
 struct CombineArgs {
-  bool bf16, vec_ok;  // vec_ok: every row in whole 16-byte pieces
+  bool bf16;
   int64_t tokens, width, num_rows;
   int top_k;
   const int32_t *place, *kept;  // NULL: row p, all rows

@@ -13,8 +13,8 @@ using namespace fp4dev;
 
 namespace {
 
-constexpr int kGroupWaves = 16;      // of a workgroup that sorts
-constexpr int kGroupPairs = 8192;    // pairs of one workgroup: 8 rounds of 64 a wave
+constexpr int kGroupWaves = 16;                     // of a workgroup that sorts
+constexpr int kGroupTurn = 64 * kGroupWaves;        // pairs of a round
 
 // The wave's lanes whose id is this lane's: one ballot for each bit of an id.
 __device__ __forceinline__ uint64_t same_id(int id, int bits) {
@@ -26,43 +26,43 @@ __device__ __forceinline__ uint64_t same_id(int id, int bits) {
   return m;
 }
 
-__device__ __forceinline__ int bucket(const GroupArgs& a, int64_t p) {
-  const int id = a.ids[p];
-  return (unsigned)id < (unsigned)a.experts ? id : a.experts;
-}
-
-// Pairs [first, last) of the workgroup, a consecutive part for each wave.
-struct Part {
-  int64_t first, last;
-};
-__device__ __forceinline__ Part wave_part(const GroupArgs& a) {
-  const int64_t lo = (int64_t)blockIdx.x * kGroupPairs;
-  const int64_t n = a.pairs - lo < kGroupPairs ? a.pairs - lo : kGroupPairs;
-  const int64_t per = ((n + 64 * kGroupWaves - 1) / (64 * kGroupWaves)) * 64;
-  const int w = threadIdx.x >> 6;
-  const int64_t f = per * w < n ? per * w : n, l = per * (w + 1) < n ? per * (w + 1) : n;
-  return {lo + f, lo + l};
-}
-
 // A wave's lanes see what its other lanes wrote to LDS.
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
 }
 
-// counts[w * (experts + 1) + e] = pairs of bucket e in wave w's part (at most
-// kGroupPairs in all: 16 bits).
-__device__ __forceinline__ void count_parts(const GroupArgs& a, uint16_t* counts) {
-  const int n = a.experts + 1, lane = threadIdx.x & 63;
-  for (int i = threadIdx.x; i < n * kGroupWaves; i += blockDim.x) counts[i] = 0;
+// The workgroup's pairs, R times 64 consecutive ones for each wave; the lane's
+// in registers, as buckets (a.experts: no expert; -1: no pair).
+template <int R>
+struct Pairs {
+  int bucket[R];
+  int first;  // the lane's pair of round 0
+  __device__ __forceinline__ Pairs(const GroupArgs& a) {
+    const int n = (int)a.pairs;
+    first = blockIdx.x * (R * kGroupTurn) + (threadIdx.x >> 6) * (R * 64) + (threadIdx.x & 63);
+#pragma unroll
+    for (int r = 0; r < R; r++) bucket[r] = a.ids[first + r * 64 < n ? first + r * 64 : 0];
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+      const int e = (unsigned)bucket[r] < (unsigned)a.experts ? bucket[r] : a.experts;
+      bucket[r] = first + r * 64 < n ? e : -1;
+    }
+  }
+};
+
+// counts[w * n + e] = pairs of bucket e in wave w's part, n the buckets
+// rounded up to even: 16 bits each, added to by halves of words.
+__device__ __forceinline__ int padded(int buckets) { return buckets + (buckets & 1); }
+template <int R>
+__device__ __forceinline__ void count_parts(const GroupArgs& a, const Pairs<R>& p, uint32_t* words) {
+  const int n = padded(a.experts + 1);
+  for (int i = threadIdx.x; i < n / 2 * kGroupWaves; i += 64 * kGroupWaves) words[i] = 0;
   __syncthreads();
-  uint16_t* mine = counts + (threadIdx.x >> 6) * n;
-  const Part part = wave_part(a);
-  for (int64_t p = part.first + lane; p < part.last; p += 64) {
-    const int e = bucket(a, p);
-    const uint64_t m = same_id(e, a.id_bits);
-    if ((m & ((1ull << lane) - 1)) == 0) mine[e] += __builtin_popcountll(m);  // (the lowest lane of each bucket)
-    wave_sync();
+  uint32_t* mine = words + (threadIdx.x >> 6) * (n / 2);
+#pragma unroll
+  for (int r = 0; r < R; r++) {
+    if (p.bucket[r] >= 0) atomicAdd(&mine[p.bucket[r] >> 1], p.bucket[r] & 1 ? 1u << 16 : 1u);
   }
   __syncthreads();
 }
@@ -70,14 +70,16 @@ __device__ __forceinline__ void count_parts(const GroupArgs& a, uint16_t* counts
 }  // namespace
 
 // Each workgroup's pairs of each bucket, for the scan that follows.
+template <int R>
 __global__ __launch_bounds__(64 * kGroupWaves) void group_count_kernel(GroupArgs a) {
   extern __shared__ uint32_t lds[];
-  uint16_t* counts = reinterpret_cast<uint16_t*>(lds);
-  count_parts(a, counts);
+  const Pairs<R> pairs(a);
+  count_parts(a, pairs, lds);
+  const uint16_t* counts = reinterpret_cast<uint16_t*>(lds);
   const int n = a.experts + 1;
-  for (int e = threadIdx.x; e < n; e += blockDim.x) {
+  for (int e = threadIdx.x; e < n; e += 64 * kGroupWaves) {
     uint32_t sum = 0;
-    for (int w = 0; w < kGroupWaves; w++) sum += counts[w * n + e];
+    for (int w = 0; w < kGroupWaves; w++) sum += counts[w * padded(n) + e];
     a.counts[(int64_t)blockIdx.x * n + e] = sum;
   }
 }
@@ -85,25 +87,34 @@ __global__ __launch_bounds__(64 * kGroupWaves) void group_count_kernel(GroupArgs
 // Scan and placement. With one workgroup the counts are its own; with more
 // they come from group_count_kernel, and each workgroup adds up what lies
 // before it.
+template <int R>
 __global__ __launch_bounds__(64 * kGroupWaves) void group_place_kernel(GroupArgs a) {
   extern __shared__ uint32_t lds[];
   const int n = a.experts + 1, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint32_t* base = lds;        // [n]: first row of each bucket
-  uint32_t* before = base + n; // [n]: pairs of the bucket in earlier workgroups
-  uint16_t* counts = reinterpret_cast<uint16_t*>(before + n);
-  count_parts(a, counts);
-  for (int e = threadIdx.x; e < n; e += blockDim.x) {
+  uint32_t* base = lds;         // [n]: first row of each bucket
+  uint32_t* before = base + n;  // [n]: pairs of the bucket in earlier workgroups
+  uint32_t* words = before + n;
+  uint16_t* counts = reinterpret_cast<uint16_t*>(words);
+  const Pairs<R> pairs(a);
+  count_parts(a, pairs, words);
+  for (int e = threadIdx.x; e < n; e += 64 * kGroupWaves) {
     uint32_t all = 0, early = 0;
-    if (gridDim.x == 1) {
-      for (int w = 0; w < kGroupWaves; w++) all += counts[w * n + e];
-    } else {
+    if (gridDim.x > 1) {
+#pragma unroll 8
       for (unsigned g = 0; g < gridDim.x; g++) {
         const uint32_t c = a.counts[(int64_t)g * n + e];
         all += c;
         early += g < blockIdx.x ? c : 0;
       }
     }
-    base[e] = all;
+    // each wave's next row of the bucket, counted from the workgroup's first
+    uint32_t at = 0;
+    for (int w = 0; w < kGroupWaves; w++) {
+      const uint32_t c = counts[w * padded(n) + e];
+      counts[w * padded(n) + e] = (uint16_t)at;
+      at += c;
+    }
+    base[e] = gridDim.x > 1 ? all : at;
     before[e] = early;
   }
   __syncthreads();
@@ -117,52 +128,69 @@ __global__ __launch_bounds__(64 * kGroupWaves) void group_place_kernel(GroupArgs
         const uint32_t o = __shfl_up(s, step, 64);
         s += lane >= step ? o : 0;
       }
-      if (e < n) base[e] = carry + s - own;
+      if (e < n) {
+        if (blockIdx.x == 0) a.offsets[e] = (int32_t)(carry + s - own);
+        base[e] = carry + s - own + before[e];
+      }
       carry += __shfl(s, 63, 64);
     }
   }
   __syncthreads();
-  if (blockIdx.x == 0)
-    for (int e = threadIdx.x; e < n; e += blockDim.x) a.offsets[e] = (int32_t)base[e];
-  // each wave's next row of each bucket, counted from the workgroup's first
-  for (int e = threadIdx.x; e < n; e += blockDim.x) {
-    base[e] += before[e];
-    uint32_t at = 0;
-    for (int w = 0; w < kGroupWaves; w++) {
-      const uint32_t c = counts[w * n + e];
-      counts[w * n + e] = at;
-      at += c;
+  uint16_t* mine = counts + wave * padded(n);
+#pragma unroll
+  for (int r = 0; r < R; r++) {
+    const int e = pairs.bucket[r];
+    if (e >= 0) {
+      const uint64_t m = same_id(e, a.id_bits), earlier = m & ((1ull << lane) - 1);
+      const uint32_t row = base[e] + mine[e] + __builtin_popcountll(earlier);
+      wave_sync();
+      if (earlier == 0) mine[e] += __builtin_popcountll(m);  // (the lowest lane of each bucket)
+      const int p = pairs.first + r * 64;
+      a.order[row] = p;
+      a.place[p] = (int32_t)row;
     }
-  }
-  __syncthreads();
-  uint16_t* mine = counts + wave * n;
-  const Part part = wave_part(a);
-  for (int64_t p = part.first + lane; p < part.last; p += 64) {
-    const int e = bucket(a, p);
-    const uint64_t m = same_id(e, a.id_bits), earlier = m & ((1ull << lane) - 1);
-    const uint32_t row = base[e] + mine[e] + __builtin_popcountll(earlier);
     wave_sync();
-    if (earlier == 0) mine[e] += __builtin_popcountll(m);
-    wave_sync();
-    a.order[row] = (int32_t)p;
-    a.place[p] = (int32_t)row;
   }
 }
 
-int64_t moe_group_blocks(int64_t pairs) { return (pairs + kGroupPairs - 1) / kGroupPairs; }
+// Rounds of a workgroup: one workgroup up to 4096 pairs (one launch: 2.7 us for
+// 128 of them); beyond, workgroups of 1024 as long as there are 32 at most to
+// add up, since one CU alone is slow at the scattered stores (16384 pairs: 13.8
+// us as one workgroup of 16 rounds).
+static int group_rounds(int64_t pairs) {
+  if (pairs <= kGroupTurn) return 1;
+  if (pairs <= 4 * kGroupTurn) return 4;
+  return pairs <= 32 * kGroupTurn ? 1 : pairs <= 128 * kGroupTurn ? 4 : 16;
+}
 
-hipError_t launch_moe_group(GroupArgs a, hipStream_t s) {
-  const unsigned blocks = (unsigned)moe_group_blocks(a.pairs);
+int64_t moe_group_blocks(int64_t pairs) {
+  const int64_t per = (int64_t)group_rounds(pairs) * kGroupTurn;
+  return (pairs + per - 1) / per;
+}
+
+template <int R>
+static hipError_t group_with(const GroupArgs& a, unsigned blocks, hipStream_t s) {
   const int n = a.experts + 1;
-  a.id_bits = 32 - __builtin_clz((unsigned)a.experts);
-  const unsigned lds = (unsigned)(n * (kGroupWaves * 2 + 8));  // 41 KB at 1024 experts
+  const unsigned lds = (unsigned)(n * 8 + (n + (n & 1)) * kGroupWaves * 2);  // 41 KB at 1024 experts
+  const dim3 grid(blocks > 0 ? blocks : 1), block(64 * kGroupWaves);
   if (blocks > 1) {
-    hipLaunchKernelGGL(group_count_kernel, dim3(blocks), dim3(64 * kGroupWaves), lds, s, a);
+    hipLaunchKernelGGL(group_count_kernel<R>, grid, block, lds, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(group_place_kernel, dim3(blocks > 0 ? blocks : 1), dim3(64 * kGroupWaves), lds, s, a);
+  hipLaunchKernelGGL(group_place_kernel<R>, grid, block, lds, s, a);
   return hipGetLastError();
+}
+
+hipError_t launch_moe_group(GroupArgs a, hipStream_t s) {
+  const unsigned blocks = (unsigned)moe_group_blocks(a.pairs);
+  a.id_bits = 32 - __builtin_clz((unsigned)a.experts);
+  if (a.pairs == 0) a.ids = a.offsets;  // (somewhere to read; no pair is one)
+  switch (group_rounds(a.pairs)) {
+    case 1: return group_with<1>(a, blocks, s);
+    case 4: return group_with<4>(a, blocks, s);
+    default: return group_with<16>(a, blocks, s);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -230,37 +258,51 @@ hipError_t launch_moe_dispatch(const DispatchArgs& a, hipStream_t s) {
 // ---------------------------------------------------------------------------
 namespace {
 
-// N consecutive elements, 16 bytes of them (or one).
-template <bool BF16, int N>
+// Sixteen bytes of a row, wherever they start, or less at its end.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
+template <bool BF16>
 struct Elements {
+  static constexpr int N = BF16 ? 8 : 4;
   float v[N];
-  __device__ __forceinline__ void load(const void* p, int64_t i) {
-    if constexpr (N == 1) {
-      v[0] = BF16 ? bf16_lo(reinterpret_cast<const uint16_t*>(p)[i]) : reinterpret_cast<const float*>(p)[i];
-    } else if constexpr (BF16) {
-      const u32x4 w = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(p) + i);
+  __device__ __forceinline__ void load(const void* p, int64_t i, int64_t width) {
+    if (i + N <= width) {
+      const u32x4 w = *reinterpret_cast<const u32x4_any*>(reinterpret_cast<const char*>(p) + i * (16 / N));
 #pragma unroll
       for (int k = 0; k < 4; k++) {
-        v[2 * k] = bf16_lo(w[k]);
-        v[2 * k + 1] = bf16_hi(w[k]);
+        const uint32_t x = w[k];
+        if constexpr (BF16) {
+          v[2 * k] = bf16_lo(x);
+          v[2 * k + 1] = bf16_hi(x);
+        } else {
+          v[k] = __builtin_bit_cast(float, x);
+        }
       }
     } else {
-      const f32x4 w = *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(p) + i);
 #pragma unroll
-      for (int k = 0; k < 4; k++) v[k] = w[k];
+      for (int k = 0; k < N; k++) {
+        v[k] = 0.0f;
+        if (i + k < width)
+          v[k] = BF16 ? bf16_lo(reinterpret_cast<const uint16_t*>(p)[i + k]) : reinterpret_cast<const float*>(p)[i + k];
+      }
     }
   }
-  __device__ __forceinline__ void store(void* p, int64_t i) const {
-    if constexpr (N == 1) {
-      if (BF16) reinterpret_cast<__bf16*>(p)[i] = (__bf16)v[0];
-      else reinterpret_cast<float*>(p)[i] = v[0];
-    } else if constexpr (BF16) {
+  __device__ __forceinline__ void store(void* p, int64_t i, int64_t width) const {
+    if (i + N <= width) {
       u32x4 w;
 #pragma unroll
-      for (int k = 0; k < 4; k++) w[k] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[2 * k], (__bf16)v[2 * k + 1]});
-      *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(p) + i) = w;
+      for (int k = 0; k < 4; k++) {
+        if constexpr (BF16) w[k] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[2 * k], (__bf16)v[2 * k + 1]});
+        else w[k] = __builtin_bit_cast(uint32_t, v[k]);
+      }
+      *reinterpret_cast<u32x4_any*>(reinterpret_cast<char*>(p) + i * (16 / N)) = w;
     } else {
-      *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p) + i) = f32x4{v[0], v[1], v[2], v[3]};
+#pragma unroll
+      for (int k = 0; k < N; k++) {
+        if (i + k >= width) continue;
+        if constexpr (BF16) reinterpret_cast<__bf16*>(p)[i + k] = (__bf16)v[k];
+        else reinterpret_cast<float*>(p)[i + k] = v[k];
+      }
     }
   }
 };
@@ -269,82 +311,112 @@ __device__ __forceinline__ int64_t pair_row(const CombineArgs& a, int64_t p) { r
 
 }  // namespace
 
-// One lane, N elements of one token's row: each slot's row in turn.
-template <bool BF16, int N>
+// One lane, 16 bytes of one token's row: each slot's row in turn.
+template <bool BF16>
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
+  constexpr int N = Elements<BF16>::N;
   const int64_t t = blockIdx.x;
   const int64_t i = ((int64_t)blockIdx.y * 256 + threadIdx.x) * N;
   if (i >= a.width) return;
   const int64_t kept = a.kept && *a.kept < a.num_rows ? *a.kept : a.num_rows;
   constexpr int64_t size = BF16 ? 2 : 4;
-  Elements<BF16, N> sum, x;
+  Elements<BF16> sum, x;
 #pragma unroll
   for (int k = 0; k < N; k++) sum.v[k] = 0.0f;
+#pragma unroll 4
   for (int j = 0; j < a.top_k; j++) {
     const int64_t p = t * a.top_k + j, r = pair_row(a, p);
     if ((uint64_t)r >= (uint64_t)kept) continue;
     const float w = a.weights ? a.weights[p] : 1.0f;
-    x.load(reinterpret_cast<const char*>(a.rows) + r * a.ld_rows * size, i);
+    x.load(reinterpret_cast<const char*>(a.rows) + r * a.ld_rows * size, i, a.width);
 #pragma unroll
     for (int k = 0; k < N; k++) sum.v[k] = __builtin_fmaf(w, x.v[k], sum.v[k]);
   }
-  sum.store(reinterpret_cast<char*>(a.out) + t * a.ld_out * size, i);
+  sum.store(reinterpret_cast<char*>(a.out) + t * a.ld_out * size, i, a.width);
 }
 
-// A workgroup for each pair: its gradient row, and the product of the two rows.
-template <bool BF16, int N>
+// A workgroup for four pairs of a token: the gradient's row is read once for
+// them, four rows are on their way at once, and each gives its product with
+// the gradient's.
+constexpr int kBackPairs = 4;
+
+template <bool BF16>
 __global__ __launch_bounds__(256) void combine_backward_kernel(CombineBackwardArgs b) {
+  constexpr int N = Elements<BF16>::N;
   const CombineArgs& a = b.a;
-  const int64_t p = blockIdx.x, t = p / a.top_k, r = pair_row(a, p);
+  const int64_t t = blockIdx.x;
   const int64_t kept = a.kept && *a.kept < a.num_rows ? *a.kept : a.num_rows;
   constexpr int64_t size = BF16 ? 2 : 4;
-  const bool there = (uint64_t)r < (uint64_t)kept, write = (uint64_t)r < (uint64_t)a.num_rows;
   const char* g = reinterpret_cast<const char*>(b.grad) + t * b.ld_grad * size;
-  const char* x = reinterpret_cast<const char*>(a.rows) + r * a.ld_rows * size;
-  char* out = reinterpret_cast<char*>(b.grad_rows) + r * b.ld_grad_rows * size;
-  const float w = there ? (a.weights ? a.weights[p] : 1.0f) : 0.0f;
-  float dot = 0.0f;
-  for (int64_t i = threadIdx.x * N; i < a.width; i += 256 * N) {
-    Elements<BF16, N> gv, xv;
-    gv.load(g, i);
-    if (there && b.grad_weights) {
-      xv.load(x, i);
+  const int j0 = blockIdx.y * kBackPairs;
+  const char* x[kBackPairs];
+  char* out[kBackPairs];
+  float w[kBackPairs], dot[kBackPairs];
+  bool there[kBackPairs], write[kBackPairs];
 #pragma unroll
-      for (int k = 0; k < N; k++) dot = __builtin_fmaf(gv.v[k], xv.v[k], dot);
+  for (int q = 0; q < kBackPairs; q++) {
+    const bool real = j0 + q < a.top_k;
+    const int64_t p = t * a.top_k + (real ? j0 + q : j0), r = pair_row(a, p);
+    there[q] = real && (uint64_t)r < (uint64_t)kept;
+    write[q] = real && (uint64_t)r < (uint64_t)a.num_rows;
+    w[q] = there[q] ? (a.weights ? a.weights[p] : 1.0f) : 0.0f;
+    x[q] = reinterpret_cast<const char*>(a.rows) + r * a.ld_rows * size;
+    out[q] = reinterpret_cast<char*>(b.grad_rows) + r * b.ld_grad_rows * size;
+    dot[q] = 0.0f;
+  }
+  for (int64_t i = threadIdx.x * N; i < a.width; i += 256 * N) {
+    Elements<BF16> gv, xv[kBackPairs];
+    gv.load(g, i, a.width);
+#pragma unroll
+    for (int q = 0; q < kBackPairs; q++) {
+      if (there[q] && b.grad_weights) xv[q].load(x[q], i, a.width);
     }
 #pragma unroll
-    for (int k = 0; k < N; k++) gv.v[k] = there ? gv.v[k] * w : 0.0f;
-    if (write) gv.store(out, i);
+    for (int q = 0; q < kBackPairs; q++) {
+      if (there[q] && b.grad_weights) {
+#pragma unroll
+        for (int k = 0; k < N; k++) dot[q] = __builtin_fmaf(gv.v[k], xv[q].v[k], dot[q]);
+      }
+      if (write[q]) {
+        Elements<BF16> y;
+        // (a pair without an expert: zeros, whatever the gradient holds)
+#pragma unroll
+        for (int k = 0; k < N; k++) y.v[k] = there[q] ? gv.v[k] * w[q] : 0.0f;
+        y.store(out[q], i, a.width);
+      }
+    }
   }
   if (!b.grad_weights) return;
-  dot += xor_shfl<1>(dot);
-  dot += xor_shfl<2>(dot);
-  dot += xor_shfl<4>(dot);
-  dot += xor_shfl<8>(dot);
-  dot += xor_shfl<16>(dot);
-  dot += xor_shfl<32>(dot);
-  __shared__ float part[4];
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
+  __shared__ float part[kBackPairs][4];
+#pragma unroll
+  for (int q = 0; q < kBackPairs; q++) {
+    float d = dot[q];
+    d += xor_shfl<1>(d);
+    d += xor_shfl<2>(d);
+    d += xor_shfl<4>(d);
+    d += xor_shfl<8>(d);
+    d += xor_shfl<16>(d);
+    d += xor_shfl<32>(d);
+    if ((threadIdx.x & 63) == 0) part[q][threadIdx.x >> 6] = d;
+  }
   __syncthreads();
-  if (threadIdx.x == 0) b.grad_weights[p] = part[0] + part[1] + part[2] + part[3];
+  const int q = threadIdx.x;
+  if (q < kBackPairs && j0 + q < a.top_k)
+    b.grad_weights[t * a.top_k + j0 + q] = part[q][0] + part[q][1] + part[q][2] + part[q][3];
 }
 
 hipError_t launch_moe_combine(const CombineArgs& a, hipStream_t s) {
-  const int n = a.vec_ok ? (a.bf16 ? 8 : 4) : 1;
+  const int n = a.bf16 ? 8 : 4;
   const dim3 grid((unsigned)a.tokens, (unsigned)((a.width + 256 * n - 1) / (256 * n))), block(256);
-  if (a.bf16 && n > 1) hipLaunchKernelGGL((combine_kernel<true, 8>), grid, block, 0, s, a);
-  else if (a.bf16) hipLaunchKernelGGL((combine_kernel<true, 1>), grid, block, 0, s, a);
-  else if (n > 1) hipLaunchKernelGGL((combine_kernel<false, 4>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((combine_kernel<false, 1>), grid, block, 0, s, a);
+  if (a.bf16) hipLaunchKernelGGL(combine_kernel<true>, grid, block, 0, s, a);
+  else hipLaunchKernelGGL(combine_kernel<false>, grid, block, 0, s, a);
   return hipGetLastError();
 }
 
 hipError_t launch_moe_combine_backward(const CombineBackwardArgs& b, hipStream_t s) {
-  const dim3 grid((unsigned)(b.a.tokens * b.a.top_k)), block(256);
-  if (b.a.bf16 && b.a.vec_ok) hipLaunchKernelGGL((combine_backward_kernel<true, 8>), grid, block, 0, s, b);
-  else if (b.a.bf16) hipLaunchKernelGGL((combine_backward_kernel<true, 1>), grid, block, 0, s, b);
-  else if (b.a.vec_ok) hipLaunchKernelGGL((combine_backward_kernel<false, 4>), grid, block, 0, s, b);
-  else hipLaunchKernelGGL((combine_backward_kernel<false, 1>), grid, block, 0, s, b);
+  const dim3 grid((unsigned)b.a.tokens, (unsigned)((b.a.top_k + kBackPairs - 1) / kBackPairs)), block(256);
+  if (b.a.bf16) hipLaunchKernelGGL(combine_backward_kernel<true>, grid, block, 0, s, b);
+  else hipLaunchKernelGGL(combine_backward_kernel<false>, grid, block, 0, s, b);
   return hipGetLastError();
 }
 
