@@ -1350,6 +1350,8 @@ def matvec(x, w: Quantized, ids=None, *, out_dtype=None, out=None, stream=None):
     ts = w.tensor_scale
     at_ts = 0
     if w.fmt == FP4_NVFP4:
+        if ts is None:
+            raise ValueError("NVFP4 weights need their tensor scale")
         at_ts = _dense(ts, index, torch.float32, (experts,), "tensor_scale")
     args = _pack_matvec(_MATVEC_SIZE, w.fmt, xt, _kv_dtype(out, "out"), pairs, max(repeat, 1), N, K, flat.data_ptr(), ld,
                         codes.data_ptr(), codes.stride(-2), ces, scales.data_ptr(), scales.stride(-2), ses, at_ts,
