@@ -1023,31 +1023,25 @@ class MoeGroups:
     place: "torch.Tensor"
 
 
-def _gpu(t, what):
-    """The index of a tensor's GPU."""
+def _here(t, what, stream):
+    """The index of a tensor's GPU and, as a handle, the stream to launch on:
+    torch's current one there; None if that GPU, or the stream asked for, is
+    not the current one (the call is then made again where it is: _there)."""
+    import torch
     index = t.get_device()
     if index < 0:
         raise ValueError(f"{what} must be on a GPU")
-    return index
-
-
-def _raw_stream(index):
-    """torch's current stream on a GPU, as a handle."""
-    import torch
-    return torch._C._cuda_getCurrentRawStream(index)
-
-
-def _away(index, stream):
-    """Is this GPU, or the stream asked for, not the current one?"""
-    import torch
-    return torch._C._cuda_getDevice() != index or (stream is not None and stream != _raw_stream(index))
+    if torch._C._cuda_getDevice() != index:
+        return index, None
+    raw = torch._C._cuda_getCurrentRawStream(index)
+    return index, raw if stream is None or stream == raw else None
 
 
 def _there(call, index, stream, given, *args, **kw):
     """The call again, with that GPU and stream current."""
     import torch
     with torch.cuda.device(index):
-        if stream is None or stream == _raw_stream(index):
+        if stream is None or stream == torch._C._cuda_getCurrentRawStream(index):
             return call(*args, **kw)
         return _on_stream(call, torch.device("cuda", index), stream, given, *args, **kw)
 
@@ -1089,8 +1083,8 @@ def moe_route(logits, top_k, *, score="softmax", bias=None, groups=1, top_groups
     to the lowest index; an expert whose logit or bias is -inf or NaN is never
     chosen, slots left over are id -1 with weight 0."""
     import torch
-    index = _gpu(logits, "logits")
-    if _away(index, stream):
+    index, raw = _here(logits, "logits", stream)
+    if raw is None:
         return _there(moe_route, index, stream, None, logits, top_k, score=score, bias=bias, groups=groups,
                       top_groups=top_groups, group_best=group_best, renormalize=renormalize, scale=scale)
     ld = _matrix(logits, index, "logits")
@@ -1102,7 +1096,7 @@ def moe_route(logits, top_k, *, score="softmax", bias=None, groups=1, top_groups
     args = _pack_route(_ROUTE_SIZE, dt, _route_flags(score, renormalize), experts, top_k, groups,
                        groups if top_groups is None else top_groups, group_best, tokens, logits.data_ptr(), ld,
                        at_bias, weights.data_ptr(), ids.data_ptr(), scale, 0)
-    st = lib().fp4_moe_route(args, _raw_stream(index))
+    st = lib().fp4_moe_route(args, raw)
     if st != FP4_OK:
         raise Fp4Error(st, "fp4_moe_route")
     return weights, ids
@@ -1113,8 +1107,8 @@ def moe_route_backward(grad_weights, logits, ids, *, score="softmax", renormaliz
     weights (fp32 [tokens, top_k]), for the ids it chose and the same score,
     renormalize and scale."""
     import torch
-    index = _gpu(logits, "logits")
-    if _away(index, stream):
+    index, raw = _here(logits, "logits", stream)
+    if raw is None:
         return _there(moe_route_backward, index, stream, None, grad_weights, logits, ids, score=score,
                       renormalize=renormalize, scale=scale)
     ld = _matrix(logits, index, "logits")
@@ -1127,7 +1121,7 @@ def moe_route_backward(grad_weights, logits, ids, *, score="softmax", renormaliz
     out = torch.empty_like(logits, memory_format=torch.contiguous_format)
     args = _pack_route(_ROUTE_SIZE, dt, _route_flags(score, renormalize), experts, ids.shape[1], 1, 1, 1, tokens,
                        logits.data_ptr(), ld, 0, 0, at_ids, scale, 0)
-    st = lib().fp4_moe_route_backward(args, at_grad, out.data_ptr(), experts, _raw_stream(index))
+    st = lib().fp4_moe_route_backward(args, at_grad, out.data_ptr(), experts, raw)
     if st != FP4_OK:
         raise Fp4Error(st, "fp4_moe_route_backward")
     return out
@@ -1138,8 +1132,8 @@ def moe_group(ids, experts, *, stream=None) -> MoeGroups:
     gives them) by expert; ids outside [0, experts) belong to none (a GPU that
     holds experts a to b - 1 passes ids - a and b - a)."""
     import torch
-    index = _gpu(ids, "ids")
-    if _away(index, stream):
+    index, raw = _here(ids, "ids", stream)
+    if raw is None:
         return _there(moe_group, index, stream, None, ids, experts)
     at_ids = _dense(ids, index, torch.int32, ids.shape, "ids")
     pairs = ids.numel()
@@ -1150,7 +1144,7 @@ def moe_group(ids, experts, *, stream=None) -> MoeGroups:
     need = L.fp4_moe_group_workspace(pairs, experts)
     ws = ids.new_empty((need,), dtype=torch.uint8) if need else None
     st = L.fp4_moe_group(pairs, at_ids, experts, offsets.data_ptr(), order.data_ptr(), place.data_ptr(),
-                         ws.data_ptr() if need else None, need, _raw_stream(index))
+                         ws.data_ptr() if need else None, need, raw)
     if st != FP4_OK:
         raise Fp4Error(st, "fp4_moe_group")
     return MoeGroups(offsets, order, place)
@@ -1175,8 +1169,8 @@ def moe_dispatch(x, groups: MoeGroups, *, stream=None):
     import torch
     packed = isinstance(x, Quantized)
     first = x.codes if packed else x
-    index = _gpu(first, "x")
-    if _away(index, stream):
+    index, raw = _here(first, "x", stream)
+    if raw is None:
         return _there(moe_dispatch, index, stream, x.tensor_scale if packed else None, x, groups)
     ld = _matrix(first, index, "x.codes" if packed else "x")
     tokens, width = first.shape
@@ -1186,7 +1180,6 @@ def moe_dispatch(x, groups: MoeGroups, *, stream=None):
             raise ValueError(f"groups of {pairs} pairs for {tokens} tokens")
     top_k = pairs // tokens if tokens else 1
     at_place, at_kept = _places(groups, tokens, top_k, index)
-    stream = _raw_stream(index)
     if packed:
         blocks = x.scales.shape[-1]
         ld2 = _matrix(x.scales, index, "x.scales", torch.uint8)
@@ -1195,15 +1188,16 @@ def moe_dispatch(x, groups: MoeGroups, *, stream=None):
         ld_out, ld_out2 = code_pitch(width), scale_pitch(blocks)
         rows = first.new_empty((pairs, ld_out))[:, :width]
         scales = first.new_empty((pairs, ld_out2))[:, :blocks]
-        st = fp4_moe_dispatch(tokens, max(top_k, 1), at_place, at_kept, width, first.data_ptr(), ld, rows.data_ptr(),
-                              ld_out, blocks, x.scales.data_ptr(), ld2, scales.data_ptr(), ld_out2, stream)
+        st = lib().fp4_moe_dispatch(tokens, max(top_k, 1), at_place, at_kept, width, first.data_ptr(), ld, rows.data_ptr(),
+                              ld_out, blocks, x.scales.data_ptr(), ld2, scales.data_ptr(), ld_out2, raw)
     else:
         _kv_dtype(x, "x")
         es = x.element_size()
         rows = x.new_empty((pairs, width))
-        st = fp4_moe_dispatch(tokens, max(top_k, 1), at_place, at_kept, width * es, x.data_ptr(), ld * es,
-                              rows.data_ptr(), width * es, 0, None, 0, None, 0, stream)
-    _check(st, "fp4_moe_dispatch")
+        st = lib().fp4_moe_dispatch(tokens, max(top_k, 1), at_place, at_kept, width * es, x.data_ptr(), ld * es,
+                              rows.data_ptr(), width * es, 0, None, 0, None, 0, raw)
+    if st != FP4_OK:
+        raise Fp4Error(st, "fp4_moe_dispatch")
     return Quantized(x.fmt, rows, scales, x.tensor_scale) if packed else rows
 
 
@@ -1240,8 +1234,8 @@ def moe_combine(rows, weights=None, groups: Optional[MoeGroups] = None, *, out=N
     them; without, they are [tokens, top_k, width] or [pairs, width] in the
     pairs' order, as matvec leaves them. Rows of pairs without an expert have no
     part. moe_combine(grad_rows, None, groups) is moe_dispatch's backward."""
-    index = _gpu(rows, "rows")
-    if _away(index, stream):
+    index, raw = _here(rows, "rows", stream)
+    if raw is None:
         return _there(moe_combine, index, stream, out, rows, weights, groups, out=out)
     dt = _kv_dtype(rows, "rows")
     tokens = rows.shape[0] if rows.dim() == 3 and groups is None else None
@@ -1254,9 +1248,10 @@ def moe_combine(rows, weights=None, groups: Optional[MoeGroups] = None, *, out=N
         ld_out = _matrix(out, index, "out", rows.dtype)
         if out.shape != (tokens, width):
             raise ValueError(f"out must be [{tokens}, {width}]")
-    st = fp4_moe_combine(dt, tokens, max(top_k, 1), width, rows.data_ptr(), ld, rows.shape[0], at_place, at_kept, at_w,
-                         out.data_ptr(), ld_out, _raw_stream(index))
-    _check(st, "fp4_moe_combine")
+    st = lib().fp4_moe_combine(dt, tokens, max(top_k, 1), width, rows.data_ptr(), ld, rows.shape[0], at_place, at_kept, at_w,
+                         out.data_ptr(), ld_out, raw)
+    if st != FP4_OK:
+        raise Fp4Error(st, "fp4_moe_combine")
     return out
 
 
@@ -1265,8 +1260,8 @@ def moe_combine_backward(grad_out, rows, weights=None, groups: Optional[MoeGroup
     [tokens, width]; grad_rows like rows (zeros where a pair has no expert),
     grad_weights fp32 like weights, None without weights."""
     import torch
-    index = _gpu(rows, "rows")
-    if _away(index, stream):
+    index, raw = _here(rows, "rows", stream)
+    if raw is None:
         return _there(moe_combine_backward, index, stream, None, grad_out, rows, weights, groups)
     dt = _kv_dtype(rows, "rows")
     ld_grad = _matrix(grad_out, index, "grad_out", rows.dtype)
@@ -1279,10 +1274,11 @@ def moe_combine_backward(grad_out, rows, weights=None, groups: Optional[MoeGroup
         raise ValueError(f"{rows.shape[0]} rows for {tokens} tokens of {top_k}")
     grad_rows = rows.new_empty(shape)
     grad_w = None if weights is None else torch.empty_like(weights)
-    st = fp4_moe_combine_backward(dt, tokens, max(top_k, 1), width, grad_out.data_ptr(), ld_grad, rows.data_ptr(), ld,
+    st = lib().fp4_moe_combine_backward(dt, tokens, max(top_k, 1), width, grad_out.data_ptr(), ld_grad, rows.data_ptr(), ld,
                                   rows.shape[0], at_place, at_kept, at_w, grad_rows.data_ptr(), width,
-                                  grad_w.data_ptr() if grad_w is not None else None, _raw_stream(index))
-    _check(st, "fp4_moe_combine_backward")
+                                  grad_w.data_ptr() if grad_w is not None else None, raw)
+    if st != FP4_OK:
+        raise Fp4Error(st, "fp4_moe_combine_backward")
     return grad_rows, grad_w
 
 
@@ -1298,8 +1294,8 @@ def matvec(x, w: Quantized, ids=None, *, out_dtype=None, out=None, stream=None):
     Also ids [rows] with x [rows, K] -> [rows, N]. The result has x's dtype
     unless out_dtype (or out) says otherwise."""
     import torch
-    index = _gpu(x, "x")
-    if _away(index, stream):
+    index, raw = _here(x, "x", stream)
+    if raw is None:
         return _there(matvec, index, stream, out, x, w, ids, out_dtype=out_dtype, out=out)
     xt = _kv_dtype(x, "x")
     codes, scales = w.codes, w.scales
@@ -1356,7 +1352,7 @@ def matvec(x, w: Quantized, ids=None, *, out_dtype=None, out=None, stream=None):
     args = _pack_matvec(_MATVEC_SIZE, w.fmt, xt, _kv_dtype(out, "out"), pairs, max(repeat, 1), N, K, flat.data_ptr(), ld,
                         codes.data_ptr(), codes.stride(-2), ces, scales.data_ptr(), scales.stride(-2), ses, at_ts,
                         experts, at_ids, out.data_ptr(), ld_y)
-    st = lib().fp4_matvec(args, _raw_stream(index))
+    st = lib().fp4_matvec(args, raw)
     if st != FP4_OK:
         raise Fp4Error(st, "fp4_matvec")
     return out

@@ -27,6 +27,7 @@ struct Call {
   int y_bf16;
   int part_shift;  // few rows: 2^part_shift waves share a tile of W
   int seg_units;   // few rows: units of x in LDS at once
+  int at_once;     // few rows: a wave's weights are all loaded before the first product
   int rounds;      // few rows: tiles of W a wave takes one after another
 };
 
@@ -419,6 +420,11 @@ __device__ __forceinline__ int64_t x_offset(const Call& a, int pair) {
   return row * a.ld_x;
 }
 
+// Units of bf16 calls that a wave loads before its first product, if it has no
+// more (fp32 rows need the registers for themselves).
+template <bool NV>
+constexpr int kAtOnce = NV ? 2 : 3;
+
 // LDS of a few rows' form: x, and zeros where an operand needs them.
 template <bool NV, bool XBF, int RG>
 __host__ __device__ constexpr int few_bytes(int seg_units) {
@@ -468,43 +474,29 @@ __device__ __forceinline__ void few_pairs(const Call& a, int expert, const uint1
   if constexpr (XBF) copy_all(0, in_lds);
   else if (threadIdx.x < n1 * RG) load_x(threadIdx.x, n1, 0);
   Place<1> at(a, expert, n0);
-  Weights<NV, 1> now;
-  if (units > 0) now.load(a, at, part * kUnit, g);
   FewRows<NV, XBF, RG> rows(pitch);
+  rows.clear();
   const float ts = NV ? a.ts[expert] : 1.0f;
-  for (int round = 0; round < a.rounds; round++) {
-    rows.clear();
-    const bool last_tile = round + 1 == a.rounds;
-    const Place<1> after(a, expert, last_tile ? n0 : n0 + per * 16);
-    int unit = part;
-    for (int u0 = 0; u0 < units; u0 += a.seg_units) {
-      const int here = units - u0 < a.seg_units ? units - u0 : a.seg_units;
-      if (round == 0 || units > a.seg_units) {
-        if (round > 0 || u0 > 0) __syncthreads();
-        if (FewRows<NV, XBF, RG>::DIAG && threadIdx.x < kZeros / 16)
-          *reinterpret_cast<u32x4*>(lds + ROWS * pitch + threadIdx.x * 16) = u32x4{0, 0, 0, 0};
-        if constexpr (XBF) {
-          if (round > 0 || u0 > 0) copy_all(u0, here);
-          asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (the copies to LDS are counted there)
-        } else {
-          for (int i = threadIdx.x; i < here * 64 * RG; i += 64 * W) {
-            if (round > 0 || u0 > 0 || i >= 64 * W) load_x(i, here * 64, u0 * kUnit);
-            x.put(a, live - 4 * group, u0 * kUnit + oct * 8, lds + 4 * group * pitch + oct * 16, pitch, MR * pitch);
-          }
-        }
-        __syncthreads();
-      }
-      for (; unit < u0 + here; unit += parts) {
-        Weights<NV, 1> next;
-        const bool over = unit + parts >= units;  // (of the last tile: bytes that nobody uses)
-        next.load(a, over ? after : at, over && !last_tile ? part * kUnit : (unit + parts) * kUnit, g);
-        rows.multiply(now, unit * kUnit, a.K, unit - u0, lds);
-        now = next;
+  auto stage = [&](int u0, bool loaded) {
+    const int here = units - u0 < a.seg_units ? units - u0 : a.seg_units;
+    if (!loaded) __syncthreads();
+    if (FewRows<NV, XBF, RG>::DIAG && threadIdx.x < kZeros / 16)
+      *reinterpret_cast<u32x4*>(lds + ROWS * pitch + threadIdx.x * 16) = u32x4{0, 0, 0, 0};
+    if constexpr (XBF) {
+      if (!loaded) copy_all(u0, here);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (the copies to LDS are counted there)
+    } else {
+      for (int i = threadIdx.x; i < here * 64 * RG; i += 64 * W) {
+        if (!loaded || i >= 64 * W) load_x(i, here * 64, u0 * kUnit);
+        x.put(a, live - 4 * group, u0 * kUnit + oct * 8, lds + 4 * group * pitch + oct * 16, pitch, MR * pitch);
       }
     }
+    __syncthreads();
+  };
+  // the sums of a tile, over its waves, to y
+  auto finish = [&]() {
     f32x4 acc = rows.result();
-    if (parts > 1) {
-      if (round > 0) __syncthreads();
+    if (parts > 1) {  // (one tile a wave)
       if (g < RG) {
 #pragma unroll
         for (int r = 0; r < 4; r++) red[(wave * MR + 4 * g + r) * 16 + c16] = acc[r];
@@ -524,6 +516,45 @@ __device__ __forceinline__ void few_pairs(const Call& a, int expert, const uint1
         if (row < live) store_y(a, LIST ? list[row] : first + row, n0 + c16, acc[r] * ts);
       }
     }
+  };
+  // A wave of few units has all their weights on the way at once.
+  if constexpr (XBF) if (a.at_once) {
+    constexpr int AT_ONCE = kAtOnce<NV>;
+    Weights<NV, 1> w[AT_ONCE];
+#pragma unroll
+    for (int d = 0; d < AT_ONCE; d++) {
+      if (d * parts < units) w[d].load(a, at, (part + d * parts) * kUnit, g);
+    }
+#pragma unroll
+    for (int d = 0; d < AT_ONCE; d++) {
+      const int u = d * parts;
+      if (u >= units) break;
+      const int u0 = u < a.seg_units ? 0 : u / a.seg_units * a.seg_units;
+      if (u == u0) stage(u0, d == 0);
+      if (u + part < units) rows.multiply(w[d], (u + part) * kUnit, a.K, u + part - u0, lds);
+    }
+    finish();
+    return;
+  }
+  Weights<NV, 1> now;
+  if (units > 0) now.load(a, at, part * kUnit, g);
+  for (int round = 0; round < a.rounds; round++) {
+    const bool last_tile = round + 1 == a.rounds;
+    const Place<1> after(a, expert, last_tile ? n0 : n0 + per * 16);
+    int unit = part;
+    for (int u0 = 0; u0 < units; u0 += a.seg_units) {
+      const int here = units - u0 < a.seg_units ? units - u0 : a.seg_units;
+      if (round == 0 || units > a.seg_units) stage(u0, round == 0 && u0 == 0);
+      for (; unit < u0 + here; unit += parts) {
+        Weights<NV, 1> next;
+        const bool over = unit + parts >= units;  // (of the last tile: bytes that nobody uses)
+        next.load(a, over ? after : at, over && !last_tile ? part * kUnit : (unit + parts) * kUnit, g);
+        rows.multiply(now, unit * kUnit, a.K, unit - u0, lds);
+        now = next;
+      }
+    }
+    finish();
+    rows.clear();
     at = after;
     n0 += per * 16;
   }
@@ -557,12 +588,13 @@ constexpr int kLds = 160 * 1024, kLdsApart = 4 * 1024;  // of a CU; kept for wha
 
 template <bool NV, bool XBF, int RG, int W>
 hipError_t launch_few(Call& c, int tiles, int slots, hipStream_t s) {
-  const int cus = device_cu_count(), all = W == 16 ? 1 : 2;  // workgroups a CU
-  // waves for a tile: until each CU has a workgroup
+  const int cus = device_cu_count(), all = 16 / W;  // workgroups a CU
+  // waves for a tile: as many as leave the workgroups room on the GPU at once
   c.part_shift = 0;
-  while ((1 << c.part_shift) < W && (1 << c.part_shift) < c.units && ((int64_t)tiles * slots << c.part_shift) < W * cus)
+  while ((2 << c.part_shift) <= W && (1 << c.part_shift) < c.units &&
+         ((int64_t)tiles * slots * (2 << c.part_shift) + W - 1) / W <= all * cus)
     c.part_shift++;
-  const int red = c.part_shift > 0 ? W * RG * 256 : 0, room = (kLds / all - kLdsApart - red) / (kOpRows<XBF, RG> * kUnit * 2);
+  const int red = c.part_shift > 0 ? W * RG * 256 : 0, room = (kLds / all - kLdsApart / (W < 8 ? 2 : 1) - red) / (kOpRows<XBF, RG> * kUnit * 2);
   // (all of x, or else whole turns of the waves)
   c.seg_units = c.units < room ? c.units : room >> c.part_shift > 0 ? room >> c.part_shift << c.part_shift : room;
   // tiles one after another: once there are more workgroups than twice what fits at once, unless each would bring x anew
@@ -572,6 +604,9 @@ hipError_t launch_few(Call& c, int tiles, int slots, hipStream_t s) {
     per += W;
     c.rounds++;
   }
+  const int units_of_wave = (c.units + (1 << c.part_shift) - 1) >> c.part_shift;
+  c.at_once = XBF && c.rounds == 1 && c.units > 0 && units_of_wave <= kAtOnce<NV> &&
+              (c.units <= c.seg_units || (c.seg_units & ((1 << c.part_shift) - 1)) == 0);
   const dim3 grid((tiles + per - 1) / per, slots), block(64 * W);
   int lds = few_bytes<NV, XBF, RG>(c.seg_units) + red;
   if (c.ids) {
@@ -586,6 +621,10 @@ hipError_t launch_few(Call& c, int tiles, int slots, hipStream_t s) {
 // Eight waves a workgroup where two have room on a CU with all of x, else 16.
 template <bool NV, bool XBF, int RG>
 hipError_t launch_few_rows(Call& c, int tiles, int slots, hipStream_t s) {
+  if constexpr (RG == 1) {
+    if ((int64_t)tiles * slots * 2 >= 8 * device_cu_count() && few_bytes<NV, XBF, RG>(c.units) + 4 * RG * 256 <= kLds / 4 - kLdsApart / 2)
+      return launch_few<NV, XBF, RG, 4>(c, tiles, slots, s);
+  }
   if constexpr (RG < 4) {
     if (few_bytes<NV, XBF, RG>(c.units) + 8 * RG * 256 <= kLds / 2 - kLdsApart)
       return launch_few<NV, XBF, RG, 8>(c, tiles, slots, s);
