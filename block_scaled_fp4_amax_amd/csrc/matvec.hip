@@ -10,7 +10,7 @@ using namespace fp4dev;
 
 namespace {
 
-constexpr int kUnit = 512;        // K of a wave's unit: four pieces of 128, 256 bytes of each row's codes
+constexpr int kUnit = 512;  // K of a wave's unit: four pieces of 128, 256 bytes of each row's codes
 
 // What the kernels take: sizes in 32 bits, and what only sizes decide.
 struct Call {
@@ -25,10 +25,10 @@ struct Call {
   int units;                        // of K
   uint32_t last_code, last_scale;   // where a row's last 16 bytes start
   int y_bf16;
-  int part_shift;  // few rows: 2^part_shift waves share a tile of W
-  int seg_units;   // few rows: units of x in LDS at once
-  int at_once;     // few rows: a wave's weights are all loaded before the first product
-  int rounds;      // few rows: tiles of W a wave takes one after another
+  int part_shift;  // 2^part_shift waves share a tile of W
+  int seg_units;   // units of x in LDS at once
+  int at_once;     // a wave's weights are all loaded before the first product
+  int rounds;      // tiles of W a wave takes one after another
 };
 
 // The eight values of a word of codes, times their block's scale: exact in
@@ -78,61 +78,55 @@ __device__ __forceinline__ f32x4 mfma(u32x4 x, bf16x8 w, f32x4 acc) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), w, acc, 0, 0, 0);
 }
 
-// Where 16 NT rows of W lie: bases of the first (the same for all lanes), and
-// the lane's row, lane % 16 of each tile, from there.
-template <int NT>
+// Where a tile of 16 rows of W lies: bases of the first (the same for all
+// lanes), and the lane's row, lane % 16, from there.
 struct Place {
   const uint8_t *codes, *scales;
-  uint32_t code_row[NT], scale_row[NT];
+  uint32_t code_row, scale_row;
   __device__ __forceinline__ Place(const Call& a, int expert, int n0) {
     const int c16 = threadIdx.x & 15;
     n0 = n0 < a.N ? n0 : a.N - 1;
     codes = a.codes + expert * a.c_es + (int64_t)n0 * a.ld_c;
     scales = a.scales + expert * a.s_es + (int64_t)n0 * a.ld_s;
     const int rows = a.N - 1 - n0;
-#pragma unroll
-    for (int t = 0; t < NT; t++) {
-      const uint32_t row = t * 16 + c16 < rows ? t * 16 + c16 : rows;
-      code_row[t] = row * a.ld_c;
-      scale_row[t] = row * a.ld_s;
-    }
+    const uint32_t row = c16 < rows ? c16 : rows;
+    code_row = row * a.ld_c;
+    scale_row = row * a.ld_s;
   }
 };
 
-// One unit of NT tiles of 16 rows of W in a wave's registers: a lane has 32
-// consecutive values of row lane % 16 in each of four pieces of 128, and the
-// rows' scales of all four.
-template <bool NV, int NT>
+// One unit of a tile in a wave's registers: a lane has 32 consecutive values of
+// row lane % 16 in each of four pieces of 128 (blocks lie within lanes, and its
+// four words are operands of four v_mfma_f32_16x16x32_bf16, whose k are then
+// 32 g + 8 j, g = lane / 16, j the word), and the row's scales of all four.
+template <bool NV>
 struct Weights {
-  u32x4 w[NT][4], s[NT][NV ? 2 : 1];
+  u32x4 w[4], s[NV ? 2 : 1];
   // (past the end: the row's last bytes, for which scale() gives zeros)
-  __device__ __forceinline__ void load(const Call& a, const Place<NT>& p, int k0, int g) {
+  __device__ __forceinline__ void load(const Call& a, const Place& p, int k0, int g) {
     const uint32_t last_code = a.last_code, last_scale = a.last_scale;
     const uint32_t at = (uint32_t)k0 / 2 + g * 16, sat = (uint32_t)k0 / (NV ? 16 : 32);
 #pragma unroll
-    for (int t = 0; t < NT; t++) {
+    for (int i = 0; i < (NV ? 2 : 1); i++) {
+      const uint32_t o = sat + i * 16 < last_scale ? sat + i * 16 : last_scale;
+      s[i] = *reinterpret_cast<const u32x4*>(p.scales + (p.scale_row + o));
+    }
 #pragma unroll
-      for (int i = 0; i < (NV ? 2 : 1); i++) {
-        const uint32_t o = sat + i * 16 < last_scale ? sat + i * 16 : last_scale;
-        s[t][i] = *reinterpret_cast<const u32x4*>(p.scales + (p.scale_row[t] + o));
-      }
-#pragma unroll
-      for (int u = 0; u < 4; u++) {
-        const uint32_t o = at + u * 64 < last_code ? at + u * 64 : last_code;
-        w[t][u] = *reinterpret_cast<const u32x4*>(p.codes + (p.code_row[t] + o));
-      }
+    for (int u = 0; u < 4; u++) {
+      const uint32_t o = at + u * 64 < last_code ? at + u * 64 : last_code;
+      w[u] = *reinterpret_cast<const u32x4*>(p.codes + (p.code_row + o));
     }
   }
   // The scales of the lane's first and second 16 values of piece u, which
   // starts at k.
-  __device__ __forceinline__ f32x2 scale(int t, int u, int k, int K, int g) const {
+  __device__ __forceinline__ f32x2 scale(int u, int k, int K, int g) const {
     const bool first = k + g * 32 < K, second = k + g * 32 + 16 < K;
     if constexpr (NV) {
-      const uint32_t pair = (g & 2 ? s[t][u >> 1][(2 * u + 1) & 3] : s[t][u >> 1][(2 * u) & 3]) >> (16 * (g & 1));
+      const uint32_t pair = (g & 2 ? s[u >> 1][(2 * u + 1) & 3] : s[u >> 1][(2 * u) & 3]) >> (16 * (g & 1));
       const f32x2 f = __builtin_amdgcn_cvt_pk_f32_fp8(pair, false);
       return f32x2{first ? f.x : 0.0f, second ? f.y : 0.0f};
     } else {
-      const float f = e8m0_scale_operand(first ? (s[t][0][u] >> (8 * g)) & 0xffu : 0u);
+      const float f = e8m0_scale_operand(first ? (s[0][u] >> (8 * g)) & 0xffu : 0u);
       return f32x2{f, f};
     }
   }
@@ -149,7 +143,7 @@ __device__ __forceinline__ u32x4 pinned(u32x4 v) {
 __device__ __forceinline__ u32x4 at16(const uint8_t* p) { return *reinterpret_cast<const u32x4*>(p); }
 
 // ---------------------------------------------------------------------------
-// few rows (4 RG of x): the workgroup shares x in LDS
+// 4 RG rows of x, which the workgroup shares in LDS
 // ---------------------------------------------------------------------------
 // x lies in LDS as bf16 operand rows, one for each activation row and term,
 // each 16 bytes longer than its values so that the rows' reads meet different
@@ -160,14 +154,15 @@ constexpr int kZeros = kUnit * 2;
 template <bool XBF, int RG>
 constexpr int kOpRows = (XBF ? 1 : 3) * 4 * RG;
 
-// fp32 rows on their way to LDS: a lane's eight numbers at k of four rows, of
+// fp32 rows on their way to LDS: a lane's eight numbers at k of two rows, of
 // which `live` are there (what the others hold meets only results that nobody
 // reads), cut into three terms.
+constexpr int kStageRows = 2;
 struct StageX {
-  u32x4 v[4][2];
-  __device__ __forceinline__ void load(const Call& a, const int64_t (&xo)[4], int live, int k) {
+  u32x4 v[kStageRows][2];
+  __device__ __forceinline__ void load(const Call& a, const int64_t (&xo)[kStageRows], int live, int k) {
 #pragma unroll
-    for (int r = 0; r < 4; r++) {
+    for (int r = 0; r < kStageRows; r++) {
       if (r < live) {
         const uint8_t* src = reinterpret_cast<const uint8_t*>(a.x) + (xo[r] + (k < a.K ? k : 0)) * 4;
         v[r][0] = at16(src);
@@ -178,7 +173,7 @@ struct StageX {
   // to: row 0's place; plane: bytes from one term's rows to the next's
   __device__ __forceinline__ void put(const Call& a, int live, int k, uint8_t* to, int pitch, int plane) {
 #pragma unroll
-    for (int r = 0; r < 4; r++) {
+    for (int r = 0; r < kStageRows; r++) {
       if (r < live) {
         if (k >= a.K) v[r][0] = v[r][1] = u32x4{0, 0, 0, 0};
         u32x4 t[3];
@@ -224,13 +219,14 @@ template <bool NV, bool XBF, int RG>
 constexpr bool diagonal = NV && XBF && RG <= 2;
 
 template <bool NV, bool XBF, int RG>
-struct FewRows {
+struct Product {
+  static_assert(XBF || RG <= 2);
   static constexpr bool DIAG = diagonal<NV, XBF, RG>;
   static constexpr int ROWS = kOpRows<XBF, RG>, OT = DIAG ? RG : (ROWS + 15) / 16;
   int from[OT], step[OT];  // of the lane's operands: where those of a segment's first unit lie, and from unit to unit
   f32x4 acc[OT];
 
-  __device__ __forceinline__ FewRows(int pitch) {
+  __device__ __forceinline__ Product(int pitch) {
     const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int o = 0; o < OT; o++) {
@@ -245,7 +241,7 @@ struct FewRows {
     for (int o = 0; o < OT; o++) acc[o] = f32x4{0, 0, 0, 0};
   }
   // One unit, which starts at k0 and is unit `at` of x in LDS.
-  __device__ __forceinline__ void multiply(const Weights<NV, 1>& o, int k0, int K, int at, const uint8_t* lds) {
+  __device__ __forceinline__ void multiply(const Weights<NV>& o, int k0, int K, int at, const uint8_t* lds) {
     const int g = (threadIdx.x & 63) >> 4;
     const uint8_t* x[OT];
 #pragma unroll
@@ -253,8 +249,8 @@ struct FewRows {
 #pragma unroll
     for (int u = 0; u < 4; u++) {
       __builtin_amdgcn_sched_barrier(0);  // (else the operands of all four pieces are read at once)
-      const u32x4 codes = pinned(o.w[0][u]);
-      const f32x2 sc = o.scale(0, u, k0 + u * 128, K, g);
+      const u32x4 codes = pinned(o.w[u]);
+      const f32x2 sc = o.scale(u, k0 + u * 128, K, g);
       if constexpr (DIAG) {
         bf16x8 w[4];
 #pragma unroll
@@ -299,14 +295,10 @@ struct FewRows {
 #pragma unroll
       for (int r = 0; r < 4; r++) {
         float v = acc[0][r];
-        if constexpr (RG == 4) {
-          acc[0][r] = v + acc[1][r] + acc[2][r];
-          continue;
-        }
         if constexpr (RG == 1) {
           v = g < 3 ? v : 0.0f;
           v += xor_shfl<16>(v);
-        } else if constexpr (RG == 2) {
+        } else {
           v += g < 2 ? acc[1][r] : 0.0f;
         }
         v += xor_shfl<32>(v);
@@ -425,9 +417,9 @@ __device__ __forceinline__ int64_t x_offset(const Call& a, int pair) {
 template <bool NV>
 constexpr int kAtOnce = NV ? 2 : 3;
 
-// LDS of a few rows' form: x, and zeros where an operand needs them.
+// LDS for seg_units units of x, and zeros where an operand needs them.
 template <bool NV, bool XBF, int RG>
-__host__ __device__ constexpr int few_bytes(int seg_units) {
+__host__ __device__ constexpr int x_bytes(int seg_units) {
   return kOpRows<XBF, RG> * (seg_units * (kUnit * 2) + 16) + (diagonal<NV, XBF, RG> ? kZeros : 0);
 }
 
@@ -436,34 +428,36 @@ __host__ __device__ constexpr int few_bytes(int seg_units) {
 // each wave with the next unit's weights on their way while it multiplies, over
 // the ends of tiles too.
 template <bool NV, bool XBF, int RG, int W, bool LIST>
-__device__ __forceinline__ void few_pairs(const Call& a, int expert, const uint16_t* list, int first, int live,
+__device__ __forceinline__ void tiles_of(const Call& a, int expert, const uint16_t* list, int first, int live,
                                           uint8_t* lds) {
   constexpr int MR = 4 * RG, ROWS = kOpRows<XBF, RG>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c16 = lane & 15, g = lane >> 4;
   const int per = W >> a.part_shift, parts = 1 << a.part_shift, part = wave & (parts - 1);
   const int units = a.units, pitch = a.seg_units * (kUnit * 2) + 16;
-  float* red = reinterpret_cast<float*>(lds + few_bytes<NV, XBF, RG>(a.seg_units));  // [W][MR][16], if parts > 1
+  float* red = reinterpret_cast<float*>(lds + x_bytes<NV, XBF, RG>(a.seg_units));  // [W][MR][16], if parts > 1
   int n0 = (blockIdx.x * a.rounds * per + (wave >> a.part_shift)) * 16;
   auto offset_of = [&](int row) {
     const int pair = LIST ? (int)list[row] : first + row;
     return x_offset(a, pair);
   };
-  // x for a segment: bf16 rows straight to LDS; fp32 as items i of n * RG in
-  // registers, octet i % n of row group i / n
+  // x for a segment: bf16 rows straight to LDS; fp32 as items i of n * GROUPS
+  // in registers, octet i % n of rows kStageRows * (i / n) on
+  constexpr int GROUPS = MR / kStageRows;
   StageX x;
   int group = 0, oct = 0;
   auto load_x = [&](int i, int n, int k0) {
     group = 0;
     oct = i;
 #pragma unroll
-    for (int h = 1; h < RG; h++) {
+    for (int h = 1; h < GROUPS; h++) {
       group += i >= h * n ? 1 : 0;
       oct -= i >= h * n ? n : 0;
     }
-    int64_t xo[4];
+    group *= kStageRows;
+    int64_t xo[kStageRows];
 #pragma unroll
-    for (int r = 0; r < 4; r++) xo[r] = offset_of(group * 4 + r < live ? group * 4 + r : live - 1);
-    x.load(a, xo, live - 4 * group, k0 + oct * 8);
+    for (int r = 0; r < kStageRows; r++) xo[r] = offset_of(group + r < live ? group + r : live - 1);
+    x.load(a, xo, live - group, k0 + oct * 8);
   };
   auto copy_all = [&](int u0, int here) {
     for (int row = 0; row < live; row++)
@@ -472,23 +466,23 @@ __device__ __forceinline__ void few_pairs(const Call& a, int expert, const uint1
   // (before the weights, so as not to arrive behind them)
   const int in_lds = units < a.seg_units ? units : a.seg_units, n1 = in_lds * 64;
   if constexpr (XBF) copy_all(0, in_lds);
-  else if (threadIdx.x < n1 * RG) load_x(threadIdx.x, n1, 0);
-  Place<1> at(a, expert, n0);
-  FewRows<NV, XBF, RG> rows(pitch);
+  else if (threadIdx.x < n1 * GROUPS) load_x(threadIdx.x, n1, 0);
+  Place at(a, expert, n0);
+  Product<NV, XBF, RG> rows(pitch);
   rows.clear();
   const float ts = NV ? a.ts[expert] : 1.0f;
   auto stage = [&](int u0, bool loaded) {
     const int here = units - u0 < a.seg_units ? units - u0 : a.seg_units;
     if (!loaded) __syncthreads();
-    if (FewRows<NV, XBF, RG>::DIAG && threadIdx.x < kZeros / 16)
+    if (Product<NV, XBF, RG>::DIAG && threadIdx.x < kZeros / 16)
       *reinterpret_cast<u32x4*>(lds + ROWS * pitch + threadIdx.x * 16) = u32x4{0, 0, 0, 0};
     if constexpr (XBF) {
       if (!loaded) copy_all(u0, here);
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (the copies to LDS are counted there)
     } else {
-      for (int i = threadIdx.x; i < here * 64 * RG; i += 64 * W) {
+      for (int i = threadIdx.x; i < here * 64 * GROUPS; i += 64 * W) {
         if (!loaded || i >= 64 * W) load_x(i, here * 64, u0 * kUnit);
-        x.put(a, live - 4 * group, u0 * kUnit + oct * 8, lds + 4 * group * pitch + oct * 16, pitch, MR * pitch);
+        x.put(a, live - group, u0 * kUnit + oct * 8, lds + group * pitch + oct * 16, pitch, MR * pitch);
       }
     }
     __syncthreads();
@@ -520,7 +514,7 @@ __device__ __forceinline__ void few_pairs(const Call& a, int expert, const uint1
   // A wave of few units has all their weights on the way at once.
   if constexpr (XBF) if (a.at_once) {
     constexpr int AT_ONCE = kAtOnce<NV>;
-    Weights<NV, 1> w[AT_ONCE];
+    Weights<NV> w[AT_ONCE];
 #pragma unroll
     for (int d = 0; d < AT_ONCE; d++) {
       if (d * parts < units) w[d].load(a, at, (part + d * parts) * kUnit, g);
@@ -536,17 +530,17 @@ __device__ __forceinline__ void few_pairs(const Call& a, int expert, const uint1
     finish();
     return;
   }
-  Weights<NV, 1> now;
+  Weights<NV> now;
   if (units > 0) now.load(a, at, part * kUnit, g);
   for (int round = 0; round < a.rounds; round++) {
     const bool last_tile = round + 1 == a.rounds;
-    const Place<1> after(a, expert, last_tile ? n0 : n0 + per * 16);
+    const Place after(a, expert, last_tile ? n0 : n0 + per * 16);
     int unit = part;
     for (int u0 = 0; u0 < units; u0 += a.seg_units) {
       const int here = units - u0 < a.seg_units ? units - u0 : a.seg_units;
       if (round == 0 || units > a.seg_units) stage(u0, round == 0 && u0 == 0);
       for (; unit < u0 + here; unit += parts) {
-        Weights<NV, 1> next;
+        Weights<NV> next;
         const bool over = unit + parts >= units;  // (of the last tile: bytes that nobody uses)
         next.load(a, over ? after : at, over && !last_tile ? part * kUnit : (unit + parts) * kUnit, g);
         rows.multiply(now, unit * kUnit, a.K, unit - u0, lds);
@@ -563,14 +557,14 @@ __device__ __forceinline__ void few_pairs(const Call& a, int expert, const uint1
 }  // namespace
 
 template <bool NV, bool XBF, int RG, int W>
-__global__ __launch_bounds__(64 * W, 4) void matvec_few_kernel(Call a) {
+__global__ __launch_bounds__(64 * W, 4) void matvec_kernel(Call a) {
   extern __shared__ __align__(16) uint8_t lds[];
   const int first = blockIdx.y * (4 * RG), left = a.pairs - first;
-  few_pairs<NV, XBF, RG, W, false>(a, 0, nullptr, first, left < 4 * RG ? left : 4 * RG, lds);
+  tiles_of<NV, XBF, RG, W, false>(a, 0, nullptr, first, left < 4 * RG ? left : 4 * RG, lds);
 }
 
 template <bool NV, bool XBF, int RG, int W>
-__global__ __launch_bounds__(64 * W, 4) void matvec_experts_few_kernel(Call a) {
+__global__ __launch_bounds__(64 * W, 4) void matvec_experts_kernel(Call a) {
   extern __shared__ __align__(16) uint8_t lds[];
   __shared__ Found found;
   __shared__ uint16_t list[4 * RG];
@@ -578,7 +572,7 @@ __global__ __launch_bounds__(64 * W, 4) void matvec_experts_few_kernel(Call a) {
   if (blockIdx.y == 0) zero_rows(a, blockIdx.x * cols, cols);
   find_slot(a, 4 * RG, &found, reinterpret_cast<uint32_t*>(lds), list);  // (x comes there later)
   if (found.expert < 0) return;
-  few_pairs<NV, XBF, RG, W, true>(a, __builtin_amdgcn_readfirstlane(found.expert), list, 0,
+  tiles_of<NV, XBF, RG, W, true>(a, __builtin_amdgcn_readfirstlane(found.expert), list, 0,
                                   __builtin_amdgcn_readfirstlane(found.count), lds);
 }
 
@@ -587,16 +581,18 @@ namespace {
 constexpr int kLds = 160 * 1024, kLdsApart = 4 * 1024;  // of a CU; kept for what is not x
 
 template <bool NV, bool XBF, int RG, int W>
-hipError_t launch_few(Call& c, int tiles, int slots, hipStream_t s) {
-  const int cus = device_cu_count(), all = 16 / W;  // workgroups a CU
+hipError_t launch_waves(Call& c, int tiles, int slots, hipStream_t s) {
+  const int cus = device_cu_count();
   // waves for a tile: as many as leave the workgroups room on the GPU at once
+  // (and no more than x in LDS has units for)
+  constexpr int red = W * RG * 256, all = 16 / W;  // (sums of the waves of a tile; workgroups a CU)
+  constexpr int room = (kLds / all - kLdsApart / (W < 8 ? 2 : 1) - red) / (kOpRows<XBF, RG> * kUnit * 2);
   c.part_shift = 0;
-  while ((2 << c.part_shift) <= W && (1 << c.part_shift) < c.units &&
+  while ((2 << c.part_shift) <= (W < room ? W : room) && (1 << c.part_shift) < c.units &&
          ((int64_t)tiles * slots * (2 << c.part_shift) + W - 1) / W <= all * cus)
     c.part_shift++;
-  const int red = c.part_shift > 0 ? W * RG * 256 : 0, room = (kLds / all - kLdsApart / (W < 8 ? 2 : 1) - red) / (kOpRows<XBF, RG> * kUnit * 2);
   // (all of x, or else whole turns of the waves)
-  c.seg_units = c.units < room ? c.units : room >> c.part_shift > 0 ? room >> c.part_shift << c.part_shift : room;
+  c.seg_units = c.units < room ? c.units : room >> c.part_shift << c.part_shift;
   // tiles one after another: once there are more workgroups than twice what fits at once, unless each would bring x anew
   c.rounds = 1;
   int per = W >> c.part_shift;
@@ -608,28 +604,28 @@ hipError_t launch_few(Call& c, int tiles, int slots, hipStream_t s) {
   c.at_once = XBF && c.rounds == 1 && c.units > 0 && units_of_wave <= kAtOnce<NV> &&
               (c.units <= c.seg_units || (c.seg_units & ((1 << c.part_shift) - 1)) == 0);
   const dim3 grid((tiles + per - 1) / per, slots), block(64 * W);
-  int lds = few_bytes<NV, XBF, RG>(c.seg_units) + red;
+  int lds = x_bytes<NV, XBF, RG>(c.seg_units) + (c.part_shift > 0 ? red : 0);
   if (c.ids) {
     lds = lds > 2 * c.experts + 2 ? lds : 2 * c.experts + 2;
-    hipLaunchKernelGGL((matvec_experts_few_kernel<NV, XBF, RG, W>), grid, block, lds, s, c);
+    hipLaunchKernelGGL((matvec_experts_kernel<NV, XBF, RG, W>), grid, block, lds, s, c);
   } else {
-    hipLaunchKernelGGL((matvec_few_kernel<NV, XBF, RG, W>), grid, block, lds, s, c);
+    hipLaunchKernelGGL((matvec_kernel<NV, XBF, RG, W>), grid, block, lds, s, c);
   }
   return hipGetLastError();
 }
 
 // Eight waves a workgroup where two have room on a CU with all of x, else 16.
 template <bool NV, bool XBF, int RG>
-hipError_t launch_few_rows(Call& c, int tiles, int slots, hipStream_t s) {
+hipError_t launch_rows(Call& c, int tiles, int slots, hipStream_t s) {
   if constexpr (RG == 1) {
-    if ((int64_t)tiles * slots * 2 >= 8 * device_cu_count() && few_bytes<NV, XBF, RG>(c.units) + 4 * RG * 256 <= kLds / 4 - kLdsApart / 2)
-      return launch_few<NV, XBF, RG, 4>(c, tiles, slots, s);
+    if ((int64_t)tiles * slots * 2 >= 8 * device_cu_count() && x_bytes<NV, XBF, RG>(c.units) + 4 * RG * 256 <= kLds / 4 - kLdsApart / 2)
+      return launch_waves<NV, XBF, RG, 4>(c, tiles, slots, s);
   }
   if constexpr (RG < 4) {
-    if (few_bytes<NV, XBF, RG>(c.units) + 8 * RG * 256 <= kLds / 2 - kLdsApart)
-      return launch_few<NV, XBF, RG, 8>(c, tiles, slots, s);
+    if (x_bytes<NV, XBF, RG>(c.units) + 8 * RG * 256 <= kLds / 2 - kLdsApart)
+      return launch_waves<NV, XBF, RG, 8>(c, tiles, slots, s);
   }
-  return launch_few<NV, XBF, RG, 16>(c, tiles, slots, s);
+  return launch_waves<NV, XBF, RG, 16>(c, tiles, slots, s);
 }
 
 template <bool NV, bool XBF>
@@ -665,9 +661,11 @@ hipError_t launch(const MatvecArgs& a, hipStream_t s) {
     if (!a.ids) return (c.pairs + rows - 1) / rows;
     return met + c.pairs / rows < c.pairs ? met + c.pairs / rows : c.pairs;
   };
-  if (c.pairs <= (a.ids ? 2 : 4) * met) return launch_few_rows<NV, XBF, 1>(c, tiles, slots(4), s);
-  if (c.pairs <= 8 * met) return launch_few_rows<NV, XBF, 2>(c, tiles, slots(8), s);
-  return launch_few_rows<NV, XBF, 4>(c, tiles, slots(16), s);
+  if (c.pairs <= (a.ids ? 2 : 4) * met) return launch_rows<NV, XBF, 1>(c, tiles, slots(4), s);
+  if constexpr (XBF) {
+    if (c.pairs > 8 * met) return launch_rows<NV, XBF, 4>(c, tiles, slots(16), s);
+  }
+  return launch_rows<NV, XBF, 2>(c, tiles, slots(8), s);
 }
 
 }  // namespace
