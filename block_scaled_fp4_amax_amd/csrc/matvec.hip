@@ -1,7 +1,22 @@
 // matvec.hip -- products of a few rows in 16 or 32 bits with 4-bit weights:
 //   y[p, n] = sum_k deq(W_e)[n, k] x[p / repeat, k], e = ids[p] (or 0),
-// accumulated in fp32. The weights' bytes are read once; activations are not
-// rounded.
+// accumulated in fp32. Activations are not rounded: bf16 ones are operands as
+// they are, fp32 ones three bf16 terms. Weights times their block's scale are
+// exact in bf16, so the matrix cores add exact products.
+//
+// A wave takes tiles of 16 rows of W and reads their bytes straight into
+// registers, 16 a lane, once for up to 16 rows of x (8 of fp32); the rows of x
+// lie in LDS for the whole workgroup. Where tiles are few, several waves share
+// one along K and their sums are added up in LDS, always in one order.
+//
+// What bounds it (MI355X; bytes at the 5.08 TB/s of a large copy):
+//   1 x 4096x4096 NVFP4, bf16        5.7 us  floor 1.9: launch, x to LDS, one trip to memory
+//   1 x 28672x4096 NVFP4, bf16      14.5 us        13.0: memory
+//   16 x 8192x8192 MXFP4, bf16      15.0 us         7.1: x to LDS (256 KB in two parts), then weights
+//   1 x 4 of 32 experts 5760x2880   10.0 us         6.9: memory and one trip to it
+//   8 x 4 of 32 experts 5760x2880   43   us        38.7: memory
+//   32 x 4 of 32 experts 2880x2880, fp32 rows, NVFP4  52 us  29.6: conversion and LDS reads of
+//     24 operand rows take as long as the bytes, and experts with over 8 pairs are read again
 #include "fp4_device.h"
 #include "launch.h"
 
@@ -157,7 +172,7 @@ constexpr int kOpRows = (XBF ? 1 : 3) * 4 * RG;
 // fp32 rows on their way to LDS: a lane's eight numbers at k of two rows, of
 // which `live` are there (what the others hold meets only results that nobody
 // reads), cut into three terms.
-constexpr int kStageRows = 2;
+constexpr int kStageRows = 2;  // (12 x 8192x8192 NVFP4: 27.9 us; 1 row 28.3, 4 rows 32.9 with registers spilt)
 struct StageX {
   u32x4 v[kStageRows][2];
   __device__ __forceinline__ void load(const Call& a, const int64_t (&xo)[kStageRows], int live, int k) {
@@ -431,7 +446,8 @@ template <bool NV, bool XBF, int RG, int W, bool LIST>
 __device__ __forceinline__ void tiles_of(const Call& a, int expert, const uint16_t* list, int first, int live,
                                           uint8_t* lds) {
   constexpr int MR = 4 * RG, ROWS = kOpRows<XBF, RG>;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c16 = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c16 = lane & 15, g = lane >> 4;
   const int per = W >> a.part_shift, parts = 1 << a.part_shift, part = wave & (parts - 1);
   const int units = a.units, pitch = a.seg_units * (kUnit * 2) + 16;
   float* red = reinterpret_cast<float*>(lds + x_bytes<NV, XBF, RG>(a.seg_units));  // [W][MR][16], if parts > 1
@@ -583,25 +599,35 @@ constexpr int kLds = 160 * 1024, kLdsApart = 4 * 1024;  // of a CU; kept for wha
 template <bool NV, bool XBF, int RG, int W>
 hipError_t launch_waves(Call& c, int tiles, int slots, hipStream_t s) {
   const int cus = device_cu_count();
-  // waves for a tile: as many as leave the workgroups room on the GPU at once
-  // (and no more than x in LDS has units for)
   constexpr int red = W * RG * 256, all = 16 / W;  // (sums of the waves of a tile; workgroups a CU)
   constexpr int room = (kLds / all - kLdsApart / (W < 8 ? 2 : 1) - red) / (kOpRows<XBF, RG> * kUnit * 2);
+  auto units_of = [&](int shift) { return (c.units + (1 << shift) - 1) >> shift; };  // a wave's
+  auto at_once = [&](int shift) { return XBF && units_of(shift) <= kAtOnce<NV>; };
+  // Waves for a tile: as many as leave the workgroups room on the GPU at once
+  // (one a tile: 1 x 4096x4096 13.6 us for 5.4, 16 x 8192x8192 48 for 15; as
+  // many as W has: 8 x 4 of 32 experts 54.6 for 42), or twice that where a wave
+  // then has all its weights on the way at once (1 x 28672x4096 14.3 us for
+  // 16.9). No more than x in LDS has units for.
   c.part_shift = 0;
-  while ((2 << c.part_shift) <= (W < room ? W : room) && (1 << c.part_shift) < c.units &&
-         ((int64_t)tiles * slots * (2 << c.part_shift) + W - 1) / W <= all * cus)
-    c.part_shift++;
+  for (; (2 << c.part_shift) <= (W < room ? W : room) && (1 << c.part_shift) < c.units; c.part_shift++) {
+    const int64_t blocks = ((int64_t)tiles * slots * (2 << c.part_shift) + W - 1) / W;
+    const bool more = at_once(c.part_shift + 1) && !at_once(c.part_shift);
+    if (blocks > (more ? 2 : 1) * all * cus) break;
+  }
   // (all of x, or else whole turns of the waves)
   c.seg_units = c.units < room ? c.units : room >> c.part_shift << c.part_shift;
-  // tiles one after another: once there are more workgroups than twice what fits at once, unless each would bring x anew
+  // Tiles one after another, once there are more workgroups than twice what
+  // fits at once: each would bring x anew (32 x 4 of 32 experts 5760x2880 MXFP4
+  // 60 us, else 63; fp32 rows of 2880x2880 51, else 54; 8 x 4 NVFP4 42 and 39).
+  // Not where x does not fit: every tile would bring all of it again.
   c.rounds = 1;
   int per = W >> c.part_shift;
   while (c.part_shift == 0 && c.seg_units == c.units && (int64_t)((tiles + per - 1) / per) * slots > 2 * all * cus) {
     per += W;
     c.rounds++;
   }
-  const int units_of_wave = (c.units + (1 << c.part_shift) - 1) >> c.part_shift;
-  c.at_once = XBF && c.rounds == 1 && c.units > 0 && units_of_wave <= kAtOnce<NV> &&
+  // (1 x 4096x4096 5.4 us for 6.0, 4 x 1024x4096 5.6 for 6.4, 32 x 4096x4096 8.1 for 9.4)
+  c.at_once = at_once(c.part_shift) && c.rounds == 1 && c.units > 0 &&
               (c.units <= c.seg_units || (c.seg_units & ((1 << c.part_shift) - 1)) == 0);
   const dim3 grid((tiles + per - 1) / per, slots), block(64 * W);
   int lds = x_bytes<NV, XBF, RG>(c.seg_units) + (c.part_shift > 0 ? red : 0);
@@ -614,16 +640,21 @@ hipError_t launch_waves(Call& c, int tiles, int slots, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Eight waves a workgroup where two have room on a CU with all of x, else 16.
+// Waves of a workgroup: 16 share one copy of x, but wait for all of it and for
+// each other. Eight where two such workgroups have room on a CU with all of x
+// (1 x 4096x4096 5.4 us, 16 waves 6.9; 32 x 4 of 32 experts 5760x2880 60 and 99).
+// Four where that leaves room too and there are tiles for half the GPU's eight
+// waves a CU (1 x 4 of 32 experts 5760x2880 9.5 us, 8 waves 11.6; 2 x 8 of 128
+// experts 1536x4096 14.0 and 15.8).
 template <bool NV, bool XBF, int RG>
 hipError_t launch_rows(Call& c, int tiles, int slots, hipStream_t s) {
+  const int x = x_bytes<NV, XBF, RG>(c.units);
   if constexpr (RG == 1) {
-    if ((int64_t)tiles * slots * 2 >= 8 * device_cu_count() && x_bytes<NV, XBF, RG>(c.units) + 4 * RG * 256 <= kLds / 4 - kLdsApart / 2)
+    if ((int64_t)tiles * slots * 2 >= 8 * device_cu_count() && x + 4 * RG * 256 <= kLds / 4 - kLdsApart / 2)
       return launch_waves<NV, XBF, RG, 4>(c, tiles, slots, s);
   }
   if constexpr (RG < 4) {
-    if (x_bytes<NV, XBF, RG>(c.units) + 8 * RG * 256 <= kLds / 2 - kLdsApart)
-      return launch_waves<NV, XBF, RG, 8>(c, tiles, slots, s);
+    if (x + 8 * RG * 256 <= kLds / 2 - kLdsApart) return launch_waves<NV, XBF, RG, 8>(c, tiles, slots, s);
   }
   return launch_waves<NV, XBF, RG, 16>(c, tiles, slots, s);
 }
@@ -661,6 +692,13 @@ hipError_t launch(const MatvecArgs& a, hipStream_t s) {
     if (!a.ids) return (c.pairs + rows - 1) / rows;
     return met + c.pairs / rows < c.pairs ? met + c.pairs / rows : c.pairs;
   };
+  // Rows a pass, by how many an expert has on average (some have twice that):
+  // 4 cost least where they suffice (16 rows four at a time: the weights four
+  // times); of 32 experts with 4 pairs each, slots of 8 take 60 us and of 4 77,
+  // with fp32 rows 51 and 57. 16 x 5760x2880 as 16 rows 9.1 us, 8 and 8 11.0;
+  // 32 x 4096x4096 8.1 and 10.1. fp32 rows come no more than 8 at a time: 16
+  // are 48 operand rows, and LDS then holds 1024 of K (16 x 4096x4096 27 us for
+  // 13, 12 x 8192x8192 59 for 28).
   if (c.pairs <= (a.ids ? 2 : 4) * met) return launch_rows<NV, XBF, 1>(c, tiles, slots(4), s);
   if constexpr (XBF) {
     if (c.pairs > 8 * met) return launch_rows<NV, XBF, 4>(c, tiles, slots(16), s);

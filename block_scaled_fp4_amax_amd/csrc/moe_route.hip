@@ -15,8 +15,16 @@
 // The choice is that of the exact numbers. Without a bias the order of the
 // scores is that of the logits, which are compared as they are. With one (or
 // where a group's rank is a sum of two scores) c is computed in fp32 with a
-// known error; where two neighbours of the resulting order lie within it, the
-// row is done again in double (a few rows in a thousand).
+// known error; where two neighbours of the resulting order lie within it, those
+// few candidates (or the best scores of each group) are done again in double.
+//
+// Bound by vector instructions, about 1700 a wave where four tokens have 256
+// experts in groups: 16384 tokens of 256 fp32 logits (17.8 MB, which a copy
+// moves in 3.5 us) take 16.4 us with a biased sigmoid and groups, 14.5 without
+// groups; 1 token of 32 experts 2.8. (Every choice as a maximum over all keys
+// took 53: instead each lane sorts its own keys once, and a choice is a maximum
+// of the 16 heads and a shift of one lane's keys. A row done again as a whole
+// held the kernel up for 9 us, where its candidates alone take 1.)
 #include <float.h>
 
 #include "fp4_device.h"
@@ -204,53 +212,66 @@ __device__ __forceinline__ void sort_down(double (&key)[N]) {
           }
 }
 
-// Which of the lane's experts belong to the groups kept (bit v), from the
-// choice values c; c of experts that may not be chosen is -inf. `gap`: the
+// x joins a best and second best number.
+template <typename T>
+__device__ __forceinline__ void join_best(T& b1, T& b2, T x) {
+  b2 = __builtin_elementwise_max(b2, __builtin_elementwise_min(b1, x));
+  b1 = __builtin_elementwise_max(b1, x);
+}
+
+// What of two scores a group's rank is made of, and the larger magnitude in it.
+template <typename T>
+__device__ __forceinline__ T group_rank(const RouteArgs& a, T b1, T b2, T* mag) {
+  const bool two = a.best == 2 && b2 > -(T)__builtin_inff();
+  *mag = __builtin_elementwise_max(__builtin_elementwise_abs(b1), two ? __builtin_elementwise_abs(b2) : (T)0);
+  return two ? b1 + b2 : b1;
+}
+
+// Whether the lane's group is kept, where a.lanes_of_group (1, 2, 4 or 8) lanes
+// of a row of 16 make a group, from the best two of each lane. `gap`: the
 // difference between the last rank kept and the first left out, `size` the
 // larger magnitude that entered either.
+template <typename T>
+__device__ __forceinline__ bool keep_lane(const RouteArgs& a, T b1, T b2, int lane, T* gap, T* size) {
+  const T none = -(T)__builtin_inff(), big = (T)__builtin_inff();
+  auto join = [&](T o1, T o2) {
+    b2 = __builtin_elementwise_max(__builtin_elementwise_max(b2, o2), __builtin_elementwise_min(b1, o1));
+    b1 = __builtin_elementwise_max(b1, o1);
+  };
+  const int q = a.lanes_of_group;
+  if (q > 1) join(move<1>(b1), move<1>(b2));
+  if (q > 2) join(move<2>(b1), move<2>(b2));
+  if (q > 4) join(move<4>(b1), move<4>(b2));
+  T mag;
+  const T rank = group_rank(a, b1, b2, &mag);
+  // lanes ahead of this one: those of better groups
+  const int mine = lane & -q;
+  int ahead = 0;
+  turns<1>(rank, lane, [&](T r, int from) { ahead += (int)(r > rank) | ((int)(r == rank) & (int)(from < mine)); });
+  const bool there = rank > none, kept = there && ahead < a.top_groups * q;
+  *gap = reduce<16>(kept ? rank : big, Min()) - reduce<16>(there && !kept ? rank : none, Max());
+  *size = reduce<16>(there ? mag : (T)0, Max());
+  return kept;
+}
+
+// Which of the lane's experts belong to the groups kept (bit v), from the
+// choice values c; c of experts that may not be chosen is -inf.
 template <int L, int VPL, typename T>
 __device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, const T (&c)[VPL], int lane, T* gap, T* size) {
   const int gs = a.group_size, G = a.groups;
   const T none = -(T)__builtin_inff();
   T rank = none, mag = (T)0;  // of group `lane`
   if (L == 16 && a.lanes_of_group > 0) {
-    // whole lanes make a group (1, 2, 4 or 8 of them): its best two in each of its lanes
     T b1 = none, b2 = none;
 #pragma unroll
-    for (int v = 0; v < VPL; v++) {
-      b2 = __builtin_elementwise_max(b2, __builtin_elementwise_min(b1, c[v]));
-      b1 = __builtin_elementwise_max(b1, c[v]);
-    }
-    auto join = [&](T o1, T o2) {
-      b2 = __builtin_elementwise_max(__builtin_elementwise_max(b2, o2), __builtin_elementwise_min(b1, o1));
-      b1 = __builtin_elementwise_max(b1, o1);
-    };
-    const int q = a.lanes_of_group;
-    if (q > 1) join(move<1>(b1), move<1>(b2));
-    if (q > 2) join(move<2>(b1), move<2>(b2));
-    if (q > 4) join(move<4>(b1), move<4>(b2));
-    const bool two = a.best == 2 && b2 > none;
-    rank = two ? b1 + b2 : b1;
-    mag = __builtin_elementwise_max(__builtin_elementwise_abs(b1), two ? __builtin_elementwise_abs(b2) : (T)0);
-    // lanes ahead of this one: those of better groups
-    const int mine = lane & -q;
-    int ahead = 0;
-    turns<1>(rank, lane, [&](T r, int from) { ahead += (int)(r > rank) | ((int)(r == rank) & (int)(from < mine)); });
-    const bool there = rank > none, kept = there && ahead < a.top_groups * q;
-    const T big = (T)__builtin_inff();
-    *gap = reduce<L>(kept ? rank : big, Min()) - reduce<L>(there && !kept ? rank : none, Max());
-    *size = reduce<L>(there ? mag : (T)0, Max());
-    return kept ? ~0u : 0u;
+    for (int v = 0; v < VPL; v++) join_best(b1, b2, c[v]);
+    return keep_lane(a, b1, b2, lane, gap, size) ? ~0u : 0u;
   }
-  auto add = [](T& b1, T& b2, T x) {
-    b2 = __builtin_elementwise_max(b2, __builtin_elementwise_min(b1, x));
-    b1 = __builtin_elementwise_max(b1, x);
-  };
   for (int g = 0; g < G; g++) {
     T b1 = none, b2 = none;
     const int first = lane * VPL - g * gs;  // of the lane's experts, counted in the group
 #pragma unroll
-    for (int v = 0; v < VPL; v++) add(b1, b2, (unsigned)(first + v) < (unsigned)gs ? c[v] : none);
+    for (int v = 0; v < VPL; v++) join_best(b1, b2, (unsigned)(first + v) < (unsigned)gs ? c[v] : none);
     auto join = [&](T o1, T o2) {
       b2 = __builtin_elementwise_max(__builtin_elementwise_max(b2, o2), __builtin_elementwise_min(b1, o1));
       b1 = __builtin_elementwise_max(b1, o1);
@@ -263,11 +284,7 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, const T (&c)
       join(move<16>(b1), move<16>(b2));
       join(move<32>(b1), move<32>(b2));
     }
-    const bool two = a.best == 2 && b2 > none;
-    if (lane == g) {
-      rank = two ? b1 + b2 : b1;
-      mag = __builtin_elementwise_max(__builtin_elementwise_abs(b1), two ? __builtin_elementwise_abs(b2) : (T)0);
-    }
+    if (lane == g) rank = group_rank(a, b1, b2, &mag);
   }
   int ahead = 0;
   for (int g = 0; g < G; g++) {
@@ -308,6 +325,35 @@ __device__ __forceinline__ double softmax_sum(const float (&l)[VPL], float m, do
 __device__ __forceinline__ double exact_score(const RouteArgs& a, double z, double m, double inv_sum) {
   const double p = exp(a.sigmoid ? -__builtin_fabs(z) : z - m);
   return a.sigmoid ? (z >= 0 ? 1.0 : p) / (1.0 + p) : p * inv_sum;
+}
+
+// keep_lane where errors make it unsure: the lane's best scores again in
+// double, one after another, until the next is surely behind the second
+// (`close`); two of them as a rule.
+template <int VPL, typename CLOSE>
+__device__ __forceinline__ bool keep_lane_exactly(const RouteArgs& a, const void* row, const float (&c)[VPL], int lane,
+                                                  double m, double inv_sum, CLOSE close) {
+  float left[VPL], second = neg_inf();
+#pragma unroll
+  for (int v = 0; v < VPL; v++) left[v] = c[v];
+  double b1 = -(double)__builtin_inff(), b2 = b1, gap, size;
+#pragma unroll 1
+  for (int i = 0; i < VPL; i++) {
+    float best = neg_inf();
+    int at = 0;
+#pragma unroll
+    for (int v = 0; v < VPL; v++) {
+      at = left[v] > best ? v : at;
+      best = __builtin_fmaxf(best, left[v]);
+    }
+    if (!(best > neg_inf()) || (i > 1 && !close(second, best))) break;
+    second = i < 2 ? best : second;
+#pragma unroll
+    for (int v = 0; v < VPL; v++) left[v] = v == at ? neg_inf() : left[v];
+    const int e = lane * VPL + at;
+    join_best(b1, b2, exact_score(a, load_logit(a, row, e), m, inv_sum) + (a.bias ? a.bias[e] : 0.0f));
+  }
+  return keep_lane(a, b1, b2, lane, &gap, &size);
 }
 
 // The first n lanes hold one candidate each, in an order that their scores'
@@ -438,12 +484,21 @@ __global__ __launch_bounds__(256, 4) void route_kernel(RouteArgs a) {
       c[v] = c[v] > neg_inf() && s == s ? s : neg_inf();
     }
   }
+  // Could two neighbours of the order be the other way round?
+  auto close = [&](float x, float y) {
+    return !(x - y > 2.0f * unsure + 0x1p-24f * (__builtin_fabsf(x) + __builtin_fabsf(y)));
+  };
   uint32_t in = ~0u;
   if (limited) {
     float gap, size;
     in = keep_groups<L, VPL>(a, c, lane, &gap, &size);
     // a rank of two scores: each with its error, and three roundings
     if (group_score) sure = !(gap <= 4.0f * unsure + 0x1p-22f * size);
+    if (L == 16 && !sure && a.lanes_of_group > 0) {
+      const double inv_sum = a.sigmoid ? 1.0 : 1.0 / softmax_sum<L>(l, m, spare);
+      in = keep_lane_exactly<VPL>(a, row, c, lane, m, inv_sum, close) ? ~0u : 0u;
+      sure = true;
+    }
   }
 #pragma unroll
   for (int v = 0; v < VPL; v++) {
@@ -461,10 +516,6 @@ __global__ __launch_bounds__(256, 4) void route_kernel(RouteArgs a) {
       key[D - 1] = -DBL_MAX;
     }
     return best;
-  };
-  // Could two neighbours of the order be the other way round?
-  auto close = [&](float x, float y) {
-    return !(x - y > 2.0f * unsure + 0x1p-24f * (__builtin_fabsf(x) + __builtin_fabsf(y)));
   };
   bool ordered = true, next = false;  // next: lane top_k of a row of 16 holds the one after the chosen
   for (int j = 0; j < a.top_k + (by_score ? 1 : 0); j++) {
@@ -541,6 +592,9 @@ __global__ __launch_bounds__(256, 4) void route_kernel(RouteArgs a) {
 // scaled dw of the chosen and 0 elsewhere, sigmoid g_e s (1 - s); with it, and
 // q_j the chosen scores over their sum, softmax q_j (g_j - sum q g), sigmoid
 // that times (1 - s_j). One pass: the row is read once and written once.
+// 16384 tokens of 160 bf16 logits, 6 chosen: 10.7 us, 1 TB/s (22 MB; a copy
+// takes 4.3): bound by the exponentials and their sums, a lane's ten experts
+// against few bytes. (As two passes over the row: 22.)
 template <int L, int VPL>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackwardArgs b) {
   const RouteArgs& a = b.a;
@@ -655,10 +709,17 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackwardArgs b
 
 namespace {
 
-// Lanes for one token: a row of 16 where that fills the GPU, else a wave,
-// which is done sooner (and what more than 16 groups, or more than 256 experts, need).
-bool wide_route(const RouteArgs& a) {
-  return a.experts > 256 || a.groups > 16 || a.tokens <= 4 * device_cu_count();
+// Lanes for one token: a row of 16, but a wave for more than 256 experts or 16
+// groups. (A wave for each of a few tokens is no sooner done: 1024 tokens of 32
+// experts 4.3 us, rows 3.8; of 256 in groups 9.8 and 8.4; of 160 5.2 and 5.6.)
+bool wide_route(const RouteArgs& a) { return a.experts > 256 || a.groups > 16; }
+
+// The gradient, which has no steps from choice to choice, does gain from a
+// wave's shorter turns up to some thousand tokens of many experts: 64 tokens of
+// 256 4.3 us, rows 4.9; 4096 of them 5.6 and 6.3; 16384 of 160 12.9 and 10.7.
+// (64 experts: 3.8 and 3.2.)
+bool wide_backward(const RouteArgs& a) {
+  return a.experts > 256 || (a.experts > 64 && a.tokens <= 16 * device_cu_count());
 }
 
 // What depends on the lanes' shares: 16-byte rows, and lanes that make a group.
@@ -673,10 +734,9 @@ void set_shares(RouteArgs& a) {
 }
 
 template <template <int, int> class LAUNCH, typename ARGS>
-hipError_t route_by_size(const RouteArgs& a, const ARGS& args, hipStream_t s) {
-  if (wide_route(a)) {
+hipError_t route_by_size(bool wide, const RouteArgs& a, const ARGS& args, hipStream_t s) {
+  if (wide) {
     const int per = (a.experts + 63) / 64;
-    if (per <= 1) return LAUNCH<64, 1>::go(args, a.tokens, s);
     if (per <= 2) return LAUNCH<64, 2>::go(args, a.tokens, s);
     if (per <= 4) return LAUNCH<64, 4>::go(args, a.tokens, s);
     if (per <= 8) return LAUNCH<64, 8>::go(args, a.tokens, s);
@@ -713,13 +773,13 @@ struct Backward {
 
 hipError_t launch_moe_route(RouteArgs a, hipStream_t s) {
   set_shares(a);
-  return route_by_size<Forward>(a, a, s);
+  return route_by_size<Forward>(wide_route(a), a, a, s);
 }
 hipError_t launch_moe_route_backward(RouteBackwardArgs b, hipStream_t s) {
   set_shares(b.a);
   const int64_t piece = b.a.bf16 ? 8 : 16;
   b.vec_out = (uintptr_t)b.out % piece == 0 && (b.ld_out * (b.a.bf16 ? 2 : 4)) % piece == 0 && b.a.experts % 4 == 0;
-  return route_by_size<Backward>(b.a, b, s);
+  return route_by_size<Backward>(wide_backward(b.a), b.a, b, s);
 }
 
 }  // namespace fp4impl

@@ -59,7 +59,9 @@ CASES = [
     (9, 1024, 32, dict(score="sigmoid")),
     (9, 1000, 10, dict(groups=10, top_groups=4, best=2, renormalize=False)),
     (9, 257, 9, dict(score="sigmoid", groups=1)),
-    # enough tokens for the form of 16 lanes a token
+    (31, 240, 6, dict(groups=24, top_groups=7, best=2)),
+    (31, 200, 15, dict(score="sigmoid", groups=40, top_groups=17)),
+    # more tokens
     (1500, 8, 2, dict()),
     (1501, 16, 16, dict(score="sigmoid")),
     (2000, 32, 4, dict(scale=0.5)),
@@ -123,6 +125,40 @@ def test_choice_is_that_of_the_exact_scores(fp4, score, T, E):
     check(fp4, z, 4, torch.from_numpy(bias), score=score)
     check(fp4, z, 4, torch.from_numpy(bias), score=score, groups=8, top_groups=3, best=2)
     check(fp4, z, 4, score=score, groups=8, top_groups=3, best=2)
+
+
+def near_ranks(T, E, score, bias, groups, top_groups, best):
+    """Logits whose last group kept and first left out have ranks that differ by less than fp32 resolves."""
+    z = logits(T, E, "f32", 21).double().numpy()
+    b = 0.0 if bias is None else bias.double().numpy()
+    rows = np.arange(T)
+
+    def ranks():
+        parts = np.sort((M.scores(z, score) + b).reshape(T, groups, -1), -1)
+        return parts[..., -best:].sum(-1)
+
+    order = np.argsort(-ranks(), 1)
+    a, f = order[:, top_groups - 1], order[:, top_groups]
+    e = f * (E // groups) + np.argmax((M.scores(z, score) + b).reshape(T, groups, -1)[rows, f], -1)
+    for _ in range(60):  # the best score of the one left out moves to where the ranks meet
+        r, s = ranks(), M.scores(z, score)[rows, e]
+        want = np.clip(s + r[rows, a] - r[rows, f], 0.5 * s, 1 - 1e-6)
+        z[rows, e] += np.log(want / s) + (np.log((1 - s) / (1 - want)) if score == "sigmoid" else 0)
+    z = z.astype(np.float32).astype(np.float64)
+    gap = np.abs(ranks()[rows, a] - ranks()[rows, f])
+    assert ((gap > 1e-13) & (gap < 2e-7)).mean() > 0.3  # (the rows are what they are meant to be)
+    z[gap < 1e-13] = np.arange(E) / E                   # (nearer than 64 bits tell: another row)
+    return torch.from_numpy(z).float()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("E,groups,top_groups,best", [(256, 8, 4, 2), (64, 8, 3, 2), (160, 10, 4, 2), (96, 3, 1, 2),
+                                                      (32, 16, 5, 2), (40, 5, 2, 2), (640, 20, 6, 2)])
+def test_groups_are_those_of_the_exact_ranks(fp4, E, groups, top_groups, best, with_bias, score):
+    bias = 0.1 * torch.randn(E, generator=torch.Generator().manual_seed(8)) if with_bias else None
+    z = near_ranks(300, E, score, bias, groups, top_groups, best)
+    check(fp4, z, 4, bias, score=score, groups=groups, top_groups=top_groups, best=best)
 
 
 @pytest.mark.parametrize("T", [6, 1500])
@@ -198,7 +234,8 @@ def test_row_pitch_and_empty(fp4):
     assert fp4.moe_route_backward(g[:0], wide[:0], ids).shape == (0, 90)
 
 
-BACKWARD = [(1, 32, 4), (5, 1, 1), (37, 60, 6), (33, 1024, 32), (1500, 16, 16), (1501, 160, 6), (1400, 256, 20)]
+BACKWARD = [(1, 32, 4), (5, 1, 1), (37, 60, 6), (33, 1024, 32), (1500, 16, 16), (1501, 160, 6), (1400, 256, 20),
+            (4400, 160, 6), (4500, 100, 7)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
