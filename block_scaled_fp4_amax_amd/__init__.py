@@ -1,5 +1,6 @@
-"""block_scaled_fp4_amax_amd -- block-scaled FP4 (E2M1) quantization and the
-W4A4 block-scaled GEMM on AMD MI355X (gfx950).
+"""block_scaled_fp4_amax_amd -- block-scaled FP4 (E2M1) quantization, the
+W4A4 block-scaled GEMM, a paged key-value cache and a mixture of experts around
+4-bit weights, on AMD MI355X (gfx950).
 
 The compute lives in ``libfp4.so`` (hand-written HIP kernels behind the C ABI
 of ``include/fp4.h``). This module only marshals arguments:

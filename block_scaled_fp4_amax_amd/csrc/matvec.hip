@@ -15,8 +15,8 @@
 //   16 x 8192x8192 MXFP4, bf16      15.0 us         7.1: x to LDS (256 KB in two parts), then weights
 //   1 x 4 of 32 experts 5760x2880   10.0 us         6.9: memory and one trip to it
 //   8 x 4 of 32 experts 5760x2880   43   us        38.7: memory
-//   32 x 4 of 32 experts 2880x2880, fp32 rows, NVFP4  52 us  29.6: conversion and LDS reads of
-//     24 operand rows take as long as the bytes, and experts with over 8 pairs are read again
+//   32 x 4 of 32 experts 2880x2880, fp32 rows, NVFP4  49 us  29.6: vector instructions 59 % of
+//     the cycles (every weight scaled and rounded), matrix ones 20 %; experts of over 8 pairs read again
 #include "fp4_device.h"
 #include "launch.h"
 

@@ -20,7 +20,7 @@
 //
 // Bound by vector instructions, about 1700 a wave where four tokens have 256
 // experts in groups: 16384 tokens of 256 fp32 logits (17.8 MB, which a copy
-// moves in 3.5 us) take 16.4 us with a biased sigmoid and groups, 14.5 without
+// moves in 3.5 us) take 16.5 us with a biased sigmoid and groups, 14.5 without
 // groups; 1 token of 32 experts 2.8. (Every choice as a maximum over all keys
 // took 53: instead each lane sorts its own keys once, and a choice is a maximum
 // of the 16 heads and a shift of one lane's keys. A row done again as a whole
@@ -592,9 +592,9 @@ __global__ __launch_bounds__(256, 4) void route_kernel(RouteArgs a) {
 // scaled dw of the chosen and 0 elsewhere, sigmoid g_e s (1 - s); with it, and
 // q_j the chosen scores over their sum, softmax q_j (g_j - sum q g), sigmoid
 // that times (1 - s_j). One pass: the row is read once and written once.
-// 16384 tokens of 160 bf16 logits, 6 chosen: 10.7 us, 1 TB/s (22 MB; a copy
-// takes 4.3): bound by the exponentials and their sums, a lane's ten experts
-// against few bytes. (As two passes over the row: 22.)
+// 16384 tokens of 160 fp32 logits, 6 chosen: 10.0 us, 2.1 TB/s (21 MB; a copy
+// takes 4.3): bound by vector instructions, 745 a wave (57 % of the cycles), that
+// stand behind one trip to memory. (As two passes over the row: 22.)
 template <int L, int VPL>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackwardArgs b) {
   const RouteArgs& a = b.a;

@@ -1,6 +1,7 @@
 /*
  * fp4.h -- C ABI of the block-scaled FP4 (E2M1) library for AMD Instinct
- * MI355X (gfx950): quantize, dequantize and the W4A4 block-scaled GEMM.
+ * MI355X (gfx950): quantize, dequantize, the W4A4 block-scaled GEMM, a paged
+ * key-value cache, and a mixture of experts around 4-bit weights.
  *
  * Formats (Ultralytics glossary page "FP4", section "Como funciona FP4"):
  *   E2M1 element: 1 sign, 2 exponent, 1 mantissa bit; magnitudes
