@@ -972,10 +972,10 @@ fp4_status fp4_matvec(const fp4_matvec_args* m, void* stream) {
   const int64_t blk = nv ? 16 : 32;
   if (m->pairs < 0 || m->repeat < 1 || m->N < 0 || m->K < 0 || m->K % blk != 0 || m->experts < 1) return FP4_ERR_INVALID;
   if (m->experts > 4096 || m->K > (int64_t(1) << 24) || m->N > (int64_t(1) << 30)) return FP4_ERR_UNSUPPORTED;
-  // (passes of 16 rows along y, and up to 1024 work items for each 16 columns along x)
-  if (m->pairs > 16 * kMaxGridYZ || (m->N + 15) / 16 > kMaxItemsX / 1024) return FP4_ERR_UNSUPPORTED;
+  // (passes of 16 rows, 8 of fp32, along y; up to 1024 work items for each 16 columns along x)
+  if (m->pairs > (m->x_dtype == FP4_BF16 ? 16 : 8) * kMaxGridYZ || (m->N + 15) / 16 > kMaxItemsX / 1024) return FP4_ERR_UNSUPPORTED;
   if (m->ids && m->pairs > 4096) return FP4_ERR_UNSUPPORTED;
-  // (a tile of 32 rows is addressed with 32 bits)
+  // (a tile of 16 rows is addressed with 32 bits)
   if (m->ld_codes >= (int64_t(1) << 23) || m->ld_scales >= (int64_t(1) << 23)) return FP4_ERR_UNSUPPORTED;
   if (m->pairs == 0 || m->N == 0) return FP4_OK;
   if (!m->y || m->ld_y < m->N) return FP4_ERR_INVALID;

@@ -631,10 +631,10 @@ typedef struct fp4_matvec_args {
  * bytes are all the work: they are read in 4 bits, once, and the activations
  * are not quantized, nor rounded at all (fp32 as three bf16 terms that hold
  * its 24 bits). Sums in fp32, y rounded once. The work grows with every 16
- * rows; past some dozens (of one matrix) fp4_gemm and fp4_gemm_grouped on
+ * rows (8 of fp32); past some dozens (of one matrix) fp4_gemm and fp4_gemm_grouped on
  * quantized activations are faster.
  *   ids outside [0, experts) give rows of zeros. Limits (beyond:
- *   FP4_ERR_UNSUPPORTED): 2^20 - 16 pairs, with ids 4096; N 2^26 - 64; K 2^24;
+ *   FP4_ERR_UNSUPPORTED): 2^20 - 16 pairs, 2^19 - 8 of fp32, with ids 4096; N 2^26 - 64; K 2^24;
  *   row pitches of codes and scales below 8 MiB.
  *   Weights quantized with FP4_HADAMARD stand for rotated ones: x has to be
  *   rotated by the same signs.

@@ -139,6 +139,14 @@ def test_matvec_refusals(fp4):
         assert F.fp4_matvec(matvec_args(F, **kw), None) == F.FP4_OK, kw
 
 
+def test_fp32_rows_of_matvec_past_the_grid(fp4):
+    """fp32 rows go eight a pass: 65535 passes are 2^19 - 8 rows."""
+    F = fp4
+    assert F.fp4_matvec(matvec_args(F, x_dtype=0, pairs=(1 << 19) - 7, ld_x=256), None) == F.FP4_ERR_UNSUPPORTED
+    if NO_GPU:
+        assert F.fp4_matvec(matvec_args(F, x_dtype=0, pairs=(1 << 19) - 8, ld_x=256), None) == F.FP4_ERR_DEVICE
+
+
 @cpu_only
 def test_good_calls_reach_the_device_check(fp4):
     F = fp4
