@@ -754,7 +754,7 @@ fp4_status fp4_kv_attention(const fp4_kv_cache* cache, const fp4_kv_attention_ar
 namespace {
 
 // Routed layers: what a launch's first grid dimension and 32-bit places hold.
-constexpr int64_t kMaxRouteTokens = int64_t(1) << 26;
+constexpr int64_t kMaxRouteTokens = kMaxItemsX / 256 * 4;  // (workgroups of 256 for four tokens)
 constexpr int64_t kMaxPairs = int64_t(1) << 24;
 constexpr int kMaxTopK = 1024;
 
@@ -770,7 +770,7 @@ fp4_status plan_moe_route(const fp4_moe_route_args* r, RouteArgs* a) {
   if (r->groups > 64) return FP4_ERR_UNSUPPORTED;
   if (r->group_best != 1 && r->group_best != 2) return FP4_ERR_INVALID;
   if (!finite(r->scale)) return FP4_ERR_INVALID;
-  if (r->tokens >= kMaxRouteTokens) return FP4_ERR_UNSUPPORTED;
+  if (r->tokens > kMaxRouteTokens) return FP4_ERR_UNSUPPORTED;
   if (r->tokens > 0) {
     if (!r->logits || !r->ids || r->ld_logits < r->experts) return FP4_ERR_INVALID;
     if (!aligned(r->logits, r->dtype == FP4_BF16 ? 2 : 4) || !aligned(r->ids, 4) || !aligned(r->bias, 4))

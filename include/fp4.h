@@ -521,7 +521,7 @@ typedef struct fp4_moe_route_args {
  *   with a logit of NaN or +inf the weights are unspecified, and the ids
  *   distinct experts or -1.
  * weights and ids are dense. tokens = 0 is a valid empty call.
- * Errors: FP4_ERR_INVALID, FP4_ERR_UNSUPPORTED (2^26 tokens and more),
+ * Errors: FP4_ERR_INVALID, FP4_ERR_UNSUPPORTED (more than 2^26 - 4 tokens),
  * FP4_ERR_ALIGN (pointers below their elements' size), FP4_ERR_DEVICE,
  * FP4_ERR_HIP.
  */

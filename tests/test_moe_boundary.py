@@ -50,6 +50,16 @@ def test_route_refusals(fp4):
     assert back(tokens=0, logits=None, ids=None) == F.FP4_OK
 
 
+def test_route_tokens_past_the_grid(fp4):
+    """Four tokens a workgroup of 256, and 2^32 - 1 work items in all."""
+    F = fp4
+    for call in (lambda n: F.fp4_moe_route(route_args(F, tokens=n), None),
+                 lambda n: F.fp4_moe_route_backward(route_args(F, tokens=n), FAKE, FAKE, 32, None)):
+        assert call((1 << 26) - 3) == F.FP4_ERR_UNSUPPORTED
+        if NO_GPU:
+            assert call((1 << 26) - 4) == F.FP4_ERR_DEVICE
+
+
 def test_group_refusals(fp4):
     F = fp4
     ws = F.fp4_moe_group_workspace(100000, 64)
