@@ -1189,14 +1189,15 @@ def moe_dispatch(x, groups: MoeGroups, *, stream=None):
         ld_out, ld_out2 = code_pitch(width), scale_pitch(blocks)
         rows = first.new_empty((pairs, ld_out))[:, :width]
         scales = first.new_empty((pairs, ld_out2))[:, :blocks]
-        st = lib().fp4_moe_dispatch(tokens, max(top_k, 1), at_place, at_kept, width, first.data_ptr(), ld, rows.data_ptr(),
-                              ld_out, blocks, x.scales.data_ptr(), ld2, scales.data_ptr(), ld_out2, raw)
+        st = lib().fp4_moe_dispatch(tokens if pairs else 0, max(top_k, 1), at_place, at_kept, width, first.data_ptr(), ld,
+                                    rows.data_ptr(), ld_out, blocks, x.scales.data_ptr(), ld2, scales.data_ptr(),
+                                    ld_out2, raw)
     else:
         _kv_dtype(x, "x")
         es = x.element_size()
         rows = x.new_empty((pairs, width))
-        st = lib().fp4_moe_dispatch(tokens, max(top_k, 1), at_place, at_kept, width * es, x.data_ptr(), ld * es,
-                              rows.data_ptr(), width * es, 0, None, 0, None, 0, raw)
+        st = lib().fp4_moe_dispatch(tokens if pairs else 0, max(top_k, 1), at_place, at_kept, width * es, x.data_ptr(),
+                                    ld * es, rows.data_ptr(), width * es, 0, None, 0, None, 0, raw)
     if st != FP4_OK:
         raise Fp4Error(st, "fp4_moe_dispatch")
     return Quantized(x.fmt, rows, scales, x.tensor_scale) if packed else rows
@@ -1249,8 +1250,9 @@ def moe_combine(rows, weights=None, groups: Optional[MoeGroups] = None, *, out=N
         ld_out = _matrix(out, index, "out", rows.dtype)
         if out.shape != (tokens, width):
             raise ValueError(f"out must be [{tokens}, {width}]")
-    st = lib().fp4_moe_combine(dt, tokens, max(top_k, 1), width, rows.data_ptr(), ld, rows.shape[0], at_place, at_kept, at_w,
-                         out.data_ptr(), ld_out, raw)
+    # (without slots no row has a part)
+    st = lib().fp4_moe_combine(dt, tokens, max(top_k, 1), width, rows.data_ptr(), ld, rows.shape[0] if top_k else 0,
+                               at_place, at_kept, at_w, out.data_ptr(), ld_out, raw)
     if st != FP4_OK:
         raise Fp4Error(st, "fp4_moe_combine")
     return out
@@ -1274,10 +1276,11 @@ def moe_combine_backward(grad_out, rows, weights=None, groups: Optional[MoeGroup
     if groups is not None and rows.shape[0] != tokens * top_k:
         raise ValueError(f"{rows.shape[0]} rows for {tokens} tokens of {top_k}")
     grad_rows = rows.new_empty(shape)
-    grad_w = None if weights is None else torch.empty_like(weights)
-    st = lib().fp4_moe_combine_backward(dt, tokens, max(top_k, 1), width, grad_out.data_ptr(), ld_grad, rows.data_ptr(), ld,
-                                  rows.shape[0], at_place, at_kept, at_w, grad_rows.data_ptr(), width,
-                                  grad_w.data_ptr() if grad_w is not None else None, raw)
+    # (rows without columns: an empty call, which writes nothing)
+    grad_w = None if weights is None else torch.empty_like(weights) if width else torch.zeros_like(weights)
+    st = lib().fp4_moe_combine_backward(dt, tokens, max(top_k, 1), width, grad_out.data_ptr(), ld_grad, rows.data_ptr(),
+                                        ld, rows.shape[0], at_place, at_kept, at_w, grad_rows.data_ptr(), width,
+                                        grad_w.data_ptr() if grad_w is not None else None, raw)
     if st != FP4_OK:
         raise Fp4Error(st, "fp4_moe_combine_backward")
     return grad_rows, grad_w

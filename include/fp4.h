@@ -631,18 +631,18 @@ typedef struct fp4_matvec_args {
  * bytes are all the work: they are read in 4 bits, once, and the activations
  * are not quantized, nor rounded at all (fp32 as three bf16 terms that hold
  * its 24 bits). Sums in fp32, y rounded once. The work grows with every 16
- * rows (8 of fp32); past some dozens (of one matrix) fp4_gemm and fp4_gemm_grouped on
- * quantized activations are faster.
+ * rows (8 of fp32); past some dozens (of one matrix) fp4_gemm and
+ * fp4_gemm_grouped on quantized activations are faster.
  *   ids outside [0, experts) give rows of zeros. Limits (beyond:
- *   FP4_ERR_UNSUPPORTED): 2^20 - 16 pairs, 2^19 - 8 of fp32, with ids 4096; N 2^26 - 64; K 2^24;
- *   row pitches of codes and scales below 8 MiB.
+ *   FP4_ERR_UNSUPPORTED): 2^20 - 16 pairs, 2^19 - 8 of fp32, with ids 4096;
+ *   N 2^26 - 64; K 2^24; row pitches of codes and scales below 8 MiB.
  *   Weights quantized with FP4_HADAMARD stand for rotated ones: x has to be
  *   rotated by the same signs.
  * x 16-byte aligned with a row pitch of whole 16 bytes; codes and scales
  * 16-byte aligned, their pitches and expert strides multiples of 16, their rows
- * readable up to the next multiple of 16 bytes, as for fp4_gemm. Errors: FP4_ERR_INVALID, FP4_ERR_UNSUPPORTED, FP4_ERR_ALIGN,
- * FP4_ERR_DEVICE, FP4_ERR_HIP. pairs = 0 or N = 0 is a valid empty call;
- * K = 0 gives zeros.
+ * readable up to the next multiple of 16 bytes, as for fp4_gemm. Errors:
+ * FP4_ERR_INVALID, FP4_ERR_UNSUPPORTED, FP4_ERR_ALIGN, FP4_ERR_DEVICE,
+ * FP4_ERR_HIP. pairs = 0 or N = 0 is a valid empty call; K = 0 gives zeros.
  */
 fp4_status fp4_matvec(const fp4_matvec_args* args, void* stream);
 

@@ -196,3 +196,22 @@ def test_places_outside_the_rows_are_passed_over(fp4):
     assert out[:, 0].tolist() == [2, 1, 1, 0]
     gr, gw = fp4.moe_combine_backward(x, torch.ones(8, H).cuda(), torch.ones(T, k).cuda(), g)
     assert gw[1, 1] == gw[2, 0] == gw[3, 0] == gw[3, 1] == 0 and torch.equal(gr[3], x[2])
+
+
+def test_no_slots_and_no_columns(fp4):
+    """Tokens without a slot get zeros, weights of rows without columns a gradient of zero."""
+    ids = torch.empty(5, 0, dtype=torch.int32, device="cuda")
+    g = fp4.moe_group(ids, 4)
+    assert g.offsets.tolist() == [0] * 5 and g.place.shape == (5, 0)
+    x = torch.randn(5, 24, device="cuda")
+    assert fp4.moe_dispatch(x, g).shape == (0, 24)
+    none = torch.empty(5, 0, device="cuda")
+    for rows in (torch.empty(0, 24, device="cuda"), torch.ones(3, 24, device="cuda")):
+        out = torch.full((5, 24), 7.0, device="cuda")
+        assert (fp4.moe_combine(rows, none, g, out=out) == 0).all()
+    gr, gw = fp4.moe_combine_backward(x, torch.empty(0, 24, device="cuda"), none, g)
+    assert gr.shape == (0, 24) and gw.shape == (5, 0)
+    torch.full((10,), 7.0, device="cuda")  # (what an uninitialised result would show)
+    gr, gw = fp4.moe_combine_backward(torch.empty(5, 0, device="cuda"), torch.empty(10, 0, device="cuda"),
+                                      torch.ones(5, 2, device="cuda"))
+    assert gr.shape == (10, 0) and (gw == 0).all()
