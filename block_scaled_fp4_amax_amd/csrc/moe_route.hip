@@ -592,8 +592,8 @@ __global__ __launch_bounds__(256, 4) void route_kernel(RouteArgs a) {
 // scaled dw of the chosen and 0 elsewhere, sigmoid g_e s (1 - s); with it, and
 // q_j the chosen scores over their sum, softmax q_j (g_j - sum q g), sigmoid
 // that times (1 - s_j). One pass: the row is read once and written once.
-// 16384 tokens of 160 fp32 logits, 6 chosen: 10.0 us, 2.1 TB/s (21 MB; a copy
-// takes 4.3): bound by vector instructions, 745 a wave (57 % of the cycles), that
+// 16384 tokens of 160 fp32 logits, 6 chosen: 8.2 us, 2.6 TB/s (21 MB; a copy
+// takes 4.3): bound by vector instructions, 592 a wave (57 % of the cycles), that
 // stand behind one trip to memory. (As two passes over the row: 22.)
 template <int L, int VPL>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackwardArgs b) {
@@ -716,10 +716,19 @@ bool wide_route(const RouteArgs& a) { return a.experts > 256 || a.groups > 16; }
 
 // The gradient, which has no steps from choice to choice, does gain from a
 // wave's shorter turns up to some thousand tokens of many experts: 64 tokens of
-// 256 4.3 us, rows 4.9; 4096 of them 5.6 and 6.3; 16384 of 160 12.9 and 10.7.
+// 256 4.3 us, rows 4.9; 4096 of them 5.6 and 6.3; 4096 of 160 4.9 and 5.2.
 // (64 experts: 3.8 and 3.2.)
 bool wide_backward(const RouteArgs& a) {
   return a.experts > 256 || (a.experts > 64 && a.tokens <= 16 * device_cu_count());
+}
+
+// Experts for each lane of a row of 16. 12 spare a quarter of the work of 16
+// where they suffice and split no groups of whole lanes (the gradient of 16384
+// tokens of 160 8.2 us for 10.0, the choice of 192 in 8 groups 15.4 for 24.2).
+int row_share(const RouteArgs& a) {
+  const int per = (a.experts + 15) / 16;
+  if (per > 8 && per <= 12 && !(a.top_groups < a.groups && a.group_size % 16 == 0)) return 12;
+  return per <= 1 ? 1 : per <= 2 ? 2 : per <= 4 ? 4 : per <= 8 ? 8 : 16;
 }
 
 // What depends on the lanes' shares: 16-byte rows, and lanes that make a group.
@@ -727,9 +736,7 @@ void set_shares(RouteArgs& a) {
   const int64_t piece = a.bf16 ? 8 : 16;  // of four logits
   a.vec = (uintptr_t)a.logits % piece == 0 && (a.ld * (a.bf16 ? 2 : 4)) % piece == 0 && a.experts % 4 == 0;
   a.vec_bias = (uintptr_t)a.bias % 16 == 0 && a.experts % 4 == 0;
-  int vpl = 1;
-  while (vpl * 16 < a.experts) vpl *= 2;
-  const int q = a.group_size / vpl;
+  const int vpl = row_share(a), q = a.group_size / vpl;
   a.lanes_of_group = a.group_size % vpl == 0 && (q & (q - 1)) == 0 && q <= 8 ? q : 0;
 }
 
@@ -742,12 +749,14 @@ hipError_t route_by_size(bool wide, const RouteArgs& a, const ARGS& args, hipStr
     if (per <= 8) return LAUNCH<64, 8>::go(args, a.tokens, s);
     return LAUNCH<64, 16>::go(args, a.tokens, s);
   }
-  const int per = (a.experts + 15) / 16;
-  if (per <= 1) return LAUNCH<16, 1>::go(args, a.tokens, s);
-  if (per <= 2) return LAUNCH<16, 2>::go(args, a.tokens, s);
-  if (per <= 4) return LAUNCH<16, 4>::go(args, a.tokens, s);
-  if (per <= 8) return LAUNCH<16, 8>::go(args, a.tokens, s);
-  return LAUNCH<16, 16>::go(args, a.tokens, s);
+  switch (row_share(a)) {
+    case 1: return LAUNCH<16, 1>::go(args, a.tokens, s);
+    case 2: return LAUNCH<16, 2>::go(args, a.tokens, s);
+    case 4: return LAUNCH<16, 4>::go(args, a.tokens, s);
+    case 8: return LAUNCH<16, 8>::go(args, a.tokens, s);
+    case 12: return LAUNCH<16, 12>::go(args, a.tokens, s);
+    default: return LAUNCH<16, 16>::go(args, a.tokens, s);
+  }
 }
 
 template <int L, int VPL>

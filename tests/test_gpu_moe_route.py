@@ -61,6 +61,9 @@ CASES = [
     (9, 257, 9, dict(score="sigmoid", groups=1)),
     (31, 240, 6, dict(groups=24, top_groups=7, best=2)),
     (31, 200, 15, dict(score="sigmoid", groups=40, top_groups=17)),
+    (600, 190, 13, dict(score="sigmoid")),
+    (601, 192, 8, dict(score="sigmoid", groups=8, top_groups=4, best=2, scale=2.5)),
+    (37, 144, 6, dict(groups=9, top_groups=4, best=2)),
     # more tokens
     (1500, 8, 2, dict()),
     (1501, 16, 16, dict(score="sigmoid")),
@@ -153,8 +156,8 @@ def near_ranks(T, E, score, bias, groups, top_groups, best):
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("with_bias", [False, True])
-@pytest.mark.parametrize("E,groups,top_groups,best", [(256, 8, 4, 2), (64, 8, 3, 2), (160, 10, 4, 2), (96, 3, 1, 2),
-                                                      (32, 16, 5, 2), (40, 5, 2, 2), (640, 20, 6, 2)])
+@pytest.mark.parametrize("E,groups,top_groups,best", [(256, 8, 4, 2), (64, 8, 3, 2), (160, 10, 4, 2), (192, 8, 4, 2),
+                                                      (96, 3, 1, 2), (32, 16, 5, 2), (40, 5, 2, 2), (640, 20, 6, 2)])
 def test_groups_are_those_of_the_exact_ranks(fp4, E, groups, top_groups, best, with_bias, score):
     bias = 0.1 * torch.randn(E, generator=torch.Generator().manual_seed(8)) if with_bias else None
     z = near_ranks(300, E, score, bias, groups, top_groups, best)
