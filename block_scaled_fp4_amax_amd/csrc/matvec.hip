@@ -19,13 +19,14 @@
 //     the cycles (every weight scaled and rounded), matrix ones 20 %; experts of over 8 pairs read again
 #include "fp4_device.h"
 #include "launch.h"
+#include "matvec_plan.h"
 
 namespace fp4impl {
 using namespace fp4dev;
 
 namespace {
 
-constexpr int kUnit = 512;  // K of a wave's unit: four pieces of 128, 256 bytes of each row's codes
+constexpr int kUnit = kMatvecUnit;
 
 // What the kernels take: sizes in 32 bits, and what only sizes decide.
 struct Call {
@@ -40,10 +41,7 @@ struct Call {
   int units;                        // of K
   uint32_t last_code, last_scale;   // where a row's last 16 bytes start
   int y_bf16;
-  int part_shift;  // 2^part_shift waves share a tile of W
-  int seg_units;   // units of x in LDS at once
-  int at_once;     // a wave's weights are all loaded before the first product
-  int rounds;      // tiles of W a wave takes one after another
+  int part_shift, seg_units, at_once, rounds;  // as in MatvecPlan
 };
 
 // The eight values of a word of codes, times their block's scale: exact in
@@ -165,9 +163,9 @@ __device__ __forceinline__ u32x4 at16(const uint8_t* p) { return *reinterpret_ca
 // banks. Terms of fp32 are rows like others: one matrix instruction multiplies
 // all three, and their sums are added at the end. Behind the rows: zeros, as
 // many as a unit of a row has bytes.
-constexpr int kZeros = kUnit * 2;
+constexpr int kZeros = kMatvecZeros;
 template <bool XBF, int RG>
-constexpr int kOpRows = (XBF ? 1 : 3) * 4 * RG;
+constexpr int kOpRows = matvec_op_rows(XBF, RG);
 
 // fp32 rows on their way to LDS: a lane's eight numbers at k of two rows, of
 // which `live` are there (what the others hold meets only results that nobody
@@ -231,7 +229,7 @@ __device__ __forceinline__ void copy_x(const Call& a, int64_t xo, int row, int u
 // (With 16 rows that would take four such products, and scaling the weights
 // costs no more.)
 template <bool NV, bool XBF, int RG>
-constexpr bool diagonal = NV && XBF && RG <= 2;
+constexpr bool diagonal = matvec_diagonal(NV, XBF, RG);
 
 template <bool NV, bool XBF, int RG>
 struct Product {
@@ -427,17 +425,6 @@ __device__ __forceinline__ int64_t x_offset(const Call& a, int pair) {
   return row * a.ld_x;
 }
 
-// Units of bf16 calls that a wave loads before its first product, if it has no
-// more (fp32 rows need the registers for themselves).
-template <bool NV>
-constexpr int kAtOnce = NV ? 2 : 3;
-
-// LDS for seg_units units of x, and zeros where an operand needs them.
-template <bool NV, bool XBF, int RG>
-__host__ __device__ constexpr int x_bytes(int seg_units) {
-  return kOpRows<XBF, RG> * (seg_units * (kUnit * 2) + 16) + (diagonal<NV, XBF, RG> ? kZeros : 0);
-}
-
 // Up to 4 RG pairs of one expert (its list, or else pairs `first` on) against
 // the workgroup's tiles of W: `rounds` times W >> part_shift, one after another,
 // each wave with the next unit's weights on their way while it multiplies, over
@@ -450,7 +437,7 @@ __device__ __forceinline__ void tiles_of(const Call& a, int expert, const uint16
   const int c16 = lane & 15, g = lane >> 4;
   const int per = W >> a.part_shift, parts = 1 << a.part_shift, part = wave & (parts - 1);
   const int units = a.units, pitch = a.seg_units * (kUnit * 2) + 16;
-  float* red = reinterpret_cast<float*>(lds + x_bytes<NV, XBF, RG>(a.seg_units));  // [W][MR][16], if parts > 1
+  float* red = reinterpret_cast<float*>(lds + matvec_x_bytes(NV, XBF, RG, a.seg_units));  // [W][MR][16], if parts > 1
   int n0 = (blockIdx.x * a.rounds * per + (wave >> a.part_shift)) * 16;
   auto offset_of = [&](int row) {
     const int pair = LIST ? (int)list[row] : first + row;
@@ -529,7 +516,7 @@ __device__ __forceinline__ void tiles_of(const Call& a, int expert, const uint16
   };
   // A wave of few units has all their weights on the way at once.
   if constexpr (XBF) if (a.at_once) {
-    constexpr int AT_ONCE = kAtOnce<NV>;
+    constexpr int AT_ONCE = matvec_at_once(NV);
     Weights<NV> w[AT_ONCE];
 #pragma unroll
     for (int d = 0; d < AT_ONCE; d++) {
@@ -594,69 +581,12 @@ __global__ __launch_bounds__(64 * W, 4) void matvec_experts_kernel(Call a) {
 
 namespace {
 
-constexpr int kLds = 160 * 1024, kLdsApart = 4 * 1024;  // of a CU; kept for what is not x
-
 template <bool NV, bool XBF, int RG, int W>
-hipError_t launch_waves(Call& c, int tiles, int slots, hipStream_t s) {
-  const int cus = device_cu_count();
-  constexpr int red = W * RG * 256, all = 16 / W;  // (sums of the waves of a tile; workgroups a CU)
-  constexpr int room = (kLds / all - kLdsApart / (W < 8 ? 2 : 1) - red) / (kOpRows<XBF, RG> * kUnit * 2);
-  auto units_of = [&](int shift) { return (c.units + (1 << shift) - 1) >> shift; };  // a wave's
-  auto at_once = [&](int shift) { return XBF && units_of(shift) <= kAtOnce<NV>; };
-  // Waves for a tile: as many as leave the workgroups room on the GPU at once
-  // (one a tile: 1 x 4096x4096 13.6 us for 5.4, 16 x 8192x8192 48 for 15; as
-  // many as W has: 8 x 4 of 32 experts 54.6 for 42), or twice that where a wave
-  // then has all its weights on the way at once (1 x 28672x4096 14.3 us for
-  // 16.9). No more than x in LDS has units for.
-  c.part_shift = 0;
-  for (; (2 << c.part_shift) <= (W < room ? W : room) && (1 << c.part_shift) < c.units; c.part_shift++) {
-    const int64_t blocks = ((int64_t)tiles * slots * (2 << c.part_shift) + W - 1) / W;
-    const bool more = at_once(c.part_shift + 1) && !at_once(c.part_shift);
-    if (blocks > (more ? 2 : 1) * all * cus) break;
-  }
-  // (all of x, or else whole turns of the waves)
-  c.seg_units = c.units < room ? c.units : room >> c.part_shift << c.part_shift;
-  // Tiles one after another, once there are more workgroups than twice what
-  // fits at once: each would bring x anew (32 x 4 of 32 experts 5760x2880 MXFP4
-  // 60 us, else 63; fp32 rows of 2880x2880 51, else 54; 8 x 4 NVFP4 42 and 39).
-  // Not where x does not fit: every tile would bring all of it again.
-  c.rounds = 1;
-  int per = W >> c.part_shift;
-  while (c.part_shift == 0 && c.seg_units == c.units && (int64_t)((tiles + per - 1) / per) * slots > 2 * all * cus) {
-    per += W;
-    c.rounds++;
-  }
-  // (1 x 4096x4096 5.4 us for 6.0, 4 x 1024x4096 5.6 for 6.4, 32 x 4096x4096 8.1 for 9.4)
-  c.at_once = at_once(c.part_shift) && c.rounds == 1 && c.units > 0 &&
-              (c.units <= c.seg_units || (c.seg_units & ((1 << c.part_shift) - 1)) == 0);
-  const dim3 grid((tiles + per - 1) / per, slots), block(64 * W);
-  int lds = x_bytes<NV, XBF, RG>(c.seg_units) + (c.part_shift > 0 ? red : 0);
-  if (c.ids) {
-    lds = lds > 2 * c.experts + 2 ? lds : 2 * c.experts + 2;
-    hipLaunchKernelGGL((matvec_experts_kernel<NV, XBF, RG, W>), grid, block, lds, s, c);
-  } else {
-    hipLaunchKernelGGL((matvec_kernel<NV, XBF, RG, W>), grid, block, lds, s, c);
-  }
+hipError_t launch_form(const Call& c, const MatvecPlan& p, hipStream_t s) {
+  const dim3 grid((unsigned)p.grid_x, (unsigned)p.slots), block(64 * W);
+  if (c.ids) hipLaunchKernelGGL((matvec_experts_kernel<NV, XBF, RG, W>), grid, block, p.lds, s, c);
+  else hipLaunchKernelGGL((matvec_kernel<NV, XBF, RG, W>), grid, block, p.lds, s, c);
   return hipGetLastError();
-}
-
-// Waves of a workgroup: 16 share one copy of x, but wait for all of it and for
-// each other. Eight where two such workgroups have room on a CU with all of x
-// (1 x 4096x4096 5.4 us, 16 waves 6.9; 32 x 4 of 32 experts 5760x2880 60 and 99).
-// Four where that leaves room too and there are tiles for half the GPU's eight
-// waves a CU (1 x 4 of 32 experts 5760x2880 9.5 us, 8 waves 11.6; 2 x 8 of 128
-// experts 1536x4096 14.0 and 15.8).
-template <bool NV, bool XBF, int RG>
-hipError_t launch_rows(Call& c, int tiles, int slots, hipStream_t s) {
-  const int x = x_bytes<NV, XBF, RG>(c.units);
-  if constexpr (RG == 1) {
-    if ((int64_t)tiles * slots * 2 >= 8 * device_cu_count() && x + 4 * RG * 256 <= kLds / 4 - kLdsApart / 2)
-      return launch_waves<NV, XBF, RG, 4>(c, tiles, slots, s);
-  }
-  if constexpr (RG < 4) {
-    if (x + 8 * RG * 256 <= kLds / 2 - kLdsApart) return launch_waves<NV, XBF, RG, 8>(c, tiles, slots, s);
-  }
-  return launch_waves<NV, XBF, RG, 16>(c, tiles, slots, s);
 }
 
 template <bool NV, bool XBF>
@@ -681,29 +611,25 @@ hipError_t launch(const MatvecArgs& a, hipStream_t s) {
   c.N = (int)a.N;
   c.K = (int)a.K;
   c.experts = a.experts;
-  c.units = (int)((a.K + kUnit - 1) / kUnit);
   c.last_code = last16(a.K / 2);
   c.last_scale = last16(a.K / blk);
   c.y_bf16 = a.y_bf16;
-  const int tiles = (c.N + 15) / 16;
-  // experts that may have pairs, and how many slots of `rows` pairs there are at most
-  const int met = a.ids ? (c.pairs < c.experts ? c.pairs : c.experts) : 1;
-  auto slots = [&](int rows) {
-    if (!a.ids) return (c.pairs + rows - 1) / rows;
-    return met + c.pairs / rows < c.pairs ? met + c.pairs / rows : c.pairs;
-  };
-  // Rows a pass, by how many an expert has on average (some have twice that):
-  // 4 cost least where they suffice (16 rows four at a time: the weights four
-  // times); of 32 experts with 4 pairs each, slots of 8 take 60 us and of 4 77,
-  // with fp32 rows 51 and 57. 16 x 5760x2880 as 16 rows 9.1 us, 8 and 8 11.0;
-  // 32 x 4096x4096 8.1 and 10.1. fp32 rows come no more than 8 at a time: 16
-  // are 48 operand rows, and LDS then holds 1024 of K (16 x 4096x4096 27 us for
-  // 13, 12 x 8192x8192 59 for 28).
-  if (c.pairs <= (a.ids ? 2 : 4) * met) return launch_rows<NV, XBF, 1>(c, tiles, slots(4), s);
-  if constexpr (XBF) {
-    if (c.pairs > 8 * met) return launch_rows<NV, XBF, 4>(c, tiles, slots(16), s);
+  const MatvecPlan p =
+      plan_matvec(MatvecSizes{NV, XBF, a.ids != nullptr, a.pairs, a.N, a.K, a.experts, device_cu_count()});
+  c.units = p.units;
+  c.part_shift = p.part_shift;
+  c.seg_units = p.seg_units;
+  c.at_once = p.at_once;
+  c.rounds = p.rounds;
+  if (p.rg == 1) {
+    if (p.waves == 4) return launch_form<NV, XBF, 1, 4>(c, p, s);
+    if (p.waves == 8) return launch_form<NV, XBF, 1, 8>(c, p, s);
+    return launch_form<NV, XBF, 1, 16>(c, p, s);
   }
-  return launch_rows<NV, XBF, 2>(c, tiles, slots(8), s);
+  if constexpr (XBF) {
+    if (p.rg == 4) return launch_form<NV, XBF, 4, 16>(c, p, s);
+  }
+  return p.waves == 8 ? launch_form<NV, XBF, 2, 8>(c, p, s) : launch_form<NV, XBF, 2, 16>(c, p, s);
 }
 
 }  // namespace
