@@ -318,6 +318,12 @@ struct Elements {
 
 __device__ __forceinline__ int64_t pair_row(const CombineArgs& a, int64_t p) { return a.place ? (int64_t)a.place[p] : p; }
 
+// Rows that have a part: 0 to num_rows, whatever *kept says.
+__device__ __forceinline__ int64_t rows_kept(const CombineArgs& a) {
+  const int64_t n = a.kept ? *a.kept : a.num_rows;
+  return n < 0 ? 0 : n < a.num_rows ? n : a.num_rows;
+}
+
 }  // namespace
 
 // One lane, 16 bytes of one token's row: each slot's row in turn, four of them on
@@ -330,7 +336,7 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
   const int64_t t = blockIdx.x;
   const int64_t i = ((int64_t)blockIdx.y * 256 + threadIdx.x) * N;
   if (i >= a.width) return;
-  const int64_t kept = a.kept && *a.kept < a.num_rows ? *a.kept : a.num_rows;
+  const int64_t kept = rows_kept(a);
   constexpr int64_t size = BF16 ? 2 : 4;
   Elements<BF16> sum, x;
 #pragma unroll
@@ -359,7 +365,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(CombineBackwardAr
   constexpr int N = Elements<BF16>::N;
   const CombineArgs& a = b.a;
   const int64_t t = blockIdx.x;
-  const int64_t kept = a.kept && *a.kept < a.num_rows ? *a.kept : a.num_rows;
+  const int64_t kept = rows_kept(a);
   constexpr int64_t size = BF16 ? 2 : 4;
   const char* g = reinterpret_cast<const char*>(b.grad) + t * b.ld_grad * size;
   const int j0 = blockIdx.y * kBackPairs;
