@@ -44,10 +44,30 @@ struct Call {
   int part_shift, seg_units, at_once, rounds;  // as in MatvecPlan
 };
 
+// NVFP4's tensor scale in two: a power of two that multiplies the codes, as the
+// scale operand of their conversion, and the rest, which multiplies the sums.
+// The power is below the scale, so that no sum is larger than the terms it
+// stands for (without, it holds up to 2688 / max |W| times as much), and at most
+// 2^-7, so that a block's sum without its scale (16 codes of 6) stays finite
+// for every finite x. For scales below 2^-39 it is 2^-40, which no sum of 2^24
+// weights of 2688 overflows either, and small products keep their bits.
+struct TensorScale {
+  float unit;
+  float rest, wide;  // (wide: 2^7 where `rest` times that could overflow)
+  __device__ __forceinline__ TensorScale(float ts) {
+    const int e = (int)((__builtin_bit_cast(uint32_t, ts) >> 23) & 255u) - 128;  // 2^e is up to half of |ts|
+    const int p = e < -40 ? -40 : e > -7 ? -7 : e;
+    unit = power(p);
+    rest = e > -7 ? ts : ts * power(-p);
+    wide = e > -7 ? power(-p) : 1.0f;
+  }
+  static __device__ __forceinline__ float power(int p) { return __builtin_bit_cast(float, (uint32_t)(p + 127) << 23); }
+};
+
 // The eight values of a word of codes, times their block's scale: exact in
-// bf16 (E2M1 has 2 significant bits, E4M3 4).
+// bf16 (E2M1 has 2 significant bits, E4M3 4). unit: of NVFP4, above.
 template <bool NV>
-__device__ __forceinline__ bf16x8 weights8(uint32_t w, float scale) {
+__device__ __forceinline__ bf16x8 weights8(uint32_t w, float scale, float unit) {
   uint32_t o[4];
   if constexpr (!NV) {
     o[0] = e2m1_unpack2_bf16<0>(w, scale);
@@ -55,7 +75,8 @@ __device__ __forceinline__ bf16x8 weights8(uint32_t w, float scale) {
     o[2] = e2m1_unpack2_bf16<2>(w, scale);
     o[3] = e2m1_unpack2_bf16<3>(w, scale);
   } else {
-    const f32x2 v[4] = {e2m1_unpack2<0>(w), e2m1_unpack2<1>(w), e2m1_unpack2<2>(w), e2m1_unpack2<3>(w)};
+    const f32x2 v[4] = {e2m1_unpack2<0>(w, unit), e2m1_unpack2<1>(w, unit), e2m1_unpack2<2>(w, unit),
+                        e2m1_unpack2<3>(w, unit)};
 #pragma unroll
     for (int i = 0; i < 4; i++)
       o[i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)(v[i].x * scale), (__bf16)(v[i].y * scale)});
@@ -254,7 +275,7 @@ struct Product {
     for (int o = 0; o < OT; o++) acc[o] = f32x4{0, 0, 0, 0};
   }
   // One unit, which starts at k0 and is unit `at` of x in LDS.
-  __device__ __forceinline__ void multiply(const Weights<NV>& o, int k0, int K, int at, const uint8_t* lds) {
+  __device__ __forceinline__ void multiply(const Weights<NV>& o, int k0, int K, int at, const uint8_t* lds, float unit) {
     const int g = (threadIdx.x & 63) >> 4;
     const uint8_t* x[OT];
 #pragma unroll
@@ -267,7 +288,7 @@ struct Product {
       if constexpr (DIAG) {
         bf16x8 w[4];
 #pragma unroll
-        for (int j = 0; j < 4; j++) w[j] = weights8<false>(codes[j], 1.0f);
+        for (int j = 0; j < 4; j++) w[j] = weights8<false>(codes[j], unit, 1.0f);
 #pragma unroll
         for (int i = 0; i < OT; i++) {
           f32x4 d0 = {0, 0, 0, 0}, d1 = {0, 0, 0, 0};
@@ -281,7 +302,7 @@ struct Product {
       } else {
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-          const bf16x8 w = weights8<NV>(codes[j], j < 2 ? sc.x : sc.y);
+          const bf16x8 w = weights8<NV>(codes[j], j < 2 ? sc.x : sc.y, unit);
 #pragma unroll
           for (int i = 0; i < OT; i++) acc[i] = mfma(at16(x[i] + u * 256 + j * 16), w, acc[i]);
         }
@@ -473,7 +494,11 @@ __device__ __forceinline__ void tiles_of(const Call& a, int expert, const uint16
   Place at(a, expert, n0);
   Product<NV, XBF, RG> rows(pitch);
   rows.clear();
-  const float ts = NV ? a.ts[expert] : 1.0f;
+  // (by a scalar load, which is waited for where `stage` says so: the compiler
+  // would load it as a vector and wait for that, and all of x before it, ahead
+  // of the weights: 1 x 28672x4096 16.9 us for 15.4)
+  float ts = 1.0f, power = 1.0f;
+  if constexpr (NV) ts = reinterpret_cast<const __attribute__((address_space(4))) float*>((uintptr_t)a.ts)[expert];
   auto stage = [&](int u0, bool loaded) {
     const int here = units - u0 < a.seg_units ? units - u0 : a.seg_units;
     if (!loaded) __syncthreads();
@@ -489,6 +514,10 @@ __device__ __forceinline__ void tiles_of(const Call& a, int expert, const uint16
       }
     }
     __syncthreads();
+    if (NV && loaded) {
+      asm volatile("" : "+s"(ts));
+      power = TensorScale(ts).unit;
+    }
   };
   // the sums of a tile, over its waves, to y
   auto finish = [&]() {
@@ -506,11 +535,12 @@ __device__ __forceinline__ void tiles_of(const Call& a, int expert, const uint16
         }
       }
     }
+    const TensorScale scale(ts);
     if (part == 0 && g < RG && n0 + c16 < a.N) {
 #pragma unroll
       for (int r = 0; r < 4; r++) {
         const int row = 4 * g + r;
-        if (row < live) store_y(a, LIST ? list[row] : first + row, n0 + c16, acc[r] * ts);
+        if (row < live) store_y(a, LIST ? list[row] : first + row, n0 + c16, NV ? acc[r] * scale.rest * scale.wide : acc[r]);
       }
     }
   };
@@ -528,7 +558,7 @@ __device__ __forceinline__ void tiles_of(const Call& a, int expert, const uint16
       if (u >= units) break;
       const int u0 = u < a.seg_units ? 0 : u / a.seg_units * a.seg_units;
       if (u == u0) stage(u0, d == 0);
-      if (u + part < units) rows.multiply(w[d], (u + part) * kUnit, a.K, u + part - u0, lds);
+      if (u + part < units) rows.multiply(w[d], (u + part) * kUnit, a.K, u + part - u0, lds, power);
     }
     finish();
     return;
@@ -546,7 +576,7 @@ __device__ __forceinline__ void tiles_of(const Call& a, int expert, const uint16
         Weights<NV> next;
         const bool over = unit + parts >= units;  // (of the last tile: bytes that nobody uses)
         next.load(a, over ? after : at, over && !last_tile ? part * kUnit : (unit + parts) * kUnit, g);
-        rows.multiply(now, unit * kUnit, a.K, unit - u0, lds);
+        rows.multiply(now, unit * kUnit, a.K, unit - u0, lds, power);
         now = next;
       }
     }

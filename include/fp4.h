@@ -630,7 +630,10 @@ typedef struct fp4_matvec_args {
  * for the steps of a decoder that have one token or a few, where the weights'
  * bytes are all the work: they are read in 4 bits, once, and the activations
  * are not quantized, nor rounded at all (fp32 as three bf16 terms that hold
- * its 24 bits). Sums in fp32, y rounded once. The work grows with every 16
+ * its 24 bits). Sums in fp32, y rounded once. y is finite where the sum of
+ * |deq(W_e) x| is below 2^128, whatever the block and tensor scales; the sums
+ * keep nothing of products below 2^-141 (of NVFP4 with tensor scales from 2^-7
+ * on: below 2^-132 times that scale). The work grows with every 16
  * rows (8 of fp32); past some dozens (of one matrix) fp4_gemm and
  * fp4_gemm_grouped on quantized activations are faster.
  *   ids outside [0, experts) give rows of zeros. Limits (beyond:

@@ -1,0 +1,84 @@
+"""Products of a few rows at the ends of fp32's range. Sums are fp32 and hold
+no more than the products they stand for: where the sum of magnitudes is finite,
+y is, within the bound of test_gpu_matvec.py ((2 K + 4) 2^-24 of that sum, one
+rounding of y), and at the lower end within K 2^-139 besides."""
+import numpy as np
+import pytest
+import torch
+
+import moe_util as M
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+ROWS = (1, 6, 12)  # passes of 4, 8 and 16 rows
+
+
+def check(y, x, W):
+    """y fp32. Elements whose magnitudes sum up to more than fp32 holds are passed over; returns how many are left."""
+    x, y = x.double().cpu().numpy(), y.double().cpu().numpy()
+    want, size = x @ W.T, np.abs(x) @ np.abs(W).T
+    fits = size * (1 + (2 * x.shape[1] + 4) * U) < 2.0 ** 128 * (1 - U)
+    tol = (2 * x.shape[1] + 4) * U * size + U * np.abs(want) + x.shape[1] * 2.0 ** -139
+    err = np.abs(y - want)
+    assert (err <= tol)[fits].all(), f"worst {np.nanmax((err / tol)[fits]):.3g} of the bound, {np.isnan(y[fits]).sum()} NaN"
+    return fits.sum()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("weight", [1e-3, 0.1, 20.0])
+def test_nvfp4_holds_no_more_than_its_products(fp4, rows, weight, dtype):
+    """Activations up to fp32's largest against weights far below 2688 times the tensor scale's reciprocal."""
+    N, K = 40, 96
+    g = torch.Generator().manual_seed(rows)
+    q = fp4.quantize((weight * torch.randn(N, K, generator=g)).cuda(), "nvfp4")
+    W = M.values(q)
+    for size in (1e35, 1e36, 1e37):
+        x = torch.randn(rows, K, generator=g).clamp(-3, 3) * size
+        x[:, 5::7] = 3.3e38 / max(1.0, 200 * weight)
+        x = x.to(DT[dtype]).cuda()
+        many = check(fp4.matvec(x, q, out_dtype=torch.float32), x, W)
+        assert many == rows * N or weight > 1
+        one = torch.zeros(rows, K)
+        one[:, 11] = torch.linspace(0.3, 1.0, rows) * 3.3e38 / max(1.0, weight)
+        one = one.to(DT[dtype]).cuda()
+        assert check(fp4.matvec(one, q, out_dtype=torch.float32), one, W) > 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", ROWS)
+def test_nvfp4_tensor_scales_of_every_size(fp4, rows, dtype):
+    """Blocks with every E4M3 scale under tensor scales over fp32's whole range, activations as large as leave y finite."""
+    N, K = 32, 128
+    g = torch.Generator().manual_seed(7)
+    codes = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, generator=g).cuda()
+    s = torch.zeros(N, 16, dtype=torch.uint8)
+    s[:, :K // 16] = torch.arange(N * K // 16).view(N, -1) % 127
+    x = torch.randn(rows, K, generator=g)
+    for e in (-149, -130, -120, -100, -60, -42, -41, -40, -39, -38, -20, -9, -8, -7, -6, -5, 0, 20, 90, 116, 120, 121, 126):
+        ts = torch.tensor([2.0 ** e * (1.0 if e < -126 else 1.37)], dtype=torch.float64).float().cuda()
+        q = fp4.Quantized(fp4.FP4_NVFP4, codes, s.cuda()[:, :K // 16], ts)
+        W = M.values(q)
+        largest = min(2.0 ** 126, 2.0 ** 127 / np.abs(W).sum(1).max()) / 4
+        for size in (largest, 1.0 if largest > 1 else largest * 2.0 ** -10):
+            z = (x * size).to(DT[dtype]).cuda()
+            assert check(fp4.matvec(z, q, out_dtype=torch.float32), z, W) == rows * N, e
+    q = fp4.Quantized(fp4.FP4_NVFP4, codes, s.cuda()[:, :K // 16], torch.zeros(1).cuda())
+    assert (fp4.matvec(x.to(DT[dtype]).cuda(), q) == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_nvfp4_by_experts_of_different_tensor_scales(fp4, dtype):
+    """Each expert's power of two is its own."""
+    E, N, K, T, k = 5, 48, 64, 6, 3
+    g = torch.Generator().manual_seed(3)
+    size = torch.tensor([1e-20, 1e-3, 0.5, 300.0, 1e20])[:, None, None]
+    q = fp4.quantize((size * torch.randn(E, N, K, generator=g)).cuda(), "nvfp4")
+    W = M.values(q)
+    ids = torch.randint(0, E, (T, k), dtype=torch.int32, generator=g)
+    x = (torch.randn(T, K, generator=g) * 1e16).to(DT[dtype]).cuda()
+    y = fp4.matvec(x, q, ids.cuda(), out_dtype=torch.float32)
+    for t in range(T):
+        for j in range(k):
+            check(y[t, j][None], x[t][None], W[ids[t, j]])
