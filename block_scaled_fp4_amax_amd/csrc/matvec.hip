@@ -95,8 +95,9 @@ __device__ __forceinline__ void split3(const u32x4 lo, const u32x4 hi, u32x4 (&t
       const int e = 2 * i + h;
       const uint32_t b0 = e < 4 ? lo[e] : hi[e - 4];
       const float v = __builtin_bit_cast(float, b0);
-      // (an infinity is its first term alone)
-      const float r1 = (b0 & 0x7f800000u) != 0x7f800000u ? v - __builtin_bit_cast(float, b0 & 0xffff0000u) : 0.0f;
+      // (an infinity is its first term alone; a NaN whose first term is an
+      // infinity, since only its low bits say so, is one in the second)
+      const float r1 = __builtin_fabsf(v) != __builtin_inff() ? v - __builtin_bit_cast(float, b0 & 0xffff0000u) : 0.0f;
       const uint32_t b1 = __builtin_bit_cast(uint32_t, r1);
       const float r2 = r1 - __builtin_bit_cast(float, b1 & 0xffff0000u);
       part[0][h] = b0;

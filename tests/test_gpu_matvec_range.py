@@ -82,3 +82,21 @@ def test_nvfp4_by_experts_of_different_tensor_scales(fp4, dtype):
     for t in range(T):
         for j in range(k):
             check(y[t, j][None], x[t][None], W[ids[t, j]])
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("rows", ROWS)
+def test_any_nan_is_a_nan(fp4, fmt, rows):
+    """Also one that only the lower 16 bits tell from an infinity."""
+    q = fp4.quantize(torch.randn(40, 128, generator=torch.Generator().manual_seed(2)).cuda(), fmt)
+    for bits in (0x7f800001, 0xff800001, 0x7f80ffff, 0xff808000, 0x7f810000, 0x7fc00000, 0xffffffff):
+        x = torch.ones(rows, 128)
+        x[rows - 1, 77] = torch.tensor(bits - (1 << 32) if bits >> 31 else bits, dtype=torch.int32).view(torch.float32)
+        y = fp4.matvec(x.cuda(), q)
+        assert y[rows - 1].isnan().all() and y[:rows - 1].isfinite().all(), hex(bits)
+    for inf in (torch.inf, -torch.inf):
+        x = torch.zeros(rows, 128)
+        x[rows - 1, 77] = inf
+        y = fp4.matvec(x.cuda(), q)[rows - 1].cpu()
+        w = torch.from_numpy(M.values(q)[:, 77])
+        assert torch.equal(y.nan_to_num(nan=7.0, posinf=1.0, neginf=-1.0), torch.where(w == 0, 7.0, torch.sign(w * inf)).float())
