@@ -84,8 +84,12 @@ __device__ __forceinline__ bf16x8 weights8(uint32_t w, float scale, float unit) 
   return __builtin_bit_cast(bf16x8, u32x4{o[0], o[1], o[2], o[3]});
 }
 
-// Eight fp32 numbers as three bf16 terms that hold all their 24 bits: each the
-// leading 8 bits of what is left, cut off, so that nothing overflows.
+// Eight fp32 numbers as three bf16 terms that hold all their bits from 2^-148
+// on: each the leading 8 bits of what is left, cut off, so that nothing
+// overflows, and what is left times a power of two (kLeft: 2^7 and 2^8, 2^15 in
+// all), no larger than the number itself. Without it, terms of numbers below
+// 2^-110 would lie under bf16's smallest number.
+constexpr float kLeft[2] = {0x1p7f, 0x1p8f};
 __device__ __forceinline__ void split3(const u32x4 lo, const u32x4 hi, u32x4 (&t)[3]) {
 #pragma unroll
   for (int i = 0; i < 4; i++) {
@@ -97,9 +101,9 @@ __device__ __forceinline__ void split3(const u32x4 lo, const u32x4 hi, u32x4 (&t
       const float v = __builtin_bit_cast(float, b0);
       // (an infinity is its first term alone; a NaN whose first term is an
       // infinity, since only its low bits say so, is one in the second)
-      const float r1 = __builtin_fabsf(v) != __builtin_inff() ? v - __builtin_bit_cast(float, b0 & 0xffff0000u) : 0.0f;
+      const float r1 = __builtin_fabsf(v) != __builtin_inff() ? (v - __builtin_bit_cast(float, b0 & 0xffff0000u)) * kLeft[0] : 0.0f;
       const uint32_t b1 = __builtin_bit_cast(uint32_t, r1);
-      const float r2 = r1 - __builtin_bit_cast(float, b1 & 0xffff0000u);
+      const float r2 = (r1 - __builtin_bit_cast(float, b1 & 0xffff0000u)) * kLeft[1];
       part[0][h] = b0;
       part[1][h] = b1;
       part[2][h] = __builtin_bit_cast(uint32_t, r2);
@@ -327,14 +331,15 @@ struct Product {
       if constexpr (RG == 2) acc[0] = g == 1 ? acc[1] : acc[0];
     } else if constexpr (!XBF) {
       // operand row term * 4 RG + m: group o * 4 + g is term (o * 4 + g) / RG
+      constexpr float second = 1.0f / kLeft[0], third = second / kLeft[1];
 #pragma unroll
       for (int r = 0; r < 4; r++) {
         float v = acc[0][r];
         if constexpr (RG == 1) {
-          v = g < 3 ? v : 0.0f;
+          v = g == 0 ? v : g == 1 ? v * second : g == 2 ? v * third : 0.0f;
           v += xor_shfl<16>(v);
         } else {
-          v += g < 2 ? acc[1][r] : 0.0f;
+          v = g < 2 ? v + acc[1][r] * third : v * second;
         }
         v += xor_shfl<32>(v);
         acc[0][r] = v;

@@ -629,16 +629,16 @@ typedef struct fp4_matvec_args {
  *   y[p, n] = sum_k deq(W_e)[n, k] * x[p / repeat, k],  e = ids[p],
  * for the steps of a decoder that have one token or a few, where the weights'
  * bytes are all the work: they are read in 4 bits, once, and the activations
- * are not quantized, nor rounded at all (fp32 as three bf16 terms that hold
- * its 24 bits). Sums in fp32, y rounded once. y is finite where the sum of
- * |deq(W_e) x| is below 2^128, whatever the block and tensor scales; the sums
- * keep nothing of products below 2^-141 (of NVFP4 with tensor scales from 2^-7
- * on: below 2^-132 times that scale). The work grows with every 16
+ * are not quantized, nor rounded (fp32 as three bf16 terms that hold its 24
+ * bits, as far as they lie above 2^-149). Sums in fp32, y rounded once. y is
+ * finite where the sum of |deq(W_e) x| is below 2^128, whatever the block and
+ * tensor scales; small products lose up to 2^-139 each (in NVFP4 with tensor
+ * scales from 2^-7 on 2^-132 times that scale). The work grows with every 16
  * rows (8 of fp32); past some dozens (of one matrix) fp4_gemm and
  * fp4_gemm_grouped on quantized activations are faster.
  *   ids outside [0, experts) give rows of zeros. Limits (beyond:
  *   FP4_ERR_UNSUPPORTED): 2^20 - 16 pairs, 2^19 - 8 of fp32, with ids 4096;
- *   N 2^26 - 64; K 2^24; row pitches of codes and scales below 8 MiB.
+ *   N 2^26 - 16; K below 2^24, with row pitches of codes and scales below 8 MiB.
  *   Weights quantized with FP4_HADAMARD stand for rotated ones: x has to be
  *   rotated by the same signs.
  * x 16-byte aligned with a row pitch of whole 16 bytes; codes and scales

@@ -100,3 +100,58 @@ def test_any_nan_is_a_nan(fp4, fmt, rows):
         y = fp4.matvec(x.cuda(), q)[rows - 1].cpu()
         w = torch.from_numpy(M.values(q)[:, 77])
         assert torch.equal(y.nan_to_num(nan=7.0, posinf=1.0, neginf=-1.0), torch.where(w == 0, 7.0, torch.sign(w * inf)).float())
+
+
+def large_weights(fp4, N, K, byte, seed=5):
+    """MXFP4 weights with the scale 2^(byte - 127) everywhere."""
+    codes = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, generator=torch.Generator().manual_seed(seed)).cuda()
+    return fp4.Quantized(fp4.FP4_MXFP4, codes, torch.full((N, 16), byte, dtype=torch.uint8).cuda()[:, :K // 32], None)
+
+
+@pytest.mark.parametrize("rows", ROWS)
+def test_small_fp32_activations_keep_their_bits(fp4, rows):
+    """Down to 2^-148: one activation alone is its product with a weight, rounded
+    in sums of three terms (exact products, two additions); the bit of 2^-149 may be cut off."""
+    N, K = 48, 64
+    g = torch.Generator().manual_seed(rows)
+    q = large_weights(fp4, N, K, 230)  # 2^103
+    W = M.values(q)
+    for e in (-100, -108, -110, -112, -116, -120, -124, -125, -126, -130, -140, -148, -149):
+        x = torch.zeros(rows, K)
+        x[:, 11] = ((1 + torch.rand(rows, generator=g).double()) * 2.0 ** e).float()
+        y = fp4.matvec(x.cuda(), q).double().cpu().numpy()
+        want = x[:, 11:12].double().numpy() * W[None, :, 11]
+        assert (np.abs(y - want) <= 2 * U * np.abs(want) + 2.0 ** -149 * np.abs(W[None, :, 11])).all(), e
+        full = (torch.randn(rows, K, generator=g).double() * 2.0 ** e).float()
+        y = fp4.matvec(full.cuda(), q).double().cpu().numpy()
+        want, size = full.double().numpy() @ W.T, full.abs().double().numpy() @ np.abs(W).T
+        assert (np.abs(y - want) <= (2 * K + 4) * U * size + 2.0 ** -149 * np.abs(W).sum(1)).all(), e
+
+
+@pytest.mark.parametrize("rows", ROWS)
+def test_small_bf16_activations(fp4, rows):
+    """bf16 rows are operands as they are, subnormal numbers too."""
+    N, K = 48, 64
+    g = torch.Generator().manual_seed(rows)
+    for q in (large_weights(fp4, N, K, 230), fp4.quantize((1e30 * torch.randn(N, K, generator=g)).cuda(), "nvfp4")):
+        W = M.values(q)
+        for e in (-110, -126, -128, -131):
+            x = (torch.randn(rows, K, generator=g).double() * 2.0 ** e).bfloat16()
+            want, size = x.double().numpy() @ W.T, x.abs().double().numpy() @ np.abs(W).T
+            y = fp4.matvec(x.cuda(), q, out_dtype=torch.float32).double().cpu().numpy()
+            lost = 2.0 ** -132 * K * (float(q.tensor_scale) if q.tensor_scale is not None else 0.0)
+            assert (np.abs(y - want) <= (2 * K + 4) * U * size + lost).all(), e
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("byte", [0, 1, 2, 3, 5])
+def test_smallest_scales_of_mxfp4(fp4, byte, rows, dtype):
+    """Weights that are subnormal in bf16."""
+    N, K = 48, 64
+    q = large_weights(fp4, N, K, byte)
+    x = (torch.randn(rows, K, generator=torch.Generator().manual_seed(rows)) * 1e30).to(DT[dtype])
+    W = M.values(q)
+    want, size = x.double().numpy() @ W.T, x.abs().double().numpy() @ np.abs(W).T
+    y = fp4.matvec(x.cuda(), q, out_dtype=torch.float32).double().cpu().numpy()
+    assert (np.abs(y - want) <= (2 * K + 4) * U * size).all()
