@@ -492,8 +492,10 @@ __global__ __launch_bounds__(256, 4) void route_kernel(RouteArgs a) {
   if (limited) {
     float gap, size;
     in = keep_groups<L, VPL>(a, c, lane, &gap, &size);
-    // a rank of two scores: each with its error, and three roundings
-    if (group_score) sure = !(gap <= 4.0f * unsure + 0x1p-22f * size);
+    // two ranks of two scores: each score with its error and the rounding of
+    // its bias (2^-24 size), each sum with one (2^-23 size); and what the
+    // bound's own arithmetic rounds
+    if (group_score) sure = !(gap <= 4.0f * unsure + 0x1.01p-21f * size);
     if (L == 16 && !sure && a.lanes_of_group > 0) {
       const double inv_sum = a.sigmoid ? 1.0 : 1.0 / softmax_sum<L>(l, m, spare);
       in = keep_lane_exactly<VPL>(a, row, c, lane, m, inv_sum, close) ? ~0u : 0u;
