@@ -224,6 +224,10 @@ template <typename T>
 __device__ __forceinline__ T group_rank(const RouteArgs& a, T b1, T b2, T* mag) {
   const bool two = a.best == 2 && b2 > -(T)__builtin_inff();
   *mag = __builtin_elementwise_max(__builtin_elementwise_abs(b1), two ? __builtin_elementwise_abs(b2) : (T)0);
+  if constexpr (sizeof(T) == 4) {
+    // (a sum beyond fp32 is a group too, and one whose order is unsure: the gap to its like is 0)
+    return two ? __builtin_amdgcn_fmed3f(b1 + b2, -FLT_MAX, FLT_MAX) : b1;
+  }
   return two ? b1 + b2 : b1;
 }
 

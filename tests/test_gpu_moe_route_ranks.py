@@ -55,3 +55,26 @@ def test_large_biases_of_either_sign(fp4, score, size):
     for best in (1, 2):
         check(fp4, z, 6, bias, score=score, groups=8, top_groups=3, best=best)
         check(fp4, z, 6, bias, score=score, groups=16, top_groups=5, best=best)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(32, 4), (24, 3), (60, 5), (256, 8), (640, 20)])
+def test_ranks_beyond_fp32(fp4, score, E, groups):
+    """A bias of the type's lowest number is no mask: its experts fill the slots
+    that others leave, though the sum of two lies beyond fp32. So at the other end."""
+    gs, low = E // groups, torch.finfo(torch.float32).min
+    z = torch.randn(200, E, generator=torch.Generator().manual_seed(E))
+    bias = torch.zeros(E)
+    bias[gs:] = low
+    check(fp4, z, min(gs + 2, 32), bias, score=score, groups=groups, top_groups=2, best=2)
+    check(fp4, z, 4, bias, score=score, groups=groups, top_groups=1, best=2)
+    bias[:] = low
+    check(fp4, z, 4, bias, score=score, groups=groups, top_groups=2, best=2)
+    bias[gs:2 * gs] = -torch.inf                       # and one group that is masked
+    check(fp4, z, 4, bias, score=score, groups=groups, top_groups=2, best=2)
+    bias = torch.zeros(E)
+    bias[:gs], bias[gs:2 * gs] = 2e38, 3e38            # 4e38 and 6e38
+    bias[2 * gs], bias[2 * gs + 1] = 3.3e38, 1e38      # 4.3e38
+    for top in (1, 2):
+        check(fp4, z, 4, bias, score=score, groups=groups, top_groups=top, best=2)
+    check(fp4, z, 4, -bias, score=score, groups=groups, top_groups=groups - 1, best=2)
