@@ -1329,7 +1329,7 @@ def matvec(x, w: Quantized, ids=None, *, out_dtype=None, out=None, stream=None):
         elif ids.shape != lead and (len(lead) != 1 or ids.numel() != lead[0]):
             raise ValueError("x must be [tokens, K] or [tokens, top_k, K] for ids [tokens, top_k]")
         lead = ids.shape
-    flat = x if x.dim() == 2 else x.reshape(-1, K)
+    flat = x if x.dim() == 2 else x.reshape(x.shape[:-1].numel(), K)
     ld, es = flat.stride(0) if flat.shape[0] > 1 else K, x.element_size()
     if (K > 1 and flat.stride(1) != 1) or ld < K or (ld * es) % 16 or flat.data_ptr() % 16:
         flat = flat.clone(memory_format=torch.contiguous_format)
@@ -1343,7 +1343,7 @@ def matvec(x, w: Quantized, ids=None, *, out_dtype=None, out=None, stream=None):
     else:
         if out.shape != (*lead, N) or out.get_device() != index or (out_dtype or out.dtype) is not out.dtype:
             raise ValueError(f"out must be {(*lead, N)} on the same GPU")
-        rows = out.view(-1, N)
+        rows = out.view(pairs, N)
         ld_y = rows.stride(0) if pairs > 1 else N
         if N > 1 and rows.stride(1) != 1:
             raise ValueError("out rows must be contiguous")
