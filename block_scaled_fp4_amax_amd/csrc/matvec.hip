@@ -10,12 +10,16 @@
 // one along K and their sums are added up in LDS, always in one order.
 //
 // What bounds it (MI355X; bytes at the 5.08 TB/s of a large copy):
-//   1 x 4096x4096 NVFP4, bf16        5.7 us  floor 1.9: launch, x to LDS, one trip to memory
-//   1 x 28672x4096 NVFP4, bf16      14.5 us        13.0: memory
-//   16 x 8192x8192 MXFP4, bf16      15.0 us         7.1: x to LDS (256 KB in two parts), then weights
-//   1 x 4 of 32 experts 5760x2880   10.0 us         6.9: memory and one trip to it
+//   1 x 4096x4096 NVFP4, bf16        5.4 us  floor 1.9: launch, x to LDS, one trip to memory
+//   1 x 28672x4096 NVFP4, bf16      14.2 us        13.0: memory
+//   16 x 8192x8192 MXFP4, bf16      15.6 us         7.1: x to LDS (256 KB in two parts), then weights
+//   16 x 4096x4096 NVFP4, fp32      15.1 us         2.0: each workgroup (128 in all) brings x,
+//     in two parts, and cuts it into terms; the weights are read for each pass of 8 rows
+//   12 x 8192x8192 NVFP4, fp32      27.0 us         7.6: the same, in four parts; vector
+//     instructions 62 % of the cycles
+//   1 x 4 of 32 experts 5760x2880    9.7 us         6.9: memory and one trip to it
 //   8 x 4 of 32 experts 5760x2880   43   us        38.7: memory
-//   32 x 4 of 32 experts 2880x2880, fp32 rows, NVFP4  49 us  29.6: vector instructions 59 % of
+//   32 x 4 of 32 experts 2880x2880, fp32 rows, NVFP4  51 us  29.6: vector instructions 59 % of
 //     the cycles (every weight scaled and rounded), matrix ones 20 %; experts of over 8 pairs read again
 #include "fp4_device.h"
 #include "launch.h"

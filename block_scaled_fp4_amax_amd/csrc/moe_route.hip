@@ -12,11 +12,11 @@
 // zero), turned so that the larger double is the better candidate and, of
 // equal values, the lower index: one v_max_f64 compares both.
 //
-// The choice is that of the exact numbers. Without a bias the order of the
-// scores is that of the logits, which are compared as they are. With one (or
-// where a group's rank is a sum of two scores) c is computed in fp32 with a
-// known error; where two neighbours of the resulting order lie within it, those
-// few candidates (or the best scores of each group) are done again in double.
+// Without a bias the order of the scores is that of the logits, which are
+// compared as they are. With one (or where a group's rank is a sum of two
+// scores) c is computed in fp32 with a known error; where two neighbours of the
+// resulting order lie within it, those few candidates (or the best scores of
+// each group) are done again in double, so that the choice is that of c in double.
 //
 // Bound by vector instructions, about 1700 a wave where four tokens have 256
 // experts in groups: 16384 tokens of 256 fp32 logits (17.8 MB, which a copy

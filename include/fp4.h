@@ -512,10 +512,13 @@ typedef struct fp4_moe_route_args {
  *   of the top_groups groups with the largest ranks, the top_k largest c, best
  *   first; w_j = scale * s_ij, divided by the sum of the chosen s if
  *   FP4_MOE_RENORMALIZE.
- * Equal values go to the lowest index (of experts and of groups). Values are
- * compared as exact numbers: without a bias by the logits themselves, else
- * by scores whose fp32 rounding does not decide (rows where it could are done
- * in fp64). Weights are accurate to fp32.
+ * Equal values go to the lowest index (of experts and of groups). Without a
+ * bias experts, and groups by their best one, are compared by the logits
+ * themselves. Else by scores in fp64: fp32's roundings do not decide (rows where
+ * they could are done again), but scores that fp64 cannot tell apart are equal,
+ * as logistic ones of logits beyond 37, which are all 1 there. A weight is within
+ * (48 + 2 d) 2^-24 of its own size (and 1e-30), d its logit's distance from the
+ * largest of the row.
  *   An expert whose logit or bias is -inf or NaN is never chosen; where fewer
  *   than top_k can be, the remaining slots get id -1 and weight 0. In a row
  *   with a logit of NaN or +inf the weights are unspecified, and the ids
